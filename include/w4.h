@@ -379,6 +379,166 @@ int w4_nf4_gemv(const uint16_t* x, int64_t K, const uint8_t* packed, const uint8
                 int64_t N, uint16_t* y, hipStream_t stream);
 
 /*
+ * Decoding around the products: a paged cache of keys and values, attention
+ * over it for decode steps, drafted trees and prompt chunks, token choice, and
+ * keeping the accepted path of a tree.  They serve the loop the products run
+ * in (gowda.ai "LLM fast inference", "Runtime": paged KV, graph replay); the
+ * 8-bit cache follows gsantana.dev "Quantizing LLMs Without Guesswork", "KV
+ * cache".
+ *
+ * w4_kv_cache describes the caller's cache (a HOST struct; k, v and the scales
+ * are device pointers).  A page holds page_size tokens of every KV head, as
+ * blocks of 16 tokens.  With e = 16 / bytes per element (8 for bf16, 16 for
+ * E4M3) the arrays are, for each layer,
+ *   k [pages, kv_heads, page_size/16, head_dim/e, 16, e]
+ *       (token s of its block, dim d) at [d / e, s, d % e],
+ *   v [pages, kv_heads, page_size/16, 16/e, head_dim, e]
+ *       (token s of its block, dim d) at [s / e, d, s % e]:
+ * 16-byte pieces that are the matrix cores' operands of both products of
+ * attention as they lie (along the dims for K, along the tokens for V).
+ * Slot n of a layer is token n % page_size of page n / page_size; token i of
+ * sequence b is token i % page_size of page page_table[b, i / page_size].
+ * E4M3 values stand for code * k_scale[head] (v_scale for V).
+ *   head_dim 64, 128 or 256; page_size a multiple of 16 up to 1024; kv_heads >= 1;
+ *   layers >= 1 (w4_kv_move moves in all of them; the other calls take one
+ *   layer); pages * page_size < 2^31.
+ */
+#define W4_KV_BF16 0
+#define W4_KV_E4M3 1
+typedef struct {
+    void* k;
+    void* v;
+    const float* k_scale;    /* [kv_heads] fp32, positive; NULL for bf16 and for w4_kv_move */
+    const float* v_scale;
+    int64_t pages;
+    int32_t layers;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t dtype;           /* W4_KV_BF16 or W4_KV_E4M3 */
+} w4_kv_cache;
+
+/*
+ * w4_kv_append -- one pass over the rows of a QKV product: query and key heads
+ * are optionally RMS-normed, then rotated by position; queries go to Q, keys
+ * and values into the cache.  Per token t and head, in fp32 with one rounding
+ * at the end:
+ *   y = x                                  (norm weight NULL)
+ *   y = x / sqrt(mean(x^2) + eps) * w      (w fp32 [head_dim])
+ *   z_a = y_a cos - y_b sin,  z_b = y_b cos + y_a sin   over the first `rot`
+ *     dims, with (a, b) = (j, j + rot/2) or, interleaved, (2j, 2j + 1), and
+ *     cos = rope[p, j], sin = rope[p, rot/2 + j], p = positions[t], j < rot/2;
+ *   Q and a bf16 cache: bf16(z); an E4M3 cache: e4m3(z / k_scale[head])
+ *   saturating at +-448 (NaN stays NaN).  Values are stored without norm and
+ *   rotation.
+ *   q, k, v    bf16 rows [T, heads, head_dim] whose rows are q_stride (...)
+ *              elements apart, a multiple of 8 (views of one [T, (Hq + 2 Hk)
+ *              head_dim] product, say); q and Q may both be NULL: append only.
+ *   Q          [T, Hq, head_dim] bf16 out, contiguous; may be q itself if
+ *              q_stride == Hq * head_dim.
+ *   slots      [T] int32: the cache slot of each token; negative or past the
+ *              cache: the token is not stored (padding).  No two tokens share a
+ *              slot.
+ *   rope       [rope_rows, rot] fp32, 16-byte aligned, with positions [T]
+ *              int32; both NULL: no rotation.  rot a multiple of 16 up to
+ *              head_dim.  A position outside the table gives NaN in the
+ *              rotated dims, never a read outside it.
+ *   q_norm, k_norm   fp32 [head_dim], 16-byte aligned, or NULL.
+ */
+int w4_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                 int64_t v_stride, int64_t T, int Hq, const w4_kv_cache* cache, const int32_t* slots,
+                 const float* rope, int64_t rope_rows, int rot, int interleaved, const int32_t* positions,
+                 const float* q_norm, const float* k_norm, float eps, uint16_t* Q, hipStream_t stream);
+
+/*
+ * w4_tree_attention -- attention of each sequence's last tokens over its
+ * cached keys and values.  Sequence b has the rows q_start[b] .. q_start[b+1]
+ * - 1 of q (its nodes) and kv_len[b] cached tokens, the nodes' own keys and
+ * values the last of them (appended before the call); with n nodes the tokens
+ * below past = kv_len[b] - n are its context.  Node i sees
+ *   - every token j < past, and of the nodes those whose bit is set in its
+ *     mask (tree), or nodes 0 .. i without one (tree NULL: a decode step, a
+ *     prompt chunk);
+ *   - with window > 0 only tokens whose position is > its own - window; a
+ *     context token's position is its index, a node's positions[row] (NULL,
+ *     allowed without a tree: past + i).
+ * For query head h on KV head h / (Hq / kv_heads):
+ *   O = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale (q . k_j) - max),
+ * softmax statistics and sums in fp32, p rounded to bf16 as the operand of the
+ * second product, one rounding to bf16 at the end.  A node that sees nothing
+ * gets zeros.  Keys and values that a node does not see do not reach its
+ * output, whatever they hold (infinities and NaN included).
+ *   q            [T, Hq, head_dim] bf16, rows q_stride elements apart (a
+ *                multiple of 8); O [T, Hq, head_dim] bf16, contiguous.  Rows of
+ *                T outside every sequence are not written.
+ *   page_table   [B, table_pages] int32; a page outside the cache counts as
+ *                not seen.
+ *   kv_len [B], q_start [B + 1] int32.  max_q and max_kv bound the sequences'
+ *                nodes and lengths from above (they set the launch; a sequence
+ *                over them is cut to them).  max_kv <= table_pages * page_size.
+ *   tree         [T, tree_words] uint64: bit j % 64 of word j / 64 is node j
+ *                of the row's sequence; tree_words >= ceil(max_q / 64).
+ *   Hq           a multiple of kv_heads.
+ *   scale        of q . k (1 / sqrt(head_dim) usually), finite.
+ *   workspace    w4_tree_attention_workspace_bytes bytes, 16-byte aligned, its
+ *                contents irrelevant: fp32 partial results where the cached
+ *                tokens of a sequence are split over workgroups; joined in a
+ *                fixed order, so results do not depend on timing.  Too small or
+ *                NULL when needed: W4_EINVAL.
+ */
+int w4_tree_attention(const uint16_t* q, int64_t q_stride, int64_t T, int Hq, const w4_kv_cache* cache,
+                      const int32_t* page_table, int64_t table_pages, const int32_t* kv_len, const int32_t* q_start,
+                      int64_t B, int64_t max_q, int64_t max_kv, const uint64_t* tree, int tree_words,
+                      const int32_t* positions, int64_t window, float scale, uint16_t* O, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+/* Bytes of workspace w4_tree_attention needs (0: none): a function of these
+ * sizes only. */
+size_t w4_tree_attention_workspace_bytes(int64_t T, int64_t B, int Hq, int kv_heads, int head_dim, int dtype,
+                                         int64_t max_q, int64_t max_kv, int64_t window);
+
+/*
+ * w4_sample -- one token per row of logits from one given uniform number per
+ * row.  With x the row (NaN counts as -inf), m its maximum and T its
+ * temperature, tokens are ordered by x descending, then by index; each has the
+ * whole-number weight
+ *   w = rint(2^31 exp((x - m) (1 / T)))   (fp32; (x - m) rounded, then the product)
+ * of which top_k keeps the first k, top_p the shortest prefix of those whose
+ * weight reaches p of theirs (at least one token), min_p those with w >= min_p
+ * 2^31.  The token is the first, in index order, up to which the kept weights
+ * sum to more than floor(u total), u and p taken in units of 2^-24.  Sums of
+ * whole numbers do not depend on their order: the same inputs give the same
+ * token on every launch shape.  T = 0 takes the largest logit's lowest index.
+ *   logits       bf16 or fp32 (W4_LOGITS_*), [B, V], rows row_stride elements
+ *                apart; V <= 2^20.  The rows need no alignment beyond the
+ *                element's; `logits` itself is 16-byte aligned.
+ *   u            [B] fp32 in [0, 1).
+ *   temperature, top_p, min_p  [B] fp32, top_k [B] int32; each may be NULL: 1,
+ *                1, 0, none.  top_k <= 0: none.  temperature >= 0.
+ *   tokens       [B] int32 out; -1 for a row without any weight (all -inf).
+ *   probs        [B] fp32 out, the token's share of the kept weight; or NULL.
+ *   workspace    w4_sample_workspace_bytes bytes, 16-byte aligned, contents
+ *                irrelevant.
+ */
+#define W4_LOGITS_BF16 0
+#define W4_LOGITS_F32 1
+int w4_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride, const float* u,
+              const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+              int32_t* tokens, float* probs, void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t w4_sample_workspace_bytes(int64_t B, int64_t V);
+
+/*
+ * w4_kv_move -- keep an accepted path: in every layer, the token base[b] +
+ * path[b, j] of sequence b moves to base[b] + j, for j < count[b], keys and
+ * values alike.  path rows ascend strictly (path[b, j] >= j), so no token is
+ * overwritten before it has moved.  Tokens outside the page table or on a page
+ * outside the cache are left alone.
+ *   cache        all layers, one after the other in k and v.
+ *   base, count  [B] int32;  path [B, path_len] int32, count[b] <= path_len.
+ */
+int w4_kv_move(const w4_kv_cache* cache, const int32_t* page_table, int64_t table_pages, const int32_t* base,
+               const int32_t* path, int64_t path_len, const int32_t* count, int64_t B, hipStream_t stream);
+
+/*
  * Portable on-disk form of a quantized weight (gowda.ai "LLM fast inference",
  * "MSE clipping", last paragraph: the packed codes, scales and zero terms are
  * exported once in a portable representation and rearranged into the GPU
@@ -425,7 +585,8 @@ const char* w4_status_string(int status);
  * (thread-local storage, valid until the next failing call). */
 const char* w4_last_error(void);
 
-/* Version of this ABI, currently 4 (4: w4a16_gate_up takes an optional
+/* Version of this ABI, currently 4; it counts changes of calls that were there,
+ * so the decoding calls, added since, kept it (4: w4a16_gate_up takes an optional
  * workspace, w4a16_gate_up_workspace_bytes; 3: w4a8_gate_up emits the down
  * projection's E4M3 input; w4a8_gemm_e4m3; w4a16_gemm_noalloc). */
 int w4_abi_version(void);

@@ -24,6 +24,8 @@ __all__ = [
     "w4a16_gate_up", "w4a16_gate_up_workspace_bytes", "w4a8_gate_up", "w4a8_gate_up_workspace_bytes", "w4a8_gemm_e4m3", "ACT_SILU", "ACT_GELU_TANH",
     "w4_nf4_levels", "w4_nf4_quantize", "w4_nf4_gemv",
     "FRACS_PLAIN", "FRACS_11",
+    "w4_kv_cache", "w4_kv_append", "w4_tree_attention", "w4_tree_attention_workspace_bytes", "w4_sample",
+    "w4_sample_workspace_bytes", "w4_kv_move",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -55,6 +57,14 @@ class _PortableInfo(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("G", ctypes.c_int32), ("mode", ctypes.c_int32),
                 ("n_fracs", ctypes.c_int32), ("has_clip", ctypes.c_int32), ("payload_bytes", ctypes.c_uint64),
                 ("fracs", ctypes.c_float * MAX_FRACS)]
+
+
+class _KvCache(ctypes.Structure):
+    """``w4_kv_cache`` of ``include/w4.h``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("layers", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -106,6 +116,17 @@ def lib():
         getattr(L, name).restype = I
     for name in ("w4_quantize_blockwise", "w4_mse_clip_search", "w4_prepack", "w4_quantize_rows_e4m3",
                  "w4a16_gemm", "w4a8_gemm"):
+        getattr(L, name).restype = I
+    f32, C = ctypes.c_float, ctypes.POINTER(_KvCache)
+    L.w4_kv_append.argtypes = [P, i64, P, i64, P, i64, i64, I, C, P, P, i64, I, I, P, P, P, f32, P, P]
+    L.w4_tree_attention.argtypes = [P, i64, i64, I, C, P, i64, P, P, i64, i64, i64, P, I, P, i64, f32, P, P, sz_t, P]
+    L.w4_tree_attention_workspace_bytes.argtypes = [i64, i64, I, I, I, I, i64, i64, i64]
+    L.w4_tree_attention_workspace_bytes.restype = sz_t
+    L.w4_sample.argtypes = [P, I, i64, i64, i64, P, P, P, P, P, P, P, P, sz_t, P]
+    L.w4_sample_workspace_bytes.argtypes = [i64, i64]
+    L.w4_sample_workspace_bytes.restype = sz_t
+    L.w4_kv_move.argtypes = [C, P, i64, P, P, i64, P, i64, P]
+    for name in ("w4_kv_append", "w4_tree_attention", "w4_sample", "w4_kv_move"):
         getattr(L, name).restype = I
     L.w4_status_string.argtypes = [I]
     L.w4_status_string.restype = ctypes.c_char_p
@@ -558,3 +579,201 @@ def w4_nf4_gemv(x: torch.Tensor, nf4: dict, *, y=None, stream=None):
                            _stream(dev, stream))
     _check("w4_nf4_gemv", rc)
     return y
+
+
+# ------------------------------------------- decoding around the products
+
+def w4_kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int, *, e4m3: bool = False, layers=None,
+                device="cuda"):
+    """A zeroed paged cache ``(k, v)`` in the library's layout (``w4_kv_cache`` in ``w4.h``): bf16, or E4M3
+    codes (uint8).  With ``layers`` the arrays hold that many layers; ``k[i]``, ``v[i]`` is one of them."""
+    c = 16 if e4m3 else 8
+    lead = (pages, kv_heads, page_size // 16)
+    lead = lead if layers is None else (layers, *lead)
+    dtype = torch.uint8 if e4m3 else torch.bfloat16
+    return (torch.zeros((*lead, head_dim // c, 16, c), dtype=dtype, device=device),
+            torch.zeros((*lead, 16 // c, head_dim, c), dtype=dtype, device=device))
+
+
+def _cache_arg(fn: str, k, v, k_scale, v_scale, layers: bool = False):
+    """The C description of a cache (k, v) of ``w4_kv_cache``'s shapes, and its (kv_heads, head_dim, page_size)."""
+    shape, sv = k.shape, v.shape
+    n = len(shape)
+    if n != 6 and not (layers and n == 7):
+        raise ValueError(f"{fn}: k_cache must be [pages, kv_heads, page_size/16, head_dim/c, 16, c]"
+                         f"{' or have the layers first' if layers else ''}, got {tuple(shape)}")
+    pages, heads, blocks, chunks, rows, c = shape[-6:]
+    one_byte = k.element_size() == 1
+    if rows != 16 or c != (16 if one_byte else 8):
+        raise ValueError(f"{fn}: k_cache of {k.dtype} must end in [head_dim/{16 if one_byte else 8}, 16, "
+                         f"{16 if one_byte else 8}], got {tuple(shape)}")
+    if not one_byte and k.dtype != torch.bfloat16:
+        raise ValueError(f"{fn}: the cache must be bf16 or hold one byte per element, got {k.dtype}")
+    if v.dtype != k.dtype or tuple(sv) != (*shape[:-3], 16 // c, chunks * c, c):
+        raise ValueError(f"{fn}: v_cache {tuple(sv)} of {v.dtype} does not belong to k_cache {tuple(shape)} of {k.dtype}")
+    for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if s is not None and s.numel() != heads:
+            raise ValueError(f"{fn}: {name} has {s.numel()} elements, expected {heads}")
+    a = _KvCache(_dev(k, "k_cache"), _dev(v, "v_cache"), _dev(k_scale, "k_scale", torch.float32),
+                 _dev(v_scale, "v_scale", torch.float32), pages, shape[0] if n == 7 else 1, heads, chunks * c,
+                 16 * blocks, 1 if one_byte else 0)
+    return a, heads, chunks * c, 16 * blocks
+
+
+def _rows_arg(fn: str, x, name: str, heads: int, dim: int, T=None):
+    """Pointer and row stride of bf16 rows [T, heads, dim] whose heads are contiguous."""
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or (T is not None and shape[0] != T):
+        raise ValueError(f"{fn}: {name} must be [{'T' if T is None else T}, {heads}, {dim}], got {tuple(shape)}")
+    if x.dtype != torch.bfloat16:
+        raise ValueError(f"{fn}: {name} must be torch.bfloat16, got {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError(f"{fn}: {name} must be a device tensor")
+    st, sh, sd = x.stride()
+    if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
+        raise ValueError(f"{fn}: the heads of a row of {name} must be contiguous (strides {x.stride()})")
+    return x.data_ptr(), (st if shape[0] > 1 else max(st, heads * dim))
+
+
+def _vec(fn: str, x, name: str, n: int, dtype):
+    if x is None:
+        return None
+    if x.numel() != n:
+        raise ValueError(f"{fn}: {name} has {x.numel()} elements, expected {n}")
+    return _dev(x, name, dtype)
+
+
+def w4_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                 k_cache: torch.Tensor, v_cache: torch.Tensor, *, rope=None, positions=None, interleaved: bool = False,
+                 q_norm=None, k_norm=None, eps: float = 1e-6, k_scale=None, v_scale=None, Q=None, stream=None):
+    """Norm (optional) and rotate (optional) the query and key heads of ``q``, ``k`` [T, heads, D]; keys and the
+    values ``v`` go to the cache slots ``slots`` (int32 [T], negative: not stored), the queries are returned
+    (bf16 [T, Hq, D]; None without ``q``).  ``rope`` is fp32 [positions, rot]: rot/2 cosines, then the sines."""
+    fn = "w4_kv_append"
+    cache, hk, dim, _ = _cache_arg(fn, k_cache, v_cache, k_scale, v_scale)
+    T = k.shape[0]
+    kp, ks = _rows_arg(fn, k, "k", hk, dim, T)
+    vp, vs = _rows_arg(fn, v, "v", hk, dim, T)
+    qp, qs, hq, Qp = None, 0, 0, None
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 3 else 0
+        qp, qs = _rows_arg(fn, q, "q", hq, dim, T)
+        if Q is None:
+            Q = torch.empty((T, hq, dim), dtype=torch.bfloat16, device=q.device)
+        elif tuple(Q.shape) != (T, hq, dim):
+            raise ValueError(f"{fn}: Q has shape {tuple(Q.shape)}, expected {(T, hq, dim)}")
+        Qp = _dev(Q, "Q", torch.bfloat16)
+    rot = rows = 0
+    if rope is not None:
+        if rope.dim() != 2:
+            raise ValueError(f"{fn}: rope must be [positions, rot], got {tuple(rope.shape)}")
+        rows, rot = rope.shape
+    rc = lib().w4_kv_append(qp, qs, kp, ks, vp, vs, T, hq, cache, _vec(fn, slots, "slots", T, torch.int32),
+                            _dev(rope, "rope", torch.float32), rows, rot, interleaved,
+                            _vec(fn, positions, "positions", T, torch.int32), _vec(fn, q_norm, "q_norm", dim, torch.float32),
+                            _vec(fn, k_norm, "k_norm", dim, torch.float32), eps, Qp, _stream(k.device, stream))
+    _check(fn, rc)
+    return Q
+
+
+@functools.lru_cache(maxsize=4096)
+def w4_tree_attention_workspace_bytes(T: int, B: int, Hq: int, kv_heads: int, head_dim: int, e4m3: bool, max_q: int,
+                                      max_kv: int, window: int = 0) -> int:
+    """Workspace bytes ``w4_tree_attention`` needs for these sizes (0: none)."""
+    return int(lib().w4_tree_attention_workspace_bytes(T, B, Hq, kv_heads, head_dim, 1 if e4m3 else 0, max_q, max_kv, window))
+
+
+def w4_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                      kv_len: torch.Tensor, q_start: torch.Tensor, max_q: int, max_kv: int, *, tree=None,
+                      positions=None, window: int = 0, scale: Optional[float] = None, k_scale=None, v_scale=None,
+                      O=None, workspace=None, stream=None):
+    """Attention of each sequence's last tokens, ``q`` [T, Hq, D], over its cached keys and values (the tokens'
+    own among them).  Sequence b has rows q_start[b] .. q_start[b + 1] - 1 and kv_len[b] cached tokens on the
+    pages page_table[b] (all int32); ``max_q`` and ``max_kv`` bound them from above.  ``tree``: int64
+    [T, ceil(max_q / 64)] masks of the nodes each node sees; None: a chain.  ``window`` > 0 needs ``positions``
+    (int32 [T]) with a tree.  Returns bf16 [T, Hq, D]."""
+    fn = "w4_tree_attention"
+    cache, hk, dim, page_size = _cache_arg(fn, k_cache, v_cache, k_scale, v_scale)
+    T, Hq = (q.shape[0], q.shape[1]) if q.dim() == 3 else (0, 0)
+    qp, qs = _rows_arg(fn, q, "q", Hq, dim)
+    if page_table.dim() != 2:
+        raise ValueError(f"{fn}: page_table must be [B, pages], got {tuple(page_table.shape)}")
+    B, table_pages = page_table.shape
+    words = 0
+    if tree is not None:
+        if tree.dim() != 2 or tree.shape[0] != T:
+            raise ValueError(f"{fn}: tree must be [{T}, words], got {tuple(tree.shape)}")
+        words = tree.shape[1]
+    if O is None:
+        O = torch.empty((T, Hq, dim), dtype=torch.bfloat16, device=q.device)
+    elif tuple(O.shape) != (T, Hq, dim):
+        raise ValueError(f"{fn}: O has shape {tuple(O.shape)}, expected {(T, Hq, dim)}")
+    if workspace is None:
+        need = w4_tree_attention_workspace_bytes(T, B, Hq, hk, dim, cache.dtype == 1, max_q, max_kv, window)
+        if need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+            if stream is not None:
+                workspace.record_stream(stream)
+    ws_bytes = _nbytes(workspace) if workspace is not None else 0
+    rc = lib().w4_tree_attention(qp, qs, T, Hq, cache, _dev(page_table, "page_table", torch.int32), table_pages,
+                                 _vec(fn, kv_len, "kv_len", B, torch.int32),
+                                 _vec(fn, q_start, "q_start", B + 1, torch.int32), B, max_q, max_kv,
+                                 _dev(tree, "tree", torch.int64), words,
+                                 _vec(fn, positions, "positions", T, torch.int32), window,
+                                 dim ** -0.5 if scale is None else scale, _dev(O, "O", torch.bfloat16),
+                                 _dev(workspace, "workspace"), ws_bytes, _stream(q.device, stream))
+    _check(fn, rc)
+    return O
+
+
+@functools.lru_cache(maxsize=4096)
+def w4_sample_workspace_bytes(B: int, V: int) -> int:
+    """Workspace bytes ``w4_sample`` needs for B rows of V logits."""
+    return int(lib().w4_sample_workspace_bytes(B, V))
+
+
+def w4_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=None, top_k=None, top_p=None, min_p=None,
+              tokens=None, probs=None, workspace=None, stream=None):
+    """One token per row of ``logits`` [B, V] (bf16 or fp32; rows may be strided) from the uniform numbers ``u``
+    [B].  ``temperature``, ``top_p``, ``min_p`` (fp32 [B]) and ``top_k`` (int32 [B]) are per row or None.
+    Returns (tokens int32 [B], probs fp32 [B])."""
+    fn = "w4_sample"
+    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"{fn}: logits must be a device tensor [B, V] with contiguous rows")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{fn}: logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
+    B, V = logits.shape
+    dev = logits.device
+    tokens = _empty((B,), torch.int32, dev) if tokens is None else tokens
+    probs = _empty((B,), torch.float32, dev) if probs is None else probs
+    if workspace is None:
+        need = w4_sample_workspace_bytes(B, V)
+        if need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+            if stream is not None:
+                workspace.record_stream(stream)
+    rc = lib().w4_sample(logits.data_ptr(), 1 if logits.dtype == torch.float32 else 0, B, V,
+                         logits.stride(0) if B > 1 else V,
+                         _vec(fn, u, "u", B, torch.float32), _vec(fn, temperature, "temperature", B, torch.float32),
+                         _vec(fn, top_k, "top_k", B, torch.int32), _vec(fn, top_p, "top_p", B, torch.float32),
+                         _vec(fn, min_p, "min_p", B, torch.float32), _vec(fn, tokens, "tokens", B, torch.int32),
+                         _vec(fn, probs, "probs", B, torch.float32), _dev(workspace, "workspace"),
+                         _nbytes(workspace) if workspace is not None else 0, _stream(dev, stream))
+    _check(fn, rc)
+    return tokens, probs
+
+
+def w4_kv_move(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor, base: torch.Tensor,
+               path: torch.Tensor, count: torch.Tensor, *, stream=None) -> None:
+    """Token base[b] + path[b, j] of sequence b moves to base[b] + j for j < count[b] (int32, path rows strictly
+    ascending), in every layer of the cache ([layers, ...] or one layer)."""
+    fn = "w4_kv_move"
+    cache, _, _, _ = _cache_arg(fn, k_cache, v_cache, None, None, layers=True)
+    if page_table.dim() != 2 or path.dim() != 2 or path.shape[0] != page_table.shape[0]:
+        raise ValueError(f"{fn}: page_table must be [B, pages] and path [B, length], got {tuple(page_table.shape)} and "
+                         f"{tuple(path.shape)}")
+    B, table_pages = page_table.shape
+    rc = lib().w4_kv_move(cache, _dev(page_table, "page_table", torch.int32), table_pages,
+                          _vec(fn, base, "base", B, torch.int32), _dev(path, "path", torch.int32), path.shape[1],
+                          _vec(fn, count, "count", B, torch.int32), B, _stream(k_cache.device, stream))
+    _check(fn, rc)

@@ -22,11 +22,12 @@ PROBE_OUT = os.path.join(HERE, "libw4probe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-KERNELS = ["quantize.hip", "prepack.hip", "rowquant.hip", "skinny.hip", "gemm.hip", "nf4.hip", "noalloc.hip", "gemm_f8.hip"]
+KERNELS = ["quantize.hip", "prepack.hip", "rowquant.hip", "skinny.hip", "gemm.hip", "nf4.hip", "noalloc.hip", "gemm_f8.hip",
+           "kvcache.hip", "attention.hip", "sample.hip"]
 NO_CONTRACT = {"quantize.hip", "rowquant.hip", "nf4.hip"}
 # kernels whose MFMA results take VALU work: results in VGPRs, not AGPRs
-MFMA_VGPR = {"gemm_f8.hip"}
-HOST_SOURCES = ["api.cpp", "portable.cpp"]   # host C++ (argument checks, file I/O)
+MFMA_VGPR = {"gemm_f8.hip", "attention.hip"}
+HOST_SOURCES = ["api.cpp", "decode_api.cpp", "portable.cpp"]   # host C++ (argument checks, file I/O)
 
 HIP_FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
              "-fhip-fp32-correctly-rounded-divide-sqrt",

@@ -12,6 +12,7 @@
 #include <cstring>
 
 #include "../../include/w4.h"
+#include "checks.hpp"
 #include "kernels.hpp"
 #include "status.hpp"
 
@@ -30,12 +31,8 @@ int w4::fail(int status, const char* fmt, ...) {
 namespace {
 using w4::fail;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int hip_status(hipError_t e, const char* what) {
-    if (e == hipSuccess) return W4_OK;
-    return fail(W4_EHIP, "%s: %s", what, hipGetErrorString(e));
-}
+using w4::aligned16;
+using w4::hip_status;
 
 int check_group(const char* fn, int64_t N, int64_t K, int G) {
     if (N < 0) return fail(W4_EINVAL, "%s: N = %lld must be >= 0", fn, static_cast<long long>(N));
@@ -70,12 +67,6 @@ int check_mode(const char* fn, int mode) {
     if (mode != W4_SYM && mode != W4_ASYM) return fail(W4_EINVAL, "%s: mode %d is neither W4_SYM nor W4_ASYM", fn, mode);
     return W4_OK;
 }
-
-#define W4_REQUIRE_PTR(fn, p)                                                        \
-    do {                                                                             \
-        if (!(p)) return fail(W4_EINVAL, "%s: %s is NULL", fn, #p);                  \
-        if (!aligned16(p)) return fail(W4_EINVAL, "%s: %s is not 16-byte aligned", fn, #p); \
-    } while (0)
 
 int quantize_common(const char* fn, const float* W, int64_t N, int64_t K, int G, int mode,
                     const float* fracs, int n_fracs, bool encode, uint8_t* packed, uint16_t* scale,
