@@ -509,8 +509,8 @@ size_t w4_tree_attention_workspace_bytes(int64_t T, int64_t B, int Hq, int kv_he
  * whole numbers do not depend on their order: the same inputs give the same
  * token on every launch shape.  T = 0 takes the largest logit's lowest index.
  *   logits       bf16 or fp32 (W4_LOGITS_*), [B, V], rows row_stride elements
- *                apart; V <= 2^20.  The rows need no alignment beyond the
- *                element's; `logits` itself is 16-byte aligned.
+ *                apart (0: the same row for all); V <= 2^20.  No alignment
+ *                beyond the elements'.
  *   u            [B] fp32 in [0, 1).
  *   temperature, top_p, min_p  [B] fp32, top_k [B] int32; each may be NULL: 1,
  *                1, 0, none.  top_k <= 0: none.  temperature >= 0.

@@ -198,9 +198,12 @@ int w4_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_s
     if (B < 0 || B > 65535) return fail(W4_EINVAL, "%s: B = %lld outside 0..65535", fn, ll(B));
     if (V <= 0) return fail(W4_EINVAL, "%s: V = %lld must be > 0", fn, ll(V));
     if (V > kMaxVocab) return fail(W4_EUNSUPPORTED, "%s: V = %lld above 2^20", fn, ll(V));
-    if (row_stride < V) return fail(W4_EINVAL, "%s: row_stride = %lld is less than V = %lld", fn, ll(row_stride), ll(V));
+    if (row_stride != 0 && row_stride < V)
+        return fail(W4_EINVAL, "%s: row_stride = %lld is neither 0 (one row for all) nor at least V = %lld", fn, ll(row_stride), ll(V));
     if (B == 0) return W4_OK;
-    W4_REQUIRE_PTR(fn, logits);
+    if (!logits) return fail(W4_EINVAL, "%s: logits is NULL", fn);
+    if (reinterpret_cast<uintptr_t>(logits) % (dtype == W4_LOGITS_F32 ? 4 : 2) != 0)
+        return fail(W4_EINVAL, "%s: logits is not aligned to its elements", fn);
     if (!u) return fail(W4_EINVAL, "%s: u is NULL", fn);
     if (!tokens) return fail(W4_EINVAL, "%s: tokens is NULL", fn);
     if (workspace && !aligned16(workspace)) return fail(W4_EINVAL, "%s: workspace is not 16-byte aligned", fn);
