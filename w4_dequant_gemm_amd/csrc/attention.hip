@@ -2,9 +2,9 @@
 // chunk) over the paged cache.
 //
 // Per KV head the rows are the nodes times the query heads of its group.  A
-// wavefront takes steps of 64 bytes of one dim's tokens (S = 32 bf16 or 64
-// E4M3 tokens) with both products on v_mfma_f32_16x16x32_bf16, transposed so
-// that a row is a column of both results:
+// wavefront takes units of S tokens (32 bf16, 64 E4M3: 16 bytes of a dim's
+// tokens in each lane group) with both products on v_mfma_f32_16x16x32_bf16,
+// transposed so that a row is a column of both results:
 //   S^T [16 tokens x 16 rows] = K [16 x D] Q^T,   O^T [16 dims x 16 rows] += V^T [16 x S] P^T.
 // A result holds row l % 16 in lane l, tokens 4 (l / 16) + 0..3; an operand
 // holds 8 values of the summed index in group l / 16.  Which token is which
@@ -12,11 +12,15 @@
 // takes the S/4 tokens from S/4 g on: the K rows of tile t are the tokens
 // S/4 (m / 4) + 4 t + m % 4 (m = l % 16), which puts P's values where its
 // operand needs them, and V's operand is one 16-byte piece of the cache as it
-// lies.  Neither P nor V passes through shared memory.
+// lies.  Neither P nor V is transposed or passes through shared memory for it.
 //
-// Softmax in one pass: running maximum and sum (fp32, base 2), the sums of O
-// rescaled when the maximum rises.  p is rounded to bf16 for the second
-// product (the matrix cores' operand); the sum keeps the unrounded p.
+// Softmax in one pass, base 2, statistics in fp32.  The reference that is
+// subtracted in the exponent need not be the maximum: it is raised (and the
+// sums faded) only when a score exceeds it by more than 8, so p <= 2^8 and
+// most steps neither exchange maxima between lanes nor touch the sums.  p is
+// rounded to bf16, the matrix cores' operand; the sum of the same rounded p
+// comes from one more product with ones, so a weight that dominates is not
+// biased by its rounding.
 #include "device.hpp"
 #include "kernels.hpp"
 
@@ -28,11 +32,24 @@ namespace {
 struct AttentionPlan {
     int chunk, splits, tiles;
     int group;               // query heads a KV head
+    int tile_rows;           // rows a workgroup
     uint32_t page_magic;     // block / page_blocks as a high product (page_blocks > 1)
 };
 
-__device__ __forceinline__ bool nonfinite_bf16x2(uint32_t w) {
-    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+constexpr float kRaise = 8.0f;               // log2 of the largest p
+
+// whether any of a piece's values (8 bf16 or 16 E4M3) is infinite or NaN
+template <int E>
+__device__ __forceinline__ bool nonfinite(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // all exponent (E4M3: all) bits set: adding one to the field carries into the sign's place
+        if constexpr (E == 2) any = any || (((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) != 0;
+        else any = any || (((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+    }
+    return any;
 }
 
 // 16 E4M3 codes -> two bf16 operands of 8 (exact).
@@ -55,32 +72,436 @@ __device__ __forceinline__ float4_t mfma(const uint4& a, const uint4& b, const f
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// one element of eight kept, the others zero
-__device__ __forceinline__ uint4 only(const uint4& v, int e) {
-    const uint32_t keep = (e & 1) ? 0xFFFF0000u : 0x0000FFFFu;
-    const int w = e >> 1;
-    return make_uint4(w == 0 ? v.x & keep : 0, w == 1 ? v.y & keep : 0, w == 2 ? v.z & keep : 0, w == 3 ? v.w & keep : 0);
+// maximum over the four lane groups (lanes m, m + 16, m + 32, m + 48)
+__device__ __forceinline__ float max_groups(float x) {
+    const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false));
+    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false));
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
-// the first n of eight elements kept
-__device__ __forceinline__ uint4 first_of(const uint4& v, int n) {
-    auto m = [&](int i) { return n >= 2 * i + 2 ? 0xFFFFFFFFu : n == 2 * i + 1 ? 0x0000FFFFu : 0u; };
-    return make_uint4(v.x & m(0), v.y & m(1), v.z & m(2), v.w & m(3));
+// Eight bf16 values with infinities and NaN replaced by 0; `plus` is 1 where
+// +inf or NaN stood, `minus` where -inf or NaN did.
+__device__ __forceinline__ uint4 finite_part(const uint4& v, uint4& plus, uint4& minus) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t f[4], a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t out = (((((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) >> 15)) * 0xFFFFu;
+        const uint32_t nan = ((((w[i] & 0x007F007Fu) + 0x007F007Fu) & 0x00800080u) >> 7) * 0xFFFFu;
+        const uint32_t neg = ((w[i] & 0x80008000u) >> 15) * 0xFFFFu;
+        f[i] = w[i] & ~out;
+        a[i] = out & (nan | ~neg) & 0x3F803F80u;
+        b[i] = out & (nan | neg) & 0x3F803F80u;
+    }
+    plus = make_uint4(a[0], a[1], a[2], a[3]);
+    minus = make_uint4(b[0], b[1], b[2], b[3]);
+    return make_uint4(f[0], f[1], f[2], f[3]);
 }
 
-// D dims, E bytes a cached element, R tiles of 16 rows a wave, WK waves along
-// the tokens (the other 4 / WK along the rows).
-template <int D, int E, int R, int WK>
-__global__ void __launch_bounds__(256) attention_kernel(AttentionParams p, AttentionPlan pl) {
-    constexpr int S = 64 / E;                // tokens a step
-    constexpr int NT = S / 16;               // K tiles a step
-    constexpr int KS = D / 32;               // operands of a K tile
-    constexpr int DT = D / 16;
-    constexpr int NP = S / 32;               // operands of P and of a V tile
-    constexpr int WR = 4 / WK;
-    constexpr int ROWS = 16 * R * WR;        // rows a workgroup
-    constexpr int BPS = S / 16;              // 16-token blocks a step
+// A cached piece with its infinities and NaN replaced by 0.
+template <int E>
+__device__ __forceinline__ uint4 finite_piece(const uint4& v) {
+    if constexpr (E == 2) {
+        uint4 plus, minus;
+        return finite_part(v, plus, minus);
+    } else {
+        auto fine = [](uint32_t w) {
+            const uint32_t out = ((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
+            return w & ~out;
+        };
+        return make_uint4(fine(v.x), fine(v.y), fine(v.z), fine(v.w));
+    }
+}
 
+// bf16 1 at the elements whose bit is set
+__device__ __forceinline__ uint4 ones_at(uint32_t bits) {
+    auto two = [&](int i) { return ((bits >> i) & 1 ? 0x3F80u : 0u) | ((bits >> i) & 2 ? 0x3F800000u : 0u); };
+    return make_uint4(two(0), two(2), two(4), two(6));
+}
+
+// the low n bits (n may lie outside 0 .. 32)
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+
+// A sequence as one workgroup sees it.
+struct Sequence {
+    int q0, n;               // its rows of q
+    int len, past;           // cached tokens; those before its nodes
+    int first;               // token that split 0 starts at
+    const int32_t* table;
+    int last_block;
+    bool holes;              // a page of the split's range lies outside the cache
+};
+
+__device__ __forceinline__ void sequence_rows(const AttentionParams& p, int b, int& q0, int& n) {
+    const int T = static_cast<int>(p.T);
+    int a = p.q_start[b], e = p.q_start[b + 1];
+    a = a < 0 ? 0 : a > T ? T : a;
+    e = e > T ? T : e;
+    n = e > a ? e - a : 0;
+    n = n < p.max_q ? n : p.max_q;
+    q0 = a;
+}
+
+__device__ __forceinline__ int page_of(const AttentionParams& p, const AttentionPlan& pl, int blk) {
+    return p.cache.page_blocks > 1 ? static_cast<int>(__umulhi(static_cast<uint32_t>(blk), pl.page_magic)) : blk;
+}
+
+// The tokens [begin, end) of one split that rows up to node `node_last` can
+// see (begin a multiple of 64).
+__device__ __forceinline__ void split_range(const AttentionParams& p, const AttentionPlan& pl, Sequence& s, int b,
+                                            int split, int node_first, int node_last, int& begin, int& end) {
+    const int lane = threadIdx.x & 63;
+    s.table = p.page_table + static_cast<int64_t>(b) * p.table_pages;
+    s.last_block = s.len > 0 ? (s.len - 1) >> 4 : 0;
+    s.first = 0;
+    int lowest = 0;                          // no row of the tile sees a context token below
+    if (p.window > 0) {
+        int least = s.past;                  // the lowest position
+        if (p.positions) {
+            least = 0x7FFFFFFF;
+            for (int i = lane; i < s.n; i += 64) least = min(least, p.positions[s.q0 + i]);
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) least = min(least, __shfl_xor(least, off));
+            least = __builtin_amdgcn_readfirstlane(least);
+        }
+        lowest = least + (p.positions ? 0 : node_first) - p.window + 1;
+        least = least - p.window + 1;
+        least = least < s.past ? least : s.past;
+        lowest = lowest < s.past ? lowest : s.past;
+        s.first = least > 0 ? least & ~63 : 0;
+        lowest = lowest > 0 ? lowest & ~63 : 0;
+    }
+    begin = s.first + split * pl.chunk;
+    end = split == pl.splits - 1 ? s.len : begin + pl.chunk;
+    if (!p.tree && end > s.past + node_last + 1) end = s.past + node_last + 1;
+    if (end > s.len) end = s.len;
+    if (begin < lowest) begin = lowest;
+    bool bad = false;
+    if (begin < end)
+        for (int i = page_of(p, pl, begin >> 4) + lane; i <= page_of(p, pl, (end - 1) >> 4); i += 64) {
+            const int64_t page = s.table[i];
+            bad = bad || page < 0 || page >= p.cache.pages;
+        }
+    s.holes = __any(bad);
+}
+
+// R tiles of 16 rows of one wavefront: their queries, running sums, and the
+// work of a step of U units.
+template <int D, int E, int R>
+struct Core {
+    static constexpr int S = 64 / E;         // tokens a unit
+    static constexpr int NT = S / 16;        // K tiles a unit
+    static constexpr int KP = D * E / 64;    // 16-byte pieces of a K tile in a lane
+    static constexpr int KS = D / 32;        // operands of a K tile
+    static constexpr int DT = D / 16;
+    static constexpr int NP = S / 32;        // operands of P, and of V's piece
+    static constexpr int BPU = S / 16;       // 16-token blocks a unit
+
+    uint4 Q[R][KS];
+    float4_t O[R][DT], L[R];                 // sums of p v and of p (every component)
+    float ref[R], scale;
+    int node[R], low[R];
+    bool live[R];
+    int low_most;
+    bool repairs;                            // see repair()
+
+    __device__ __forceinline__ void init(const AttentionParams& p, const AttentionPlan& pl, const Sequence& s, int head,
+                                         int row0, int rows) {
+        const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+        // a negative scale turns the queries' signs, so that the largest score is the largest product
+        scale = p.scale * 1.4426950408889634f * (E == 1 ? p.cache.k_scale[head] : 1.0f);
+        const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;
+        scale = fmaxf(fabsf(scale), 1.17549435e-38f);
+        low_most = 0;
+        repairs = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = row0 + 16 * r + m;
+            live[r] = row < rows;
+            const int at = live[r] ? row : rows - 1;
+            node[r] = at / pl.group;
+            const int h = head * pl.group + (at - node[r] * pl.group);
+            const uint16_t* q = p.q + static_cast<int64_t>(s.q0 + node[r]) * p.q_stride + static_cast<int64_t>(h) * D;
+            const int pos = p.positions ? p.positions[s.q0 + node[r]] : s.past + node[r];
+            low[r] = p.window > 0 ? pos - p.window + 1 : 0;
+            low_most = low[r] > low_most ? low[r] : low_most;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                // dims of operand i in lane group g, as K's pieces hold them
+                const int d = E == 2 ? 32 * i + 8 * g : 64 * (i >> 1) + 16 * g + 8 * (i & 1);
+                uint4 v = *reinterpret_cast<const uint4*>(q + d);
+                Q[r][i] = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+            }
+            ref[r] = -INFINITY;
+            L[r] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) O[r][dt] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        if (p.window > 0) {
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1) low_most = max(low_most, __shfl_xor(low_most, off));
+            low_most = __builtin_amdgcn_readfirstlane(low_most);
+        }
+    }
+
+    // bit i: row r sees token kf + i (this lane's S/4 tokens of a unit)
+    __device__ __forceinline__ uint32_t sees(const AttentionParams& p, const AttentionPlan& pl, const Sequence& s, int r,
+                                             int kf) const {
+        const int c = s.past - kf;           // tokens of the context among them
+        const int j0 = kf - s.past;          // node of the first
+        uint32_t context = low_bits(c) & ~low_bits(low[r] - kf);
+        uint32_t nodes = 0;
+        if (c < S / 4 && kf < s.len) {
+            if (p.tree) {
+                const uint64_t* words = p.tree + static_cast<int64_t>(s.q0 + node[r]) * p.tree_words;
+                if (j0 >= 0) {
+                    const int w = j0 >> 6, o = j0 & 63;
+                    uint64_t bits = w < p.tree_words ? words[w] >> o : 0;
+                    if (o > 64 - S / 4 && w + 1 < p.tree_words) bits |= words[w + 1] << (64 - o);
+                    nodes = static_cast<uint32_t>(bits);
+                } else {
+                    nodes = static_cast<uint32_t>(words[0] << c);
+                }
+            } else {
+                nodes = low_bits(node[r] - j0 + 1);
+            }
+            if (p.window > 0) {
+                if (p.positions) {
+                    for (int i = c > 0 ? c : 0; i < S / 4 && kf + i < s.len; ++i)
+                        if (p.positions[s.q0 + j0 + i] < low[r]) nodes &= ~(1u << i);
+                } else {
+                    nodes &= ~low_bits(low[r] - kf);
+                }
+            }
+        }
+        uint32_t bits = (context | (nodes & ~low_bits(c))) & low_bits(s.len - kf) & low_bits(S / 4);
+        if (s.holes && kf < s.len) {
+            // (a lane's tokens lie in one block)
+            const int64_t page = s.table[page_of(p, pl, kf >> 4)];
+            if (page < 0 || page >= p.cache.pages) bits = 0;
+        }
+        return live[r] ? bits : 0;
+    }
+
+    // Tokens k0 .. k0 + U S - 1: kget(u, i) and vget(u, dt) give the lane's
+    // 16-byte pieces of unit u (i = tile * KP + piece); keys_done is called
+    // when the K pieces are used up.  OWN: V's pieces are the wave's own
+    // registers, vown[dt].
+    template <int U, bool OWN, class KGet, class VGet, class Done>
+    __device__ __forceinline__ void step(const AttentionParams& p, const AttentionPlan& pl, const Sequence& s, int k0,
+                                         KGet kget, VGet vget, Done keys_done, uint4* vown) {
+        const int g = (threadIdx.x & 63) >> 4;
+        constexpr int N = U * NT;
+        float4_t acc[R][N];
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[r][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < KP; ++i) {
+                const uint4 c = kget(t / NT, (t % NT) * KP + i);
+                if constexpr (E == 2) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) acc[r][t] = mfma(c, Q[r][i], acc[r][t]);
+                } else {
+                    uint4 a, b;
+                    widen16(c, a, b);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) acc[r][t] = mfma(a, Q[r][2 * i], acc[r][t]);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) acc[r][t] = mfma(b, Q[r][2 * i + 1], acc[r][t]);
+                }
+            }
+        }
+
+        keys_done();
+
+        const bool masked = needs_mask(s, k0, U * S);
+        if (masked) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const uint32_t seen = sees(p, pl, s, r, k0 + u * S + (S / 4) * g);
+#pragma unroll
+                    for (int i = 0; i < 4 * NT; ++i)
+                        if (!((seen >> i) & 1)) acc[r][u * NT + (i >> 2)][i & 3] = -INFINITY;
+                }
+        }
+        float top[R];
+        bool raise = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            top[r] = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < N; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) top[r] = fmaxf(top[r], fmaxf(acc[r][t][j], acc[r][t][j + 1]));
+            top[r] *= scale;
+            raise = raise || top[r] > ref[r] + kRaise;
+        }
+        if (__any(raise)) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float now = fmaxf(ref[r], max_groups(top[r]));
+                const float fade = now == -INFINITY ? 1.0f : exp2_fast(ref[r] - now);
+                ref[r] = now;
+                L[r] *= fade;
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) O[r][dt] *= fade;
+            }
+        }
+        uint4 P[R][U * NP];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float base = ref[r] == -INFINITY ? 0.0f : ref[r];
+#pragma unroll
+            for (int q = 0; q < U * NP; ++q) {
+                float e[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i] = exp2_fast(__builtin_fmaf(acc[r][2 * q + (i >> 2)][i & 3], scale, -base));
+                P[r][q] = make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                                     pack_bf16x2(e[6], e[7]));
+            }
+        }
+        const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int q = 0; q < U * NP; ++q) L[r] = mfma(ones, P[r][q], L[r]);
+
+        auto operands = [&](int u, int dt, uint4 (&V)[NP]) {
+            const uint4 c = vget(u, dt);
+            if constexpr (E == 2) V[0] = c;
+            else widen16(c, V[0], V[NP - 1]);
+        };
+        bool odd = false;
+        if (masked) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) odd = odd || nonfinite<E>(vget(u, dt));
+            odd = __any(odd);
+        }
+        if (odd) {
+            // an infinity or NaN among the values of a step that not every row
+            // sees, or behind the last token (0 times it would be NaN): without
+            // them here, and repair() adds them to the rows that see them
+            repairs = true;
+            if constexpr (OWN) {
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) vown[dt] = finite_piece<E>(vown[dt]);
+            }
+        }
+        if (odd && !OWN) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) {
+                    uint4 V[NP];
+                    operands(u, dt, V);
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) {
+                        uint4 plus, minus;
+                        const uint4 fine = finite_part(V[q], plus, minus);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) O[r][dt] = mfma(fine, P[r][u * NP + q], O[r][dt]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);   // registers are scarcer than time here
+                }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) {
+                    uint4 V[NP];
+                    operands(u, dt, V);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int q = 0; q < NP; ++q) O[r][dt] = mfma(V[q], P[r][u * NP + q], O[r][dt]);
+                }
+        }
+    }
+
+    // Whether a unit at k0 needs the rows' masks.
+    __device__ __forceinline__ bool needs_mask(const Sequence& s, int k0, int tokens) const {
+        return s.holes || k0 + tokens > (s.past < s.len ? s.past : s.len) || k0 < low_most;
+    }
+
+    // The infinities and NaN that step() left out of the units k0, k0 + stride,
+    // ... < end: for each output, how many +inf and NaN, -inf and NaN its row
+    // sees (products of the rows' masks with indicators).
+    __device__ __forceinline__ void repair(const AttentionParams& p, const AttentionPlan& pl, const Sequence& s, int head,
+                                           int k0, int stride, int end) {
+        const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+#pragma unroll 1
+        for (; k0 < end; k0 += stride) {
+            if (!needs_mask(s, k0, S)) continue;
+            const int blk = min((k0 >> 4) + (g * BPU >> 2), s.last_block);
+            int64_t page = s.table[page_of(p, pl, blk)];
+            page = page < 0 || page >= p.cache.pages ? 0 : page;
+            const int64_t at = (page * p.cache.heads + head) * p.cache.page_blocks + (blk - page_of(p, pl, blk) * p.cache.page_blocks);
+            const uint8_t* from = static_cast<const uint8_t*>(p.cache.v) + at * (16 * D * E) + (E == 2 ? (g & 1) * (16 * D) : 0) + m * 16;
+            uint32_t bits[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) bits[r] = sees(p, pl, s, r, k0 + (S / 4) * g);
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) {
+                uint4 V[NP];
+                const uint4 c = *reinterpret_cast<const uint4*>(from + dt * 256);
+                if constexpr (E == 2) V[0] = c;
+                else widen16(c, V[0], V[NP - 1]);
+#pragma unroll
+                for (int q = 0; q < NP; ++q) {
+                    uint4 plus, minus;
+                    finite_part(V[q], plus, minus);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const uint4 one = ones_at(bits[r] >> (8 * q));
+                        const float4_t a = mfma(plus, one, float4_t{0.0f, 0.0f, 0.0f, 0.0f});
+                        const float4_t b = mfma(minus, one, float4_t{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            O[r][dt][j] += (a[j] > 0.0f ? INFINITY : 0.0f) + (b[j] > 0.0f ? -INFINITY : 0.0f);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
+        }
+    }
+};
+
+// Four dims of one row: to O, or as a partial result to the workspace
+// (partials [split][T hq][D], then reference and sum [split][T hq][2]).
+template <int D, int E>
+__device__ __forceinline__ void put(const AttentionParams& p, const AttentionPlan& pl, int q0, int head, int split, int row,
+                                    int d, float4_t o, float ref, float total) {
+    const int nd = row / pl.group;
+    const int64_t at = static_cast<int64_t>(q0 + nd) * p.hq + head * pl.group + (row - nd * pl.group);
+    if (pl.splits == 1) {
+        const float f = total != 0.0f ? (E == 1 ? p.cache.v_scale[head] : 1.0f) / total : 0.0f;
+        *reinterpret_cast<uint2*>(p.O + at * D + d) = make_uint2(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f));
+    } else {
+        const int64_t all = p.T * p.hq;
+        const int64_t slice = static_cast<int64_t>(split) * all + at;
+        *reinterpret_cast<float4_t*>(p.ws + slice * D + d) = o;
+        if (d == 0)
+            *reinterpret_cast<float2_t*>(p.ws + static_cast<int64_t>(pl.splits) * all * D + 2 * slice) = float2_t{ref, total};
+    }
+}
+
+// Up to 32 rows: the time is that of reading the cache once.  The four waves
+// of a workgroup hold the same rows and take steps of one unit in turn, each
+// straight from memory into operand registers; their sums are joined through
+// shared memory.
+template <int D, int E, int R>
+__global__ void __launch_bounds__(256, 2) attention_stream_kernel(AttentionParams p, AttentionPlan pl) {
+    using C = Core<D, E, R>;
+    constexpr int S = C::S, WK = 4, DT = C::DT;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int m = lane & 15, g = lane >> 4;
     const int hk = p.cache.heads, pb = p.cache.page_blocks;
@@ -91,313 +512,221 @@ __global__ void __launch_bounds__(256) attention_kernel(AttentionParams p, Atten
     id /= pl.splits;
     const int head = id % hk, b = id / hk;
 
-    const int T = static_cast<int>(p.T);
-    int q0 = p.q_start[b], q1 = p.q_start[b + 1];
-    q0 = q0 < 0 ? 0 : q0 > T ? T : q0;
-    q1 = q1 > T ? T : q1;
-    q1 = q1 > q0 + p.max_q ? q0 + p.max_q : q1;
-    const int n = q1 > q0 ? q1 - q0 : 0;
-    const int rows = n * pl.group;
-    const int tile_row = tile * ROWS;
+    Sequence s;
+    sequence_rows(p, b, s.q0, s.n);
+    const int rows = s.n * pl.group;
+    const int tile_row = tile * 16 * R;
     if (tile_row >= rows) return;
-    int len = p.kv_len[b];
-    len = len < 0 ? 0 : len > p.max_kv ? p.max_kv : len;
-    const int past = len - n;
+    s.len = p.kv_len[b];
+    s.len = s.len < 0 ? 0 : s.len > p.max_kv ? p.max_kv : s.len;
+    s.past = s.len - s.n;
+    const int row_last = (tile_row + 16 * R < rows ? tile_row + 16 * R : rows) - 1;
+    int begin, end;
+    split_range(p, pl, s, b, split, tile_row / pl.group, row_last / pl.group, begin, end);
+    C c;
+    c.init(p, pl, s, head, tile_row, rows);
 
-    // this lane's rows
-    const int wk = WK > 1 ? wave : 0;
-    const int row0 = tile_row + (WK > 1 ? 0 : wave * 16 * R);
-    int node[R], low[R];
-    bool live[R];
-    const uint16_t* qp[R];
-    int lo_min = 0x7FFFFFFF, lo_max = 0, node_max = 0;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int row = row0 + 16 * r + m;
-        live[r] = row < rows;
-        const int at = live[r] ? row : rows - 1;
-        node[r] = at / pl.group;
-        const int h = head * pl.group + (at - node[r] * pl.group);
-        qp[r] = p.q + static_cast<int64_t>(q0 + node[r]) * p.q_stride + static_cast<int64_t>(h) * D;
-        const int pos = p.positions ? p.positions[q0 + node[r]] : past + node[r];
-        low[r] = p.window > 0 ? pos - p.window + 1 : 0;
-        lo_min = low[r] < lo_min ? low[r] : lo_min;
-        lo_max = low[r] > lo_max ? low[r] : lo_max;
-        node_max = node[r] > node_max ? node[r] : node_max;
-    }
-#pragma unroll
-    for (int off = 1; off < 16; off <<= 1) {
-        lo_min = min(lo_min, __shfl_xor(lo_min, off));
-        lo_max = max(lo_max, __shfl_xor(lo_max, off));
-        node_max = max(node_max, __shfl_xor(node_max, off));
-    }
-    lo_min = __builtin_amdgcn_readfirstlane(lo_min);
-    lo_max = __builtin_amdgcn_readfirstlane(lo_max);
-    node_max = __builtin_amdgcn_readfirstlane(node_max);
-
-    // the sequence's first visible token, where split 0 starts
-    int first = 0;
-    if (p.window > 0) {
-        int least = past;
-        if (p.positions) {
-            least = 0x7FFFFFFF;
-            for (int i = lane; i < n; i += 64) least = min(least, p.positions[q0 + i]);
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1) least = min(least, __shfl_xor(least, off));
-            least = __builtin_amdgcn_readfirstlane(least);
-        }
-        least = least - p.window + 1;
-        first = least > past ? past : least;
-        first = first < 0 ? 0 : first & ~63;
-    }
-    int begin = first + split * pl.chunk;
-    int end = split == pl.splits - 1 ? len : begin + pl.chunk;
-    // nodes beyond the last row of a chain, and tokens before every window, are seen by none
-    if (!p.tree && end > past + node_max + 1) end = past + node_max + 1;
-    if (end > len) end = len;
-    // (with a window, nodes are seen by their positions: only context tokens are skipped by index)
-    const int from = lo_min < past ? lo_min : past;
-    if (begin < from) begin = from & ~63;
-
-    uint4 Q[R][KS];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            // dims of operand s in lane group g, as K's pieces hold them
-            const int d = E == 2 ? 32 * s + 8 * g : 64 * (s >> 1) + 16 * g + 8 * (s & 1);
-            Q[r][s] = *reinterpret_cast<const uint4*>(qp[r] + d);
-        }
-
-    float4_t O[R][DT];
-    float mx[R], sum[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        mx[r] = -INFINITY;
-        sum[r] = 0.0f;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) O[r][dt] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    const float scale = p.scale * 1.4426950408889634f * (E == 1 ? p.cache.k_scale[head] : 1.0f);
-    const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.table_pages;
-    const int last_block = len > 0 ? (len - 1) >> 4 : 0;
-
-    // index of a block of the cache (in 16-token blocks of this head), or -1
-    auto block_at = [&](int blk) -> int64_t {
-        blk = blk > last_block ? last_block : blk;
-        const int pg = pb > 1 ? static_cast<int>(__umulhi(static_cast<uint32_t>(blk), pl.page_magic)) : blk;
-        const int64_t page = table[pg];
-        if (page < 0 || page >= p.cache.pages) return -1;
-        return (page * hk + head) * pb + (blk - pg * pb);
+    uint4 kx[C::NT * C::KP], vx[DT];         // the pieces of the step
+    auto k_block = [&](int st) { return min(st * C::BPU + (m * C::BPU >> 4), s.last_block); };
+    auto v_block = [&](int st) { return min(st * C::BPU + (g * C::BPU >> 2), s.last_block); };
+    auto address = [&](const void* base, int blk, int page) {
+        page = page < 0 || page >= p.cache.pages ? 0 : page;
+        const int64_t block = (static_cast<int64_t>(page) * hk + head) * pb + (blk - page_of(p, pl, blk) * pb);
+        return static_cast<const uint8_t*>(base) + block * (16 * D * E);
     };
-
-    for (int st = begin / S + wk; st * S < end; st += WK) {
-        const int k0 = st * S;
-        const int64_t kb = block_at(st * BPS + (m * BPS >> 4));
-        const int64_t vb = block_at(st * BPS + (g * BPS >> 2));
-        const bool absent = vb < 0;
-        const uint8_t* kp = static_cast<const uint8_t*>(p.cache.k) + (kb < 0 ? 0 : kb) * (16 * D * E);
-        const uint8_t* vp = static_cast<const uint8_t*>(p.cache.v) + (absent ? 0 : vb) * (16 * D * E);
-        // V: the piece of this lane's dim and group of tokens (two groups share a block of bf16)
-        vp += (E == 2 ? (g & 1) * (16 * D) : 0) + m * 16;
-
-        float4_t acc[R][NT];
+    auto load_k = [&](int st, int page) {
+        const uint8_t* from = address(p.cache.k, k_block(st), page) + g * 256;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int token = (S / 4) * (m >> 2) + 4 * t + (m & 3);   // of the step
-            const uint8_t* row = kp + (token & 15) * 16;
-            uint4 K[KS];
-            if constexpr (E == 2) {
+        for (int t = 0; t < C::NT; ++t) {
+            const int token = (S / 4) * (m >> 2) + 4 * t + (m & 3);
 #pragma unroll
-                for (int s = 0; s < KS; ++s) K[s] = *reinterpret_cast<const uint4*>(row + (4 * s + g) * 256);
-            } else {
-#pragma unroll
-                for (int s = 0; s < KS; s += 2) {
-                    const uint4 c = *reinterpret_cast<const uint4*>(row + (2 * s + g) * 256);
-                    widen16(c, K[s], K[s + 1]);
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                acc[r][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < KS; ++s) acc[r][t] = mfma(K[s], Q[r][s], acc[r][t]);
-            }
-        }
-
-        const bool masked = k0 + S > (past < len ? past : len) || k0 < lo_max || __any(absent);
-        uint32_t seen[R];                    // bit 4 t + j: this lane's row sees token (S/4) g + 4 t + j
-        uint4 P[R][NP];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            seen[r] = 0xFFFFFFFFu;
-            if (masked) {
-                seen[r] = 0;
-#pragma unroll
-                for (int i = 0; i < 4 * NT; ++i) {
-                    const int key = k0 + (S / 4) * g + i;
-                    bool ok = live[r] && !absent && key < len;
-                    if (ok && key < past) {
-                        ok = key >= low[r];
-                    } else if (ok) {
-                        const int j = key - past;
-                        ok = p.tree ? (p.tree[static_cast<int64_t>(q0 + node[r]) * p.tree_words + (j >> 6)] >> (j & 63)) & 1
-                                    : j <= node[r];
-                        if (p.window > 0) ok = ok && (p.positions ? p.positions[q0 + j] : key) >= low[r];
-                    }
-                    seen[r] |= (ok ? 1u : 0u) << i;
-                }
-            }
-            float s[4 * NT];
-            float top = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 4 * NT; ++i) {
-                s[i] = acc[r][i >> 2][i & 3] * scale;
-                if (masked) s[i] = (seen[r] >> i) & 1 ? s[i] : -INFINITY;
-                top = fmaxf(top, s[i]);
-            }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float now = fmaxf(mx[r], top);
-            const float ref = now == -INFINITY ? 0.0f : now;
-            const float fade = exp2_fast(mx[r] - ref);
-            mx[r] = now;
-            float part = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4 * NT; ++i) {
-                s[i] = exp2_fast(s[i] - ref);
-                part += s[i];
-            }
-            sum[r] = sum[r] * fade + part;
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) O[r][dt] *= fade;
-#pragma unroll
-            for (int q = 0; q < NP; ++q)
-                P[r][q] = make_uint4(pack_bf16x2(s[8 * q], s[8 * q + 1]), pack_bf16x2(s[8 * q + 2], s[8 * q + 3]),
-                                     pack_bf16x2(s[8 * q + 4], s[8 * q + 5]), pack_bf16x2(s[8 * q + 6], s[8 * q + 7]));
-        }
-
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-            uint4 V[NP];
-            const uint4 c = *reinterpret_cast<const uint4*>(vp + dt * 256);
-            if constexpr (E == 2) V[0] = c;
-            else widen16(c, V[0], V[NP - 1]);
-            bool odd = false;
-            if (masked) {
-                // what lies behind the last token is not data
-                const int left = len - (k0 + (S / 4) * g);
-#pragma unroll
-                for (int q = 0; q < NP; ++q) {
-                    V[q] = first_of(V[q], left - 8 * q);
-                    odd = odd || nonfinite_bf16x2(V[q].x) || nonfinite_bf16x2(V[q].y) || nonfinite_bf16x2(V[q].z) ||
-                          nonfinite_bf16x2(V[q].w);
-                }
-            }
-            if (masked && __any(odd)) {
-                // an infinity or NaN among the values of a step that not every
-                // row sees (0 times it would be NaN): token by token, each
-                // added only to the rows that see it
-                for (int i = 0; i < 4 * NT; ++i)
-                    for (int gg = 0; gg < 4; ++gg) {
-                        const uint4 zero = make_uint4(0, 0, 0, 0);
-                        const int q = i >> 3;
-                        const uint4 v1 = g == gg ? only(NP > 1 && q ? V[NP - 1] : V[0], i & 7) : zero;
-#pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            const uint4 p1 = g == gg ? only(NP > 1 && q ? P[r][NP - 1] : P[r][0], i & 7) : zero;
-                            const float4_t add = mfma(v1, p1, float4_t{0.0f, 0.0f, 0.0f, 0.0f});
-                            const uint32_t sees = static_cast<uint32_t>(__shfl(static_cast<int>(seen[r]), 16 * gg + m));
-                            if ((sees >> i) & 1) O[r][dt] += add;
-                        }
-                    }
-            } else {
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int q = 0; q < NP; ++q) O[r][dt] = mfma(V[q], P[r][q], O[r][dt]);
-            }
-        }
-    }
-
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        sum[r] += __shfl_xor(sum[r], 16);
-        sum[r] += __shfl_xor(sum[r], 32);
-    }
-
-    const float v_scale = E == 1 ? p.cache.v_scale[head] : 1.0f;
-    const int64_t all = p.T * p.hq;
-    float* part_ml = p.ws + static_cast<int64_t>(pl.splits) * all * D;
-    // four dims of one row: to O, or as a partial result to the workspace
-    auto put = [&](int row, int d, float4_t o, float top, float total) {
-        const int nd = row / pl.group;
-        const int64_t at = static_cast<int64_t>(q0 + nd) * p.hq + head * pl.group + (row - nd * pl.group);
-        if (pl.splits == 1) {
-            const float f = total > 0.0f || total != total ? v_scale / total : 0.0f;
-            *reinterpret_cast<uint2*>(p.O + at * D + d) = make_uint2(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f));
-        } else {
-            const int64_t slice = static_cast<int64_t>(split) * all + at;
-            *reinterpret_cast<float4_t*>(p.ws + slice * D + d) = o;
-            if (d == 0) *reinterpret_cast<float2_t*>(part_ml + 2 * slice) = float2_t{top, total};
+            for (int i = 0; i < C::KP; ++i)
+                kx[t * C::KP + i] = load_nt_16(reinterpret_cast<const uint32_t*>(from + (token & 15) * 16 + i * 1024));
         }
     };
+    auto load_v = [&](int st, int page) {
+        const uint8_t* from = address(p.cache.v, v_block(st), page) + (E == 2 ? (g & 1) * (16 * D) : 0) + m * 16;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) vx[dt] = load_nt_16(reinterpret_cast<const uint32_t*>(from + dt * 256));
+    };
+    auto k_page = [&](int st) { return s.table[page_of(p, pl, k_block(st))]; };
+    auto v_page = [&](int st) { return s.table[page_of(p, pl, v_block(st))]; };
 
-    if constexpr (WK == 1) {
+    // the next step's K is loaded once the present scores are done, its V once
+    // the present products are; the pages are looked up a step before that
+    int st = begin / S + wave;
+    if (st * S < end) {
+        load_k(st, k_page(st));
+        load_v(st, v_page(st));
+        int kp = k_page(st + WK), vp = v_page(st + WK);
+        while (true) {
+            const int next = st + WK;
+            const bool more = next * S < end;
+            const int kp2 = k_page(next + WK), vp2 = v_page(next + WK);
+            c.template step<1, true>(p, pl, s, st * S, [&](int, int i) { return kx[i]; }, [&](int, int dt) { return vx[dt]; },
+                               [&] { if (more) load_k(next, kp); }, vx);
+            if (!more) break;
+            load_v(next, vp);
+            kp = kp2;
+            vp = vp2;
+            st = next;
+        }
+        if (c.repairs) c.repair(p, pl, s, head, (begin / S + wave) * S, WK * S, end);
+    }
+
+    // join the waves, a quarter of the dims at a time
+    constexpr int DQ = DT / 4;
+    __shared__ float sm_ref[WK][16 * R], sm_sum[WK][16 * R];
+    __shared__ float4_t sm_o[WK][DQ * 4][16 * R];
+    if (g == 0)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (!live[r]) continue;
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) put(row0 + 16 * r + m, 16 * dt + 4 * g, O[r][dt], mx[r], sum[r]);
+            sm_ref[wave][16 * r + m] = c.ref[r];
+            sm_sum[wave][16 * r + m] = c.L[r][0];
         }
-    } else {
-        // the waves hold the same rows over different tokens: join them, a
-        // quarter of the dims at a time
-        constexpr int DQ = DT / 4;
-        __shared__ float sm_top[WK][16 * R], sm_sum[WK][16 * R];
-        __shared__ float4_t sm_o[WK][DQ * 4][16 * R];
-        if (g == 0)
+    __syncthreads();
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                sm_top[wave][16 * r + m] = mx[r];
-                sm_sum[wave][16 * r + m] = sum[r];
-            }
+    for (int r = 0; r < R; ++r) {
+        float top = sm_ref[0][16 * r + m];
+#pragma unroll
+        for (int w = 1; w < WK; ++w) top = fmaxf(top, sm_ref[w][16 * r + m]);
+        const float f = c.ref[r] == -INFINITY ? (c.L[r][0] != 0.0f ? 1.0f : 0.0f) : exp2_fast(c.ref[r] - top);
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) c.O[r][dt] *= f;
+    }
+#pragma unroll
+    for (int quarter = 0; quarter < 4; ++quarter) {
+        if (quarter) __syncthreads();
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int x = 0; x < DQ; ++x) sm_o[wave][4 * x + g][16 * r + m] = c.O[r][quarter * DQ + x];
         __syncthreads();
+        for (int u = threadIdx.x; u < DQ * 4 * 16 * R; u += 256) {
+            const int lr = u / (DQ * 4), d4 = u - lr * (DQ * 4);
+            if (tile_row + lr >= rows) continue;
+            float top = sm_ref[0][lr];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float top = sm_top[0][16 * r + m];
+            for (int w = 1; w < WK; ++w) top = fmaxf(top, sm_ref[w][lr]);
+            float total = 0.0f;
+            float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int w = 1; w < WK; ++w) top = fmaxf(top, sm_top[w][16 * r + m]);
-            const float f = mx[r] == -INFINITY ? 0.0f : exp2_fast(mx[r] - top);
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) O[r][dt] *= f;
-        }
-#pragma unroll
-        for (int quarter = 0; quarter < 4; ++quarter) {
-            if (quarter) __syncthreads();
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int x = 0; x < DQ; ++x) sm_o[wave][4 * x + g][16 * r + m] = O[r][quarter * DQ + x];
-            __syncthreads();
-            for (int u = threadIdx.x; u < DQ * 4 * 16 * R; u += 256) {
-                const int lr = u / (DQ * 4), d4 = u - lr * (DQ * 4);
-                if (tile_row + lr >= rows) continue;
-                float top = sm_top[0][lr];
-#pragma unroll
-                for (int w = 1; w < WK; ++w) top = fmaxf(top, sm_top[w][lr]);
-                float total = 0.0f;
-                float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int w = 0; w < WK; ++w) {
-                    // (a NaN sum stays one)
-                    const float t = sm_top[w][lr];
-                    total += sm_sum[w][lr] * (t == -INFINITY ? 0.0f : exp2_fast(t - top));
-                    o += sm_o[w][d4][lr];
-                }
-                put(tile_row + lr, quarter * (D / 4) + 4 * d4, o, top, total);
+            for (int w = 0; w < WK; ++w) {
+                // (a wave that saw nothing has sum 0; a NaN sum stays one)
+                const float t = sm_ref[w][lr];
+                total += sm_sum[w][lr] * (t == -INFINITY ? 1.0f : exp2_fast(t - top));
+                o += sm_o[w][d4][lr];
             }
+            put<D, E>(p, pl, s.q0, head, split, tile_row + lr, quarter * (D / 4) + 4 * d4, o, top, total);
         }
+    }
+}
+
+// More rows: each wave has R tiles of its own, and the tokens' pieces pass
+// through shared memory once for the workgroup, in the order in which the
+// operands are read (one linear 1 KB a piece and wavefront: no bank is asked
+// twice).  Two stages: the loads of the next KT tokens go straight to shared
+// memory while the present ones are used, one barrier a stage.
+template <int D, int E, int R, int KT>
+__global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams p, AttentionPlan pl) {
+    using C = Core<D, E, R>;
+    constexpr int S = C::S, U = KT / S, DT = C::DT;
+    constexpr int PER = D / 16;              // 1 KB pieces of K, and of V, a unit
+    constexpr int STAGE = 2 * U * PER;
+    constexpr int MINE = STAGE / 4;          // pieces a wave loads
+    static_assert(U == 1 || U == 2, "a wave loads pieces of one unit and kind");
+    __shared__ __attribute__((aligned(16))) uint4 stage0[STAGE * 64];
+    __shared__ __attribute__((aligned(16))) uint4 stage1[STAGE * 64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m = lane & 15, g = lane >> 4;
+    const int hk = p.cache.heads, pb = p.cache.page_blocks;
+    // the tiles of one (split, head, sequence) on one XCD, which then reads its tokens once
+    const int xcd = blockIdx.x & 7;
+    const int turn = blockIdx.x >> 3;
+    const int tile = turn % pl.tiles;
+    int id = (turn / pl.tiles) * 8 + xcd;
+    if (id >= pl.splits * hk * p.B) return;
+    const int split = id % pl.splits;
+    id /= pl.splits;
+    const int head = id % hk, b = id / hk;
+
+    Sequence s;
+    sequence_rows(p, b, s.q0, s.n);
+    const int rows = s.n * pl.group;
+    const int tile_row = tile * 64 * R;
+    if (tile_row >= rows) return;
+    s.len = p.kv_len[b];
+    s.len = s.len < 0 ? 0 : s.len > p.max_kv ? p.max_kv : s.len;
+    s.past = s.len - s.n;
+    const int row_last = (tile_row + 64 * R < rows ? tile_row + 64 * R : rows) - 1;
+    int begin, end;
+    split_range(p, pl, s, b, split, tile_row / pl.group, row_last / pl.group, begin, end);
+    C c;
+    c.init(p, pl, s, head, tile_row + wave * 16 * R, rows);
+
+    // this wave's pieces of a stage: K or V of one unit, or half of them
+    const int unit = U == 2 ? wave >> 1 : 0;
+    const bool values = U == 2 ? wave & 1 : wave >> 1;
+    const int part = U == 2 ? 0 : (wave & 1) * MINE;
+    auto block = [&](int k0) {
+        return min((k0 >> 4) + unit * C::BPU + (values ? g * C::BPU >> 2 : m * C::BPU >> 4), s.last_block);
+    };
+    auto page_at = [&](int k0) { return s.table[page_of(p, pl, block(k0))]; };
+    auto load = [&](uint4* stage, int k0, int page) {
+        page = page < 0 || page >= p.cache.pages ? 0 : page;
+        const int blk = block(k0);
+        const int64_t at = (static_cast<int64_t>(page) * hk + head) * pb + (blk - page_of(p, pl, blk) * pb);
+        const uint8_t* src = static_cast<const uint8_t*>(values ? p.cache.v : p.cache.k) + at * (16 * D * E);
+        src += values ? (E == 2 ? (g & 1) * (16 * D) : 0) + m * 16 : g * 256;
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+            const int x = part + i;          // of the unit's pieces of this kind
+            const int t = x / C::KP;
+            const uint8_t* from = src + (values ? x * 256
+                                                : (((S / 4) * (m >> 2) + 4 * t + (m & 3)) & 15) * 16 + (x - t * C::KP) * 1024);
+            // As plain instructions: the compiler would wait for all of them
+            // before any read of shared memory.  The wait is the explicit one
+            // at the stage's end; a load the compiler does not know of only
+            // makes its own waits stricter.
+            const uint32_t m0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
+                reinterpret_cast<uintptr_t>(stage + ((unit * 2 + (values ? 1 : 0)) * PER + x) * 64)));
+            asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(m0) : "memory", "m0");
+        }
+    };
+    auto compute = [&](const uint4* stage, int k0) {
+        c.template step<U, false>(p, pl, s, k0, [&](int u, int i) { return stage[(u * 2 * PER + i) * 64 + lane]; },
+                           [&](int u, int dt) { return stage[((u * 2 + 1) * PER + dt) * 64 + lane]; }, [] {}, nullptr);
+    };
+
+    if (begin < end) {
+        int k0 = begin;
+        load(stage0, k0, page_at(k0));
+        int page = page_at(k0 + KT);
+        while (true) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            if (k0 + KT < end) load(stage1, k0 + KT, page);
+            page = page_at(k0 + 2 * KT);
+            compute(stage0, k0);
+            k0 += KT;
+            if (k0 >= end) break;
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            if (k0 + KT < end) load(stage0, k0 + KT, page);
+            page = page_at(k0 + 2 * KT);
+            compute(stage1, k0);
+            k0 += KT;
+            if (k0 >= end) break;
+        }
+        if (c.repairs) c.repair(p, pl, s, head, begin, S, end);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (!c.live[r]) continue;
+        const int row = tile_row + wave * 16 * R + 16 * r + m;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) put<D, E>(p, pl, s.q0, head, split, row, 16 * dt + 4 * g, c.O[r][dt], c.ref[r], c.L[r][0]);
     }
 }
 
@@ -406,14 +735,10 @@ template <int D>
 __global__ void __launch_bounds__(256) attention_join_kernel(AttentionParams p, AttentionPlan pl) {
     constexpr int N = D / 64;                // dims a lane
     const int lane = threadIdx.x & 63;
-    const int b = blockIdx.y;
-    const int T = static_cast<int>(p.T);
-    int q0 = p.q_start[b], q1 = p.q_start[b + 1];
-    q0 = q0 < 0 ? 0 : q0 > T ? T : q0;
-    q1 = q1 > T ? T : q1;
-    q1 = q1 > q0 + p.max_q ? q0 + p.max_q : q1;
+    int q0, n;
+    sequence_rows(p, blockIdx.y, q0, n);
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (row >= static_cast<int64_t>(q1 - q0) * p.hq) return;
+    if (row >= static_cast<int64_t>(n) * p.hq) return;
     const int64_t at = static_cast<int64_t>(q0) * p.hq + row;
     const int64_t all = p.T * p.hq;
     const float* ml = p.ws + static_cast<int64_t>(pl.splits) * all * D;
@@ -425,35 +750,35 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttentionParams p, 
     for (int i = 0; i < N; ++i) o[i] = 0.0f;
     for (int s = 0; s < pl.splits; ++s) {
         const float2_t t = *reinterpret_cast<const float2_t*>(ml + 2 * (s * all + at));
-        if (t[0] == -INFINITY && t[1] == 0.0f) continue;   // saw nothing
-        const float f = t[0] == -INFINITY ? 0.0f : exp2_fast(t[0] - top);
+        if (t[1] == 0.0f) continue;          // saw nothing
+        const float f = t[0] == -INFINITY ? 1.0f : exp2_fast(t[0] - top);
         total += t[1] * f;
         const float* src = p.ws + (s * all + at) * D + N * lane;
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] += src[i] * f;
     }
     const float v_scale = p.cache.e4m3 ? p.cache.v_scale[(row % p.hq) / pl.group] : 1.0f;
-    const float f = total > 0.0f || total != total ? v_scale / total : 0.0f;
+    const float f = total != 0.0f ? v_scale / total : 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) p.O[at * D + N * lane + i] = float_to_bf16_bits(o[i] * f);
 }
 
-// Rows a workgroup holds, by the rows a (sequence, head) has: up to 16, 32 or
-// 64 rows its four waves share them and divide the tokens; above, each wave
-// has rows of its own.
+// Rows a workgroup holds, by the rows a (sequence, head) has.  Up to 32: the
+// streaming kernel on 16 or 32.  Above: the tile kernel, a wave on 16 rows
+// (64 in all) up to 64, else on 32 (128).  With 256 dims a step's pieces and
+// the sums of more rows do not fit a wave's registers: the tile kernel on 64.
 int rows_per_tile(int dim, int64_t rows) {
-    if (rows <= 16) return 16;
-    if (rows <= 32) return 32;
-    if (dim == 256) return rows <= 64 ? 32 : 128;
-    return rows <= 64 ? 64 : 256;
+    if (dim == 256) return 64;
+    if (rows <= 32) return rows <= 16 ? 16 : 32;
+    return rows <= 64 ? 64 : 128;
 }
 
 AttentionPlan make_plan(int64_t B, int hq, int hk, int dim, int64_t max_q, int64_t max_kv, int64_t window) {
     AttentionPlan pl{};
     pl.group = hq / hk;
     const int64_t rows = max_q * pl.group;
-    const int tile = rows_per_tile(dim, rows);
-    pl.tiles = static_cast<int>((rows + tile - 1) / tile);
+    pl.tile_rows = rows_per_tile(dim, rows);
+    pl.tiles = static_cast<int>((rows + pl.tile_rows - 1) / pl.tile_rows);
     // tokens that one sequence's rows can see (a window starts at a multiple of 64)
     int64_t span = max_kv;
     if (window > 0 && window + max_q + 64 < span) span = window + max_q + 64;
@@ -471,15 +796,30 @@ AttentionPlan make_plan(int64_t B, int hq, int hk, int dim, int64_t max_q, int64
 }
 
 template <int D, int E>
-void launch_tiles(const AttentionParams& p, const AttentionPlan& pl, dim3 grid, hipStream_t stream) {
-    switch (rows_per_tile(D, static_cast<int64_t>(p.max_q) * pl.group)) {
-        case 16: hipLaunchKernelGGL((attention_kernel<D, E, 1, 4>), grid, dim3(256), 0, stream, p, pl); break;
-        case 32: hipLaunchKernelGGL((attention_kernel<D, E, 2, 4>), grid, dim3(256), 0, stream, p, pl); break;
-        case 64:
-            if constexpr (D < 256) hipLaunchKernelGGL((attention_kernel<D, E, 4, 4>), grid, dim3(256), 0, stream, p, pl);
+hipError_t launch_kind(const AttentionParams& p, const AttentionPlan& pl, hipStream_t stream) {
+    const int64_t groups = static_cast<int64_t>(pl.splits) * p.cache.heads * p.B;
+    const int64_t wgs = pl.tile_rows <= 32 ? groups * pl.tiles : (groups + 7) / 8 * 8 * pl.tiles;
+    if (wgs > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(wgs));
+    // tokens a stage of the tile kernel: 32 KB of shared memory or less, two workgroups a compute unit
+    constexpr int KT = E == 2 && D == 256 ? 32 : 64;
+    switch (pl.tile_rows) {
+        case 16:
+            if constexpr (D < 256) hipLaunchKernelGGL((attention_stream_kernel<D, E, 1>), grid, dim3(256), 0, stream, p, pl);
             break;
-        default: hipLaunchKernelGGL((attention_kernel<D, E, D == 256 ? 2 : 4, 1>), grid, dim3(256), 0, stream, p, pl); break;
+        case 32:
+            if constexpr (D < 256) hipLaunchKernelGGL((attention_stream_kernel<D, E, 2>), grid, dim3(256), 0, stream, p, pl);
+            break;
+        case 64: hipLaunchKernelGGL((attention_tile_kernel<D, E, 1, KT>), grid, dim3(256), 0, stream, p, pl); break;
+        default:
+            if constexpr (D < 256) hipLaunchKernelGGL((attention_tile_kernel<D, E, 2, KT>), grid, dim3(256), 0, stream, p, pl);
+            break;
     }
+    if (pl.splits > 1) {
+        const dim3 jgrid(static_cast<unsigned>((static_cast<int64_t>(p.max_q) * p.hq + 3) / 4), p.B);
+        hipLaunchKernelGGL(attention_join_kernel<D>, jgrid, dim3(256), 0, stream, p, pl);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -495,25 +835,11 @@ hipError_t launch_attention(const AttentionParams& p, hipStream_t stream) {
     AttentionPlan pl = make_plan(p.B, p.hq, p.cache.heads, p.cache.dim, p.max_q, p.max_kv, p.window);
     const int pb = p.cache.page_blocks;
     pl.page_magic = pb > 1 ? static_cast<uint32_t>(((uint64_t{1} << 32) + pb - 1) / pb) : 0;
-    const int64_t groups = static_cast<int64_t>(pl.tiles) * pl.splits * p.cache.heads * p.B;
-    if (groups > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    const dim3 grid(static_cast<unsigned>(groups));
-    if (p.cache.e4m3) {
-        if (p.cache.dim == 64) launch_tiles<64, 1>(p, pl, grid, stream);
-        else if (p.cache.dim == 128) launch_tiles<128, 1>(p, pl, grid, stream);
-        else launch_tiles<256, 1>(p, pl, grid, stream);
-    } else {
-        if (p.cache.dim == 64) launch_tiles<64, 2>(p, pl, grid, stream);
-        else if (p.cache.dim == 128) launch_tiles<128, 2>(p, pl, grid, stream);
-        else launch_tiles<256, 2>(p, pl, grid, stream);
-    }
-    if (pl.splits > 1) {
-        const dim3 jgrid(static_cast<unsigned>((static_cast<int64_t>(p.max_q) * p.hq + 3) / 4), p.B);
-        if (p.cache.dim == 64) hipLaunchKernelGGL(attention_join_kernel<64>, jgrid, dim3(256), 0, stream, p, pl);
-        else if (p.cache.dim == 128) hipLaunchKernelGGL(attention_join_kernel<128>, jgrid, dim3(256), 0, stream, p, pl);
-        else hipLaunchKernelGGL(attention_join_kernel<256>, jgrid, dim3(256), 0, stream, p, pl);
-    }
-    return hipGetLastError();
+    if (p.cache.e4m3)
+        return p.cache.dim == 64 ? launch_kind<64, 1>(p, pl, stream)
+               : p.cache.dim == 128 ? launch_kind<128, 1>(p, pl, stream) : launch_kind<256, 1>(p, pl, stream);
+    return p.cache.dim == 64 ? launch_kind<64, 2>(p, pl, stream)
+           : p.cache.dim == 128 ? launch_kind<128, 2>(p, pl, stream) : launch_kind<256, 2>(p, pl, stream);
 }
 
 }  // namespace w4
