@@ -21,172 +21,11 @@
 // rounded to bf16, the matrix cores' operand; the sum of the same rounded p
 // comes from one more product with ones, so a weight that dominates is not
 // biased by its rounding.
-#include "device.hpp"
-#include "kernels.hpp"
+#include "attention.hpp"
 
 namespace w4 {
 namespace {
-
-// Launch plan: tokens [c * chunk, (c + 1) * chunk) of a sequence (from its
-// first visible one) are split c; `tiles` row tiles a (sequence, head).
-struct AttentionPlan {
-    int chunk, splits, tiles;
-    int group;               // query heads a KV head
-    int tile_rows;           // rows a workgroup
-    uint32_t page_magic;     // block / page_blocks as a high product (page_blocks > 1)
-};
-
-constexpr float kRaise = 8.0f;               // log2 of the largest p
-
-// whether any of a piece's values (8 bf16 or 16 E4M3) is infinite or NaN
-template <int E>
-__device__ __forceinline__ bool nonfinite(const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        // all exponent (E4M3: all) bits set: adding one to the field carries into the sign's place
-        if constexpr (E == 2) any = any || (((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) != 0;
-        else any = any || (((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-    }
-    return any;
-}
-
-// 16 E4M3 codes -> two bf16 operands of 8 (exact).
-__device__ __forceinline__ void widen16(const uint4& c, uint4& lo, uint4& hi) {
-    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
-    uint32_t o[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(in[i], 1.0f, false));
-        o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(in[i], 1.0f, true));
-    }
-    lo = make_uint4(o[0], o[1], o[2], o[3]);
-    hi = make_uint4(o[4], o[5], o[6], o[7]);
-}
-
-__device__ __forceinline__ float4_t mfma(const uint4& a, const uint4& b, const float4_t& c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
-                                                   0, 0, 0);
-}
-
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// maximum over the four lane groups (lanes m, m + 16, m + 32, m + 48)
-__device__ __forceinline__ float max_groups(float x) {
-    const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false));
-    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-    const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false));
-    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
-}
-
-// Eight bf16 values with infinities and NaN replaced by 0; `plus` is 1 where
-// +inf or NaN stood, `minus` where -inf or NaN did.
-__device__ __forceinline__ uint4 finite_part(const uint4& v, uint4& plus, uint4& minus) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t f[4], a[4], b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t out = (((((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) >> 15)) * 0xFFFFu;
-        const uint32_t nan = ((((w[i] & 0x007F007Fu) + 0x007F007Fu) & 0x00800080u) >> 7) * 0xFFFFu;
-        const uint32_t neg = ((w[i] & 0x80008000u) >> 15) * 0xFFFFu;
-        f[i] = w[i] & ~out;
-        a[i] = out & (nan | ~neg) & 0x3F803F80u;
-        b[i] = out & (nan | neg) & 0x3F803F80u;
-    }
-    plus = make_uint4(a[0], a[1], a[2], a[3]);
-    minus = make_uint4(b[0], b[1], b[2], b[3]);
-    return make_uint4(f[0], f[1], f[2], f[3]);
-}
-
-// A cached piece with its infinities and NaN replaced by 0.
-template <int E>
-__device__ __forceinline__ uint4 finite_piece(const uint4& v) {
-    if constexpr (E == 2) {
-        uint4 plus, minus;
-        return finite_part(v, plus, minus);
-    } else {
-        auto fine = [](uint32_t w) {
-            const uint32_t out = ((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
-            return w & ~out;
-        };
-        return make_uint4(fine(v.x), fine(v.y), fine(v.z), fine(v.w));
-    }
-}
-
-// bf16 1 at the elements whose bit is set
-__device__ __forceinline__ uint4 ones_at(uint32_t bits) {
-    auto two = [&](int i) { return ((bits >> i) & 1 ? 0x3F80u : 0u) | ((bits >> i) & 2 ? 0x3F800000u : 0u); };
-    return make_uint4(two(0), two(2), two(4), two(6));
-}
-
-// the low n bits (n may lie outside 0 .. 32)
-__device__ __forceinline__ uint32_t low_bits(int n) {
-    return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
-}
-
-// A sequence as one workgroup sees it.
-struct Sequence {
-    int q0, n;               // its rows of q
-    int len, past;           // cached tokens; those before its nodes
-    int first;               // token that split 0 starts at
-    const int32_t* table;
-    int last_block;
-    bool holes;              // a page of the split's range lies outside the cache
-};
-
-__device__ __forceinline__ void sequence_rows(const AttentionParams& p, int b, int& q0, int& n) {
-    const int T = static_cast<int>(p.T);
-    int a = p.q_start[b], e = p.q_start[b + 1];
-    a = a < 0 ? 0 : a > T ? T : a;
-    e = e > T ? T : e;
-    n = e > a ? e - a : 0;
-    n = n < p.max_q ? n : p.max_q;
-    q0 = a;
-}
-
-__device__ __forceinline__ int page_of(const AttentionParams& p, const AttentionPlan& pl, int blk) {
-    return p.cache.page_blocks > 1 ? static_cast<int>(__umulhi(static_cast<uint32_t>(blk), pl.page_magic)) : blk;
-}
-
-// The tokens [begin, end) of one split that rows up to node `node_last` can
-// see (begin a multiple of 64).
-__device__ __forceinline__ void split_range(const AttentionParams& p, const AttentionPlan& pl, Sequence& s, int b,
-                                            int split, int node_first, int node_last, int& begin, int& end) {
-    const int lane = threadIdx.x & 63;
-    s.table = p.page_table + static_cast<int64_t>(b) * p.table_pages;
-    s.last_block = s.len > 0 ? (s.len - 1) >> 4 : 0;
-    s.first = 0;
-    int lowest = 0;                          // no row of the tile sees a context token below
-    if (p.window > 0) {
-        int least = s.past;                  // the lowest position
-        if (p.positions) {
-            least = 0x7FFFFFFF;
-            for (int i = lane; i < s.n; i += 64) least = min(least, p.positions[s.q0 + i]);
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1) least = min(least, __shfl_xor(least, off));
-            least = __builtin_amdgcn_readfirstlane(least);
-        }
-        lowest = least + (p.positions ? 0 : node_first) - p.window + 1;
-        least = least - p.window + 1;
-        least = least < s.past ? least : s.past;
-        lowest = lowest < s.past ? lowest : s.past;
-        s.first = least > 0 ? least & ~63 : 0;
-        lowest = lowest > 0 ? lowest & ~63 : 0;
-    }
-    begin = s.first + split * pl.chunk;
-    end = split == pl.splits - 1 ? s.len : begin + pl.chunk;
-    if (!p.tree && end > s.past + node_last + 1) end = s.past + node_last + 1;
-    if (end > s.len) end = s.len;
-    if (begin < lowest) begin = lowest;
-    bool bad = false;
-    if (begin < end)
-        for (int i = page_of(p, pl, begin >> 4) + lane; i <= page_of(p, pl, (end - 1) >> 4); i += 64) {
-            const int64_t page = s.table[i];
-            bad = bad || page < 0 || page >= p.cache.pages;
-        }
-    s.holes = __any(bad);
-}
+using namespace attn;
 
 // R tiles of 16 rows of one wavefront: their queries, running sums, and the
 // work of a step of U units.
@@ -247,45 +86,6 @@ struct Core {
         }
     }
 
-    // bit i: row r sees token kf + i (this lane's S/4 tokens of a unit)
-    __device__ __forceinline__ uint32_t sees(const AttentionParams& p, const AttentionPlan& pl, const Sequence& s, int r,
-                                             int kf) const {
-        const int c = s.past - kf;           // tokens of the context among them
-        const int j0 = kf - s.past;          // node of the first
-        uint32_t context = low_bits(c) & ~low_bits(low[r] - kf);
-        uint32_t nodes = 0;
-        if (c < S / 4 && kf < s.len) {
-            if (p.tree) {
-                const uint64_t* words = p.tree + static_cast<int64_t>(s.q0 + node[r]) * p.tree_words;
-                if (j0 >= 0) {
-                    const int w = j0 >> 6, o = j0 & 63;
-                    uint64_t bits = w < p.tree_words ? words[w] >> o : 0;
-                    if (o > 64 - S / 4 && w + 1 < p.tree_words) bits |= words[w + 1] << (64 - o);
-                    nodes = static_cast<uint32_t>(bits);
-                } else {
-                    nodes = static_cast<uint32_t>(words[0] << c);
-                }
-            } else {
-                nodes = low_bits(node[r] - j0 + 1);
-            }
-            if (p.window > 0) {
-                if (p.positions) {
-                    for (int i = c > 0 ? c : 0; i < S / 4 && kf + i < s.len; ++i)
-                        if (p.positions[s.q0 + j0 + i] < low[r]) nodes &= ~(1u << i);
-                } else {
-                    nodes &= ~low_bits(low[r] - kf);
-                }
-            }
-        }
-        uint32_t bits = (context | (nodes & ~low_bits(c))) & low_bits(s.len - kf) & low_bits(S / 4);
-        if (s.holes && kf < s.len) {
-            // (a lane's tokens lie in one block)
-            const int64_t page = s.table[page_of(p, pl, kf >> 4)];
-            if (page < 0 || page >= p.cache.pages) bits = 0;
-        }
-        return live[r] ? bits : 0;
-    }
-
     // Tokens k0 .. k0 + U S - 1: kget(u, i) and vget(u, dt) give the lane's
     // 16-byte pieces of unit u (i = tile * KP + piece); keys_done is called
     // when the K pieces are used up.  OWN: V's pieces are the wave's own
@@ -325,7 +125,7 @@ struct Core {
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const uint32_t seen = sees(p, pl, s, r, k0 + u * S + (S / 4) * g);
+                    const uint32_t seen = live[r] ? sees(p, pl, s, node[r], low[r], k0 + u * S + (S / 4) * g, S / 4) : 0;
 #pragma unroll
                     for (int i = 0; i < 4 * NT; ++i)
                         if (!((seen >> i) & 1)) acc[r][u * NT + (i >> 2)][i & 3] = -INFINITY;
@@ -448,7 +248,7 @@ struct Core {
             const uint8_t* from = static_cast<const uint8_t*>(p.cache.v) + at * (16 * D * E) + (E == 2 ? (g & 1) * (16 * D) : 0) + m * 16;
             uint32_t bits[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) bits[r] = sees(p, pl, s, r, k0 + (S / 4) * g);
+            for (int r = 0; r < R; ++r) bits[r] = live[r] ? sees(p, pl, s, node[r], low[r], k0 + (S / 4) * g, S / 4) : 0;
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt) {
                 uint4 V[NP];
@@ -474,25 +274,6 @@ struct Core {
         }
     }
 };
-
-// Four dims of one row: to O, or as a partial result to the workspace
-// (partials [split][T hq][D], then reference and sum [split][T hq][2]).
-template <int D, int E>
-__device__ __forceinline__ void put(const AttentionParams& p, const AttentionPlan& pl, int q0, int head, int split, int row,
-                                    int d, float4_t o, float ref, float total) {
-    const int nd = row / pl.group;
-    const int64_t at = static_cast<int64_t>(q0 + nd) * p.hq + head * pl.group + (row - nd * pl.group);
-    if (pl.splits == 1) {
-        const float f = total != 0.0f ? (E == 1 ? p.cache.v_scale[head] : 1.0f) / total : 0.0f;
-        *reinterpret_cast<uint2*>(p.O + at * D + d) = make_uint2(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f));
-    } else {
-        const int64_t all = p.T * p.hq;
-        const int64_t slice = static_cast<int64_t>(split) * all + at;
-        *reinterpret_cast<float4_t*>(p.ws + slice * D + d) = o;
-        if (d == 0)
-            *reinterpret_cast<float2_t*>(p.ws + static_cast<int64_t>(pl.splits) * all * D + 2 * slice) = float2_t{ref, total};
-    }
-}
 
 // Up to 32 rows: the time is that of reading the cache once.  The four waves
 // of a workgroup hold the same rows and take steps of one unit in turn, each
@@ -622,13 +403,14 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(AttentionParam
     }
 }
 
-// More rows: each wave has R tiles of its own, and the tokens' pieces pass
-// through shared memory once for the workgroup, in the order in which the
+// Heads of 256 dims, whose pieces and sums do not fit a wave's registers in
+// the other forms: each of four waves has R tiles of its own, and the tokens'
+// pieces pass through shared memory once for the workgroup, in the order in which the
 // operands are read (one linear 1 KB a piece and wavefront: no bank is asked
 // twice).  Two stages: the loads of the next KT tokens go straight to shared
 // memory while the present ones are used, one barrier a stage.
 template <int D, int E, int R, int KT>
-__global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams p, AttentionPlan pl) {
+__global__ void __launch_bounds__(256, 2) attention_wide_kernel(AttentionParams p, AttentionPlan pl) {
     using C = Core<D, E, R>;
     constexpr int S = C::S, U = KT / S, DT = C::DT;
     constexpr int PER = D / 16;              // 1 KB pieces of K, and of V, a unit
@@ -764,13 +546,11 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttentionParams p, 
 }
 
 // Rows a workgroup holds, by the rows a (sequence, head) has.  Up to 32: the
-// streaming kernel on 16 or 32.  Above: the tile kernel, a wave on 16 rows
-// (64 in all) up to 64, else on 32 (128).  With 256 dims a step's pieces and
-// the sums of more rows do not fit a wave's registers: the tile kernel on 64.
+// streaming kernel on 16 or 32.  Above: the tile kernel on 128.  256 dims: the
+// wide kernel on 64.
 int rows_per_tile(int dim, int64_t rows) {
     if (dim == 256) return 64;
-    if (rows <= 32) return rows <= 16 ? 16 : 32;
-    return rows <= 64 ? 64 : 128;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
 }
 
 AttentionPlan make_plan(int64_t B, int hq, int hk, int dim, int64_t max_q, int64_t max_kv, int64_t window) {
@@ -798,22 +578,19 @@ AttentionPlan make_plan(int64_t B, int hq, int hk, int dim, int64_t max_q, int64
 template <int D, int E>
 hipError_t launch_kind(const AttentionParams& p, const AttentionPlan& pl, hipStream_t stream) {
     const int64_t groups = static_cast<int64_t>(pl.splits) * p.cache.heads * p.B;
-    const int64_t wgs = pl.tile_rows <= 32 ? groups * pl.tiles : (groups + 7) / 8 * 8 * pl.tiles;
+    const bool tiled = pl.tile_rows > 32;
+    const int64_t wgs = tiled ? (groups + 7) / 8 * 8 * pl.tiles : groups * pl.tiles;
     if (wgs > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    const dim3 grid(static_cast<unsigned>(wgs));
-    // tokens a stage of the tile kernel: 32 KB of shared memory or less, two workgroups a compute unit
-    constexpr int KT = E == 2 && D == 256 ? 32 : 64;
-    switch (pl.tile_rows) {
-        case 16:
-            if constexpr (D < 256) hipLaunchKernelGGL((attention_stream_kernel<D, E, 1>), grid, dim3(256), 0, stream, p, pl);
-            break;
-        case 32:
-            if constexpr (D < 256) hipLaunchKernelGGL((attention_stream_kernel<D, E, 2>), grid, dim3(256), 0, stream, p, pl);
-            break;
-        case 64: hipLaunchKernelGGL((attention_tile_kernel<D, E, 1, KT>), grid, dim3(256), 0, stream, p, pl); break;
-        default:
-            if constexpr (D < 256) hipLaunchKernelGGL((attention_tile_kernel<D, E, 2, KT>), grid, dim3(256), 0, stream, p, pl);
-            break;
+    const unsigned grid = static_cast<unsigned>(wgs);
+    if constexpr (D == 256) {
+        // 64 KB of shared memory: two workgroups a compute unit
+        hipLaunchKernelGGL((attention_wide_kernel<D, E, 1, E == 2 ? 32 : 64>), dim3(grid), dim3(256), 0, stream, p, pl);
+    } else if (tiled) {
+        const hipError_t e = launch_attention_tiles(p, pl, grid, stream);
+        if (e != hipSuccess) return e;
+    } else {
+        if (pl.tile_rows == 16) hipLaunchKernelGGL((attention_stream_kernel<D, E, 1>), dim3(grid), dim3(256), 0, stream, p, pl);
+        else hipLaunchKernelGGL((attention_stream_kernel<D, E, 2>), dim3(grid), dim3(256), 0, stream, p, pl);
     }
     if (pl.splits > 1) {
         const dim3 jgrid(static_cast<unsigned>((static_cast<int64_t>(p.max_q) * p.hq + 3) / 4), p.B);
