@@ -429,9 +429,11 @@ __global__ void __launch_bounds__(256, 2) attention_wide_kernel(AttentionParams 
     const int tile = turn % pl.tiles;
     int id = (turn / pl.tiles) * 8 + xcd;
     if (id >= pl.splits * hk * p.B) return;
-    const int split = id % pl.splits;
-    id /= pl.splits;
-    const int head = id % hk, b = id / hk;
+    // (heads before splits: the splits of a sequence differ in length, and would
+    // fall on the same XCDs for every head)
+    const int head = id % hk;
+    id /= hk;
+    const int split = id % pl.splits, b = id / pl.splits;
 
     Sequence s;
     sequence_rows(p, b, s.q0, s.n);
@@ -512,37 +514,64 @@ __global__ void __launch_bounds__(256, 2) attention_wide_kernel(AttentionParams 
     }
 }
 
-// The splits of a row joined in order: one wavefront a row.
+// The splits of a row joined, in a fixed order: `parts` threads for each four
+// dims of a row take every parts-th split, four loads in flight, and are
+// joined through shared memory.
 template <int D>
-__global__ void __launch_bounds__(256) attention_join_kernel(AttentionParams p, AttentionPlan pl) {
-    constexpr int N = D / 64;                // dims a lane
-    const int lane = threadIdx.x & 63;
+__global__ void __launch_bounds__(256) attention_join_kernel(AttentionParams p, AttentionPlan pl, int parts) {
+    constexpr int L = D / 4;                 // threads a row and part
+    __shared__ float4_t sm_o[256];
+    __shared__ float2_t sm_ml[256];
+    const int vec = threadIdx.x % L;
+    const int part = (threadIdx.x / L) % parts;
     int q0, n;
     sequence_rows(p, blockIdx.y, q0, n);
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (row >= static_cast<int64_t>(n) * p.hq) return;
-    const int64_t at = static_cast<int64_t>(q0) * p.hq + row;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / (L * parts)) + threadIdx.x / (L * parts);
+    const bool live = row < static_cast<int64_t>(n) * p.hq;
+    const int64_t at = static_cast<int64_t>(q0) * p.hq + (live ? row : 0);
     const int64_t all = p.T * p.hq;
     const float* ml = p.ws + static_cast<int64_t>(pl.splits) * all * D;
-    float top = -INFINITY;
-    for (int s = lane; s < pl.splits; s += 64) top = fmaxf(top, ml[2 * (s * all + at)]);
-    top = wave_max(top);
-    float total = 0.0f, o[N];
+    float top = -INFINITY, total = 0.0f;
+    float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto add = [&](float2_t t, float4_t x) {
+        if (t[1] == 0.0f) return;            // saw nothing
+        const float now = fmaxf(top, t[0]);
+        const float f = t[0] == -INFINITY ? 1.0f : exp2_fast(t[0] - now);
+        const float g = top == -INFINITY ? 1.0f : exp2_fast(top - now);
+        total = total * g + t[1] * f;
+        o = o * g + x * f;
+        top = now;
+    };
+    if (live) {
+        int s = part;
+        for (; s + 3 * parts < pl.splits; s += 4 * parts) {
+            float2_t t[4];
+            float4_t x[4];
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = 0.0f;
-    for (int s = 0; s < pl.splits; ++s) {
-        const float2_t t = *reinterpret_cast<const float2_t*>(ml + 2 * (s * all + at));
-        if (t[1] == 0.0f) continue;          // saw nothing
-        const float f = t[0] == -INFINITY ? 1.0f : exp2_fast(t[0] - top);
-        total += t[1] * f;
-        const float* src = p.ws + (s * all + at) * D + N * lane;
+            for (int i = 0; i < 4; ++i) {
+                const int64_t slice = static_cast<int64_t>(s + i * parts) * all + at;
+                t[i] = *reinterpret_cast<const float2_t*>(ml + 2 * slice);
+                x[i] = *reinterpret_cast<const float4_t*>(p.ws + slice * D + 4 * vec);
+            }
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] += src[i] * f;
+            for (int i = 0; i < 4; ++i) add(t[i], x[i]);
+        }
+        for (; s < pl.splits; s += parts) {
+            const int64_t slice = static_cast<int64_t>(s) * all + at;
+            add(*reinterpret_cast<const float2_t*>(ml + 2 * slice), *reinterpret_cast<const float4_t*>(p.ws + slice * D + 4 * vec));
+        }
     }
+    if (parts > 1) {
+        sm_o[threadIdx.x] = o;
+        sm_ml[threadIdx.x] = float2_t{top, total};
+        __syncthreads();
+        if (part == 0)
+            for (int i = 1; i < parts; ++i) add(sm_ml[threadIdx.x + i * L], sm_o[threadIdx.x + i * L]);
+    }
+    if (!live || part) return;
     const float v_scale = p.cache.e4m3 ? p.cache.v_scale[(row % p.hq) / pl.group] : 1.0f;
     const float f = total != 0.0f ? v_scale / total : 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) p.O[at * D + N * lane + i] = float_to_bf16_bits(o[i] * f);
+    *reinterpret_cast<uint2*>(p.O + at * D + 4 * vec) = make_uint2(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f));
 }
 
 // Rows a workgroup holds, by the rows a (sequence, head) has.  Up to 32: the
@@ -593,8 +622,12 @@ hipError_t launch_kind(const AttentionParams& p, const AttentionPlan& pl, hipStr
         else hipLaunchKernelGGL((attention_stream_kernel<D, E, 2>), dim3(grid), dim3(256), 0, stream, p, pl);
     }
     if (pl.splits > 1) {
-        const dim3 jgrid(static_cast<unsigned>((static_cast<int64_t>(p.max_q) * p.hq + 3) / 4), p.B);
-        hipLaunchKernelGGL(attention_join_kernel<D>, jgrid, dim3(256), 0, stream, p, pl);
+        // threads a row and four dims: one for few splits, more while they have four each
+        int parts = 1;
+        while (parts * (D / 4) < 256 && parts * 4 < pl.splits) parts *= 2;
+        const int rows = 256 / (D / 4 * parts);
+        const dim3 jgrid(static_cast<unsigned>((static_cast<int64_t>(p.max_q) * p.hq + rows - 1) / rows), p.B);
+        hipLaunchKernelGGL(attention_join_kernel<D>, jgrid, dim3(256), 0, stream, p, pl, parts);
     }
     return hipGetLastError();
 }

@@ -63,9 +63,11 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
     const int tile = turn % pl.tiles;
     int id = (turn / pl.tiles) * 8 + xcd;
     if (id >= pl.splits * hk * p.B) return;
-    const int split = id % pl.splits;
-    id /= pl.splits;
-    const int head = id % hk, b = id / hk;
+    // (heads before splits: the splits of a sequence differ in length, and would
+    // fall on the same XCDs for every head)
+    const int head = id % hk;
+    id /= hk;
+    const int split = id % pl.splits, b = id / pl.splits;
 
     Sequence s;
     sequence_rows(p, b, s.q0, s.n);
@@ -169,7 +171,9 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
     };
     // tokens [plain, plain_end) are seen by all rows of the wave
     const int plain = low_most;
-    const int plain_end = s.holes ? 0 : s.past < s.len ? s.past : s.len;
+    // (a chain's tokens up to the first row's own node too)
+    int plain_end = p.tree || p.positions ? s.past : s.past + row0 / pl.group + 1;
+    plain_end = s.holes ? 0 : plain_end < s.len ? plain_end : s.len;
     auto needs_mask = [&](int k0, int tokens) { return k0 < plain || k0 + tokens > plain_end; };
 
     for (int from_token = begin; from_token < end; from_token += 16 * kTableBlocks) {
@@ -199,25 +203,25 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
             if (!works) continue;
             const int k0 = from_token + 64 * st;
             const uint4* at = ring + (st & 1) * STAGE * 64 + lane;
-            float16_t acc[2];
+            float16_t acc[2] = {zero16(), zero16()};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint4 kx[KC];
+            for (int c = 0; c < KC; ++c)
 #pragma unroll
-                for (int c = 0; c < KC; ++c) kx[c] = at[(u * 2 * KC + c) * 64];
-                acc[u] = zero16();
-#pragma unroll
-                for (int c = 0; c < KC; ++c) {
+                for (int u = 0; u < 2; ++u) {
+                    const uint4 x = at[(u * 2 * KC + c) * 64];
                     if constexpr (E == 2) {
-                        acc[u] = mfma32(kx[c], Q[0][c], acc[u]);
+                        acc[u] = mfma32(x, Q[0][c], acc[u]);
                     } else {
                         uint4 lo, hi;
-                        widen16(kx[c], lo, hi);
+                        widen16(x, lo, hi);
                         acc[u] = mfma32(lo, Q[0][2 * c], acc[u]);
                         acc[u] = mfma32(hi, Q[0][2 * c + 1], acc[u]);
                     }
                 }
-            }
+            // the first unit's values on their way under the exponentials
+            uint4 vx[KC];
+#pragma unroll
+            for (int c = 0; c < KC; ++c) vx[c] = at[(KC + c) * 64];
             const bool masked = needs_mask(k0, 64);
             bool odd = false;
             if (masked) {
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
                 for (int u = 0; u < 2; ++u) {
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
-                        uint4 x = at[((u * 2 + 1) * KC + c) * 64];
+                        uint4 x = u == 0 ? vx[c] : at[((u * 2 + 1) * KC + c) * 64];
                         if constexpr (decltype(clean)::value) x = finite_piece<E>(x);
                         if constexpr (E == 2) {
                             O[0][c % DB] = mfma32(x, P[u][c / DB], O[0][c % DB]);
