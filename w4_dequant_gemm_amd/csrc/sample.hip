@@ -9,7 +9,9 @@
 // follows by division.
 //
 // One workgroup of 1024 threads a row, which is read from memory for the
-// maximum and again from the caches for what follows:
+// maximum and kept in registers (up to 16 vectors of 16 bytes a thread: 131072
+// bf16, 65536 fp32) for what compares every element; what takes an exponential
+// of every element reads it again from the caches.  Then
 //  - top-k: the k-th largest of the threads' own maxima bounds the k-th largest
 //    logit from below, so few tokens besides the top k lie above it: they are
 //    collected in shared memory and the filters and the draw work on them;
@@ -33,9 +35,11 @@ constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kCandidates = 4096;            // tokens collected in shared memory
 constexpr int kMine = kCandidates / kThreads;
-constexpr int kBins = 2048;
-constexpr float kBinsPerUnit = 64.0f;        // bins of 1/64 of the scaled distance
+constexpr int kKept = 16;                    // 16-byte vectors of a row a thread keeps
+constexpr int kBins = 512;
+constexpr float kBinsPerUnit = 16.0f;        // bins of 1/16 of the scaled distance, down to exp(-32)
 constexpr int kSegments = (1 << 20) / 256 + 1;
+constexpr int kLevels = 18;                  // of all selections of a call: 4 + 4 by key, 3 + 3 by index, and spare
 
 // fp32 (not NaN) -> a key in the order of the values; -0 like +0
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -52,10 +56,10 @@ __device__ __forceinline__ uint32_t weight_of(float x, float top, float r) {
     const float e = x == -INFINITY ? 0.0f : expf((x - top) * r);
     return static_cast<uint32_t>(rintf(e * 2147483648.0f));
 }
-// a distance that grows as the weight falls, the same for equal values; the bin is its whole part
-__device__ __forceinline__ float bin_of(float x, float top, float r) {
-    return x == top ? 0.0f : fminf((top - x) * r * kBinsPerUnit, 1e9f);
-}
+// a distance that grows as the weight falls, the same for equal values (NaN for
+// infinities: like 0); a bin is its whole part
+__device__ __forceinline__ float distance(float x, float top, float r) { return (top - x) * (r * kBinsPerUnit); }
+__device__ __forceinline__ int bin_of(float d) { return static_cast<int>(fminf(fmaxf(d, 0.0f), static_cast<float>(kBins))); }
 
 __device__ __forceinline__ uint64_t units_of_2_24(float x, uint64_t most) {
     const float f = floorf(x * 16777216.0f);
@@ -68,84 +72,85 @@ __device__ __forceinline__ uint64_t part_of(uint64_t m, uint64_t total, bool& mo
     return m * (total >> 24) + (low >> 24);
 }
 
-__device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(static_cast<unsigned long long>(v), off);
-    return v;
+// lane i gets lane i - n's value by a data-parallel move (0 where there is none)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t moved(uint64_t v) {
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), CTRL, ROWS, 0xF, false);
+    return static_cast<uint64_t>(hi) << 32 | lo;
 }
-// running sum over the lanes, this one included
+// running sum over the 64 lanes, this one included: shifts by 1, 2, 4, 8 within
+// rows of 16 lanes, then each row's last lane to the rows after it
 __device__ __forceinline__ uint64_t wave_scan64(uint64_t v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const uint64_t o = __shfl_up(static_cast<unsigned long long>(v), off);
-        if (lane >= off) v += o;
-    }
+    v += moved<0x111, 0xF>(v);
+    v += moved<0x112, 0xF>(v);
+    v += moved<0x114, 0xF>(v);
+    v += moved<0x118, 0xF>(v);
+    v += moved<0x142, 0xA>(v);
+    v += moved<0x143, 0xC>(v);
     return v;
 }
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), lane);
+    return static_cast<uint64_t>(hi) << 32 | lo;
+}
+__device__ __forceinline__ uint64_t wave_sum64(uint64_t v) { return lane_value(wave_scan64(v), 63); }
 
 struct Shared {
-    union {
-        struct {
-            uint64_t bins[kBins];            // weights by distance
-            uint32_t counts[kBins];
-        };
-        uint64_t segments[kSegments];
-    };
-    uint64_t hist[256];
-    uint64_t wave64[kWaves];
-    uint32_t wave32[kWaves];
+    uint64_t hist[kLevels][256];             // one a level: cleared at the start, used once
+    uint64_t bins[kBins];                    // weights by distance
+    uint64_t segments[kSegments];
+    uint64_t wave64[2][kWaves];
+    uint32_t counts[kBins];                  // threads' maxima by distance
+    uint32_t wave32[2][kWaves];
     uint32_t key[kCandidates], index[kCandidates];
     uint32_t candidates;
-    uint32_t pick;
-    uint64_t above;
 };
 
-__device__ __forceinline__ uint64_t block_sum(Shared& sh, uint64_t v) {
-    v = wave_sum64(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) sh.wave64[threadIdx.x >> 6] = v;
-    __syncthreads();
-    uint64_t t = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) t += sh.wave64[w];
-    return t;
-}
-
-// The first of n bins (ascending) at which their running sum reaches need, and
-// the sum before it, by the first wavefront; n (a multiple of 64) if it is not
-// reached.  Every thread gets the result.
-template <class Get>
-__device__ __forceinline__ int reach(Shared& sh, int n, uint64_t need, uint64_t& before, Get get) {
-    if (threadIdx.x < 64) {
-        const int lane = threadIdx.x;
-        const int per = n / 64;              // consecutive bins of a lane
-        uint64_t mine = 0;
-        for (int i = 0; i < per; ++i) mine += get(lane * per + i);
-        const uint64_t upto = wave_scan64(mine);
-        const uint64_t hit = __ballot(upto >= need);
-        if (!hit) {
-            if (lane == 63) {
-                sh.pick = static_cast<uint32_t>(n);
-                sh.above = upto;
-            }
-        } else if (lane == __ffsll(static_cast<unsigned long long>(hit)) - 1) {
-            uint64_t sum = upto - mine;
-            int i = 0;
-            for (; i < per - 1; ++i) {
-                const uint64_t w = get(lane * per + i);
-                if (sum + w >= need) break;
-                sum += w;
-            }
-            sh.pick = static_cast<uint32_t>(lane * per + i);
-            sh.above = sum;
-        }
+// What every wavefront of the row knows alike.
+struct Turn {
+    Shared& sh;
+    int level = 0, sums = 0;
+    // (two places in turn: one barrier a sum)
+    __device__ __forceinline__ uint64_t block_sum(uint64_t v) {
+        v = wave_sum64(v);
+        uint64_t* at = sh.wave64[sums++ & 1];
+        if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6] = v;
+        __syncthreads();
+        return wave_sum64((threadIdx.x & 63) < kWaves ? at[threadIdx.x & 63] : 0);
     }
-    __syncthreads();
-    before = sh.above;
-    const int at = static_cast<int>(sh.pick);
-    __syncthreads();
-    return at;
+};
+
+// The first of 64 PER bins (ascending) at which their running sum reaches need,
+// and the sum before it; 64 PER and the whole sum if it is not reached.  Every
+// wavefront searches for itself, which saves the barriers of telling.
+template <int PER, class Get>
+__device__ __forceinline__ int reach(uint64_t need, uint64_t& before, Get get) {
+    const int lane = threadIdx.x & 63;
+    uint64_t w[PER], mine = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        w[i] = get(lane * PER + i);
+        mine += w[i];
+    }
+    const uint64_t upto = wave_scan64(mine);
+    const uint64_t hit = __ballot(upto >= need);
+    if (!hit) {
+        before = lane_value(upto, 63);
+        return 64 * PER;
+    }
+    const int at = __ffsll(static_cast<unsigned long long>(hit)) - 1;
+    uint64_t sum = upto - mine;
+    int skip = 0;
+#pragma unroll
+    for (int i = 0; i < PER - 1; ++i)
+        if (skip == i && sum + w[i] < need) {
+            sum += w[i];
+            ++skip;
+        }
+    before = lane_value(sum, at);
+    return at * PER + __builtin_amdgcn_readlane(skip, at);
 }
 
 // The key (of `bits` bits, a multiple of 8) at which the running sum of weights
@@ -153,23 +158,22 @@ __device__ __forceinline__ int reach(Shared& sh, int n, uint64_t need, uint64_t&
 // above it.  each(f) calls f(key, weight) for this thread's items, weight being
 // a function.
 template <class Each>
-__device__ __forceinline__ uint32_t select(Shared& sh, int bits, int stop, uint64_t need, uint64_t& above, Each each) {
+__device__ __forceinline__ uint32_t select(Turn& turn, int bits, int stop, uint64_t need, uint64_t& above, Each each) {
     uint32_t prefix = 0;
     above = 0;
+#pragma unroll 1
     for (int shift = bits - 8; shift >= stop; shift -= 8) {
-        __syncthreads();
-        if (threadIdx.x < 256) sh.hist[threadIdx.x] = 0;
-        __syncthreads();
+        uint64_t* hist = turn.sh.hist[turn.level++];
         const uint32_t mask = shift + 8 >= 32 ? 0u : 0xFFFFFFFFu << (shift + 8);
         each([&](uint32_t key, auto weight) {
             if (((key ^ prefix) & mask) == 0) {
                 const unsigned long long w = weight();
-                if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.hist[(key >> shift) & 255]), w);
+                if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&hist[255 - ((key >> shift) & 255)]), w);
             }
         });
         __syncthreads();
         uint64_t before;
-        const int at = reach(sh, 256, need - above, before, [&](int i) { return sh.hist[255 - i]; });
+        const int at = reach<4>(need - above, before, [&](int i) { return hist[i]; });
         above += before;
         prefix |= static_cast<uint32_t>(255 - at) << shift;
     }
@@ -219,18 +223,19 @@ struct Row {
             f(fmaxf(y, -INFINITY), v * N + i - shift);   // (NaN like -inf)
         }
     }
-    // f(vector, its number, turn) for this thread's vectors
+    // f(vector, its number, turn) for this thread's vectors, read ahead
     template <class F>
     __device__ __forceinline__ void all(F f) const {
-        for (int j = 0; j * kThreads < count; j += 4) {
-            uint4 x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = load(static_cast<int>(threadIdx.x) + (j + i) * kThreads);
+        const int tid = static_cast<int>(threadIdx.x);
+        uint4 a = load(tid), b = load(tid + kThreads), c = load(tid + 2 * kThreads), d = load(tid + 3 * kThreads);
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-                const uint4 y = i == 0 ? x[0] : i == 1 ? x[1] : i == 2 ? x[2] : x[3];
-                if ((j + i) * kThreads < count) f(y, static_cast<int>(threadIdx.x) + (j + i) * kThreads, j + i);
-            }
+        for (int j = 0; j * kThreads < count; ++j) {
+            const uint4 e = load(tid + (j + 4) * kThreads);
+            f(a, tid + j * kThreads, j);
+            a = b;
+            b = c;
+            c = d;
+            d = e;
         }
     }
     template <class F>
@@ -239,11 +244,27 @@ struct Row {
     }
 };
 
-template <bool F32>
+// KEEP: the row's vectors stay in registers from the first reading, for what
+// is done to every element with few instructions.
+template <bool F32, bool KEEP>
 __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     __shared__ Shared sh;
     const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    Row<F32> row(p.logits, b * p.row_stride, p.V);
+    const Row<F32> row(p.logits, b * p.row_stride, p.V);
+    uint4 kept[KEEP ? kKept : 1];
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int j = 0; j < kKept; ++j) kept[j] = row.load(static_cast<int>(threadIdx.x) + j * kThreads);
+    }
+    auto light = [&](auto f) {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int j = 0; j < kKept; ++j)
+                if (j * kThreads < row.count) row.elements(kept[j], static_cast<int>(threadIdx.x) + j * kThreads, f);
+        } else {
+            row.values(f);
+        }
+    };
     const float t = p.temperature ? p.temperature[b] : 1.0f;
     const bool greedy = !(t > 0.0f);
     const float r = greedy ? 1.0f : 1.0f / t;
@@ -251,9 +272,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     if (k < 0 || k >= p.V) k = 0;
     const uint64_t p_units = p.top_p ? units_of_2_24(p.top_p[b], 1u << 24) : 1u << 24;
     const bool cuts = p_units < (1u << 24);
+    const float min_p = p.min_p ? p.min_p[b] : 0.0f;
     uint32_t least = 1;                      // smallest weight kept
-    if (p.min_p) {
-        const float f = ceilf(p.min_p[b] * 2147483648.0f);
+    {
+        const float f = ceilf(min_p * 2147483648.0f);
         least = f >= 4294967040.0f ? 0xFFFFFFFFu : f > 1.0f ? static_cast<uint32_t>(f) : 1u;
     }
     const float uniform = p.u[b];
@@ -261,53 +283,56 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         p.tokens[b] = token;
         if (p.probs) p.probs[b] = prob;
     };
-
-    float mine = -INFINITY;
-    row.values([&](float x, int) { mine = fmaxf(mine, x); });
-    float top = wave_max(mine);
-    if (lane == 0) sh.wave32[wave] = __float_as_uint(top);
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
-        sh.bins[i] = 0;
-        sh.counts[i] = 0;
+    Turn turn{sh};
+    for (int i = threadIdx.x; i < kLevels * 256; i += kThreads) (&sh.hist[0][0])[i] = 0;
+    if (threadIdx.x < kBins) {
+        sh.bins[threadIdx.x] = 0;
+        sh.counts[threadIdx.x] = 0;
     }
     if (threadIdx.x == 0) sh.candidates = 0;
+
+    float mine = -INFINITY;
+    light([&](float x, int) { mine = fmaxf(mine, x); });
+    float top = wave_max(mine);
+    if (lane == 0) sh.wave32[0][wave] = __float_as_uint(top);
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, __uint_as_float(sh.wave32[w]));
+    top = max16(__uint_as_float(sh.wave32[0][lane & (kWaves - 1)]));
     if (top == -INFINITY) {
         if (threadIdx.x == 0) answer(-1, 0.0f);
         return;
     }
     if (greedy) {
         int first = 0x7FFFFFFF;
-        row.values([&](float x, int i) { first = x == top && i < first ? i : first; });
+        if (mine == top) light([&](float x, int i) { first = x == top && i < first ? i : first; });
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) first = min(first, __shfl_xor(first, off));
+        if (lane == 0) sh.wave32[1][wave] = static_cast<uint32_t>(first);
         __syncthreads();
-        if (lane == 0) sh.wave32[wave] = static_cast<uint32_t>(first);
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) first = min(first, static_cast<int>(sh.wave32[w]));
-        if (threadIdx.x == 0) answer(first, least <= 0x80000000u ? 1.0f : 0.0f);
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kWaves; ++w) first = min(first, static_cast<int>(sh.wave32[1][w]));
+            const bool kept_one = least <= 0x80000000u;
+            answer(kept_one ? first : -1, kept_one ? 1.0f : 0.0f);
+        }
         return;
     }
 
     uint32_t kappa = 0, iota = 0xFFFFFFFFu;  // kept: keys above kappa, and equal ones up to index iota
     uint64_t take = 0;                       // how many equal ones
-    // the threads' maxima by distance: the bin in which the n-th largest lies
+    // a distance within which at least n of the threads' maxima lie
     auto bound = [&](int n) -> float {
         if (p.V <= kCandidates) return 1e30f;
-        const float at = bin_of(mine, top, r);
-        if (at < kBins) atomicAdd(&sh.counts[static_cast<int>(at)], 1u);
+        const int at = bin_of(distance(mine, top, r));
+        if (at < kBins) atomicAdd(&sh.counts[at], 1u);
         __syncthreads();
         uint64_t before;
-        const int bin = reach(sh, kBins, n, before, [&](int i) { return static_cast<uint64_t>(sh.counts[i]); });
+        const int bin = reach<kBins / 64>(n, before, [&](int i) { return static_cast<uint64_t>(sh.counts[i]); });
         return bin < kBins ? static_cast<float>(bin + 1) : 1e30f;
     };
+    // the tokens with from <= distance < below (infinities' NaN is 0)
     auto collect = [&](float from, float below) -> int {
-        row.values([&](float x, int i) {
-            const float at = bin_of(x, top, r);
-            if (at >= from && at < below) {
+        light([&](float x, int i) {
+            const float d = distance(x, top, r);
+            if (!(d >= below) && !(d < from)) {
                 const uint32_t n = atomicAdd(&sh.candidates, 1u);
                 if (n < kCandidates) {
                     sh.key[n] = key_of(x);
@@ -355,24 +380,25 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         uint64_t above;
         if (n <= kCandidates) {
             few = listed = true;
+            k = k < n ? k : n;               // (fewer than k above -inf)
             own(n);
-            kappa = whole_key(select(sh, 32, kStop, k, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t) { f(key, [] { return 1ull; }); }); }));
+            kappa = whole_key(select(turn, 32, kStop, k, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t) { f(key, [] { return 1ull; }); }); }));
         } else {
-            kappa = whole_key(select(sh, 32, kStop, k, above, [&](auto f) { everything([&](uint32_t key, uint32_t, auto) { f(key, [] { return 1ull; }); }); }));
+            kappa = whole_key(select(turn, 32, kStop, k, above, [&](auto f) { everything([&](uint32_t key, uint32_t, auto) { f(key, [] { return 1ull; }); }); }));
         }
         take = k - above;
         if (cuts) {
             uint64_t sum = 0;
             if (few) collected([&](uint32_t key, uint32_t, uint32_t w) { sum += key > kappa ? w : 0; });
             else everything([&](uint32_t key, uint32_t, auto w) { if (key > kappa) sum += w(); });
-            const uint64_t total = block_sum(sh, sum) + take * weight_at(kappa);
+            const uint64_t total = turn.block_sum(sum) + take * weight_at(kappa);
             bool more;
             uint64_t need = part_of(p_units, total, more);
             need += more ? 1 : 0;
             need = need < 1 ? 1 : need;
             uint32_t at;
-            if (few) at = select(sh, 32, kStop, need, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t w) { f(key, [&] { return static_cast<unsigned long long>(w); }); }); });
-            else at = select(sh, 32, kStop, need, above, [&](auto f) { everything([&](uint32_t key, uint32_t, auto w) { f(key, [&] { return static_cast<unsigned long long>(w()); }); }); });
+            if (few) at = select(turn, 32, kStop, need, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t w) { f(key, [&] { return static_cast<unsigned long long>(w); }); }); });
+            else at = select(turn, 32, kStop, need, above, [&](auto f) { everything([&](uint32_t key, uint32_t, auto w) { f(key, [&] { return static_cast<unsigned long long>(w()); }); }); });
             at = whole_key(at);
             const uint64_t w = weight_at(at);
             const uint64_t n_at = w ? (need - above + w - 1) / w : 1;
@@ -386,46 +412,49 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     } else if (cuts) {
         // weights by distance, down to the 512th largest of the threads'
         // maxima; if p of the total lies further down, all
-        float limit = bound(512);
-        uint64_t total = 0, need = 0, before = 0;
-        int bin = kBins;
-        float from = 0.0f;
-        while (true) {
-            uint64_t rest = 0;
+        const float limit = bound(512);
+        uint64_t rest = 0, before;
+        row.values([&](float x, int) {
+            const float d = distance(x, top, r);
+            const uint32_t w = weight_of(x, top, r);
+            if (!(d >= limit)) {
+                const int at = bin_of(d);
+                if (w && at < kBins) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[at]), static_cast<unsigned long long>(w));
+            } else {
+                rest += w;
+            }
+        });
+        rest = turn.block_sum(rest);         // (its barrier is also that after the atomics)
+        auto bins = [&](int i) { return sh.bins[i]; };
+        reach<kBins / 64>(~uint64_t{0}, before, bins);
+        const uint64_t total = before + rest;
+        bool more;
+        uint64_t need = part_of(p_units, total, more);
+        need += more ? 1 : 0;
+        need = need < 1 ? 1 : need;
+        int bin = reach<kBins / 64>(need, before, bins);
+        if (bin == kBins) {
+            __syncthreads();
             row.values([&](float x, int) {
-                const float at = bin_of(x, top, r);
-                const uint32_t w = weight_of(x, top, r);
-                if (at >= from && at < limit && at < kBins) {
-                    if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[static_cast<int>(at)]), static_cast<unsigned long long>(w));
-                } else if (at >= limit) {
-                    rest += w;
+                const float d = distance(x, top, r);
+                if (d >= limit) {
+                    const uint32_t w = weight_of(x, top, r);
+                    const int at = bin_of(d);
+                    if (w && at < kBins) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[at]), static_cast<unsigned long long>(w));
                 }
             });
-            rest = block_sum(sh, rest);      // (also a barrier after the atomics)
-            if (from == 0.0f) {
-                uint64_t binned = 0;
-                for (int i = threadIdx.x; i < kBins; i += kThreads) binned += sh.bins[i];
-                total = block_sum(sh, binned) + rest;
-                bool more;
-                need = part_of(p_units, total, more);
-                need += more ? 1 : 0;
-                need = need < 1 ? 1 : need;
-            }
-            bin = reach(sh, kBins, need, before, [&](int i) { return sh.bins[i]; });
-            if (bin < kBins || !(limit < 1e29f)) break;
-            from = limit;
-            limit = 1e30f;
+            __syncthreads();
+            bin = reach<kBins / 64>(need, before, bins);   // (a weight of a unit or more is nearer than the last bin)
         }
-        // (2048 bins reach further than any weight of a unit or more)
         const int n = collect(static_cast<float>(bin), static_cast<float>(bin + 1));
         uint64_t above;
         if (n <= kCandidates) {
             listed = true;
             own(n);
-            kappa = whole_key(select(sh, 32, kStop, need - before, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t w) { f(key, [&] { return static_cast<unsigned long long>(w); }); }); }));
+            kappa = whole_key(select(turn, 32, kStop, need - before, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t w) { f(key, [&] { return static_cast<unsigned long long>(w); }); }); }));
             above += before;
         } else {
-            kappa = whole_key(select(sh, 32, kStop, need, above, [&](auto f) { everything([&](uint32_t key, uint32_t, auto w) { f(key, [&] { return static_cast<unsigned long long>(w()); }); }); }));
+            kappa = whole_key(select(turn, 32, kStop, need, above, [&](auto f) { everything([&](uint32_t key, uint32_t, auto w) { f(key, [&] { return static_cast<unsigned long long>(w()); }); }); }));
         }
         const uint64_t w = weight_at(kappa);
         take = w ? (need - above + w - 1) / w : 1;
@@ -435,11 +464,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         uint64_t ties = 0, above;
         if (listed) collected([&](uint32_t key, uint32_t, uint32_t) { ties += key == kappa; });
         else everything([&](uint32_t key, uint32_t, auto) { ties += key == kappa; });
-        ties = block_sum(sh, ties);
+        ties = turn.block_sum(ties);
         if (take < ties) {
             uint32_t at;
-            if (listed) at = select(sh, 24, 0, take, above, [&](auto f) { collected([&](uint32_t key, uint32_t i, uint32_t) { if (key == kappa) f(i ^ 0xFFFFFFu, [] { return 1ull; }); }); });
-            else at = select(sh, 24, 0, take, above, [&](auto f) { everything([&](uint32_t key, uint32_t i, auto) { if (key == kappa) f(i ^ 0xFFFFFFu, [] { return 1ull; }); }); });
+            if (listed) at = select(turn, 24, 0, take, above, [&](auto f) { collected([&](uint32_t key, uint32_t i, uint32_t) { if (key == kappa) f(i ^ 0xFFFFFFu, [] { return 1ull; }); }); });
+            else at = select(turn, 24, 0, take, above, [&](auto f) { everything([&](uint32_t key, uint32_t i, auto) { if (key == kappa) f(i ^ 0xFFFFFFu, [] { return 1ull; }); }); });
             iota = at ^ 0xFFFFFFu;
         }
     }
@@ -450,14 +479,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     if (few) {
         uint64_t sum = 0;
         collected([&](uint32_t key, uint32_t i, uint32_t w) { sum += keeps(key, i) && w >= least ? w : 0; });
-        const uint64_t total = block_sum(sh, sum);
+        const uint64_t total = turn.block_sum(sum);
         if (total == 0) {                    // min_p above 1
             if (threadIdx.x == 0) answer(-1, 0.0f);
             return;
         }
         const uint64_t target = part_of(u_units, total, more);
         uint64_t above;
-        const uint32_t token = select(sh, 24, 0, target + 1, above, [&](auto f) {
+        const uint32_t token = select(turn, 24, 0, target + 1, above, [&](auto f) {
                                    collected([&](uint32_t key, uint32_t i, uint32_t w) {
                                        if (keeps(key, i) && w >= least) f(i ^ 0xFFFFFFu, [&] { return static_cast<unsigned long long>(w); });
                                    });
@@ -470,11 +499,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
 
     // the kept weight of each 64 vectors (a wavefront's turn), then of the
     // vectors and elements where the target is reached
-    __syncthreads();                         // (the segments lie where the bins did)
     const int segments = (row.count + 63) / 64;
+    // values below this one are not kept: kappa's, or that of min_p less 2^-7 in the exponent
+    const float lowest = fmaxf(kappa ? value_of(kappa) : -INFINITY, least > 1 ? top + (logf(min_p) - 0.0078125f) * t : -INFINITY);
     auto kept_weight = [&](float x, int i) -> uint32_t {
-        const uint32_t key = key_of(x);
-        if (!keeps(key, static_cast<uint32_t>(i))) return 0u;
+        if (x < lowest || !keeps(key_of(x), static_cast<uint32_t>(i))) return 0u;
         const uint32_t w = weight_of(x, top, r);
         return w >= least ? w : 0u;
     };
@@ -487,16 +516,23 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     __syncthreads();
     uint64_t total = 0;
     for (int i = threadIdx.x; i < segments; i += kThreads) total += sh.segments[i];
-    total = block_sum(sh, total);
+    total = turn.block_sum(total);
     if (total == 0) {
         if (threadIdx.x == 0) answer(-1, 0.0f);
         return;
     }
-    const uint64_t target = part_of(u_units, total, more);
-    uint64_t before;
-    const int segment = reach(sh, (segments + 63) / 64 * 64, target + 1, before,
-                              [&](int i) { return i < segments ? sh.segments[i] : uint64_t{0}; });
     if (wave != 0) return;
+    const uint64_t target = part_of(u_units, total, more);
+    uint64_t before = 0, upto_before = 0;
+    int segment = 0;
+    for (;; segment += 64) {
+        const int at = reach<1>(target + 1 - before, upto_before, [&](int i) { return segment + i < segments ? sh.segments[segment + i] : uint64_t{0}; });
+        before += upto_before;
+        if (at < 64) {
+            segment += at;
+            break;
+        }
+    }
     const int v = segment * 64 + lane;
     const uint4 x = row.load(v);
     uint64_t sum = 0;
@@ -522,8 +558,18 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
 size_t sample_workspace_bytes(int64_t, int64_t) { return 0; }
 
 hipError_t launch_sample(const SampleParams& p, hipStream_t stream) {
-    if (p.f32) hipLaunchKernelGGL(sample_kernel<true>, dim3(p.B), dim3(kThreads), 0, stream, p);
-    else hipLaunchKernelGGL(sample_kernel<false>, dim3(p.B), dim3(kThreads), 0, stream, p);
+    // the vectors of a row (which may start inside one) fit the registers of its workgroup
+    const int n = p.f32 ? 4 : 8;
+    const bool aligned = (reinterpret_cast<uintptr_t>(p.logits) & 15) == 0 && (p.B == 1 || p.row_stride % n == 0);
+    const bool keep = p.V + (aligned ? 0 : n - 1) <= kThreads * kKept * n;
+    const dim3 grid(p.B), block(kThreads);
+    if (p.f32) {
+        if (keep) hipLaunchKernelGGL((sample_kernel<true, true>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((sample_kernel<true, false>), grid, block, 0, stream, p);
+    } else {
+        if (keep) hipLaunchKernelGGL((sample_kernel<false, true>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((sample_kernel<false, false>), grid, block, 0, stream, p);
+    }
     return hipGetLastError();
 }
 
