@@ -50,16 +50,23 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float((key >> 31) ? key ^ 0x80000000u : ~key);
 }
 
-// rint(2^31 exp((x - top) r))
+// rint(2^31 exp((x - top) r)), without branches
 __device__ __forceinline__ uint32_t weight_of(float x, float top, float r) {
-    if (x == top) return 0x80000000u;
-    const float e = x == -INFINITY ? 0.0f : expf((x - top) * r);
+    const float d = x == top ? 0.0f : (x - top) * r;   // (infinities' NaN at the top)
+    const float e = fmaxf(expf(d), 0.0f);              // (NaN, of -inf at T = inf, is 0)
     return static_cast<uint32_t>(rintf(e * 2147483648.0f));
 }
 // a distance that grows as the weight falls, the same for equal values (NaN for
 // infinities: like 0); a bin is its whole part
 __device__ __forceinline__ float distance(float x, float top, float r) { return (top - x) * (r * kBinsPerUnit); }
 __device__ __forceinline__ int bin_of(float d) { return static_cast<int>(fminf(fmaxf(d, 0.0f), static_cast<float>(kBins))); }
+
+// (as an instruction: fmaxf first makes signalling NaN quiet, one more operation an element)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float m;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(c));
+    return m;
+}
 
 __device__ __forceinline__ uint64_t units_of_2_24(float x, uint64_t most) {
     const float f = floorf(x * 16777216.0f);
@@ -97,7 +104,16 @@ __device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
 }
 __device__ __forceinline__ uint64_t wave_sum64(uint64_t v) { return lane_value(wave_scan64(v), 63); }
 
+// Weights of the bf16 values of magnitude 2^-14 .. 2^8, by sign and bits: of a
+// row's many logits few are different, and reading a weight takes a fourth of
+// the time of computing it (an exponential of every one of 131072 logits: 35
+// us on the row's compute unit).
+constexpr uint32_t kTableFrom = (127 - 14) << 7, kTableHalf = 22 << 7;
+
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+
 struct Shared {
+    uint32_t table[2 * kTableHalf];
     uint64_t hist[kLevels][256];             // one a level: cleared at the start, used once
     uint64_t bins[kBins];                    // weights by distance
     uint64_t segments[kSegments];
@@ -213,15 +229,17 @@ struct Row {
         }
         return x;
     }
-    // f(value, index) for each element of vector v
-    template <class F>
-    __device__ __forceinline__ void elements(const uint4& x, int v, F f) const {
+    // the values of vector v; that of element i has the index v N + i - shift
+    static __device__ __forceinline__ void unpack(const uint4& x, float (&y)[N]) {
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float y = F32 ? __uint_as_float(w[i & 3]) : (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-            f(fmaxf(y, -INFINITY), v * N + i - shift);   // (NaN like -inf)
-        }
+        for (int i = 0; i < N; ++i) y[i] = F32 ? __uint_as_float(w[i & 3]) : (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+    }
+    // the largest of m and the values, NaN left out
+    static __device__ __forceinline__ float largest(const float (&y)[N], float m = -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) m = max3(m, y[i], y[i + 1]);
+        return m;
     }
     // f(vector, its number, turn) for this thread's vectors, read ahead
     template <class F>
@@ -238,9 +256,14 @@ struct Row {
             d = e;
         }
     }
+    // f(values, number of the vector, the vector)
     template <class F>
     __device__ __forceinline__ void values(F f) const {
-        all([&](const uint4& x, int v, int) { elements(x, v, f); });
+        all([&](const uint4& x, int v, int) {
+            float y[N];
+            unpack(x, y);
+            f(y, v, x);
+        });
     }
 };
 
@@ -249,6 +272,7 @@ struct Row {
 template <bool F32, bool KEEP>
 __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     __shared__ Shared sh;
+    constexpr int N = Row<F32>::N;
     const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const Row<F32> row(p.logits, b * p.row_stride, p.V);
     uint4 kept[KEEP ? kKept : 1];
@@ -260,7 +284,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         if constexpr (KEEP) {
 #pragma unroll
             for (int j = 0; j < kKept; ++j)
-                if (j * kThreads < row.count) row.elements(kept[j], static_cast<int>(threadIdx.x) + j * kThreads, f);
+                if (j * kThreads < row.count) {
+                    float y[N];
+                    row.unpack(kept[j], y);
+                    f(y, static_cast<int>(threadIdx.x) + j * kThreads, kept[j]);
+                }
         } else {
             row.values(f);
         }
@@ -292,7 +320,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     if (threadIdx.x == 0) sh.candidates = 0;
 
     float mine = -INFINITY;
-    light([&](float x, int) { mine = fmaxf(mine, x); });
+    light([&](const float (&y)[N], int, const uint4&) { mine = row.largest(y, mine); });
     float top = wave_max(mine);
     if (lane == 0) sh.wave32[0][wave] = __float_as_uint(top);
     __syncthreads();
@@ -303,7 +331,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     }
     if (greedy) {
         int first = 0x7FFFFFFF;
-        if (mine == top) light([&](float x, int i) { first = x == top && i < first ? i : first; });
+        if (mine == top)
+            light([&](const float (&y)[N], int v, const uint4&) {
+#pragma unroll
+                for (int i = N - 1; i >= 0; --i)
+                    if (y[i] == top && v * N + i - row.shift < first) first = v * N + i - row.shift;
+            });
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) first = min(first, __shfl_xor(first, off));
         if (lane == 0) sh.wave32[1][wave] = static_cast<uint32_t>(first);
@@ -318,6 +351,55 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
 
     uint32_t kappa = 0, iota = 0xFFFFFFFFu;  // kept: keys above kappa, and equal ones up to index iota
     uint64_t take = 0;                       // how many equal ones
+    // the weights of a vector's values
+    const float weightless = top - 22.5f / r;  // exp(-22.5) 2^31 < 1/2
+    bool tabled = false;
+    auto fill_table = [&] {
+        if (F32) return;
+        for (uint32_t i = threadIdx.x; i < 2 * kTableHalf; i += kThreads) {
+            const uint32_t bits = i < kTableHalf ? kTableFrom + i : 0x8000u + kTableFrom + i - kTableHalf;
+            const float x = __uint_as_float(bits << 16);
+            sh.table[i] = x <= top ? weight_of(x, top, r) : 0;
+        }
+        tabled = true;
+        __syncthreads();
+    };
+    auto weights = [&](const uint4& x, const float (&y)[N], uint32_t (&w)[N]) {
+        if constexpr (F32) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = weight_of(y[i], top, r);
+        } else {
+            // two at a time in 16 bits: magnitude above the table's first, the
+            // largest of them (all inside it, of most vectors), index
+            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+            u16x2_t most = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const u16x2_t bits = __builtin_bit_cast(u16x2_t, in[i]);
+                const u16x2_t above = (bits & static_cast<uint16_t>(0x7FFF)) - static_cast<uint16_t>(kTableFrom);
+                most = __builtin_elementwise_max(most, above);
+                const u16x2_t at = __builtin_elementwise_min(above, u16x2_t{kTableHalf - 1, kTableHalf - 1}) +
+                                   (bits >> static_cast<uint16_t>(15)) * static_cast<uint16_t>(kTableHalf);
+                w[2 * i] = sh.table[at[0]];
+                w[2 * i + 1] = sh.table[at[1]];
+            }
+            if (__any(most[0] >= kTableHalf || most[1] >= kTableHalf)) {
+                // masked values (-inf, the lowest) are common: without weight; others are computed
+                bool exact = false;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t above = (((i & 1) ? in[i >> 1] >> 16 : in[i >> 1]) & 0x7FFFu) - kTableFrom;
+                    const bool outside = above >= kTableHalf;
+                    exact = exact || (outside && y[i] >= weightless);
+                    w[i] = outside ? 0 : w[i];
+                }
+                if (__any(exact)) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) w[i] = weight_of(y[i], top, r);
+                }
+            }
+        }
+    };
     // a distance within which at least n of the threads' maxima lie
     auto bound = [&](int n) -> float {
         if (p.V <= kCandidates) return 1e30f;
@@ -330,13 +412,17 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     };
     // the tokens with from <= distance < below (infinities' NaN is 0)
     auto collect = [&](float from, float below) -> int {
-        light([&](float x, int i) {
-            const float d = distance(x, top, r);
-            if (!(d >= below) && !(d < from)) {
+        light([&](const float (&y)[N], int v, const uint4&) {
+            if (distance(row.largest(y), top, r) >= below) return;   // as of nearly all vectors
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float z = fmaxf(y[i], -INFINITY);   // (NaN like -inf)
+                const float d = distance(z, top, r);
+                if (d >= below || d < from) continue;
                 const uint32_t n = atomicAdd(&sh.candidates, 1u);
                 if (n < kCandidates) {
-                    sh.key[n] = key_of(x);
-                    sh.index[n] = static_cast<uint32_t>(i);
+                    sh.key[n] = key_of(z);
+                    sh.index[n] = static_cast<uint32_t>(v * N + i - row.shift);
                 }
             }
         });
@@ -364,11 +450,19 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     };
     // ... or all tokens of the row; f(key, index, weight) with a function for the weight
     auto everything = [&](auto f) {
-        row.values([&](float x, int i) {
-            const uint32_t key = key_of(x);
-            f(key, static_cast<uint32_t>(i), [&] { return weight_of(x, top, r); });
+        row.values([&](const float (&y)[N], int v, const uint4&) {
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) {
+                float x = y[0];
+#pragma unroll
+                for (int j = 1; j < N; ++j) x = i == j ? y[j] : x;
+                x = fmaxf(x, -INFINITY);
+                f(key_of(x), static_cast<uint32_t>(v * N + i - row.shift), [&] { return weight_of(x, top, r); });
+            }
         });
     };
+    const int index_bits = p.V <= 65536 ? 16 : 24;
+    const uint32_t index_mask = (1u << index_bits) - 1u;
     constexpr int kStop = F32 ? 0 : 16;      // the low bits of a bf16 key follow from its sign
     auto whole_key = [&](uint32_t key) { return !F32 && !(key >> 31) ? key | 0xFFFFu : key; };
     auto weight_at = [&](uint32_t key) -> uint64_t { return weight_of(value_of(key), top, r); };
@@ -413,16 +507,28 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         // weights by distance, down to the 512th largest of the threads'
         // maxima; if p of the total lies further down, all
         const float limit = bound(512);
+        fill_table();
         uint64_t rest = 0, before;
-        row.values([&](float x, int) {
-            const float d = distance(x, top, r);
-            const uint32_t w = weight_of(x, top, r);
-            if (!(d >= limit)) {
+        // the weights of a vector to the bins (nearer than `limit`, or not) or the rest
+        auto to_bins = [&](const float (&y)[N], const uint32_t (&w)[N], bool near) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float d = distance(y[i], top, r);
                 const int at = bin_of(d);
-                if (w && at < kBins) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[at]), static_cast<unsigned long long>(w));
-            } else {
-                rest += w;
+                if ((d >= limit) != near && w[i] && at < kBins)
+                    atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[at]), static_cast<unsigned long long>(w[i]));
             }
+        };
+        row.values([&](const float (&y)[N], int, const uint4& x) {
+            uint32_t w[N];
+            weights(x, y, w);
+            if (!(distance(row.largest(y), top, r) >= limit)) {
+                to_bins(y, w, true);
+#pragma unroll
+                for (int i = 0; i < N; ++i) w[i] = distance(y[i], top, r) >= limit ? w[i] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) rest += w[i];
         });
         rest = turn.block_sum(rest);         // (its barrier is also that after the atomics)
         auto bins = [&](int i) { return sh.bins[i]; };
@@ -435,29 +541,41 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         int bin = reach<kBins / 64>(need, before, bins);
         if (bin == kBins) {
             __syncthreads();
-            row.values([&](float x, int) {
-                const float d = distance(x, top, r);
-                if (d >= limit) {
-                    const uint32_t w = weight_of(x, top, r);
-                    const int at = bin_of(d);
-                    if (w && at < kBins) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[at]), static_cast<unsigned long long>(w));
-                }
+            row.values([&](const float (&y)[N], int, const uint4& x) {
+                uint32_t w[N];
+                weights(x, y, w);
+                to_bins(y, w, false);
             });
             __syncthreads();
             bin = reach<kBins / 64>(need, before, bins);   // (a weight of a unit or more is nearer than the last bin)
         }
-        const int n = collect(static_cast<float>(bin), static_cast<float>(bin + 1));
+        // all kept tokens, or those of the bin alone, or neither fits
+        int n = collect(0.0f, static_cast<float>(bin + 1));
+        few = n <= kCandidates;
+        if (!few) {
+            __syncthreads();
+            if (threadIdx.x == 0) sh.candidates = 0;
+            __syncthreads();
+            n = collect(static_cast<float>(bin), static_cast<float>(bin + 1));
+        }
+        listed = n <= kCandidates;
         uint64_t above;
-        if (n <= kCandidates) {
-            listed = true;
+        if (listed) {
             own(n);
-            kappa = whole_key(select(turn, 32, kStop, need - before, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t w) { f(key, [&] { return static_cast<unsigned long long>(w); }); }); }));
-            above += before;
+            const uint64_t skip = few ? 0 : before;
+            kappa = whole_key(select(turn, 32, kStop, need - skip, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t w) { f(key, [&] { return static_cast<unsigned long long>(w); }); }); }));
+            above += skip;
         } else {
             kappa = whole_key(select(turn, 32, kStop, need, above, [&](auto f) { everything([&](uint32_t key, uint32_t, auto w) { f(key, [&] { return static_cast<unsigned long long>(w()); }); }); }));
         }
         const uint64_t w = weight_at(kappa);
         take = w ? (need - above + w - 1) / w : 1;
+    } else if (least > 1) {
+        // min_p alone: what it may keep (2^-7 more than that, in the exponent), if it fits
+        const float far = (0.0078125f - logf(min_p)) * kBinsPerUnit;
+        const int n = collect(0.0f, far);
+        few = n <= kCandidates;
+        if (few) own(n);
     }
     if (kappa) {
         // the take-th of the tokens equal to kappa, by index, if not all are kept
@@ -467,9 +585,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         ties = turn.block_sum(ties);
         if (take < ties) {
             uint32_t at;
-            if (listed) at = select(turn, 24, 0, take, above, [&](auto f) { collected([&](uint32_t key, uint32_t i, uint32_t) { if (key == kappa) f(i ^ 0xFFFFFFu, [] { return 1ull; }); }); });
-            else at = select(turn, 24, 0, take, above, [&](auto f) { everything([&](uint32_t key, uint32_t i, auto) { if (key == kappa) f(i ^ 0xFFFFFFu, [] { return 1ull; }); }); });
-            iota = at ^ 0xFFFFFFu;
+            if (listed) at = select(turn, index_bits, 0, take, above, [&](auto f) { collected([&](uint32_t key, uint32_t i, uint32_t) { if (key == kappa) f(i ^ index_mask, [] { return 1ull; }); }); });
+            else at = select(turn, index_bits, 0, take, above, [&](auto f) { everything([&](uint32_t key, uint32_t i, auto) { if (key == kappa) f(i ^ index_mask, [] { return 1ull; }); }); });
+            iota = at ^ index_mask;
         }
     }
     auto keeps = [&](uint32_t key, uint32_t i) { return key > kappa || (key == kappa && i <= iota); };
@@ -486,11 +604,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         }
         const uint64_t target = part_of(u_units, total, more);
         uint64_t above;
-        const uint32_t token = select(turn, 24, 0, target + 1, above, [&](auto f) {
+        const uint32_t token = select(turn, index_bits, 0, target + 1, above, [&](auto f) {
                                    collected([&](uint32_t key, uint32_t i, uint32_t w) {
-                                       if (keeps(key, i) && w >= least) f(i ^ 0xFFFFFFu, [&] { return static_cast<unsigned long long>(w); });
+                                       if (keeps(key, i) && w >= least) f(i ^ index_mask, [&] { return static_cast<unsigned long long>(w); });
                                    });
-                               }) ^ 0xFFFFFFu;
+                               }) ^ index_mask;
         collected([&](uint32_t, uint32_t i, uint32_t w) {
             if (i == token) answer(static_cast<int>(i), static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
         });
@@ -502,15 +620,25 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     const int segments = (row.count + 63) / 64;
     // values below this one are not kept: kappa's, or that of min_p less 2^-7 in the exponent
     const float lowest = fmaxf(kappa ? value_of(kappa) : -INFINITY, least > 1 ? top + (logf(min_p) - 0.0078125f) * t : -INFINITY);
-    auto kept_weight = [&](float x, int i) -> uint32_t {
-        if (x < lowest || !keeps(key_of(x), static_cast<uint32_t>(i))) return 0u;
-        const uint32_t w = weight_of(x, top, r);
-        return w >= least ? w : 0u;
+    auto kept_weights = [&](const uint4& x, int v, uint32_t (&w)[N]) {
+        float y[N];
+        row.unpack(x, y);
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = 0;
+        if (row.largest(y) < lowest) return;
+        weights(x, y, w);
+        if (kappa || least > 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = keeps(key_of(y[i]), static_cast<uint32_t>(v * N + i - row.shift)) && w[i] >= least ? w[i] : 0u;
     };
+    if (!tabled) fill_table();
     row.all([&](const uint4& x, int v, int j) {
+        uint32_t w[N];
+        kept_weights(x, v, w);
         uint64_t sum = 0;
-        row.elements(x, v, [&](float y, int i) { sum += kept_weight(y, i); });
-        sum = wave_sum64(sum);
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum += w[i];
+        if (__any(sum != 0)) sum = wave_sum64(sum);
         if (lane == 0 && j * kWaves + wave < segments) sh.segments[j * kWaves + wave] = sum;
     });
     __syncthreads();
@@ -534,22 +662,25 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         }
     }
     const int v = segment * 64 + lane;
-    const uint4 x = row.load(v);
+    uint32_t w[N];
+    kept_weights(row.load(v), v, w);
     uint64_t sum = 0;
-    row.elements(x, v, [&](float y, int i) { sum += kept_weight(y, i); });
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += w[i];
     const uint64_t upto = before + wave_scan64(sum);
     const uint64_t hit = __ballot(upto > target);
     if (hit && lane == __ffsll(static_cast<unsigned long long>(hit)) - 1) {
         uint64_t at = upto - sum;
-        bool found = false;
-        row.elements(x, v, [&](float y, int i) {
-            const uint32_t w = kept_weight(y, i);
-            if (!found && at + w > target) {
-                found = true;
-                answer(i, static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
+        int i = 0;
+        uint32_t here = w[0];
+#pragma unroll
+        for (int j = 1; j < N; ++j)
+            if (i == j - 1 && at + here <= target) {
+                at += here;
+                here = w[j];
+                i = j;
             }
-            at += w;
-        });
+        answer(v * N + i - row.shift, static_cast<float>(static_cast<double>(here) / static_cast<double>(total)));
     }
 }
 
