@@ -9,9 +9,7 @@
 // follows by division.
 //
 // One workgroup of 1024 threads a row, which is read from memory for the
-// maximum and kept in registers (up to 16 vectors of 16 bytes a thread: 131072
-// bf16, 65536 fp32) for what compares every element; what takes an exponential
-// of every element reads it again from the caches.  Then
+// maximum, and again from the caches for what follows:
 //  - top-k: the k-th largest of the threads' own maxima bounds the k-th largest
 //    logit from below, so few tokens besides the top k lie above it: they are
 //    collected in shared memory and the filters and the draw work on them;
@@ -33,12 +31,13 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
-constexpr int kCandidates = 4096;            // tokens collected in shared memory
+constexpr int kCandidates = 2048;            // tokens collected in shared memory, and vectors that hold them
 constexpr int kMine = kCandidates / kThreads;
-constexpr int kKept = 16;                    // 16-byte vectors of a row a thread keeps
+constexpr int kAhead = 8;                    // vectors a thread has on their way
 constexpr int kBins = 512;
 constexpr float kBinsPerUnit = 16.0f;        // bins of 1/16 of the scaled distance, down to exp(-32)
-constexpr int kSegments = (1 << 20) / 256 + 1;
+constexpr int kGroup = 4;                     // 64 vectors each a segment
+constexpr int kSegments = ((1 << 20) / 4 / (64 * kGroup) / kWaves + 2) * kWaves;
 constexpr int kLevels = 18;                  // of all selections of a call: 4 + 4 by key, 3 + 3 by index, and spare
 
 // fp32 (not NaN) -> a key in the order of the values; -0 like +0
@@ -113,7 +112,8 @@ constexpr uint32_t kTableFrom = (127 - 14) << 7, kTableHalf = 22 << 7;
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 struct Shared {
-    uint32_t table[2 * kTableHalf];
+    uint32_t table[2 * kTableHalf];          // weights of bf16 values
+    uint32_t numbers[2 * kTableHalf];        // how often they occur
     uint64_t hist[kLevels][256];             // one a level: cleared at the start, used once
     uint64_t bins[kBins];                    // weights by distance
     uint64_t segments[kSegments];
@@ -121,7 +121,11 @@ struct Shared {
     uint32_t counts[kBins];                  // threads' maxima by distance
     uint32_t wave32[2][kWaves];
     uint32_t key[kCandidates], index[kCandidates];
-    uint32_t candidates;
+    uint32_t vectors[kCandidates];
+    uint64_t outside[3];                     // weights above the table's values, between its halves, below
+    uint32_t candidates, marked;
+    uint32_t found;                          // and what belongs to it
+    uint64_t found_above;
 };
 
 // What every wavefront of the row knows alike.
@@ -213,9 +217,9 @@ struct Row {
     }
     __device__ __forceinline__ uint4 load(int v) const {
         const uint32_t none = F32 ? 0xFF800000u : 0xFF80FF80u;
-        if (v >= count) return make_uint4(none, none, none, none);
-        uint4 x = vectors[v];
-        if (v == 0 || v == count - 1) {
+        uint4 x = make_uint4(none, none, none, none);
+        if (v < count) x = vectors[v];
+        if ((v == 0 && shift) || v == count - 1) {
             uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -267,30 +271,25 @@ struct Row {
     }
 };
 
-// KEEP: the row's vectors stay in registers from the first reading, for what
-// is done to every element with few instructions.
-template <bool F32, bool KEEP>
+template <bool F32>
 __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     __shared__ Shared sh;
     constexpr int N = Row<F32>::N;
     const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const Row<F32> row(p.logits, b * p.row_stride, p.V);
-    uint4 kept[KEEP ? kKept : 1];
-    if constexpr (KEEP) {
-#pragma unroll
-        for (int j = 0; j < kKept; ++j) kept[j] = row.load(static_cast<int>(threadIdx.x) + j * kThreads);
-    }
+    // what is done to every element with few instructions: f(values, vector)
     auto light = [&](auto f) {
-        if constexpr (KEEP) {
+#pragma unroll 1
+        for (int j = 0; j * kThreads < row.count; j += kAhead) {
+            uint4 x[kAhead];
 #pragma unroll
-            for (int j = 0; j < kKept; ++j)
-                if (j * kThreads < row.count) {
-                    float y[N];
-                    row.unpack(kept[j], y);
-                    f(y, static_cast<int>(threadIdx.x) + j * kThreads, kept[j]);
-                }
-        } else {
-            row.values(f);
+            for (int i = 0; i < kAhead; ++i) x[i] = row.load(static_cast<int>(threadIdx.x) + (j + i) * kThreads);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                float y[N];
+                row.unpack(x[i], y);
+                f(y, static_cast<int>(threadIdx.x) + (j + i) * kThreads);
+            }
         }
     };
     const float t = p.temperature ? p.temperature[b] : 1.0f;
@@ -317,10 +316,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         sh.bins[threadIdx.x] = 0;
         sh.counts[threadIdx.x] = 0;
     }
-    if (threadIdx.x == 0) sh.candidates = 0;
+    if (threadIdx.x == 0) sh.candidates = sh.marked = 0;
+    if (threadIdx.x < 3) sh.outside[threadIdx.x] = 0;
 
     float mine = -INFINITY;
-    light([&](const float (&y)[N], int, const uint4&) { mine = row.largest(y, mine); });
+    light([&](const float (&y)[N], int) { mine = row.largest(y, mine); });
     float top = wave_max(mine);
     if (lane == 0) sh.wave32[0][wave] = __float_as_uint(top);
     __syncthreads();
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     if (greedy) {
         int first = 0x7FFFFFFF;
         if (mine == top)
-            light([&](const float (&y)[N], int v, const uint4&) {
+            light([&](const float (&y)[N], int v) {
 #pragma unroll
                 for (int i = N - 1; i >= 0; --i)
                     if (y[i] == top && v * N + i - row.shift < first) first = v * N + i - row.shift;
@@ -351,45 +351,57 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
 
     uint32_t kappa = 0, iota = 0xFFFFFFFFu;  // kept: keys above kappa, and equal ones up to index iota
     uint64_t take = 0;                       // how many equal ones
-    // the weights of a vector's values
     const float weightless = top - 22.5f / r;  // exp(-22.5) 2^31 < 1/2
     bool tabled = false;
+    auto entry_value = [&](uint32_t i) {
+        return __uint_as_float((i < kTableHalf ? kTableFrom + i : 0x8000u + kTableFrom + i - kTableHalf) << 16);
+    };
     auto fill_table = [&] {
         if (F32) return;
         for (uint32_t i = threadIdx.x; i < 2 * kTableHalf; i += kThreads) {
-            const uint32_t bits = i < kTableHalf ? kTableFrom + i : 0x8000u + kTableFrom + i - kTableHalf;
-            const float x = __uint_as_float(bits << 16);
+            const float x = entry_value(i);
             sh.table[i] = x <= top ? weight_of(x, top, r) : 0;
+            sh.numbers[i] = 0;
         }
         tabled = true;
         __syncthreads();
     };
+    // Entries of a vector's bf16 values, two at a time in 16 bits: magnitude
+    // above the table's first, then the index.  False if some lie outside (the
+    // wavefront's vectors mostly have none).
+    auto entries = [&](const uint4& x, u16x2_t (&at)[4]) -> bool {
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+        u16x2_t most = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const u16x2_t bits = __builtin_bit_cast(u16x2_t, in[i]);
+            const u16x2_t above = (bits & static_cast<uint16_t>(0x7FFF)) - static_cast<uint16_t>(kTableFrom);
+            most = __builtin_elementwise_max(most, above);
+            at[i] = __builtin_elementwise_min(above, u16x2_t{kTableHalf - 1, kTableHalf - 1}) +
+                    (bits >> static_cast<uint16_t>(15)) * static_cast<uint16_t>(kTableHalf);
+        }
+        return !__any(most[0] >= kTableHalf || most[1] >= kTableHalf);
+    };
+    auto outside_table = [&](const uint4& x, int i) {
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+        return (((i & 1) ? in[i >> 1] >> 16 : in[i >> 1]) & 0x7FFFu) - kTableFrom >= kTableHalf;
+    };
+    // the weights of a vector's values
     auto weights = [&](const uint4& x, const float (&y)[N], uint32_t (&w)[N]) {
         if constexpr (F32) {
 #pragma unroll
             for (int i = 0; i < N; ++i) w[i] = weight_of(y[i], top, r);
         } else {
-            // two at a time in 16 bits: magnitude above the table's first, the
-            // largest of them (all inside it, of most vectors), index
-            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-            u16x2_t most = {0, 0};
+            u16x2_t at[4];
+            const bool inside = entries(x, at);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const u16x2_t bits = __builtin_bit_cast(u16x2_t, in[i]);
-                const u16x2_t above = (bits & static_cast<uint16_t>(0x7FFF)) - static_cast<uint16_t>(kTableFrom);
-                most = __builtin_elementwise_max(most, above);
-                const u16x2_t at = __builtin_elementwise_min(above, u16x2_t{kTableHalf - 1, kTableHalf - 1}) +
-                                   (bits >> static_cast<uint16_t>(15)) * static_cast<uint16_t>(kTableHalf);
-                w[2 * i] = sh.table[at[0]];
-                w[2 * i + 1] = sh.table[at[1]];
-            }
-            if (__any(most[0] >= kTableHalf || most[1] >= kTableHalf)) {
+            for (int i = 0; i < N; ++i) w[i] = sh.table[at[i >> 1][i & 1]];
+            if (!inside) {
                 // masked values (-inf, the lowest) are common: without weight; others are computed
                 bool exact = false;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t above = (((i & 1) ? in[i >> 1] >> 16 : in[i >> 1]) & 0x7FFFu) - kTableFrom;
-                    const bool outside = above >= kTableHalf;
+                for (int i = 0; i < N; ++i) {
+                    const bool outside = outside_table(x, i);
                     exact = exact || (outside && y[i] >= weightless);
                     w[i] = outside ? 0 : w[i];
                 }
@@ -410,24 +422,48 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         const int bin = reach<kBins / 64>(n, before, [&](int i) { return static_cast<uint64_t>(sh.counts[i]); });
         return bin < kBins ? static_cast<float>(bin + 1) : 1e30f;
     };
-    // the tokens with from <= distance < below (infinities' NaN is 0)
-    auto collect = [&](float from, float below) -> int {
-        light([&](const float (&y)[N], int v, const uint4&) {
-            if (distance(row.largest(y), top, r) >= below) return;   // as of nearly all vectors
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float z = fmaxf(y[i], -INFINITY);   // (NaN like -inf)
-                const float d = distance(z, top, r);
-                if (d >= below || d < from) continue;
-                const uint32_t n = atomicAdd(&sh.candidates, 1u);
-                if (n < kCandidates) {
-                    sh.key[n] = key_of(z);
-                    sh.index[n] = static_cast<uint32_t>(v * N + i - row.shift);
-                }
-            }
+    // The tokens of the vectors that has(values) marks, where wants(value):
+    // few vectors of a row, so they are listed first and then shared among the
+    // threads.  More than kCandidates: too many.
+    auto gather = [&](auto has, auto wants) -> int {
+        light([&](const float (&y)[N], int v) {
+            if (!has(y)) return;
+            const uint32_t n = atomicAdd(&sh.marked, 1u);
+            if (n < kCandidates) sh.vectors[n] = static_cast<uint32_t>(v);
         });
         __syncthreads();
-        return static_cast<int>(sh.candidates);
+        const int marked = static_cast<int>(sh.marked);
+        if (marked <= kCandidates)
+            for (int i = threadIdx.x; i < marked; i += kThreads) {
+                const int v = static_cast<int>(sh.vectors[i]);
+                float y[N];
+                row.unpack(row.load(v), y);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float z = fmaxf(y[e], -INFINITY);   // (NaN like -inf)
+                    if (!wants(z)) continue;
+                    const uint32_t n = atomicAdd(&sh.candidates, 1u);
+                    if (n < kCandidates) {
+                        sh.key[n] = key_of(z);
+                        sh.index[n] = static_cast<uint32_t>(v * N + e - row.shift);
+                    }
+                }
+            }
+        __syncthreads();
+        return marked <= kCandidates ? static_cast<int>(sh.candidates) : kCandidates + 1;
+    };
+    auto gather_again = [&] {
+        __syncthreads();
+        if (threadIdx.x == 0) sh.candidates = sh.marked = 0;
+        __syncthreads();
+    };
+    // the tokens with from <= distance < below (infinities' NaN is 0)
+    auto collect = [&](float from, float below) -> int {
+        return gather([&](const float (&y)[N]) { return !(distance(row.largest(y), top, r) >= below); },
+                      [&](float z) {
+                          const float d = distance(z, top, r);
+                          return !(d >= below || d < from);
+                      });
     };
 
     // this thread's collected tokens
@@ -504,72 +540,182 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
             }
         }
     } else if (cuts) {
-        // weights by distance, down to the 512th largest of the threads'
-        // maxima; if p of the total lies further down, all
-        const float limit = bound(512);
         fill_table();
-        uint64_t rest = 0, before;
-        // the weights of a vector to the bins (nearer than `limit`, or not) or the rest
-        auto to_bins = [&](const float (&y)[N], const uint32_t (&w)[N], bool near) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float d = distance(y[i], top, r);
-                const int at = bin_of(d);
-                if ((d >= limit) != near && w[i] && at < kBins)
-                    atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[at]), static_cast<unsigned long long>(w[i]));
-            }
+        uint64_t total = 0, need = 0, before = 0, above = 0;
+        auto set_need = [&] {
+            bool more;
+            need = part_of(p_units, total, more);
+            need += more ? 1 : 0;
+            need = need < 1 ? 1 : need;
         };
-        row.values([&](const float (&y)[N], int, const uint4& x) {
-            uint32_t w[N];
-            weights(x, y, w);
-            if (!(distance(row.largest(y), top, r) >= limit)) {
-                to_bins(y, w, true);
+        bool counted = !F32;
+        if constexpr (!F32) {
+            // how often each value of the table occurs, and from that the value
+            // at which p of the weight is reached
+            row.all([&](const uint4& x, int v, int) {
+                u16x2_t at[4];
+                const bool inside = entries(x, at);
+                if (inside) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) w[i] = distance(y[i], top, r) >= limit ? w[i] : 0;
-            }
+                    for (int i = 0; i < N; ++i) atomicAdd(&sh.numbers[at[i >> 1][i & 1]], 1u);
+                } else {
+                    float y[N];
+                    row.unpack(x, y);
 #pragma unroll
-            for (int i = 0; i < N; ++i) rest += w[i];
-        });
-        rest = turn.block_sum(rest);         // (its barrier is also that after the atomics)
-        auto bins = [&](int i) { return sh.bins[i]; };
-        reach<kBins / 64>(~uint64_t{0}, before, bins);
-        const uint64_t total = before + rest;
-        bool more;
-        uint64_t need = part_of(p_units, total, more);
-        need += more ? 1 : 0;
-        need = need < 1 ? 1 : need;
-        int bin = reach<kBins / 64>(need, before, bins);
-        if (bin == kBins) {
-            __syncthreads();
-            row.values([&](const float (&y)[N], int, const uint4& x) {
-                uint32_t w[N];
-                weights(x, y, w);
-                to_bins(y, w, false);
+                    for (int i = 0; i < N; ++i) {
+                        if (!outside_table(x, i)) atomicAdd(&sh.numbers[at[i >> 1][i & 1]], 1u);
+                        else if (y[i] >= weightless)
+                            atomicAdd(reinterpret_cast<unsigned long long*>(&sh.outside[y[i] >= 1.0f ? 0 : y[i] > -1.0f ? 1 : 2]),
+                                      static_cast<unsigned long long>(weight_of(y[i], top, r)));
+                    }
+                }
             });
             __syncthreads();
-            bin = reach<kBins / 64>(need, before, bins);   // (a weight of a unit or more is nearer than the last bin)
-        }
-        // all kept tokens, or those of the bin alone, or neither fits
-        int n = collect(0.0f, static_cast<float>(bin + 1));
-        few = n <= kCandidates;
-        if (!few) {
+            // from the largest value down: those above the table, its positive
+            // half backwards, those between, the negative half, those below
+            constexpr uint32_t kPlaces = 2 * kTableHalf + 3;
+            constexpr int kShare = (kPlaces + kThreads - 1) / kThreads;
+            auto entry_at = [&](uint32_t q) { return q <= kTableHalf ? kTableHalf - q : q - 2; };
+            auto mass_at = [&](uint32_t q) -> uint64_t {
+                if (q == 0) return sh.outside[0];
+                if (q == kTableHalf + 1) return sh.outside[1];
+                if (q >= kPlaces - 1) return q == kPlaces - 1 ? sh.outside[2] : 0;
+                const uint32_t e = entry_at(q);
+                return static_cast<uint64_t>(sh.numbers[e]) * sh.table[e];
+            };
+            uint64_t mass = 0;
+#pragma unroll 1
+            for (int i = 0; i < kShare; ++i) mass += mass_at(threadIdx.x * kShare + i);
+            const uint64_t upto = wave_scan64(mass);
+            uint64_t* sums = sh.wave64[turn.sums++ & 1];
+            if (lane == 63) sums[wave] = upto;
             __syncthreads();
-            if (threadIdx.x == 0) sh.candidates = 0;
+            uint64_t start = 0;
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                if (i < wave) start += sums[i];
+                total += sums[i];
+            }
+            set_need();
+            uint64_t sum = start + upto - mass;
+            if (sum < need && need <= start + upto) {
+#pragma unroll 1
+                for (int i = 0; i < kShare; ++i) {
+                    const uint32_t q = threadIdx.x * kShare + i;
+                    const uint64_t w = mass_at(q);
+                    if (sum + w >= need) {
+                        sh.found = q;
+                        sh.found_above = sum;
+                        break;
+                    }
+                    sum += w;
+                }
+            }
             __syncthreads();
-            n = collect(static_cast<float>(bin), static_cast<float>(bin + 1));
+            // (among those outside the table it would have to be searched for)
+            const uint32_t q = sh.found;
+            counted = q != 0 && q != kTableHalf + 1 && q != kPlaces - 1;
+            if (counted) {
+                const uint32_t entry = entry_at(q);
+                kappa = key_of(entry_value(entry));
+                above = sh.found_above;
+                // all kept tokens, or those equal to kappa alone (if not all of
+                // them are kept), or neither
+                const float value = value_of(kappa);
+                const uint64_t w = weight_at(kappa);
+                take = (need - above + w - 1) / w;
+                int n = gather([&](const float (&y)[N]) { return row.largest(y) >= value; }, [&](float z) { return z >= value; });
+                few = listed = n <= kCandidates;
+                if (!few && take < sh.numbers[entry]) {
+                    gather_again();
+                    n = gather([&](const float (&y)[N]) {
+                        bool any = false;
+#pragma unroll
+                        for (int i = 0; i < N; ++i) any = any || y[i] == value;
+                        return any;
+                    }, [&](float z) { return z == value; });
+                    listed = n <= kCandidates;
+                } else if (!few) {
+                    take = ~uint64_t{0};     // (all: no ties to look at)
+                }
+                if (listed) own(n);
+            }
         }
-        listed = n <= kCandidates;
-        uint64_t above;
-        if (listed) {
-            own(n);
-            const uint64_t skip = few ? 0 : before;
-            kappa = whole_key(select(turn, 32, kStop, need - skip, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t w) { f(key, [&] { return static_cast<unsigned long long>(w); }); }); }));
-            above += skip;
-        } else {
-            kappa = whole_key(select(turn, 32, kStop, need, above, [&](auto f) { everything([&](uint32_t key, uint32_t, auto w) { f(key, [&] { return static_cast<unsigned long long>(w()); }); }); }));
+        if (!counted) {
+            // the total, and the vectors with tokens nearer than the 512th
+            // largest of the threads' maxima, whose weights are binned by
+            // distance; if p of the total lies further down, all
+            total = 0;
+            const float limit = bound(512);
+            auto to_bins = [&](const float (&y)[N], const uint32_t (&w)[N], float below) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float d = distance(y[i], top, r);
+                    const int at = bin_of(d);
+                    if (!(d >= below) && w[i] && at < kBins)
+                        atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[at]), static_cast<unsigned long long>(w[i]));
+                }
+            };
+            row.values([&](const float (&y)[N], int v, const uint4& x) {
+                uint32_t w[N];
+                weights(x, y, w);
+#pragma unroll
+                for (int i = 0; i < N; ++i) total += w[i];
+                if (!(distance(row.largest(y), top, r) >= limit)) {
+                    const uint32_t n = atomicAdd(&sh.marked, 1u);
+                    if (n < kCandidates) sh.vectors[n] = static_cast<uint32_t>(v);
+                }
+            });
+            total = turn.block_sum(total);   // (its barrier is also that of the list)
+            set_need();
+            const int marked = static_cast<int>(sh.marked);
+            int bin = kBins;
+            auto bins = [&](int i) { return sh.bins[i]; };
+            if (marked <= kCandidates) {
+                for (int i = threadIdx.x; i < marked; i += kThreads) {
+                    const uint4 x = row.load(static_cast<int>(sh.vectors[i]));
+                    float y[N];
+                    uint32_t w[N];
+                    row.unpack(x, y);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) w[e] = weight_of(y[e], top, r);
+                    to_bins(y, w, limit);
+                }
+                __syncthreads();
+                bin = reach<kBins / 64>(need, before, bins);
+            }
+            if (bin == kBins) {
+                __syncthreads();
+                if (threadIdx.x < kBins) sh.bins[threadIdx.x] = 0;
+                __syncthreads();
+                row.values([&](const float (&y)[N], int, const uint4& x) {
+                    uint32_t w[N];
+                    weights(x, y, w);
+                    to_bins(y, w, 1e30f);
+                });
+                __syncthreads();
+                bin = reach<kBins / 64>(need, before, bins);   // (a weight of a unit or more is nearer than the last bin)
+            }
+            // all kept tokens, or those of the bin alone, or neither fits
+            gather_again();
+            int n = collect(0.0f, static_cast<float>(bin + 1));
+            few = n <= kCandidates;
+            if (!few) {
+                gather_again();
+                n = collect(static_cast<float>(bin), static_cast<float>(bin + 1));
+            }
+            listed = n <= kCandidates;
+            if (listed) {
+                own(n);
+                const uint64_t skip = few ? 0 : before;
+                kappa = whole_key(select(turn, 32, kStop, need - skip, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t w) { f(key, [&] { return static_cast<unsigned long long>(w); }); }); }));
+                above += skip;
+            } else {
+                kappa = whole_key(select(turn, 32, kStop, need, above, [&](auto f) { everything([&](uint32_t key, uint32_t, auto w) { f(key, [&] { return static_cast<unsigned long long>(w()); }); }); }));
+            }
+            const uint64_t w = weight_at(kappa);
+            take = w ? (need - above + w - 1) / w : 1;
         }
-        const uint64_t w = weight_at(kappa);
-        take = w ? (need - above + w - 1) / w : 1;
     } else if (least > 1) {
         // min_p alone: what it may keep (2^-7 more than that, in the exponent), if it fits
         const float far = (0.0078125f - logf(min_p)) * kBinsPerUnit;
@@ -577,7 +723,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         few = n <= kCandidates;
         if (few) own(n);
     }
-    if (kappa) {
+    if (kappa && take != ~uint64_t{0}) {
         // the take-th of the tokens equal to kappa, by index, if not all are kept
         uint64_t ties = 0, above;
         if (listed) collected([&](uint32_t key, uint32_t, uint32_t) { ties += key == kappa; });
@@ -615,9 +761,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         return;
     }
 
-    // the kept weight of each 64 vectors (a wavefront's turn), then of the
-    // vectors and elements where the target is reached
-    const int segments = (row.count + 63) / 64;
+    // Each wavefront takes a run of the row's vectors; the kept weight of its
+    // segments of 4 x 64 vectors, then of the vectors and elements of the
+    // segment in which the target is reached.
+    const int turns = (row.count + 64 * kWaves - 1) / (64 * kWaves);   // of 64 vectors, a wavefront
+    const int groups = (turns + kGroup - 1) / kGroup;
     // values below this one are not kept: kappa's, or that of min_p less 2^-7 in the exponent
     const float lowest = fmaxf(kappa ? value_of(kappa) : -INFINITY, least > 1 ? top + (logf(min_p) - 0.0078125f) * t : -INFINITY);
     auto kept_weights = [&](const uint4& x, int v, uint32_t (&w)[N]) {
@@ -632,16 +780,36 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
             for (int i = 0; i < N; ++i) w[i] = keeps(key_of(y[i]), static_cast<uint32_t>(v * N + i - row.shift)) && w[i] >= least ? w[i] : 0u;
     };
     if (!tabled) fill_table();
-    row.all([&](const uint4& x, int v, int j) {
-        uint32_t w[N];
-        kept_weights(x, v, w);
+    if (!F32 && kappa) {
+        // values that are not kept have no weight
+        const float value = value_of(kappa);
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < 2 * kTableHalf; i += kThreads)
+            if (entry_value(i) < value) sh.table[i] = 0;
+        __syncthreads();
+    }
+    auto segment_sum = [&](int w, int g) {   // this lane's part
         uint64_t sum = 0;
+        uint4 x[kGroup];
+        const int first = (w * turns + g * kGroup) * 64 + lane;
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum += w[i];
-        if (__any(sum != 0)) sum = wave_sum64(sum);
-        if (lane == 0 && j * kWaves + wave < segments) sh.segments[j * kWaves + wave] = sum;
-    });
+        for (int j = 0; j < kGroup; ++j) x[j] = g * kGroup + j < turns ? row.load(first + 64 * j) : row.load(row.count);
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+            uint32_t kw[N];
+            kept_weights(x[j], first + 64 * j, kw);
+#pragma unroll
+            for (int i = 0; i < N; ++i) sum += kw[i];
+        }
+        return sum;
+    };
+#pragma unroll 1
+    for (int g = 0; g < groups; ++g) {
+        const uint64_t sum = wave_sum64(segment_sum(wave, g));
+        if (lane == 0) sh.segments[wave * groups + g] = sum;
+    }
     __syncthreads();
+    const int segments = kWaves * groups;
     uint64_t total = 0;
     for (int i = threadIdx.x; i < segments; i += kThreads) total += sh.segments[i];
     total = turn.block_sum(total);
@@ -651,36 +819,45 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     }
     if (wave != 0) return;
     const uint64_t target = part_of(u_units, total, more);
-    uint64_t before = 0, upto_before = 0;
+    uint64_t before = 0, passed = 0;
     int segment = 0;
     for (;; segment += 64) {
-        const int at = reach<1>(target + 1 - before, upto_before, [&](int i) { return segment + i < segments ? sh.segments[segment + i] : uint64_t{0}; });
-        before += upto_before;
+        const int at = reach<1>(target + 1 - before, passed, [&](int i) { return segment + i < segments ? sh.segments[segment + i] : uint64_t{0}; });
+        before += passed;
         if (at < 64) {
             segment += at;
             break;
         }
     }
-    const int v = segment * 64 + lane;
-    uint32_t w[N];
-    kept_weights(row.load(v), v, w);
-    uint64_t sum = 0;
+    const int first = (segment / groups * turns + segment % groups * kGroup) * 64 + lane;
+#pragma unroll 1
+    for (int j = 0; j < kGroup; ++j) {
+        const int v = first + 64 * j;
+        uint32_t w[N];
+        kept_weights(row.load(v), v, w);
+        uint64_t sum = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) sum += w[i];
-    const uint64_t upto = before + wave_scan64(sum);
-    const uint64_t hit = __ballot(upto > target);
-    if (hit && lane == __ffsll(static_cast<unsigned long long>(hit)) - 1) {
-        uint64_t at = upto - sum;
-        int i = 0;
-        uint32_t here = w[0];
+        for (int i = 0; i < N; ++i) sum += w[i];
+        const uint64_t upto = before + wave_scan64(sum);
+        const uint64_t hit = __ballot(upto > target);
+        if (!hit) {
+            before = lane_value(upto, 63);
+            continue;
+        }
+        if (lane == __ffsll(static_cast<unsigned long long>(hit)) - 1) {
+            uint64_t at = upto - sum;
+            int i = 0;
+            uint32_t here = w[0];
 #pragma unroll
-        for (int j = 1; j < N; ++j)
-            if (i == j - 1 && at + here <= target) {
-                at += here;
-                here = w[j];
-                i = j;
-            }
-        answer(v * N + i - row.shift, static_cast<float>(static_cast<double>(here) / static_cast<double>(total)));
+            for (int e = 1; e < N; ++e)
+                if (i == e - 1 && at + here <= target) {
+                    at += here;
+                    here = w[e];
+                    i = e;
+                }
+            answer(v * N + i - row.shift, static_cast<float>(static_cast<double>(here) / static_cast<double>(total)));
+        }
+        return;
     }
 }
 
@@ -689,18 +866,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
 size_t sample_workspace_bytes(int64_t, int64_t) { return 0; }
 
 hipError_t launch_sample(const SampleParams& p, hipStream_t stream) {
-    // the vectors of a row (which may start inside one) fit the registers of its workgroup
-    const int n = p.f32 ? 4 : 8;
-    const bool aligned = (reinterpret_cast<uintptr_t>(p.logits) & 15) == 0 && (p.B == 1 || p.row_stride % n == 0);
-    const bool keep = p.V + (aligned ? 0 : n - 1) <= kThreads * kKept * n;
     const dim3 grid(p.B), block(kThreads);
-    if (p.f32) {
-        if (keep) hipLaunchKernelGGL((sample_kernel<true, true>), grid, block, 0, stream, p);
-        else hipLaunchKernelGGL((sample_kernel<true, false>), grid, block, 0, stream, p);
-    } else {
-        if (keep) hipLaunchKernelGGL((sample_kernel<false, true>), grid, block, 0, stream, p);
-        else hipLaunchKernelGGL((sample_kernel<false, false>), grid, block, 0, stream, p);
-    }
+    if (p.f32) hipLaunchKernelGGL(sample_kernel<true>, grid, block, 0, stream, p);
+    else hipLaunchKernelGGL(sample_kernel<false>, grid, block, 0, stream, p);
     return hipGetLastError();
 }
 
