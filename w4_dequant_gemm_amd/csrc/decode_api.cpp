@@ -81,7 +81,7 @@ int w4_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t
     if (!q != !Q) return fail(W4_EINVAL, "%s: q and Q must both be given or both be NULL", fn);
     if (q && (Hq <= 0 || Hq > 65535)) return fail(W4_EINVAL, "%s: Hq = %d must be in 1..65535", fn, Hq);
     const int hq = q ? Hq : 0;
-    if (T < 0 || T > kInt32Most / (hq + 2 * hk) / (dim / 8))
+    if (T < 0 || T + 16 > kInt32Most / (hq + 2 * hk) / (dim / 8))   // (a thread each 8 dims)
         return fail(W4_EINVAL, "%s: T = %lld outside 0..2^31 / (heads * head_dim / 8)", fn, ll(T));
     if (T == 0) return W4_OK;
     if (q) W4_TRY(check_rows(fn, "q", q, q_stride, hq, dim));

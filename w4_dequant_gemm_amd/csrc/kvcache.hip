@@ -1,19 +1,21 @@
 // The paged cache of keys and values: appending rows of a QKV product (with
 // the heads' norms and the rotation on the way) and moving an accepted path.
+#include <type_traits>
+
 #include "device.hpp"
 #include "kernels.hpp"
 
 namespace w4 {
 namespace {
 
-// Eight fp32 values -> E4M3 codes of v / s, saturating at +-448, NaN kept.
+// E4M3 saturates at +-448; NaN stays one.
+__device__ __forceinline__ float to_e4m3_range(float x) { return x != x ? x : fminf(fmaxf(x, -448.0f), 448.0f); }
+
+// Eight fp32 values -> E4M3 codes of v / s.
 __device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float s) {
     float f[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = v[i] / s;
-        f[i] = x != x ? x : fminf(fmaxf(x, -448.0f), 448.0f);
-    }
+    for (int i = 0; i < 8; ++i) f[i] = to_e4m3_range(v[i] / s);
     int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], lo, true);
     int hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], 0, false);
@@ -21,89 +23,169 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float s) {
     return make_uint2(static_cast<uint32_t>(lo), static_cast<uint32_t>(hi));
 }
 
-// One head row of one token: D / 8 lanes with eight dims each.  Eight
-// neighbouring heads (D = 64) share a wavefront, so the norm's sum and the
-// rotation's partner values are exchanged inside the row's own lanes.
-template <int D>
-__global__ void __launch_bounds__(256) kv_append_kernel(KvAppendParams p) {
+// The values of 16 tokens of one head, a workgroup.  A piece of V's cache holds
+// C tokens of one dim, so neighbouring tokens are put together in shared memory
+// and whole pieces written where their slots fill one (writes of single
+// elements cost the memory a read each: 4100 tokens, E4M3: 20 us of 34).  The
+// workgroup writes the pieces that begin with one of its tokens and so reads up
+// to C - 1 tokens more.
+template <int D, int E>
+__device__ __forceinline__ void append_values(const KvAppendParams& p, int tile, int head) {
+    using T = typename std::conditional<E == 1, uint8_t, uint16_t>::type;
+    constexpr int C = 16 / E;                // tokens a piece
+    constexpr int ROWS = 16 + C;             // one before this tile's, and C - 1 behind
+    __shared__ int slots[ROWS];
+    __shared__ __attribute__((aligned(16))) uint16_t rows[ROWS - 1][D];
+    const int t0 = tile * 16, tid = threadIdx.x;
+    const int page_size = 16 * p.cache.page_blocks;
+    const int64_t all = p.cache.pages * page_size;
+    if (tid < ROWS) {
+        const int t = t0 - 1 + tid;
+        const int slot = t >= 0 && t < p.T ? p.slots[t] : -1;
+        slots[tid] = slot < all ? slot : -1;
+    }
+    for (int i = tid; i < (ROWS - 1) * (D / 8); i += 256) {
+        const int row = i / (D / 8), c = i % (D / 8);
+        if (t0 + row < p.T)
+            *reinterpret_cast<uint4*>(&rows[row][8 * c]) =
+                *reinterpret_cast<const uint4*>(p.v + (t0 + row) * p.v_stride + static_cast<int64_t>(head) * D + 8 * c);
+    }
+    __syncthreads();
+    const float scale = E == 1 ? p.cache.v_scale[head] : 1.0f;
+    const int d = tid % D;
+    for (int i = tid / D; i < 16; i += 256 / D) {
+        const int slot = slots[i + 1];
+        if (slot < 0) continue;
+        // a piece begins here unless the token before lies in it, just before
+        if (slot % C != 0 && slots[i] == slot - 1) continue;
+        int n = 1;
+        while (slot % C + n < C && slots[i + 1 + n] == slot + n) ++n;
+        const uint32_t page = static_cast<uint32_t>(slot) / static_cast<uint32_t>(page_size);
+        const int in_page = slot - static_cast<int>(page) * page_size;
+        const int64_t block = (static_cast<int64_t>(page) * p.cache.heads + head) * p.cache.page_blocks + (in_page >> 4);
+        T* to = static_cast<T*>(p.cache.v) + ((block * (16 / C) + (in_page & 15) / C) * D + d) * C;
+        if (n == C) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (E == 2) {
+                    w[j] = rows[i + 2 * j][d] | static_cast<uint32_t>(rows[i + 2 * j + 1][d]) << 16;
+                } else {
+                    float f[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) f[k] = to_e4m3_range(bf16_lo(rows[i + 4 * j + k][d]) / scale);
+                    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+                    w[j] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], lo, true));
+                }
+            }
+            *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            for (int j = 0; j < n; ++j) {
+                const uint16_t x = rows[i + j][d];
+                if constexpr (E == 2) to[slot % C + j] = x;
+                else to[slot % C + j] = static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(to_e4m3_range(bf16_lo(x) / scale), 0.0f, 0, false));
+            }
+        }
+    }
+}
+
+// One head row of one token: D / 8 lanes with eight dims each, several rows a
+// wavefront; the norm's sum and the rotation's partner values are exchanged
+// inside the row's own lanes.  Query rows first, in their order in Q, then the
+// keys', 16 tokens of a head after one another (a prompt's tokens have
+// neighbouring slots, whose pieces of K lie side by side), then the values'
+// workgroups.
+template <int D, int E>
+__global__ void __launch_bounds__(256) kv_append_kernel(KvAppendParams p, uint32_t row_groups) {
     constexpr int L = D / 8;                 // lanes a row
     const int hk = p.cache.heads;
-    const int heads = p.hq + 2 * hk;
-    const uint32_t row = (blockIdx.x * 256u + threadIdx.x) / L;
-    const uint32_t t = row / static_cast<uint32_t>(heads);
-    const int h = static_cast<int>(row - t * static_cast<uint32_t>(heads));
+    if (blockIdx.x >= row_groups) {
+        const uint32_t id = blockIdx.x - row_groups;
+        append_values<D, E>(p, static_cast<int>(id / static_cast<uint32_t>(hk)), static_cast<int>(id % static_cast<uint32_t>(hk)));
+        return;
+    }
+    const uint32_t query_rows = static_cast<uint32_t>(p.T) * p.hq;
+    uint32_t row = (blockIdx.x * 256u + threadIdx.x) / L;
     const int c = threadIdx.x % L;           // dims 8c .. 8c + 7
+    const bool is_q = row < query_rows;
+    uint32_t t;
+    int head;
+    if (is_q) {
+        t = row / static_cast<uint32_t>(p.hq);
+        head = static_cast<int>(row - t * static_cast<uint32_t>(p.hq));
+    } else {
+        row -= query_rows;
+        const uint32_t sixteen = row >> 4, group = sixteen / static_cast<uint32_t>(hk);
+        t = group * 16u + (row & 15u);
+        head = static_cast<int>(sixteen - group * static_cast<uint32_t>(hk));
+    }
     if (t >= static_cast<uint32_t>(p.T)) return;   // whole rows leave together
 
-    const bool is_q = h < p.hq, is_v = h >= p.hq + hk;
-    const int head = is_q ? h : is_v ? h - p.hq - hk : h - p.hq;
-    const uint16_t* src = is_q ? p.q + t * p.q_stride : is_v ? p.v + t * p.v_stride : p.k + t * p.k_stride;
+    const uint16_t* src = is_q ? p.q + t * p.q_stride : p.k + t * p.k_stride;
     const uint4 w = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(head) * D + 8 * c);
     float x[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y),
                   bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
 
-    if (!is_v) {
-        const float* norm = is_q ? p.q_norm : p.k_norm;
-        if (norm) {
-            float s = 0.0f;
+    const float* norm = is_q ? p.q_norm : p.k_norm;
+    if (norm) {
+        float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += x[i] * x[i];
+        for (int i = 0; i < 8; ++i) s += x[i] * x[i];
 #pragma unroll
-            for (int off = L / 2; off >= 1; off >>= 1) s += __shfl_xor(s, off, L);
-            const float r = 1.0f / sqrtf(s * (1.0f / D) + p.eps);
-            const float4_t n0 = *reinterpret_cast<const float4_t*>(norm + 8 * c);
-            const float4_t n1 = *reinterpret_cast<const float4_t*>(norm + 8 * c + 4);
+        for (int off = L / 2; off >= 1; off >>= 1) s += __shfl_xor(s, off, L);
+        const float r = 1.0f / sqrtf(s * (1.0f / D) + p.eps);
+        const float4_t n0 = *reinterpret_cast<const float4_t*>(norm + 8 * c);
+        const float4_t n1 = *reinterpret_cast<const float4_t*>(norm + 8 * c + 4);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (i < 4 ? n0[i & 3] : n1[i & 3]);
-        }
-        if (p.rope) {
-            const int half = p.rot >> 4;     // lanes that hold the first of each pair (halves)
-            const int64_t pos = p.positions[t];
-            const bool inside = pos >= 0 && pos < p.rope_rows;
-            const float* cs = p.rope + (inside ? pos : 0) * p.rot;
-            const bool turns = c < 2 * half;
-            if (p.interleaved) {
-                if (turns) {
-                    const float4_t co = *reinterpret_cast<const float4_t*>(cs + 4 * c);
-                    const float4_t si = *reinterpret_cast<const float4_t*>(cs + (p.rot >> 1) + 4 * c);
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (i < 4 ? n0[i & 3] : n1[i & 3]);
+    }
+    if (p.rope) {
+        const int half = p.rot >> 4;     // lanes that hold the first of each pair (halves)
+        const int64_t pos = p.positions[t];
+        const bool inside = pos >= 0 && pos < p.rope_rows;
+        const float* cs = p.rope + (inside ? pos : 0) * p.rot;
+        const bool turns = c < 2 * half;
+        if (p.interleaved) {
+            if (turns) {
+                const float4_t co = *reinterpret_cast<const float4_t*>(cs + 4 * c);
+                const float4_t si = *reinterpret_cast<const float4_t*>(cs + (p.rot >> 1) + 4 * c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a = x[2 * i], b = x[2 * i + 1];
+                    x[2 * i] = a * co[i] - b * si[i];
+                    x[2 * i + 1] = b * co[i] + a * si[i];
+                }
+            }
+        } else {
+            const bool first = c < half;
+            const int partner = turns ? (first ? c + half : c - half) : c;
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], partner, L);
+            if (turns) {
+                const int j = 8 * (first ? c : c - half);
+#pragma unroll
+                for (int v4 = 0; v4 < 2; ++v4) {
+                    const float4_t co = *reinterpret_cast<const float4_t*>(cs + j + 4 * v4);
+                    const float4_t si = *reinterpret_cast<const float4_t*>(cs + (p.rot >> 1) + j + 4 * v4);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float a = x[2 * i], b = x[2 * i + 1];
-                        x[2 * i] = a * co[i] - b * si[i];
-                        x[2 * i + 1] = b * co[i] + a * si[i];
-                    }
-                }
-            } else {
-                const bool first = c < half;
-                const int partner = turns ? (first ? c + half : c - half) : c;
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], partner, L);
-                if (turns) {
-                    const int j = 8 * (first ? c : c - half);
-#pragma unroll
-                    for (int v4 = 0; v4 < 2; ++v4) {
-                        const float4_t co = *reinterpret_cast<const float4_t*>(cs + j + 4 * v4);
-                        const float4_t si = *reinterpret_cast<const float4_t*>(cs + (p.rot >> 1) + j + 4 * v4);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float own = x[4 * v4 + i], other = y[4 * v4 + i];
-                            x[4 * v4 + i] = first ? own * co[i] - other * si[i] : own * co[i] + other * si[i];
-                        }
+                        const float own = x[4 * v4 + i], other = y[4 * v4 + i];
+                        x[4 * v4 + i] = first ? own * co[i] - other * si[i] : own * co[i] + other * si[i];
                     }
                 }
             }
-            if (!inside && turns) {
+        }
+        if (!inside && turns) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = __builtin_nanf("");
-            }
+            for (int i = 0; i < 8; ++i) x[i] = __builtin_nanf("");
         }
-        if (is_q) {
-            const uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                       pack_bf16x2(x[6], x[7]));
-            *reinterpret_cast<uint4*>(p.Q + (static_cast<int64_t>(t) * p.hq + head) * D + 8 * c) = o;
-            return;
-        }
+    }
+    if (is_q) {
+        const uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                   pack_bf16x2(x[6], x[7]));
+        *reinterpret_cast<uint4*>(p.Q + (static_cast<int64_t>(t) * p.hq + head) * D + 8 * c) = o;
+        return;
     }
 
     const int64_t slot = p.slots[t];
@@ -113,98 +195,153 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendParams p) {
     const int in_page = static_cast<int>(slot) - static_cast<int>(page) * page_size;
     const int s = in_page & 15;
     const int64_t block = (static_cast<int64_t>(page) * hk + head) * p.cache.page_blocks + (in_page >> 4);
-    if (p.cache.e4m3) {
-        const uint2 codes = e4m3x8(x, is_v ? p.cache.v_scale[head] : p.cache.k_scale[head]);
-        if (!is_v) {
-            uint8_t* dst = static_cast<uint8_t*>(p.cache.k) + block * (16 * D);
-            *reinterpret_cast<uint2*>(dst + (c >> 1) * 256 + s * 16 + (c & 1) * 8) = codes;
-        } else {
-            uint8_t* dst = static_cast<uint8_t*>(p.cache.v) + block * (16 * D) + 8 * c * 16 + s;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i * 16] = static_cast<uint8_t>((i < 4 ? codes.x : codes.y) >> (8 * (i & 3)));
-        }
+    if constexpr (E == 1) {
+        uint8_t* dst = static_cast<uint8_t*>(p.cache.k) + block * (16 * D);
+        *reinterpret_cast<uint2*>(dst + (c >> 1) * 256 + s * 16 + (c & 1) * 8) = e4m3x8(x, p.cache.k_scale[head]);
     } else {
-        const uint32_t o[4] = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                               pack_bf16x2(x[6], x[7])};
-        if (!is_v) {
-            uint16_t* dst = static_cast<uint16_t*>(p.cache.k) + block * (16 * D);
-            *reinterpret_cast<uint4*>(dst + c * 128 + s * 8) = make_uint4(o[0], o[1], o[2], o[3]);
-        } else {
-            uint16_t* dst = static_cast<uint16_t*>(p.cache.v) + block * (16 * D) + (s >> 3) * (8 * D) + 64 * c + (s & 7);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i * 8] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
-        }
+        uint16_t* dst = static_cast<uint16_t*>(p.cache.k) + block * (16 * D);
+        *reinterpret_cast<uint4*>(dst + c * 128 + s * 8) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                                      pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
     }
 }
 
-// One thread owns one 16-byte column of the cache of one (layer, sequence,
-// head): for K the same chunk of dims of every token (16 bytes a token), for V
-// one dim (an element a token).  It walks the path in order, so no other
-// thread touches what it reads or writes; path[j] >= j and the path ascends,
-// so what a later step reads was not overwritten by an earlier one.
-template <int E>   // bytes an element
+// A workgroup moves 512 / D heads of one sequence and layer, as many tokens at a
+// time as their new places have in one piece of V (8 or 16): their blocks are
+// looked up once, then all pieces are read, the loads on their way together,
+// then, after a barrier, all written.  V's new pieces are read, filled in and
+// written whole: writes of single elements cost the memory a read each (64 paths
+// in 32 layers: 100 us).  path[j] >= j and the path ascends, so no later
+// token's source was written.
+template <int D, int E>
 __global__ void __launch_bounds__(256) kv_move_kernel(KvMoveParams p) {
     using T = typename std::conditional<E == 1, uint8_t, uint16_t>::type;
-    constexpr int C = 16 / E;
-    const int D = p.cache.dim, hk = p.cache.heads, pb = p.cache.page_blocks;
-    const int per_head = D / C + D;
-    const uint32_t unit = blockIdx.x * 256u + threadIdx.x;
-    if (unit >= static_cast<uint32_t>(hk * per_head)) return;
-    const int head = unit / per_head;
-    const int u = unit - head * per_head;
-    const int b = blockIdx.y;
+    constexpr int C = 16 / E, PIECES = D / C;
+    constexpr int KI = C * (512 / C) / 256;  // 16-byte pieces of K a thread
+    __shared__ int64_t from_block[C], to_block[C];   // by place in the piece; -1: stays
+    __shared__ int from_slot[C], to_slot[C];
+    __shared__ int64_t piece_block;
+    const int hk = p.cache.heads, pb = p.cache.page_blocks;
+    const int tid = threadIdx.x, b = blockIdx.y, head0 = blockIdx.x * (512 / D);
     int n = p.count[b];
     n = n < p.path_len ? n : static_cast<int>(p.path_len);
     const int64_t base = p.base[b];
+    if (base < 0) return;
     const int32_t* table = p.page_table + b * p.table_pages;
     const int32_t* path = p.path + b * p.path_len;
     const int64_t layer = static_cast<int64_t>(blockIdx.z) * p.cache.pages * hk * pb;
 
+    // block of head 0 (head h is h pb further), or -1
     auto block_of = [&](int64_t token) -> int64_t {
         const int64_t blk = token >> 4;
         if (token < 0 || blk >= p.table_pages * pb) return -1;
         const uint32_t pg = static_cast<uint32_t>(blk) / static_cast<uint32_t>(pb);
         const int64_t page = table[pg];
         if (page < 0 || page >= p.cache.pages) return -1;
-        return layer + (page * hk + head) * pb + (blk - static_cast<int64_t>(pg) * pb);
+        return layer + page * hk * pb + (blk - static_cast<int64_t>(pg) * pb);
     };
-    for (int j = 0; j < n; ++j) {
-        const int64_t from = base + path[j], to = base + j;
-        if (from == to) continue;
-        const int64_t fb = block_of(from), tb = block_of(to);
-        if (fb < 0 || tb < 0) continue;
-        const int fs = from & 15, ts = to & 15;
-        if (u < D / C) {
-            uint4* k = static_cast<uint4*>(p.cache.k);
-            k[(tb * (D / C) + u) * 16 + ts] = k[(fb * (D / C) + u) * 16 + fs];
-        } else {
-            T* v = static_cast<T*>(p.cache.v);
-            const int d = u - D / C;
-            v[((tb * (16 / C) + ts / C) * D + d) * C + ts % C] = v[((fb * (16 / C) + fs / C) * D + d) * C + fs % C];
+    for (int64_t piece = base / C; piece * C < base + n; ++piece) {   // the new tokens' pieces
+        if (tid < C) {
+            const int64_t to = piece * C + tid, j = to - base;
+            const bool moves = j >= 0 && j < n && path[j] != j;
+            const int64_t from = moves ? base + path[j] : 0;
+            const int64_t tb = block_of(to);
+            const int64_t fb = moves && tb >= 0 ? block_of(from) : -1;
+            from_block[tid] = fb;
+            to_block[tid] = fb < 0 ? -1 : tb;
+            from_slot[tid] = from & 15;
+            to_slot[tid] = to & 15;
+            if (tid == 0) piece_block = tb;  // (a piece lies in one block)
         }
+        __syncthreads();
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < C; ++e) any = any || from_block[e] >= 0;
+        uint4 kx[KI], vx[2];
+        auto k_item = [&](int i, int& e, int& head, int& at) {
+            const int x = tid + 256 * i;
+            e = x / (512 / C);
+            head = head0 + x % (512 / C) / PIECES;
+            at = x % PIECES;
+            return head < hk && from_block[e] >= 0;
+        };
+        auto v_item = [&](int i, int& head, int64_t& at) {
+            const int x = tid + 256 * i;
+            head = head0 + x / D;
+            at = ((piece_block + head * pb) * (16 / C) + (piece * C & 15) / C) * D + x % D;
+            return any && head < hk;
+        };
+        int e, head, at;
+        int64_t where;
+#pragma unroll
+        for (int i = 0; i < KI; ++i)
+            if (k_item(i, e, head, at))
+                kx[i] = static_cast<const uint4*>(p.cache.k)[((from_block[e] + head * pb) * PIECES + at) * 16 + from_slot[e]];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (v_item(i, head, where)) {
+                const int d = (tid + 256 * i) % D;
+                T x[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    x[c] = from_block[c] < 0 ? T{0}
+                                             : static_cast<const T*>(p.cache.v)[(((from_block[c] + head * pb) * (16 / C) + from_slot[c] / C) * D + d) * C + from_slot[c] % C];
+                const uint4 old = static_cast<const uint4*>(p.cache.v)[where];
+                uint32_t w[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int shift = 8 * E * (c % (4 / E));
+                    const uint32_t mask = (E == 1 ? 0xFFu : 0xFFFFu) << shift;
+                    if (from_block[c] >= 0) w[c * E / 4] = (w[c * E / 4] & ~mask) | static_cast<uint32_t>(x[c]) << shift;
+                }
+                vx[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < KI; ++i)
+            if (k_item(i, e, head, at))
+                static_cast<uint4*>(p.cache.k)[((to_block[e] + head * pb) * PIECES + at) * 16 + to_slot[e]] = kx[i];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (v_item(i, head, where)) static_cast<uint4*>(p.cache.v)[where] = vx[i];
+        __syncthreads();
     }
 }
 
 }  // namespace
 
+// one instance for each head size and element
+#define W4_BY_CACHE(LAUNCH)                                                  \
+    do {                                                                     \
+        const int dim = p.cache.dim;                                         \
+        if (p.cache.e4m3) {                                                  \
+            if (dim == 64) LAUNCH(64, 1);                                    \
+            else if (dim == 128) LAUNCH(128, 1);                             \
+            else LAUNCH(256, 1);                                             \
+        } else {                                                             \
+            if (dim == 64) LAUNCH(64, 2);                                    \
+            else if (dim == 128) LAUNCH(128, 2);                             \
+            else LAUNCH(256, 2);                                             \
+        }                                                                    \
+    } while (0)
+
 hipError_t launch_kv_append(const KvAppendParams& p, hipStream_t stream) {
-    const int64_t rows = static_cast<int64_t>(p.T) * (p.hq + 2 * p.cache.heads);
+    const int64_t sixteens = (static_cast<int64_t>(p.T) + 15) / 16;
+    const int64_t rows = static_cast<int64_t>(p.T) * p.hq + sixteens * 16 * p.cache.heads;
     const int64_t per_wg = 256 / (p.cache.dim / 8);
-    const dim3 grid(static_cast<unsigned>((rows + per_wg - 1) / per_wg));
-    switch (p.cache.dim) {
-        case 64: hipLaunchKernelGGL(kv_append_kernel<64>, grid, dim3(256), 0, stream, p); break;
-        case 128: hipLaunchKernelGGL(kv_append_kernel<128>, grid, dim3(256), 0, stream, p); break;
-        default: hipLaunchKernelGGL(kv_append_kernel<256>, grid, dim3(256), 0, stream, p); break;
-    }
+    const uint32_t row_groups = static_cast<uint32_t>((rows + per_wg - 1) / per_wg);
+    const dim3 grid(row_groups + static_cast<unsigned>(sixteens * p.cache.heads));
+#define W4_APPEND(D, E) hipLaunchKernelGGL((kv_append_kernel<D, E>), grid, dim3(256), 0, stream, p, row_groups)
+    W4_BY_CACHE(W4_APPEND);
+#undef W4_APPEND
     return hipGetLastError();
 }
 
 hipError_t launch_kv_move(const KvMoveParams& p, hipStream_t stream) {
-    const int c = p.cache.e4m3 ? 16 : 8;
-    const int units = p.cache.heads * (p.cache.dim / c + p.cache.dim);
-    const dim3 grid((units + 255) / 256, p.B, p.cache.layers);
-    if (p.cache.e4m3) hipLaunchKernelGGL(kv_move_kernel<1>, grid, dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL(kv_move_kernel<2>, grid, dim3(256), 0, stream, p);
+    const int heads = 512 / p.cache.dim;     // a workgroup
+    const dim3 grid((p.cache.heads + heads - 1) / heads, p.B, p.cache.layers);
+#define W4_MOVE(D, E) hipLaunchKernelGGL((kv_move_kernel<D, E>), grid, dim3(256), 0, stream, p)
+    W4_BY_CACHE(W4_MOVE);
+#undef W4_MOVE
     return hipGetLastError();
 }
 
