@@ -89,119 +89,122 @@ __device__ __forceinline__ void append_values(const KvAppendParams& p, int tile,
     }
 }
 
-// One head row of one token: D / 8 lanes with eight dims each, several rows a
-// wavefront; the norm's sum and the rotation's partner values are exchanged
-// inside the row's own lanes.  Query rows first, in their order in Q, then the
-// keys', 16 tokens of a head after one another (a prompt's tokens have
-// neighbouring slots, whose pieces of K lie side by side), then the values'
-// workgroups.
+// Query and key heads: D / 8 lanes (eight dims each) take four heads of one
+// token, whose loads are on their way together under one lookup of the token's
+// position, angles and slot (one head at a time the chain of those lookups
+// bounds it: 4100 tokens, 32 us); the norm's sum and the rotation's partner
+// values are exchanged inside the row's own lanes.  Neighbouring rows of lanes
+// have neighbouring tokens, whose pieces of K lie side by side.  Workgroups
+// from row_groups on store the values.
 template <int D, int E>
 __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendParams p, uint32_t row_groups) {
     constexpr int L = D / 8;                 // lanes a row
+    constexpr int H = 4;                     // heads of a row
     const int hk = p.cache.heads;
     if (blockIdx.x >= row_groups) {
         const uint32_t id = blockIdx.x - row_groups;
         append_values<D, E>(p, static_cast<int>(id / static_cast<uint32_t>(hk)), static_cast<int>(id % static_cast<uint32_t>(hk)));
         return;
     }
-    const uint32_t query_rows = static_cast<uint32_t>(p.T) * p.hq;
-    uint32_t row = (blockIdx.x * 256u + threadIdx.x) / L;
+    const uint32_t row = (blockIdx.x * 256u + threadIdx.x) / L;
     const int c = threadIdx.x % L;           // dims 8c .. 8c + 7
-    const bool is_q = row < query_rows;
-    uint32_t t;
-    int head;
-    if (is_q) {
-        t = row / static_cast<uint32_t>(p.hq);
-        head = static_cast<int>(row - t * static_cast<uint32_t>(p.hq));
-    } else {
-        row -= query_rows;
-        const uint32_t sixteen = row >> 4, group = sixteen / static_cast<uint32_t>(hk);
-        t = group * 16u + (row & 15u);
-        head = static_cast<int>(sixteen - group * static_cast<uint32_t>(hk));
-    }
+    const uint32_t q_quads = static_cast<uint32_t>((p.hq + H - 1) / H), quads = q_quads + static_cast<uint32_t>((hk + H - 1) / H);
+    const uint32_t sixteen = row >> 4, group = sixteen / quads;
+    const uint32_t t = group * 16u + (row & 15u);
     if (t >= static_cast<uint32_t>(p.T)) return;   // whole rows leave together
-
-    const uint16_t* src = is_q ? p.q + t * p.q_stride : p.k + t * p.k_stride;
-    const uint4 w = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(head) * D + 8 * c);
-    float x[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y),
-                  bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
-
+    const uint32_t quad = sixteen - group * quads;
+    const bool is_q = quad < q_quads;
+    const int head0 = static_cast<int>(is_q ? quad : quad - q_quads) * H;
+    const int heads = is_q ? p.hq : hk;
+    const uint16_t* src = (is_q ? p.q + t * p.q_stride : p.k + t * p.k_stride) + static_cast<int64_t>(head0) * D + 8 * c;
+    uint4 w[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i) w[i] = head0 + i < heads ? *reinterpret_cast<const uint4*>(src + i * D) : make_uint4(0, 0, 0, 0);
     const float* norm = is_q ? p.q_norm : p.k_norm;
+    float weight[8];
     if (norm) {
-        float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += x[i] * x[i];
-#pragma unroll
-        for (int off = L / 2; off >= 1; off >>= 1) s += __shfl_xor(s, off, L);
-        const float r = 1.0f / sqrtf(s * (1.0f / D) + p.eps);
-        const float4_t n0 = *reinterpret_cast<const float4_t*>(norm + 8 * c);
-        const float4_t n1 = *reinterpret_cast<const float4_t*>(norm + 8 * c + 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (i < 4 ? n0[i & 3] : n1[i & 3]);
+        for (int i = 0; i < 8; ++i) weight[i] = norm[8 * c + i];
     }
-    if (p.rope) {
-        const int half = p.rot >> 4;     // lanes that hold the first of each pair (halves)
+    // the angles' cosines and sines of this lane's dims (interleaved: of its four pairs)
+    const int half = p.rot >> 4;             // lanes that hold the first of each pair (halves)
+    const bool turns = p.rope && c < 2 * half;
+    const bool first = c < half;
+    bool inside = true;
+    float co[8], si[8];
+    if (turns) {
         const int64_t pos = p.positions[t];
-        const bool inside = pos >= 0 && pos < p.rope_rows;
-        const float* cs = p.rope + (inside ? pos : 0) * p.rot;
-        const bool turns = c < 2 * half;
-        if (p.interleaved) {
-            if (turns) {
-                const float4_t co = *reinterpret_cast<const float4_t*>(cs + 4 * c);
-                const float4_t si = *reinterpret_cast<const float4_t*>(cs + (p.rot >> 1) + 4 * c);
+        inside = pos >= 0 && pos < p.rope_rows;
+        const float* cs = p.rope + (inside ? pos : 0) * p.rot + (p.interleaved ? 4 * c : 8 * (first ? c : c - half));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = x[2 * i], b = x[2 * i + 1];
-                    x[2 * i] = a * co[i] - b * si[i];
-                    x[2 * i + 1] = b * co[i] + a * si[i];
-                }
+        for (int i = 0; i < 4; ++i) {
+            co[i] = cs[i];
+            si[i] = cs[(p.rot >> 1) + i];
+        }
+        if (!p.interleaved)
+#pragma unroll
+            for (int i = 4; i < 8; ++i) {
+                co[i] = cs[i];
+                si[i] = cs[(p.rot >> 1) + i];
             }
-        } else {
-            const bool first = c < half;
-            const int partner = turns ? (first ? c + half : c - half) : c;
-            float y[8];
+    }
+    int64_t block = -1;
+    int s = 0;
+    if (!is_q) {
+        const int64_t slot = p.slots[t];
+        const int page_size = 16 * p.cache.page_blocks;
+        if (slot >= 0 && slot < p.cache.pages * page_size) {
+            const uint32_t page = static_cast<uint32_t>(slot) / static_cast<uint32_t>(page_size);
+            const int in_page = static_cast<int>(slot) - static_cast<int>(page) * page_size;
+            s = in_page & 15;
+            block = (static_cast<int64_t>(page) * hk + head0) * p.cache.page_blocks + (in_page >> 4);
+        }
+    }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], partner, L);
-            if (turns) {
-                const int j = 8 * (first ? c : c - half);
+    for (int j = 0; j < H; ++j) {
+        if (head0 + j >= heads) break;       // (the same for a row's lanes)
+        float x[8] = {bf16_lo(w[j].x), bf16_hi(w[j].x), bf16_lo(w[j].y), bf16_hi(w[j].y),
+                      bf16_lo(w[j].z), bf16_hi(w[j].z), bf16_lo(w[j].w), bf16_hi(w[j].w)};
+        if (norm) {
+            float sum = 0.0f;
 #pragma unroll
-                for (int v4 = 0; v4 < 2; ++v4) {
-                    const float4_t co = *reinterpret_cast<const float4_t*>(cs + j + 4 * v4);
-                    const float4_t si = *reinterpret_cast<const float4_t*>(cs + (p.rot >> 1) + j + 4 * v4);
+            for (int i = 0; i < 8; ++i) sum += x[i] * x[i];
+#pragma unroll
+            for (int off = L / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, L);
+            const float r = 1.0f / sqrtf(sum * (1.0f / D) + p.eps);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = x[i] * r * weight[i];
+        }
+        if (p.rope) {
+            if (p.interleaved) {
+                if (turns)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float own = x[4 * v4 + i], other = y[4 * v4 + i];
-                        x[4 * v4 + i] = first ? own * co[i] - other * si[i] : own * co[i] + other * si[i];
+                        const float a = x[2 * i], b = x[2 * i + 1];
+                        x[2 * i] = a * co[i] - b * si[i];
+                        x[2 * i + 1] = b * co[i] + a * si[i];
                     }
-                }
-            }
-        }
-        if (!inside && turns) {
+            } else {
+                const int partner = turns ? (first ? c + half : c - half) : c;
+                float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __builtin_nanf("");
+                for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], partner, L);
+                if (turns)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = first ? x[i] * co[i] - y[i] * si[i] : x[i] * co[i] + y[i] * si[i];
+            }
+            if (turns && !inside)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = __builtin_nanf("");
         }
-    }
-    if (is_q) {
-        const uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                   pack_bf16x2(x[6], x[7]));
-        *reinterpret_cast<uint4*>(p.Q + (static_cast<int64_t>(t) * p.hq + head) * D + 8 * c) = o;
-        return;
-    }
-
-    const int64_t slot = p.slots[t];
-    const int page_size = 16 * p.cache.page_blocks;
-    if (slot < 0 || slot >= p.cache.pages * page_size) return;
-    const uint32_t page = static_cast<uint32_t>(slot) / static_cast<uint32_t>(page_size);
-    const int in_page = static_cast<int>(slot) - static_cast<int>(page) * page_size;
-    const int s = in_page & 15;
-    const int64_t block = (static_cast<int64_t>(page) * hk + head) * p.cache.page_blocks + (in_page >> 4);
-    if constexpr (E == 1) {
-        uint8_t* dst = static_cast<uint8_t*>(p.cache.k) + block * (16 * D);
-        *reinterpret_cast<uint2*>(dst + (c >> 1) * 256 + s * 16 + (c & 1) * 8) = e4m3x8(x, p.cache.k_scale[head]);
-    } else {
-        uint16_t* dst = static_cast<uint16_t*>(p.cache.k) + block * (16 * D);
-        *reinterpret_cast<uint4*>(dst + c * 128 + s * 8) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                                      pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        const uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        if (is_q) {
+            *reinterpret_cast<uint4*>(p.Q + (static_cast<int64_t>(t) * p.hq + head0 + j) * D + 8 * c) = o;
+        } else if (block >= 0) {
+            uint8_t* dst = static_cast<uint8_t*>(p.cache.k) + (block + j * p.cache.page_blocks) * (16 * D * E);
+            if constexpr (E == 1) *reinterpret_cast<uint2*>(dst + (c >> 1) * 256 + s * 16 + (c & 1) * 8) = e4m3x8(x, p.cache.k_scale[head0 + j]);
+            else *reinterpret_cast<uint4*>(dst + c * 256 + s * 16) = o;
+        }
     }
 }
 
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(256) kv_move_kernel(KvMoveParams p) {
 
 hipError_t launch_kv_append(const KvAppendParams& p, hipStream_t stream) {
     const int64_t sixteens = (static_cast<int64_t>(p.T) + 15) / 16;
-    const int64_t rows = static_cast<int64_t>(p.T) * p.hq + sixteens * 16 * p.cache.heads;
+    const int64_t rows = sixteens * 16 * ((p.hq + 3) / 4 + (p.cache.heads + 3) / 4);
     const int64_t per_wg = 256 / (p.cache.dim / 8);
     const uint32_t row_groups = static_cast<uint32_t>((rows + per_wg - 1) / per_wg);
     const dim3 grid(row_groups + static_cast<unsigned>(sixteens * p.cache.heads));
