@@ -34,7 +34,7 @@ __device__ __forceinline__ void append_values(const KvAppendParams& p, int tile,
     using T = typename std::conditional<E == 1, uint8_t, uint16_t>::type;
     constexpr int C = 16 / E;                // tokens a piece
     constexpr int ROWS = 16 + C;             // one before this tile's, and C - 1 behind
-    __shared__ int slots[ROWS];
+    __shared__ int slots[ROWS], runs[16];
     __shared__ __attribute__((aligned(16))) uint16_t rows[ROWS - 1][D];
     const int t0 = tile * 16, tid = threadIdx.x;
     const int page_size = 16 * p.cache.page_blocks;
@@ -51,15 +51,29 @@ __device__ __forceinline__ void append_values(const KvAppendParams& p, int tile,
                 *reinterpret_cast<const uint4*>(p.v + (t0 + row) * p.v_stride + static_cast<int64_t>(head) * D + 8 * c);
     }
     __syncthreads();
+    if (tid < 16) {
+        // tokens of the piece that begins here; none if it is not stored or the
+        // token before lies in the same piece, just before
+        const int slot = slots[tid + 1];
+        int n = 0;
+        if (slot >= 0 && (slot % C == 0 || slots[tid] != slot - 1)) {
+            bool on = true;
+#pragma unroll
+            for (int i = 1; i < C; ++i) {
+                on = on && slot % C + i < C && slots[tid + 1 + i] == slot + i;
+                n += on;
+            }
+            ++n;
+        }
+        runs[tid] = n;
+    }
+    __syncthreads();
     const float scale = E == 1 ? p.cache.v_scale[head] : 1.0f;
     const int d = tid % D;
     for (int i = tid / D; i < 16; i += 256 / D) {
+        const int n = runs[i];
+        if (n == 0) continue;
         const int slot = slots[i + 1];
-        if (slot < 0) continue;
-        // a piece begins here unless the token before lies in it, just before
-        if (slot % C != 0 && slots[i] == slot - 1) continue;
-        int n = 1;
-        while (slot % C + n < C && slots[i + 1 + n] == slot + n) ++n;
         const uint32_t page = static_cast<uint32_t>(slot) / static_cast<uint32_t>(page_size);
         const int in_page = slot - static_cast<int>(page) * page_size;
         const int64_t block = (static_cast<int64_t>(page) * p.cache.heads + head) * p.cache.page_blocks + (in_page >> 4);
@@ -208,9 +222,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendParams p, uint32
     }
 }
 
-// A workgroup moves 512 / D heads of one sequence and layer, as many tokens at a
-// time as their new places have in one piece of V (8 or 16): their blocks are
-// looked up once, then all pieces are read, the loads on their way together,
+// A workgroup moves 512 / D heads of one sequence and layer.  The tokens' blocks
+// are looked up 64 at a time; then, as many tokens at a time as their new places
+// have in one piece of V (8 or 16), all pieces are read, the loads on their way together,
 // then, after a barrier, all written.  V's new pieces are read, filled in and
 // written whole: writes of single elements cost the memory a read each (64 paths
 // in 32 layers: 100 us).  path[j] >= j and the path ascends, so no later
@@ -220,9 +234,10 @@ __global__ void __launch_bounds__(256) kv_move_kernel(KvMoveParams p) {
     using T = typename std::conditional<E == 1, uint8_t, uint16_t>::type;
     constexpr int C = 16 / E, PIECES = D / C;
     constexpr int KI = C * (512 / C) / 256;  // 16-byte pieces of K a thread
-    __shared__ int64_t from_block[C], to_block[C];   // by place in the piece; -1: stays
-    __shared__ int from_slot[C], to_slot[C];
-    __shared__ int64_t piece_block;
+    constexpr int kTokens = 64;              // looked up at a time
+    __shared__ int64_t from_block[kTokens];  // by new place; -1: stays
+    __shared__ int from_slot[kTokens];
+    __shared__ int64_t piece_block[kTokens / C];
     const int hk = p.cache.heads, pb = p.cache.page_blocks;
     const int tid = threadIdx.x, b = blockIdx.y, head0 = blockIdx.x * (512 / D);
     int n = p.count[b];
@@ -242,35 +257,34 @@ __global__ void __launch_bounds__(256) kv_move_kernel(KvMoveParams p) {
         if (page < 0 || page >= p.cache.pages) return -1;
         return layer + page * hk * pb + (blk - static_cast<int64_t>(pg) * pb);
     };
-    for (int64_t piece = base / C; piece * C < base + n; ++piece) {   // the new tokens' pieces
-        if (tid < C) {
-            const int64_t to = piece * C + tid, j = to - base;
-            const bool moves = j >= 0 && j < n && path[j] != j;
-            const int64_t from = moves ? base + path[j] : 0;
-            const int64_t tb = block_of(to);
-            const int64_t fb = moves && tb >= 0 ? block_of(from) : -1;
-            from_block[tid] = fb;
-            to_block[tid] = fb < 0 ? -1 : tb;
-            from_slot[tid] = from & 15;
-            to_slot[tid] = to & 15;
-            if (tid == 0) piece_block = tb;  // (a piece lies in one block)
-        }
-        __syncthreads();
+    for (int64_t piece0 = base / C; piece0 * C < base + n; piece0 += kTokens / C) {
+    if (tid < kTokens) {                     // the new tokens' places, and where they come from
+        const int64_t to = piece0 * C + tid, j = to - base;
+        const bool moves = j >= 0 && j < n && path[j] != j;
+        const int64_t from = moves ? base + path[j] : 0;
+        const int64_t tb = j < n ? block_of(to) : -1;
+        from_block[tid] = moves && tb >= 0 ? block_of(from) : -1;
+        from_slot[tid] = from & 15;
+        if (tid % C == 0) piece_block[tid / C] = tb;   // (a piece lies in one block)
+    }
+    __syncthreads();
+    for (int q = 0; q < kTokens / C && (piece0 + q) * C < base + n; ++q) {
         bool any = false;
 #pragma unroll
-        for (int e = 0; e < C; ++e) any = any || from_block[e] >= 0;
+        for (int e = 0; e < C; ++e) any = any || from_block[q * C + e] >= 0;
+        const int first_slot = static_cast<int>((piece0 + q) * C & 15);
         uint4 kx[KI], vx[2];
         auto k_item = [&](int i, int& e, int& head, int& at) {
             const int x = tid + 256 * i;
             e = x / (512 / C);
             head = head0 + x % (512 / C) / PIECES;
             at = x % PIECES;
-            return head < hk && from_block[e] >= 0;
+            return head < hk && from_block[q * C + e] >= 0;
         };
         auto v_item = [&](int i, int& head, int64_t& at) {
             const int x = tid + 256 * i;
             head = head0 + x / D;
-            at = ((piece_block + head * pb) * (16 / C) + (piece * C & 15) / C) * D + x % D;
+            at = ((piece_block[q] + head * pb) * (16 / C) + first_slot / C) * D + x % D;
             return any && head < hk;
         };
         int e, head, at;
@@ -278,23 +292,25 @@ __global__ void __launch_bounds__(256) kv_move_kernel(KvMoveParams p) {
 #pragma unroll
         for (int i = 0; i < KI; ++i)
             if (k_item(i, e, head, at))
-                kx[i] = static_cast<const uint4*>(p.cache.k)[((from_block[e] + head * pb) * PIECES + at) * 16 + from_slot[e]];
+                kx[i] = static_cast<const uint4*>(p.cache.k)[((from_block[q * C + e] + head * pb) * PIECES + at) * 16 + from_slot[q * C + e]];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (v_item(i, head, where)) {
                 const int d = (tid + 256 * i) % D;
                 T x[C];
 #pragma unroll
-                for (int c = 0; c < C; ++c)
-                    x[c] = from_block[c] < 0 ? T{0}
-                                             : static_cast<const T*>(p.cache.v)[(((from_block[c] + head * pb) * (16 / C) + from_slot[c] / C) * D + d) * C + from_slot[c] % C];
+                for (int c = 0; c < C; ++c) {
+                    const int64_t fb = from_block[q * C + c];
+                    const int fs = from_slot[q * C + c];
+                    x[c] = fb < 0 ? T{0} : static_cast<const T*>(p.cache.v)[(((fb + head * pb) * (16 / C) + fs / C) * D + d) * C + fs % C];
+                }
                 const uint4 old = static_cast<const uint4*>(p.cache.v)[where];
                 uint32_t w[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const int shift = 8 * E * (c % (4 / E));
                     const uint32_t mask = (E == 1 ? 0xFFu : 0xFFFFu) << shift;
-                    if (from_block[c] >= 0) w[c * E / 4] = (w[c * E / 4] & ~mask) | static_cast<uint32_t>(x[c]) << shift;
+                    if (from_block[q * C + c] >= 0) w[c * E / 4] = (w[c * E / 4] & ~mask) | static_cast<uint32_t>(x[c]) << shift;
                 }
                 vx[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
@@ -302,11 +318,12 @@ __global__ void __launch_bounds__(256) kv_move_kernel(KvMoveParams p) {
 #pragma unroll
         for (int i = 0; i < KI; ++i)
             if (k_item(i, e, head, at))
-                static_cast<uint4*>(p.cache.k)[((to_block[e] + head * pb) * PIECES + at) * 16 + to_slot[e]] = kx[i];
+                static_cast<uint4*>(p.cache.k)[((piece_block[q] + head * pb) * PIECES + at) * 16 + first_slot + e] = kx[i];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (v_item(i, head, where)) static_cast<uint4*>(p.cache.v)[where] = vx[i];
-        __syncthreads();
+    }
+    __syncthreads();
     }
 }
 
