@@ -591,13 +591,32 @@ AttentionPlan make_plan(int64_t B, int hq, int hk, int dim, int64_t max_q, int64
     // tokens that one sequence's rows can see (a window starts at a multiple of 64)
     int64_t span = max_kv;
     if (window > 0 && window + max_q + 64 < span) span = window + max_q + 64;
+    // Splits: 512 workgroups run at a time (two a compute unit).  Of the numbers
+    // that just fill 1 .. 8 such rounds, and none, the one with the least
+    //   rounds (tokens of a split + own cost) + cost of the join,
+    // in tokens: a split writes and reads its rows' fp32 partial results (128
+    // rows: as 1500 tokens), the join is a launch.  (16 trees of 60 nodes, 4000
+    // tokens: one split 119 us, two 138; a chunk of 777 behind 6000: 233, 217,
+    // three 231; 131000 tokens, 64 rows: 64 splits 78 us, 128 86; windows of
+    // 1024: two splits' worth 51 us, five 55.)
+    constexpr int64_t kSlots = 512;
     const int64_t whole = B * hk * pl.tiles;
-    int64_t splits = (1024 + whole - 1) / whole;
-    const int64_t most = (span + 255) / 256;
-    splits = splits < most ? splits : most;
-    splits = splits < 1 ? 1 : splits;
-    int64_t chunk = (span + splits - 1) / splits;
-    chunk = (chunk + 255) / 256 * 256;
+    const int64_t own = pl.tile_rows <= 32 ? 8 * pl.tile_rows : 12 * pl.tile_rows;
+    const int64_t join = pl.tile_rows <= 32 ? 400 : 200;
+    const int64_t step = pl.tile_rows <= 32 ? 256 : 64;   // a multiple of what a workgroup takes at a time
+    int64_t splits = 1, best = (whole + kSlots - 1) / kSlots * (span + own);
+    for (int64_t rounds = 1; rounds <= 8; ++rounds) {
+        int64_t s = rounds * kSlots / whole;
+        const int64_t most = (span + step - 1) / step;
+        if (s > most) s = most;
+        if (s < 2) continue;
+        const int64_t cost = (whole * s + kSlots - 1) / kSlots * ((span + s - 1) / s + own) + join;
+        if (cost < best) {
+            best = cost;
+            splits = s;
+        }
+    }
+    const int64_t chunk = ((span + splits - 1) / splits + step - 1) / step * step;
     pl.chunk = static_cast<int>(chunk);
     pl.splits = static_cast<int>((span + chunk - 1) / chunk);
     if (pl.splits < 1) pl.splits = 1;
