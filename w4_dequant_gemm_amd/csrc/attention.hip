@@ -575,11 +575,11 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttentionParams p, 
 }
 
 // Rows a workgroup holds, by the rows a (sequence, head) has.  Up to 32: the
-// streaming kernel on 16 or 32.  Above: the tile kernel on 128.  256 dims: the
-// wide kernel on 64.
+// streaming kernel on 16 or 32.  Above: the tile kernel on 64 up to 64 rows,
+// else on 128.  256 dims: the wide kernel on 64.
 int rows_per_tile(int dim, int64_t rows) {
     if (dim == 256) return 64;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
 AttentionPlan make_plan(int64_t B, int hq, int hk, int dim, int64_t max_q, int64_t max_kv, int64_t window) {

@@ -42,9 +42,13 @@ __device__ __forceinline__ void wait_loads() {
 
 constexpr int kTableBlocks = 1024;           // 16-token blocks looked up at a time
 
-template <int D, int E>
+// WK = 2: 64 rows a workgroup, and the waves of its two halves take one unit of
+// a stage each; their sums are joined at the end.
+template <int D, int E, int WK>
 __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams p, AttentionPlan pl) {
     constexpr int R = 1, U = 2;              // row blocks a wave, units of 32 tokens a stage
+    constexpr int UW = U / WK;               // units of a stage that a wave takes
+    constexpr int ROWS = 128 / WK;
     constexpr int KS = D / 16;               // operands of K, a unit
     constexpr int DB = D / 32;
     constexpr int KC = D * E / 32;           // 1 KB pieces of K, and of V, a unit
@@ -72,17 +76,18 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
     Sequence s;
     sequence_rows(p, b, s.q0, s.n);
     const int rows = s.n * pl.group;
-    const int tile_row = tile * 128 * R;
+    const int tile_row = tile * ROWS;
     if (tile_row >= rows) return;
     s.len = p.kv_len[b];
     s.len = s.len < 0 ? 0 : s.len > p.max_kv ? p.max_kv : s.len;
     s.past = s.len - s.n;
-    const int row_last = (tile_row + 128 * R < rows ? tile_row + 128 * R : rows) - 1;
+    const int row_last = (tile_row + ROWS < rows ? tile_row + ROWS : rows) - 1;
     int begin, end;
     split_range(p, pl, s, b, split, tile_row / pl.group, row_last / pl.group, begin, end);
 
     // this wave's rows
-    const int row0 = tile_row + wave * 32 * R;
+    const int row0 = tile_row + (wave & (4 / WK - 1)) * 32;
+    const int unit0 = WK == 2 ? wave >> 1 : 0;   // of a stage
     const bool works = row0 < rows;          // the last tile's waves may have none: they only load
     float scale = p.scale * 1.4426950408889634f * (E == 1 ? p.cache.k_scale[head] : 1.0f);
     const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;   // so that the largest score is the largest product
@@ -201,13 +206,15 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
             __syncthreads();
             if (st + 1 < stages) load(st + 1);
             if (!works) continue;
-            const int k0 = from_token + 64 * st;
-            const uint4* at = ring + (st & 1) * STAGE * 64 + lane;
-            float16_t acc[2] = {zero16(), zero16()};
+            const int k0 = from_token + 64 * st + 32 * unit0;
+            const uint4* at = ring + ((st & 1) * STAGE + unit0 * 2 * KC) * 64 + lane;
+            float16_t acc[UW];
+#pragma unroll
+            for (int u = 0; u < UW; ++u) acc[u] = zero16();
 #pragma unroll
             for (int c = 0; c < KC; ++c)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < UW; ++u) {
                     const uint4 x = at[(u * 2 * KC + c) * 64];
                     if constexpr (E == 2) {
                         acc[u] = mfma32(x, Q[0][c], acc[u]);
@@ -222,11 +229,11 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
             uint4 vx[KC];
 #pragma unroll
             for (int c = 0; c < KC; ++c) vx[c] = at[(KC + c) * 64];
-            const bool masked = needs_mask(k0, 64);
+            const bool masked = needs_mask(k0, 32 * UW);
             bool odd = false;
             if (masked) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < UW; ++u) {
                     const uint32_t bits = mask_bits(0, k0 + 32 * u);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
             // the reference is raised where a score exceeds it by more than kRaise
             float top = acc[0][0];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < UW; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) top = __builtin_elementwise_maximum(top, acc[u][i]);
             top *= scale;
@@ -253,9 +260,9 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
                 for (int db = 0; db < DB; ++db) O[0][db] *= fade;
             }
             const float base = ref[0] == -INFINITY ? 0.0f : ref[0];
-            uint4 P[2][2];
+            uint4 P[UW][2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < UW; ++u)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     uint32_t w[4];
@@ -269,7 +276,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
                 }
             auto add_values = [&](auto clean) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < UW; ++u) {
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
                         uint4 x = u == 0 ? vx[c] : at[((u * 2 + 1) * KC + c) * 64];
@@ -297,7 +304,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
 #pragma unroll 1
             for (int u = 0; u < units; ++u) {
                 const int k0 = from_token + 32 * u;
-                if (!needs_mask(k0, 32)) continue;
+                if (!needs_mask(k0, 32) || (WK == 2 && (u & 1) != unit0)) continue;
                 uint32_t bits[R];
 #pragma unroll
                 for (int r = 0; r < R; ++r) bits[r] = mask_bits(r, k0);
@@ -333,6 +340,37 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
         }
     }
 
+    if constexpr (WK == 2) {
+        // the second half's sums pass through the ring to the first half's waves
+        float4_t* shared = reinterpret_cast<float4_t*>(ring) + (wave & 1) * (DB * 4 * 64) + lane;
+        float2_t* stats = reinterpret_cast<float2_t*>(blocks) + (wave & 1) * 64 + lane;
+        __syncthreads();
+        if (wave >= 2) {
+            stats[0] = float2_t{ref[0], sum[0]};
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    shared[(4 * db + q) * 64] = float4_t{O[0][db][4 * q], O[0][db][4 * q + 1], O[0][db][4 * q + 2], O[0][db][4 * q + 3]};
+        }
+        __syncthreads();
+        if (wave >= 2) return;
+        const float2_t other = stats[0];
+        const float now = fmaxf(ref[0], other[0]);
+        // (a half that saw nothing has sums of 0, or of NaN)
+        const float mine = ref[0] == -INFINITY ? 1.0f : exp2_fast(ref[0] - now);
+        const float theirs = other[0] == -INFINITY ? 1.0f : exp2_fast(other[0] - now);
+        ref[0] = now;
+        sum[0] = sum[0] * mine + other[1] * theirs;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4_t x = shared[(4 * db + q) * 64];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) O[0][db][4 * q + i] = O[0][db][4 * q + i] * mine + x[i] * theirs;
+            }
+    }
     if (!works) return;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -352,13 +390,19 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
 
 hipError_t launch_attention_tiles(const AttentionParams& p, const AttentionPlan& pl, unsigned wgs, hipStream_t stream) {
     const dim3 grid(wgs), block(256);
+#define W4_TILES(D, E)                                                                                              \
+    do {                                                                                                            \
+        if (pl.tile_rows == 64) hipLaunchKernelGGL((attention_tile_kernel<D, E, 2>), grid, block, 0, stream, p, pl); \
+        else hipLaunchKernelGGL((attention_tile_kernel<D, E, 1>), grid, block, 0, stream, p, pl);                    \
+    } while (0)
     if (p.cache.e4m3) {
-        if (p.cache.dim == 64) hipLaunchKernelGGL((attention_tile_kernel<64, 1>), grid, block, 0, stream, p, pl);
-        else hipLaunchKernelGGL((attention_tile_kernel<128, 1>), grid, block, 0, stream, p, pl);
+        if (p.cache.dim == 64) W4_TILES(64, 1);
+        else W4_TILES(128, 1);
     } else {
-        if (p.cache.dim == 64) hipLaunchKernelGGL((attention_tile_kernel<64, 2>), grid, block, 0, stream, p, pl);
-        else hipLaunchKernelGGL((attention_tile_kernel<128, 2>), grid, block, 0, stream, p, pl);
+        if (p.cache.dim == 64) W4_TILES(64, 2);
+        else W4_TILES(128, 2);
     }
+#undef W4_TILES
     return hipGetLastError();
 }
 
