@@ -114,6 +114,7 @@ struct Sequence {
     const int32_t* table;
     int last_block;
     bool holes;              // a page of the split's range lies outside the cache
+    bool spread;             // the nodes' positions differ by the window or more
 };
 
 __device__ __forceinline__ void sequence_rows(const AttentionParams& p, int b, int& q0, int& n) {
@@ -139,15 +140,26 @@ __device__ __forceinline__ void split_range(const AttentionParams& p, const Atte
     s.last_block = s.len > 0 ? (s.len - 1) >> 4 : 0;
     s.first = 0;
     int lowest = 0;                          // no row of the tile sees a context token below
+    s.spread = false;
     if (p.window > 0) {
-        int least = s.past;                  // the lowest position
+        int least = s.past, most = s.past + s.n - 1;   // the lowest and highest position
         if (p.positions) {
             least = 0x7FFFFFFF;
-            for (int i = lane; i < s.n; i += 64) least = min(least, p.positions[s.q0 + i]);
+            most = -0x7FFFFFFF;
+            for (int i = lane; i < s.n; i += 64) {
+                const int at = p.positions[s.q0 + i];
+                least = min(least, at);
+                most = max(most, at);
+            }
 #pragma unroll
-            for (int off = 1; off < 64; off <<= 1) least = min(least, __shfl_xor(least, off));
+            for (int off = 1; off < 64; off <<= 1) {
+                least = min(least, __shfl_xor(least, off));
+                most = max(most, __shfl_xor(most, off));
+            }
             least = __builtin_amdgcn_readfirstlane(least);
+            most = __builtin_amdgcn_readfirstlane(most);
         }
+        s.spread = static_cast<int64_t>(most) - least >= p.window;
         lowest = least + (p.positions ? 0 : node_first) - p.window + 1;
         least = least - p.window + 1;
         least = least < s.past ? least : s.past;
@@ -191,7 +203,7 @@ __device__ __forceinline__ uint32_t sees(const AttentionParams& p, const Attenti
         } else {
             nodes = low_bits(node - j0 + 1);
         }
-        if (p.window > 0) {
+        if (s.spread) {
             if (p.positions) {
                 for (int i = c > 0 ? c : 0; i < run && kf + i < s.len; ++i)
                     if (p.positions[s.q0 + j0 + i] < low) nodes &= ~(1u << i);
