@@ -595,29 +595,32 @@ def w4_kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int, *, e4m
             torch.zeros((*lead, 16 // c, head_dim, c), dtype=dtype, device=device))
 
 
-def _cache_arg(fn: str, k, v, k_scale, v_scale, layers: bool = False):
-    """The C description of a cache (k, v) of ``w4_kv_cache``'s shapes, and its (kv_heads, head_dim, page_size)."""
-    shape, sv = k.shape, v.shape
+@functools.lru_cache(maxsize=4096)
+def _cache_geometry(fn: str, shape, sv, dtype, dtype_v, layers: bool):
+    # a function of the arrays' shapes and types only: the tail of _KvCache
     n = len(shape)
     if n != 6 and not (layers and n == 7):
         raise ValueError(f"{fn}: k_cache must be [pages, kv_heads, page_size/16, head_dim/c, 16, c]"
                          f"{' or have the layers first' if layers else ''}, got {tuple(shape)}")
     pages, heads, blocks, chunks, rows, c = shape[-6:]
-    one_byte = k.element_size() == 1
+    one_byte = dtype.itemsize == 1
     if rows != 16 or c != (16 if one_byte else 8):
-        raise ValueError(f"{fn}: k_cache of {k.dtype} must end in [head_dim/{16 if one_byte else 8}, 16, "
+        raise ValueError(f"{fn}: k_cache of {dtype} must end in [head_dim/{16 if one_byte else 8}, 16, "
                          f"{16 if one_byte else 8}], got {tuple(shape)}")
-    if not one_byte and k.dtype != torch.bfloat16:
-        raise ValueError(f"{fn}: the cache must be bf16 or hold one byte per element, got {k.dtype}")
-    if v.dtype != k.dtype or tuple(sv) != (*shape[:-3], 16 // c, chunks * c, c):
-        raise ValueError(f"{fn}: v_cache {tuple(sv)} of {v.dtype} does not belong to k_cache {tuple(shape)} of {k.dtype}")
-    for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if s is not None and s.numel() != heads:
-            raise ValueError(f"{fn}: {name} has {s.numel()} elements, expected {heads}")
-    a = _KvCache(_dev(k, "k_cache"), _dev(v, "v_cache"), _dev(k_scale, "k_scale", torch.float32),
-                 _dev(v_scale, "v_scale", torch.float32), pages, shape[0] if n == 7 else 1, heads, chunks * c,
-                 16 * blocks, 1 if one_byte else 0)
-    return a, heads, chunks * c, 16 * blocks
+    if not one_byte and dtype != torch.bfloat16:
+        raise ValueError(f"{fn}: the cache must be bf16 or hold one byte per element, got {dtype}")
+    if dtype_v != dtype or tuple(sv) != (*shape[:-3], 16 // c, chunks * c, c):
+        raise ValueError(f"{fn}: v_cache {tuple(sv)} of {dtype_v} does not belong to k_cache {tuple(shape)} of {dtype}")
+    return pages, shape[0] if n == 7 else 1, heads, chunks * c, 16 * blocks, 1 if one_byte else 0
+
+
+def _cache_arg(fn: str, k, v, k_scale, v_scale, layers: bool = False):
+    """The C description of a cache (k, v) of ``w4_kv_cache``'s shapes, and its (kv_heads, head_dim)."""
+    geometry = _cache_geometry(fn, k.shape, v.shape, k.dtype, v.dtype, layers)
+    heads = geometry[2]
+    a = _KvCache(_dev(k, "k_cache"), _dev(v, "v_cache"), _vec(fn, k_scale, "k_scale", heads, torch.float32),
+                 _vec(fn, v_scale, "v_scale", heads, torch.float32), *geometry)
+    return a, heads, geometry[3]
 
 
 def _rows_arg(fn: str, x, name: str, heads: int, dim: int, T=None):
@@ -650,7 +653,7 @@ def w4_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, sl
     values ``v`` go to the cache slots ``slots`` (int32 [T], negative: not stored), the queries are returned
     (bf16 [T, Hq, D]; None without ``q``).  ``rope`` is fp32 [positions, rot]: rot/2 cosines, then the sines."""
     fn = "w4_kv_append"
-    cache, hk, dim, _ = _cache_arg(fn, k_cache, v_cache, k_scale, v_scale)
+    cache, hk, dim = _cache_arg(fn, k_cache, v_cache, k_scale, v_scale)
     T = k.shape[0]
     kp, ks = _rows_arg(fn, k, "k", hk, dim, T)
     vp, vs = _rows_arg(fn, v, "v", hk, dim, T)
@@ -693,7 +696,7 @@ def w4_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     [T, ceil(max_q / 64)] masks of the nodes each node sees; None: a chain.  ``window`` > 0 needs ``positions``
     (int32 [T]) with a tree.  Returns bf16 [T, Hq, D]."""
     fn = "w4_tree_attention"
-    cache, hk, dim, page_size = _cache_arg(fn, k_cache, v_cache, k_scale, v_scale)
+    cache, hk, dim = _cache_arg(fn, k_cache, v_cache, k_scale, v_scale)
     T, Hq = (q.shape[0], q.shape[1]) if q.dim() == 3 else (0, 0)
     qp, qs = _rows_arg(fn, q, "q", Hq, dim)
     if page_table.dim() != 2:
@@ -768,7 +771,7 @@ def w4_kv_move(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.T
     """Token base[b] + path[b, j] of sequence b moves to base[b] + j for j < count[b] (int32, path rows strictly
     ascending), in every layer of the cache ([layers, ...] or one layer)."""
     fn = "w4_kv_move"
-    cache, _, _, _ = _cache_arg(fn, k_cache, v_cache, None, None, layers=True)
+    cache, _, _ = _cache_arg(fn, k_cache, v_cache, None, None, layers=True)
     if page_table.dim() != 2 or path.dim() != 2 or path.shape[0] != page_table.shape[0]:
         raise ValueError(f"{fn}: page_table must be [B, pages] and path [B, length], got {tuple(page_table.shape)} and "
                          f"{tuple(path.shape)}")
