@@ -28,7 +28,7 @@ namespace {
 using namespace attn;
 
 // R tiles of 16 rows of one wavefront: their queries, running sums, and the
-// work of a step of U units.
+// work of a step of one unit.
 template <int D, int E, int R>
 struct Core {
     static constexpr int S = 64 / E;         // tokens a unit
@@ -86,23 +86,21 @@ struct Core {
         }
     }
 
-    // Tokens k0 .. k0 + U S - 1: kget(u, i) and vget(u, dt) give the lane's
-    // 16-byte pieces of unit u (i = tile * KP + piece); keys_done is called
-    // when the K pieces are used up.  OWN: V's pieces are the wave's own
-    // registers, vown[dt].
-    template <int U, bool OWN, class KGet, class VGet, class Done>
+    // Tokens k0 .. k0 + S - 1: kget(i) and vget(dt) give the lane's 16-byte
+    // pieces (i = tile * KP + piece); keys_done is called when the K pieces are
+    // used up.  OWN: V's pieces are the wave's own registers, vown[dt].
+    template <bool OWN, class KGet, class VGet, class Done>
     __device__ __forceinline__ void step(const AttentionParams& p, const AttentionPlan& pl, const Sequence& s, int k0,
                                          KGet kget, VGet vget, Done keys_done, uint4* vown) {
         const int g = (threadIdx.x & 63) >> 4;
-        constexpr int N = U * NT;
-        float4_t acc[R][N];
+        float4_t acc[R][NT];
 #pragma unroll
-        for (int t = 0; t < N; ++t) {
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int r = 0; r < R; ++r) acc[r][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < KP; ++i) {
-                const uint4 c = kget(t / NT, (t % NT) * KP + i);
+                const uint4 c = kget(t * KP + i);
                 if constexpr (E == 2) {
 #pragma unroll
                     for (int r = 0; r < R; ++r) acc[r][t] = mfma(c, Q[r][i], acc[r][t]);
@@ -119,17 +117,15 @@ struct Core {
 
         keys_done();
 
-        const bool masked = needs_mask(s, k0, U * S);
+        const bool masked = needs_mask(s, k0);
         if (masked) {
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r) {
+                const uint32_t seen = live[r] ? sees(p, pl, s, node[r], low[r], k0 + (S / 4) * g, S / 4) : 0;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const uint32_t seen = live[r] ? sees(p, pl, s, node[r], low[r], k0 + u * S + (S / 4) * g, S / 4) : 0;
-#pragma unroll
-                    for (int i = 0; i < 4 * NT; ++i)
-                        if (!((seen >> i) & 1)) acc[r][u * NT + (i >> 2)][i & 3] = -INFINITY;
-                }
+                for (int i = 0; i < 4 * NT; ++i)
+                    if (!((seen >> i) & 1)) acc[r][i >> 2][i & 3] = -INFINITY;
+            }
         }
         float top[R];
         bool raise = false;
@@ -137,7 +133,7 @@ struct Core {
         for (int r = 0; r < R; ++r) {
             top[r] = -INFINITY;
 #pragma unroll
-            for (int t = 0; t < N; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int j = 0; j < 4; j += 2) top[r] = fmaxf(top[r], fmaxf(acc[r][t][j], acc[r][t][j + 1]));
             top[r] *= scale;
@@ -154,12 +150,12 @@ struct Core {
                 for (int dt = 0; dt < DT; ++dt) O[r][dt] *= fade;
             }
         }
-        uint4 P[R][U * NP];
+        uint4 P[R][NP];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float base = ref[r] == -INFINITY ? 0.0f : ref[r];
 #pragma unroll
-            for (int q = 0; q < U * NP; ++q) {
+            for (int q = 0; q < NP; ++q) {
                 float e[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) e[i] = exp2_fast(__builtin_fmaf(acc[r][2 * q + (i >> 2)][i & 3], scale, -base));
@@ -171,19 +167,17 @@ struct Core {
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int q = 0; q < U * NP; ++q) L[r] = mfma(ones, P[r][q], L[r]);
+            for (int q = 0; q < NP; ++q) L[r] = mfma(ones, P[r][q], L[r]);
 
-        auto operands = [&](int u, int dt, uint4 (&V)[NP]) {
-            const uint4 c = vget(u, dt);
+        auto operands = [&](int dt, uint4 (&V)[NP]) {
+            const uint4 c = vget(dt);
             if constexpr (E == 2) V[0] = c;
             else widen16(c, V[0], V[NP - 1]);
         };
         bool odd = false;
         if (masked) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) odd = odd || nonfinite<E>(vget(u, dt));
+            for (int dt = 0; dt < DT; ++dt) odd = odd || nonfinite<E>(vget(dt));
             odd = __any(odd);
         }
         if (odd) {
@@ -198,38 +192,34 @@ struct Core {
         }
         if (odd && !OWN) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int dt = 0; dt < DT; ++dt) {
+                uint4 V[NP];
+                operands(dt, V);
 #pragma unroll
-                for (int dt = 0; dt < DT; ++dt) {
-                    uint4 V[NP];
-                    operands(u, dt, V);
+                for (int q = 0; q < NP; ++q) {
+                    uint4 plus, minus;
+                    const uint4 fine = finite_part(V[q], plus, minus);
 #pragma unroll
-                    for (int q = 0; q < NP; ++q) {
-                        uint4 plus, minus;
-                        const uint4 fine = finite_part(V[q], plus, minus);
-#pragma unroll
-                        for (int r = 0; r < R; ++r) O[r][dt] = mfma(fine, P[r][u * NP + q], O[r][dt]);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);   // registers are scarcer than time here
+                    for (int r = 0; r < R; ++r) O[r][dt] = mfma(fine, P[r][q], O[r][dt]);
                 }
+                __builtin_amdgcn_sched_barrier(0);   // registers are scarcer than time here
+            }
         } else {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int dt = 0; dt < DT; ++dt) {
+                uint4 V[NP];
+                operands(dt, V);
 #pragma unroll
-                for (int dt = 0; dt < DT; ++dt) {
-                    uint4 V[NP];
-                    operands(u, dt, V);
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int q = 0; q < NP; ++q) O[r][dt] = mfma(V[q], P[r][u * NP + q], O[r][dt]);
-                }
+                    for (int q = 0; q < NP; ++q) O[r][dt] = mfma(V[q], P[r][q], O[r][dt]);
+            }
         }
     }
 
     // Whether a unit at k0 needs the rows' masks.
-    __device__ __forceinline__ bool needs_mask(const Sequence& s, int k0, int tokens) const {
-        return s.holes || k0 + tokens > (s.past < s.len ? s.past : s.len) || k0 < low_most;
+    __device__ __forceinline__ bool needs_mask(const Sequence& s, int k0) const {
+        return s.holes || k0 + S > (s.past < s.len ? s.past : s.len) || k0 < low_most;
     }
 
     // The infinities and NaN that step() left out of the units k0, k0 + stride,
@@ -240,7 +230,7 @@ struct Core {
         const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
 #pragma unroll 1
         for (; k0 < end; k0 += stride) {
-            if (!needs_mask(s, k0, S)) continue;
+            if (!needs_mask(s, k0)) continue;
             const int blk = min((k0 >> 4) + (g * BPU >> 2), s.last_block);
             int64_t page = s.table[page_of(p, pl, blk)];
             page = page < 0 || page >= p.cache.pages ? 0 : page;
@@ -287,25 +277,21 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(AttentionParam
     const int m = lane & 15, g = lane >> 4;
     const int hk = p.cache.heads, pb = p.cache.page_blocks;
     int id = blockIdx.x;
-    const int tile = id % pl.tiles;
-    id /= pl.tiles;
     const int split = id % pl.splits;
     id /= pl.splits;
     const int head = id % hk, b = id / hk;
 
     Sequence s;
     sequence_rows(p, b, s.q0, s.n);
-    const int rows = s.n * pl.group;
-    const int tile_row = tile * 16 * R;
-    if (tile_row >= rows) return;
+    const int rows = s.n * pl.group;         // 16 R at most
+    if (rows == 0) return;
     s.len = p.kv_len[b];
     s.len = s.len < 0 ? 0 : s.len > p.max_kv ? p.max_kv : s.len;
     s.past = s.len - s.n;
-    const int row_last = (tile_row + 16 * R < rows ? tile_row + 16 * R : rows) - 1;
     int begin, end;
-    split_range(p, pl, s, b, split, tile_row / pl.group, row_last / pl.group, begin, end);
+    split_range(p, pl, s, b, split, 0, s.n - 1, begin, end);
     C c;
-    c.init(p, pl, s, head, tile_row, rows);
+    c.init(p, pl, s, head, 0, rows);
 
     uint4 kx[C::NT * C::KP], vx[DT];         // the pieces of the step
     auto k_block = [&](int st) { return min(st * C::BPU + (m * C::BPU >> 4), s.last_block); };
@@ -344,8 +330,8 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(AttentionParam
             const int next = st + WK;
             const bool more = next * S < end;
             const int kp2 = k_page(next + WK), vp2 = v_page(next + WK);
-            c.template step<1, true>(p, pl, s, st * S, [&](int, int i) { return kx[i]; }, [&](int, int dt) { return vx[dt]; },
-                               [&] { if (more) load_k(next, kp); }, vx);
+            c.template step<true>(p, pl, s, st * S, [&](int i) { return kx[i]; }, [&](int dt) { return vx[dt]; },
+                                  [&] { if (more) load_k(next, kp); }, vx);
             if (!more) break;
             load_v(next, vp);
             kp = kp2;
@@ -385,7 +371,7 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(AttentionParam
         __syncthreads();
         for (int u = threadIdx.x; u < DQ * 4 * 16 * R; u += 256) {
             const int lr = u / (DQ * 4), d4 = u - lr * (DQ * 4);
-            if (tile_row + lr >= rows) continue;
+            if (lr >= rows) continue;
             float top = sm_ref[0][lr];
 #pragma unroll
             for (int w = 1; w < WK; ++w) top = fmaxf(top, sm_ref[w][lr]);
@@ -398,25 +384,26 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(AttentionParam
                 total += sm_sum[w][lr] * (t == -INFINITY ? 1.0f : exp2_fast(t - top));
                 o += sm_o[w][d4][lr];
             }
-            put<D, E>(p, pl, s.q0, head, split, tile_row + lr, quarter * (D / 4) + 4 * d4, o, top, total);
+            put<D, E>(p, pl, s.q0, head, split, lr, quarter * (D / 4) + 4 * d4, o, top, total);
         }
     }
 }
 
 // Heads of 256 dims, whose pieces and sums do not fit a wave's registers in
-// the other forms: each of four waves has R tiles of its own, and the tokens'
+// the other forms: each of four waves has a tile of 16 rows, and the tokens'
 // pieces pass through shared memory once for the workgroup, in the order in which the
 // operands are read (one linear 1 KB a piece and wavefront: no bank is asked
-// twice).  Two stages: the loads of the next KT tokens go straight to shared
-// memory while the present ones are used, one barrier a stage.
-template <int D, int E, int R, int KT>
+// twice).  Two stages of 32 KB: the loads of the next unit go straight to shared
+// memory while the present one is used, one barrier a stage.  (On 32 x 32
+// products as in attention_tile.hip the sums spill: 24 trees of 17 nodes, window
+// 1024, E4M3: 54 us against 48.)
+template <int D, int E>
 __global__ void __launch_bounds__(256, 2) attention_wide_kernel(AttentionParams p, AttentionPlan pl) {
-    using C = Core<D, E, R>;
-    constexpr int S = C::S, U = KT / S, DT = C::DT;
-    constexpr int PER = D / 16;              // 1 KB pieces of K, and of V, a unit
-    constexpr int STAGE = 2 * U * PER;
+    using C = Core<D, E, 1>;
+    constexpr int S = C::S, DT = C::DT;
+    constexpr int PER = D / 16;              // 1 KB pieces of K, and of V
+    constexpr int STAGE = 2 * PER;
     constexpr int MINE = STAGE / 4;          // pieces a wave loads
-    static_assert(U == 1 || U == 2, "a wave loads pieces of one unit and kind");
     __shared__ __attribute__((aligned(16))) uint4 stage0[STAGE * 64];
     __shared__ __attribute__((aligned(16))) uint4 stage1[STAGE * 64];
     const int lane = threadIdx.x & 63;
@@ -438,24 +425,21 @@ __global__ void __launch_bounds__(256, 2) attention_wide_kernel(AttentionParams 
     Sequence s;
     sequence_rows(p, b, s.q0, s.n);
     const int rows = s.n * pl.group;
-    const int tile_row = tile * 64 * R;
+    const int tile_row = tile * 64;
     if (tile_row >= rows) return;
     s.len = p.kv_len[b];
     s.len = s.len < 0 ? 0 : s.len > p.max_kv ? p.max_kv : s.len;
     s.past = s.len - s.n;
-    const int row_last = (tile_row + 64 * R < rows ? tile_row + 64 * R : rows) - 1;
+    const int row_last = (tile_row + 64 < rows ? tile_row + 64 : rows) - 1;
     int begin, end;
     split_range(p, pl, s, b, split, tile_row / pl.group, row_last / pl.group, begin, end);
     C c;
-    c.init(p, pl, s, head, tile_row + wave * 16 * R, rows);
+    c.init(p, pl, s, head, tile_row + wave * 16, rows);
 
-    // this wave's pieces of a stage: K or V of one unit, or half of them
-    const int unit = U == 2 ? wave >> 1 : 0;
-    const bool values = U == 2 ? wave & 1 : wave >> 1;
-    const int part = U == 2 ? 0 : (wave & 1) * MINE;
-    auto block = [&](int k0) {
-        return min((k0 >> 4) + unit * C::BPU + (values ? g * C::BPU >> 2 : m * C::BPU >> 4), s.last_block);
-    };
+    // this wave's pieces of a stage: half of K's or of V's
+    const bool values = wave >> 1;
+    const int part = (wave & 1) * MINE;
+    auto block = [&](int k0) { return min((k0 >> 4) + (values ? g * C::BPU >> 2 : m * C::BPU >> 4), s.last_block); };
     auto page_at = [&](int k0) { return s.table[page_of(p, pl, block(k0))]; };
     auto load = [&](uint4* stage, int k0, int page) {
         page = page < 0 || page >= p.cache.pages ? 0 : page;
@@ -465,7 +449,7 @@ __global__ void __launch_bounds__(256, 2) attention_wide_kernel(AttentionParams 
         src += values ? (E == 2 ? (g & 1) * (16 * D) : 0) + m * 16 : g * 256;
 #pragma unroll
         for (int i = 0; i < MINE; ++i) {
-            const int x = part + i;          // of the unit's pieces of this kind
+            const int x = part + i;
             const int t = x / C::KP;
             const uint8_t* from = src + (values ? x * 256
                                                 : (((S / 4) * (m >> 2) + 4 * t + (m & 3)) & 15) * 16 + (x - t * C::KP) * 1024);
@@ -474,44 +458,41 @@ __global__ void __launch_bounds__(256, 2) attention_wide_kernel(AttentionParams 
             // at the stage's end; a load the compiler does not know of only
             // makes its own waits stricter.
             const uint32_t m0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
-                reinterpret_cast<uintptr_t>(stage + ((unit * 2 + (values ? 1 : 0)) * PER + x) * 64)));
+                reinterpret_cast<uintptr_t>(stage + ((values ? PER : 0) + x) * 64)));
             asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(m0) : "memory", "m0");
         }
     };
     auto compute = [&](const uint4* stage, int k0) {
-        c.template step<U, false>(p, pl, s, k0, [&](int u, int i) { return stage[(u * 2 * PER + i) * 64 + lane]; },
-                           [&](int u, int dt) { return stage[((u * 2 + 1) * PER + dt) * 64 + lane]; }, [] {}, nullptr);
+        c.template step<false>(p, pl, s, k0, [&](int i) { return stage[i * 64 + lane]; },
+                               [&](int dt) { return stage[(PER + dt) * 64 + lane]; }, [] {}, nullptr);
     };
 
     if (begin < end) {
         int k0 = begin;
         load(stage0, k0, page_at(k0));
-        int page = page_at(k0 + KT);
+        int page = page_at(k0 + S);
         while (true) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             __syncthreads();
-            if (k0 + KT < end) load(stage1, k0 + KT, page);
-            page = page_at(k0 + 2 * KT);
+            if (k0 + S < end) load(stage1, k0 + S, page);
+            page = page_at(k0 + 2 * S);
             compute(stage0, k0);
-            k0 += KT;
+            k0 += S;
             if (k0 >= end) break;
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             __syncthreads();
-            if (k0 + KT < end) load(stage0, k0 + KT, page);
-            page = page_at(k0 + 2 * KT);
+            if (k0 + S < end) load(stage0, k0 + S, page);
+            page = page_at(k0 + 2 * S);
             compute(stage1, k0);
-            k0 += KT;
+            k0 += S;
             if (k0 >= end) break;
         }
         if (c.repairs) c.repair(p, pl, s, head, begin, S, end);
     }
+    if (!c.live[0]) return;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (!c.live[r]) continue;
-        const int row = tile_row + wave * 16 * R + 16 * r + m;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) put<D, E>(p, pl, s.q0, head, split, row, 16 * dt + 4 * g, c.O[r][dt], c.ref[r], c.L[r][0]);
-    }
+    for (int dt = 0; dt < DT; ++dt)
+        put<D, E>(p, pl, s.q0, head, split, tile_row + wave * 16 + m, 16 * dt + 4 * g, c.O[0][dt], c.ref[0], c.L[0][0]);
 }
 
 // The splits of a row joined, in a fixed order: `parts` threads for each four
@@ -627,12 +608,12 @@ template <int D, int E>
 hipError_t launch_kind(const AttentionParams& p, const AttentionPlan& pl, hipStream_t stream) {
     const int64_t groups = static_cast<int64_t>(pl.splits) * p.cache.heads * p.B;
     const bool tiled = pl.tile_rows > 32;
-    const int64_t wgs = tiled ? (groups + 7) / 8 * 8 * pl.tiles : groups * pl.tiles;
+    const int64_t wgs = tiled ? (groups + 7) / 8 * 8 * pl.tiles : groups;
     if (wgs > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(wgs);
     if constexpr (D == 256) {
         // 64 KB of shared memory: two workgroups a compute unit
-        hipLaunchKernelGGL((attention_wide_kernel<D, E, 1, E == 2 ? 32 : 64>), dim3(grid), dim3(256), 0, stream, p, pl);
+        hipLaunchKernelGGL((attention_wide_kernel<D, E>), dim3(grid), dim3(256), 0, stream, p, pl);
     } else if (tiled) {
         const hipError_t e = launch_attention_tiles(p, pl, grid, stream);
         if (e != hipSuccess) return e;

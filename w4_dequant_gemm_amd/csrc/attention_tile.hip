@@ -46,7 +46,7 @@ constexpr int kTableBlocks = 1024;           // 16-token blocks looked up at a t
 // a stage each; their sums are joined at the end.
 template <int D, int E, int WK>
 __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams p, AttentionPlan pl) {
-    constexpr int R = 1, U = 2;              // row blocks a wave, units of 32 tokens a stage
+    constexpr int U = 2;                     // units of 32 tokens a stage
     constexpr int UW = U / WK;               // units of a stage that a wave takes
     constexpr int ROWS = 128 / WK;
     constexpr int KS = D / 16;               // operands of K, a unit
@@ -92,42 +92,34 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
     float scale = p.scale * 1.4426950408889634f * (E == 1 ? p.cache.k_scale[head] : 1.0f);
     const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;   // so that the largest score is the largest product
     scale = fmaxf(fabsf(scale), 1.17549435e-38f);
-    uint4 Q[R][KS];
-    float16_t O[R][DB];
-    float ref[R], sum[R];                    // sum: of this half's p
-    int node[R], low[R];
-    bool live[R];
-    int low_most = 0;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int row = row0 + 32 * r + m;
-        live[r] = row < rows;
-        const int at = live[r] ? row : rows - 1;
-        node[r] = at / pl.group;
-        const int qh = head * pl.group + (at - node[r] * pl.group);
-        const uint16_t* q = p.q + static_cast<int64_t>(s.q0 + node[r]) * p.q_stride + static_cast<int64_t>(qh) * D;
-        const int pos = p.positions ? p.positions[s.q0 + node[r]] : s.past + node[r];
-        low[r] = p.window > 0 ? pos - p.window + 1 : 0;
-        low_most = low[r] > low_most ? low[r] : low_most;
+    uint4 Q[KS];
+    float16_t O[DB];
+    float ref = -INFINITY, sum = 0.0f;       // sum: of this half's p
+    const bool live = row0 + m < rows;
+    const int node = (live ? row0 + m : rows - 1) / pl.group;
+    const int pos = p.positions ? p.positions[s.q0 + node] : s.past + node;
+    const int low = p.window > 0 ? pos - p.window + 1 : 0;
+    int low_most = low > 0 ? low : 0;
+    {
+        const int qh = head * pl.group + (live ? row0 + m : rows - 1) - node * pl.group;
+        const uint16_t* q = p.q + static_cast<int64_t>(s.q0 + node) * p.q_stride + static_cast<int64_t>(qh) * D;
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
             // dims of operand i in half h, as K's pieces hold them
             const int d = E == 2 ? 16 * i + 8 * h : 32 * (i >> 1) + 16 * h + 8 * (i & 1);
             const uint4 v = *reinterpret_cast<const uint4*>(q + d);
-            Q[r][i] = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+            Q[i] = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
         }
-        ref[r] = -INFINITY;
-        sum[r] = 0.0f;
-#pragma unroll
-        for (int db = 0; db < DB; ++db) O[r][db] = zero16();
     }
+#pragma unroll
+    for (int db = 0; db < DB; ++db) O[db] = zero16();
     if (p.window > 0) {
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) low_most = max(low_most, __shfl_xor(low_most, off));
         low_most = __builtin_amdgcn_readfirstlane(low_most);
     }
 
-    // this wave's pieces of a stage: K or V of one unit, or half of them
+    // this wave's pieces of a stage: K or V of one unit
     const int my_unit = wave >> 1;
     const bool values = wave & 1;
     // the token of K's row m in a unit, and the block of this lane's pieces
@@ -168,11 +160,11 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
             pieces(block(lane_block), to, std::integral_constant<int, KC>{});
         }
     };
-    auto mask_bits = [&](int r, int k0) -> uint32_t {
-        if (!live[r]) return 0u;
+    auto mask_bits = [&](int k0) -> uint32_t {
+        if (!live) return 0u;
         if (E == 2)
-            return sees(p, pl, s, node[r], low[r], k0 + 8 * h, 8) | sees(p, pl, s, node[r], low[r], k0 + 16 + 8 * h, 8) << 8;
-        return sees(p, pl, s, node[r], low[r], k0 + 16 * h, 16);
+            return sees(p, pl, s, node, low, k0 + 8 * h, 8) | sees(p, pl, s, node, low, k0 + 16 + 8 * h, 8) << 8;
+        return sees(p, pl, s, node, low, k0 + 16 * h, 16);
     };
     // tokens [plain, plain_end) are seen by all rows of the wave
     const int plain = low_most;
@@ -193,6 +185,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
             const int64_t page = s.table[pg];
             blocks[i] = page < 0 || page >= p.cache.pages ? -1
                                                           : static_cast<int>((page * hk + head) * pb + (blk - pg * pb));
+            // (2^31 blocks of at least 1 KB are more than the memory holds)
         }
         // every load the compiler knows of is done before the first it does not
         wait_loads<0>();
@@ -217,12 +210,12 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
                 for (int u = 0; u < UW; ++u) {
                     const uint4 x = at[(u * 2 * KC + c) * 64];
                     if constexpr (E == 2) {
-                        acc[u] = mfma32(x, Q[0][c], acc[u]);
+                        acc[u] = mfma32(x, Q[c], acc[u]);
                     } else {
                         uint4 lo, hi;
                         widen16(x, lo, hi);
-                        acc[u] = mfma32(lo, Q[0][2 * c], acc[u]);
-                        acc[u] = mfma32(hi, Q[0][2 * c + 1], acc[u]);
+                        acc[u] = mfma32(lo, Q[2 * c], acc[u]);
+                        acc[u] = mfma32(hi, Q[2 * c + 1], acc[u]);
                     }
                 }
             // the first unit's values on their way under the exponentials
@@ -234,7 +227,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
             if (masked) {
 #pragma unroll
                 for (int u = 0; u < UW; ++u) {
-                    const uint32_t bits = mask_bits(0, k0 + 32 * u);
+                    const uint32_t bits = mask_bits(k0 + 32 * u);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (!((bits >> i) & 1)) acc[u][i] = -INFINITY;
@@ -251,15 +244,15 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
 #pragma unroll
                 for (int i = 0; i < 16; ++i) top = __builtin_elementwise_maximum(top, acc[u][i]);
             top *= scale;
-            if (__any(top > ref[0] + kRaise)) {
-                const float now = fmaxf(ref[0], max_halves(top));
-                const float fade = now == -INFINITY ? 1.0f : exp2_fast(ref[0] - now);
-                ref[0] = now;
-                sum[0] *= fade;
+            if (__any(top > ref + kRaise)) {
+                const float now = fmaxf(ref, max_halves(top));
+                const float fade = now == -INFINITY ? 1.0f : exp2_fast(ref - now);
+                ref = now;
+                sum *= fade;
 #pragma unroll
-                for (int db = 0; db < DB; ++db) O[0][db] *= fade;
+                for (int db = 0; db < DB; ++db) O[db] *= fade;
             }
-            const float base = ref[0] == -INFINITY ? 0.0f : ref[0];
+            const float base = ref == -INFINITY ? 0.0f : ref;
             uint4 P[UW][2];
 #pragma unroll
             for (int u = 0; u < UW; ++u)
@@ -270,7 +263,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
                     for (int i = 0; i < 4; ++i) {
                         w[i] = pack_bf16x2(exp2_fast(__builtin_fmaf(acc[u][8 * j + 2 * i], scale, -base)),
                                            exp2_fast(__builtin_fmaf(acc[u][8 * j + 2 * i + 1], scale, -base)));
-                        sum[0] = dot2_bf16(w[i], 0x3F803F80u, sum[0]);   // of the rounded p
+                        sum = dot2_bf16(w[i], 0x3F803F80u, sum);   // of the rounded p
                     }
                     P[u][j] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
@@ -282,12 +275,12 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
                         uint4 x = u == 0 ? vx[c] : at[((u * 2 + 1) * KC + c) * 64];
                         if constexpr (decltype(clean)::value) x = finite_piece<E>(x);
                         if constexpr (E == 2) {
-                            O[0][c % DB] = mfma32(x, P[u][c / DB], O[0][c % DB]);
+                            O[c % DB] = mfma32(x, P[u][c / DB], O[c % DB]);
                         } else {
                             uint4 lo, hi;
                             widen16(x, lo, hi);
-                            O[0][c] = mfma32(lo, P[u][0], O[0][c]);
-                            O[0][c] = mfma32(hi, P[u][1], O[0][c]);
+                            O[c] = mfma32(lo, P[u][0], O[c]);
+                            O[c] = mfma32(hi, P[u][1], O[c]);
                         }
                     }
                 }
@@ -305,9 +298,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
             for (int u = 0; u < units; ++u) {
                 const int k0 = from_token + 32 * u;
                 if (!needs_mask(k0, 32) || (WK == 2 && (u & 1) != unit0)) continue;
-                uint32_t bits[R];
-#pragma unroll
-                for (int r = 0; r < R; ++r) bits[r] = mask_bits(r, k0);
+                const uint32_t bits = mask_bits(k0);
 #pragma unroll
                 for (int db = 0; db < DB; ++db)
 #pragma unroll
@@ -324,17 +315,14 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
                         }
                         uint4 plus, minus;
                         finite_part(x, plus, minus);
+                        const uint4 one = ones_at(bits >> (8 * j));
+                        const float16_t a = mfma32(plus, one, zero16());
 #pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            const uint4 one = ones_at(bits[r] >> (8 * j));
-                            const float16_t a = mfma32(plus, one, zero16());
+                        for (int i = 0; i < 16; ++i) O[db][i] += a[i] > 0.0f ? INFINITY : 0.0f;
+                        const float16_t z = mfma32(minus, one, zero16());
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) O[r][db][i] += a[i] > 0.0f ? INFINITY : 0.0f;
-                            const float16_t z = mfma32(minus, one, zero16());
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) O[r][db][i] += z[i] > 0.0f ? -INFINITY : 0.0f;
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
+                        for (int i = 0; i < 16; ++i) O[db][i] += z[i] > 0.0f ? -INFINITY : 0.0f;
+                        __builtin_amdgcn_sched_barrier(0);
                     }
             }
         }
@@ -346,44 +334,40 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
         float2_t* stats = reinterpret_cast<float2_t*>(blocks) + (wave & 1) * 64 + lane;
         __syncthreads();
         if (wave >= 2) {
-            stats[0] = float2_t{ref[0], sum[0]};
+            stats[0] = float2_t{ref, sum};
 #pragma unroll
             for (int db = 0; db < DB; ++db)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    shared[(4 * db + q) * 64] = float4_t{O[0][db][4 * q], O[0][db][4 * q + 1], O[0][db][4 * q + 2], O[0][db][4 * q + 3]};
+                    shared[(4 * db + q) * 64] = float4_t{O[db][4 * q], O[db][4 * q + 1], O[db][4 * q + 2], O[db][4 * q + 3]};
         }
         __syncthreads();
         if (wave >= 2) return;
         const float2_t other = stats[0];
-        const float now = fmaxf(ref[0], other[0]);
+        const float now = fmaxf(ref, other[0]);
         // (a half that saw nothing has sums of 0, or of NaN)
-        const float mine = ref[0] == -INFINITY ? 1.0f : exp2_fast(ref[0] - now);
+        const float mine = ref == -INFINITY ? 1.0f : exp2_fast(ref - now);
         const float theirs = other[0] == -INFINITY ? 1.0f : exp2_fast(other[0] - now);
-        ref[0] = now;
-        sum[0] = sum[0] * mine + other[1] * theirs;
+        ref = now;
+        sum = sum * mine + other[1] * theirs;
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float4_t x = shared[(4 * db + q) * 64];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) O[0][db][4 * q + i] = O[0][db][4 * q + i] * mine + x[i] * theirs;
+                for (int i = 0; i < 4; ++i) O[db][4 * q + i] = O[db][4 * q + i] * mine + x[i] * theirs;
             }
     }
     if (!works) return;
+    const float total = sum + __shfl_xor(sum, 32);
+    if (!live) return;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const float total = sum[r] + __shfl_xor(sum[r], 32);
-        if (!live[r]) continue;
-        const int row = row0 + 32 * r + m;
+    for (int db = 0; db < DB; ++db)
 #pragma unroll
-        for (int db = 0; db < DB; ++db)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                put<D, E>(p, pl, s.q0, head, split, row, 32 * db + 8 * q + 4 * h,
-                          float4_t{O[r][db][4 * q], O[r][db][4 * q + 1], O[r][db][4 * q + 2], O[r][db][4 * q + 3]}, ref[r], total);
-    }
+        for (int q = 0; q < 4; ++q)
+            put<D, E>(p, pl, s.q0, head, split, row0 + m, 32 * db + 8 * q + 4 * h,
+                      float4_t{O[db][4 * q], O[db][4 * q + 1], O[db][4 * q + 2], O[db][4 * q + 3]}, ref, total);
 }
 
 }  // namespace

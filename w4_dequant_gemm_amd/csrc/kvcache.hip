@@ -258,72 +258,72 @@ __global__ void __launch_bounds__(256) kv_move_kernel(KvMoveParams p) {
         return layer + page * hk * pb + (blk - static_cast<int64_t>(pg) * pb);
     };
     for (int64_t piece0 = base / C; piece0 * C < base + n; piece0 += kTokens / C) {
-    if (tid < kTokens) {                     // the new tokens' places, and where they come from
-        const int64_t to = piece0 * C + tid, j = to - base;
-        const bool moves = j >= 0 && j < n && path[j] != j;
-        const int64_t from = moves ? base + path[j] : 0;
-        const int64_t tb = j < n ? block_of(to) : -1;
-        from_block[tid] = moves && tb >= 0 ? block_of(from) : -1;
-        from_slot[tid] = from & 15;
-        if (tid % C == 0) piece_block[tid / C] = tb;   // (a piece lies in one block)
-    }
-    __syncthreads();
-    for (int q = 0; q < kTokens / C && (piece0 + q) * C < base + n; ++q) {
-        bool any = false;
-#pragma unroll
-        for (int e = 0; e < C; ++e) any = any || from_block[q * C + e] >= 0;
-        const int first_slot = static_cast<int>((piece0 + q) * C & 15);
-        uint4 kx[KI], vx[2];
-        auto k_item = [&](int i, int& e, int& head, int& at) {
-            const int x = tid + 256 * i;
-            e = x / (512 / C);
-            head = head0 + x % (512 / C) / PIECES;
-            at = x % PIECES;
-            return head < hk && from_block[q * C + e] >= 0;
-        };
-        auto v_item = [&](int i, int& head, int64_t& at) {
-            const int x = tid + 256 * i;
-            head = head0 + x / D;
-            at = ((piece_block[q] + head * pb) * (16 / C) + first_slot / C) * D + x % D;
-            return any && head < hk;
-        };
-        int e, head, at;
-        int64_t where;
-#pragma unroll
-        for (int i = 0; i < KI; ++i)
-            if (k_item(i, e, head, at))
-                kx[i] = static_cast<const uint4*>(p.cache.k)[((from_block[q * C + e] + head * pb) * PIECES + at) * 16 + from_slot[q * C + e]];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (v_item(i, head, where)) {
-                const int d = (tid + 256 * i) % D;
-                T x[C];
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const int64_t fb = from_block[q * C + c];
-                    const int fs = from_slot[q * C + c];
-                    x[c] = fb < 0 ? T{0} : static_cast<const T*>(p.cache.v)[(((fb + head * pb) * (16 / C) + fs / C) * D + d) * C + fs % C];
-                }
-                const uint4 old = static_cast<const uint4*>(p.cache.v)[where];
-                uint32_t w[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const int shift = 8 * E * (c % (4 / E));
-                    const uint32_t mask = (E == 1 ? 0xFFu : 0xFFFFu) << shift;
-                    if (from_block[q * C + c] >= 0) w[c * E / 4] = (w[c * E / 4] & ~mask) | static_cast<uint32_t>(x[c]) << shift;
-                }
-                vx[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+        if (tid < kTokens) {                     // the new tokens' places, and where they come from
+            const int64_t to = piece0 * C + tid, j = to - base;
+            const bool moves = j >= 0 && j < n && path[j] != j;
+            const int64_t from = moves ? base + path[j] : 0;
+            const int64_t tb = j < n ? block_of(to) : -1;
+            from_block[tid] = moves && tb >= 0 ? block_of(from) : -1;
+            from_slot[tid] = from & 15;
+            if (tid % C == 0) piece_block[tid / C] = tb;   // (a piece lies in one block)
+        }
         __syncthreads();
+        for (int q = 0; q < kTokens / C && (piece0 + q) * C < base + n; ++q) {
+            bool any = false;
 #pragma unroll
-        for (int i = 0; i < KI; ++i)
-            if (k_item(i, e, head, at))
-                static_cast<uint4*>(p.cache.k)[((piece_block[q] + head * pb) * PIECES + at) * 16 + first_slot + e] = kx[i];
+            for (int e = 0; e < C; ++e) any = any || from_block[q * C + e] >= 0;
+            const int first_slot = static_cast<int>((piece0 + q) * C & 15);
+            uint4 kx[KI], vx[2];
+            auto k_item = [&](int i, int& e, int& head, int& at) {
+                const int x = tid + 256 * i;
+                e = x / (512 / C);
+                head = head0 + x % (512 / C) / PIECES;
+                at = x % PIECES;
+                return head < hk && from_block[q * C + e] >= 0;
+            };
+            auto v_item = [&](int i, int& head, int64_t& at) {
+                const int x = tid + 256 * i;
+                head = head0 + x / D;
+                at = ((piece_block[q] + head * pb) * (16 / C) + first_slot / C) * D + x % D;
+                return any && head < hk;
+            };
+            int e, head, at;
+            int64_t where;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (v_item(i, head, where)) static_cast<uint4*>(p.cache.v)[where] = vx[i];
-    }
-    __syncthreads();
+            for (int i = 0; i < KI; ++i)
+                if (k_item(i, e, head, at))
+                    kx[i] = static_cast<const uint4*>(p.cache.k)[((from_block[q * C + e] + head * pb) * PIECES + at) * 16 + from_slot[q * C + e]];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (v_item(i, head, where)) {
+                    const int d = (tid + 256 * i) % D;
+                    T x[C];
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const int64_t fb = from_block[q * C + c];
+                        const int fs = from_slot[q * C + c];
+                        x[c] = fb < 0 ? T{0} : static_cast<const T*>(p.cache.v)[(((fb + head * pb) * (16 / C) + fs / C) * D + d) * C + fs % C];
+                    }
+                    const uint4 old = static_cast<const uint4*>(p.cache.v)[where];
+                    uint32_t w[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const int shift = 8 * E * (c % (4 / E));
+                        const uint32_t mask = (E == 1 ? 0xFFu : 0xFFFFu) << shift;
+                        if (from_block[q * C + c] >= 0) w[c * E / 4] = (w[c * E / 4] & ~mask) | static_cast<uint32_t>(x[c]) << shift;
+                    }
+                    vx[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < KI; ++i)
+                if (k_item(i, e, head, at))
+                    static_cast<uint4*>(p.cache.k)[((piece_block[q] + head * pb) * PIECES + at) * 16 + first_slot + e] = kx[i];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (v_item(i, head, where)) static_cast<uint4*>(p.cache.v)[where] = vx[i];
+        }
+        __syncthreads();
     }
 }
 
