@@ -19,6 +19,11 @@ def _bf16(a):
     return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(torch.bfloat16).to(dev())
 
 
+def _f32(a):
+    import torch
+    return torch.tensor(np.asarray(a, np.float32), device=dev())
+
+
 def _f64(t):
     return t.detach().double().cpu().numpy()
 
@@ -124,6 +129,35 @@ def test_append_in_place_without_queries_and_outside_the_table():
     assert np.isnan(kt).sum() == 1 and np.isnan(vt).sum() == 1
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hk,d", [(3, 64), (2, 128), (1, 256)])
+def test_append_runs_of_slots(hk, d, e4m3):
+    """Slots in runs that begin and end inside a block, inside 8 and 16 tokens of it, and at the tokens the kernel
+    takes together; a prompt's padding between; runs backwards.  The cache is what storing token by token gives."""
+    require_gpu()
+    import w4_dequant_gemm_amd as w4
+    rng = np.random.default_rng(d)
+    page, pages = 48, 14
+    slots = np.concatenate([np.arange(5, 42), [-1, -1], np.arange(200, 216), np.arange(112, 96, -1), [pages * page + 3],
+                            np.arange(311, 343), [64, 65, 67, 68], np.arange(500, 507), [-5], np.arange(508, 531)]).astype(np.int32)
+    T = len(slots)
+    assert len(set(slots[slots >= 0])) == np.sum(slots >= 0)
+    k, v = (_bf16(rng.standard_normal((T, hk, d))) for _ in range(2))
+    scales = {"k_scale": _f32(np.full(hk, 0.01)), "v_scale": _f32(np.full(hk, 0.01))} if e4m3 else {}
+    start = ref.random_cache(rng, pages, hk, d, page, e4m3, dev())
+    got, want = [x.clone() for x in start], [x.clone() for x in start]
+    w4.w4_kv_append(None, k, v, _i32(slots), *got, **scales)
+    for t in range(T):
+        w4.w4_kv_append(None, k[t:t + 1], v[t:t + 1], _i32(slots[t:t + 1]), *want, **scales)
+    for a, b, c in zip(got, want, start):
+        assert np.array_equal(_f64(a), _f64(b))
+        assert not np.array_equal(_f64(a), _f64(c))
+    gv = ref.to_tokens(*got)[1]
+    stored = (slots >= 0) & (slots < pages * page)
+    x = _f64(v)[stored]
+    assert np.all(np.abs(gv[slots[stored]] * (np.float32(0.01) if e4m3 else 1) - x) <= (0.01 * np.maximum(2.0 ** -4 * np.abs(x) / 0.01, 2.0 ** -10) * 1.001 if e4m3 else 0))
+
+
 # --------------------------------------------------------------- attention
 
 def _attend(rng, nodes, lengths, hq, hk, d, page, e4m3, tree, window=0, scale=None, poison=True, out=None):
@@ -189,6 +223,20 @@ ATTEND = [
     ([90, 33], [420, 33], 8, 4, 256, 16, False, False, 0),
     ([150], [150], 6, 1, 128, 32, False, False, 40),
     ([2, 2, 2, 2, 2], [2, 18, 34, 259, 515], 4, 4, 128, 16, False, True, 0),
+    # windows that part a tree's nodes, and a chain's
+    ([30, 9], [300, 9], 8, 2, 64, 16, False, True, 3),
+    ([17, 5], [900, 20], 16, 8, 256, 32, True, True, 4),
+    ([60, 2], [500, 70], 4, 2, 128, 64, True, True, 2),
+    ([70], [70], 8, 4, 128, 16, True, False, 1),
+    ([9], [600], 4, 2, 64, 32, True, True, 2),
+    # 17 to 32 rows a KV head, and 33 to 64
+    ([5, 4], [77, 1040], 20, 5, 64, 16, True, False, 0),
+    ([8], [600], 16, 4, 128, 64, True, True, 0),
+    ([12, 1], [700, 1], 8, 2, 64, 16, False, True, 0),
+    ([16, 9], [1300, 9], 16, 4, 128, 32, True, True, 0),
+    ([40, 33], [200, 97], 2, 2, 64, 1024, True, True, 0),
+    ([33], [2500], 1, 1, 128, 128, False, False, 0),
+    ([12, 7], [1500, 40], 16, 4, 128, 16, False, False, 50),
 ]
 
 
@@ -247,6 +295,73 @@ def test_attention_long_context_split(e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n", [64, 100])
+def test_attention_long_context_of_many_heads(n, e4m3):
+    # 150000 tokens in few splits: more of them than a workgroup looks up at a time; three heads checked on the device
+    require_gpu()
+    import torch
+    import w4_dequant_gemm_amd as w4
+    length, hk, d, page = 150001, 64, 64, 64
+    pages = -(-length // page)
+    gen = torch.Generator(device=dev()).manual_seed(n)
+    k_cache, v_cache = w4.w4_kv_cache(pages, hk, d, page, e4m3=e4m3, device=dev())
+    for x in (k_cache, v_cache):
+        for part in x.split(256):            # (a piece of the normal numbers at a time)
+            r = torch.randn(part.shape, generator=gen, device=dev())
+            part.copy_((40 * r).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) if e4m3 else r)
+    scales = {"k_scale": _f32(np.full(hk, 0.02)), "v_scale": _f32(np.full(hk, 0.03))} if e4m3 else {}
+    table = torch.randperm(pages, generator=gen, device=dev()).to(torch.int32)
+    q = torch.randn((n, hk, d), generator=gen, device=dev()).to(torch.bfloat16)
+    O = w4.w4_tree_attention(q, k_cache, v_cache, table[None].contiguous(), _i32([length]), _i32([0, n]), n, length, **scales)
+    mask = torch.arange(length, device=dev())[None] > length - n + torch.arange(n, device=dev())[:, None]
+    for h in (0, 31, 63):
+        def tokens(x, order):
+            x = x[table.long(), h].contiguous()
+            x = (x.view(torch.float8_e4m3fn) if e4m3 else x).double()
+            return x.permute(order).reshape(pages * page, d)[:length]
+        kt = tokens(k_cache, (0, 1, 3, 2, 4)) * (float(np.float32(0.02)) if e4m3 else 1)
+        vt = tokens(v_cache, (0, 1, 2, 4, 3)) * (float(np.float32(0.03)) if e4m3 else 1)
+        x = q[:, h].double()
+        p = (x @ kt.T * d ** -0.5).masked_fill(mask, -float("inf")).softmax(1)
+        o, big = p @ vt, p @ vt.abs()
+        spread = (d + 2) * 2.0 ** -24 * (x.abs() @ kt.abs().T).amax(1, keepdim=True) * d ** -0.5 + 2.0 ** -21
+        tol = 2.0 ** -8 * o.abs() + big * (2.0 ** -8 + 2 * spread + 2 * length * 2.0 ** -24)
+        assert bool(((O[:, h].double() - o).abs() <= 1.02 * tol).all())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_offsets_past_32_bits(e4m3):
+    """Append, attention and move at the end of a cache whose arrays pass 2^32 elements and bytes."""
+    require_gpu()
+    import torch
+    import w4_dequant_gemm_amd as w4
+    hk, hq, d, page, n = 8, 16, 128, 64, 5
+    pages = 2 ** 32 // (hk * d * page) + 9
+    k_cache, v_cache = w4.w4_kv_cache(pages, hk, d, page, e4m3=e4m3, device=dev())
+    scales = {"k_scale": _f32(np.full(hk, 0.02)), "v_scale": _f32(np.full(hk, 0.02))} if e4m3 else {}
+    rng = np.random.default_rng(1)
+    length = 2 * page + 20
+    table = np.array([[pages - 1, pages - 7, pages - 3]], np.int32)
+    small = w4.w4_kv_cache(3, hk, d, page, e4m3=e4m3, device=dev())
+    near = np.array([[0, 1, 2]], np.int32)
+    q, k, v = (_bf16(rng.standard_normal((length, h, d))) for h in (hq, hk, hk))
+    at = np.arange(length)
+    out = []
+    for cache, t in (((k_cache, v_cache), table), (small, near)):
+        slots = t[0][at // page] * page + at % page
+        w4.w4_kv_append(None, k, v, _i32(slots), *cache, **scales)
+        first = w4.w4_tree_attention(q[-n:], *cache, _i32(t), _i32([length]), _i32([0, n]), n, length, **scales)
+        many = w4.w4_tree_attention(q[-40:], *cache, _i32(t), _i32([length]), _i32([0, 40]), 40, length, **scales)
+        w4.w4_kv_move(*cache, _i32(t), _i32([length - n]), _i32([[1, 3, 4]]), _i32([3]))
+        out.append((first, many, [x[torch.from_numpy(t[0]).long().to(dev())] for x in cache]))
+    (a, b, c), (x, y, z) = out
+    assert torch.equal(a.view(torch.int16), x.view(torch.int16)) and torch.equal(b.view(torch.int16), y.view(torch.int16))
+    assert float(a.float().abs().max()) > 0
+    for l, r in zip(c, z):
+        assert torch.equal(l, r) and bool((l != 0).any())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_attention_unseen_infinities_and_nan(e4m3, d):
     """A node's own key and value are NaN or infinite: only the nodes that see it may show it."""
@@ -254,7 +369,7 @@ def test_attention_unseen_infinities_and_nan(e4m3, d):
     import torch
     import w4_dequant_gemm_amd as w4
     rng = np.random.default_rng(d)
-    for n, length, hq in ((6, 75, 4), (40, 400, 8)):
+    for n, length, hq in ((6, 75, 4), (40, 400, 8), (6, 75, 8), (12, 130, 8)):
         args, kw, want, tol = _attend(rng, [n], [length], hq, 2, d, 16, e4m3, True)
         q, k_cache, v_cache, table = args[:4]
         bad = n - 2
