@@ -531,7 +531,7 @@ size_t w4_sample_workspace_bytes(int64_t B, int64_t V);
  * path[b, j] of sequence b moves to base[b] + j, for j < count[b], keys and
  * values alike.  path rows ascend strictly (path[b, j] >= j), so no token is
  * overwritten before it has moved.  Tokens outside the page table or on a page
- * outside the cache are left alone.
+ * outside the cache are left alone, and so is a sequence with base < 0.
  *   cache        all layers, one after the other in k and v.
  *   base, count  [B] int32;  path [B, path_len] int32, count[b] <= path_len.
  */

@@ -608,6 +608,37 @@ def test_move(layers, hk, d, page, e4m3):
             assert np.array_equal(g, want, equal_nan=True)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_move_long_paths_and_places_outside(e4m3):
+    """More tokens than are looked up at a time; a base below zero; pages outside the cache; a path past the table."""
+    require_gpu()
+    import w4_dequant_gemm_amd as w4
+    rng = np.random.default_rng(4)
+    hk, d, page, nodes = 3, 128, 32, 300
+    base = [9, 0, -1, 70]
+    pages, table = ref.page_table(rng, [max(b, 0) + nodes for b in base], page)
+    table[3, 4], table[3, 9] = -1, pages
+    k, v = ref.random_cache(rng, pages, hk, d, page, e4m3, dev())
+    before = ref.to_tokens(k, v)
+    count = [211, 150, 20, 100]
+    path = np.zeros((4, 211), np.int32)
+    for b, c in enumerate(count):
+        path[b, :c] = np.sort(rng.choice(nodes, c, replace=False))
+    path[1, 149] = 10 ** 9
+    w4.w4_kv_move(k, v, _i32(table), _i32(base), _i32(path), _i32(count))
+    for got, old in zip(ref.to_tokens(k, v), before):
+        want = old.copy()
+        for b, c in enumerate(count):
+            def slot(t):
+                p = int(table[b, t // page]) if 0 <= t // page < table.shape[1] else -1  # noqa: B023
+                return p * page + t % page if 0 <= p < pages else None
+            for j in range(c if base[b] >= 0 else 0):
+                to, source = slot(base[b] + j), slot(base[b] + int(path[b, j]))
+                if to is not None and source is not None:
+                    want[to] = old[source]
+        assert np.array_equal(got, want, equal_nan=True)
+
+
 # ------------------------------------------------------------ graph capture
 
 def test_calls_replay_from_a_graph():
