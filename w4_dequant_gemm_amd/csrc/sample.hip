@@ -386,8 +386,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         const uint32_t in[4] = {x.x, x.y, x.z, x.w};
         return (((i & 1) ? in[i >> 1] >> 16 : in[i >> 1]) & 0x7FFFu) - kTableFrom >= kTableHalf;
     };
-    // the weights of a vector's values
-    auto weights = [&](const uint4& x, const float (&y)[N], uint32_t (&w)[N]) {
+    // the weights of a vector's values; whether they were computed, not read
+    auto weights = [&](const uint4& x, const float (&y)[N], uint32_t (&w)[N]) -> bool {
+        bool exact = F32;
         if constexpr (F32) {
 #pragma unroll
             for (int i = 0; i < N; ++i) w[i] = weight_of(y[i], top, r);
@@ -398,19 +399,20 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
             for (int i = 0; i < N; ++i) w[i] = sh.table[at[i >> 1][i & 1]];
             if (!inside) {
                 // masked values (-inf, the lowest) are common: without weight; others are computed
-                bool exact = false;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     const bool outside = outside_table(x, i);
                     exact = exact || (outside && y[i] >= weightless);
                     w[i] = outside ? 0 : w[i];
                 }
-                if (__any(exact)) {
+                exact = __any(exact);
+                if (exact) {
 #pragma unroll
                     for (int i = 0; i < N; ++i) w[i] = weight_of(y[i], top, r);
                 }
             }
         }
+        return exact;
     };
     // a distance within which at least n of the threads' maxima lie
     auto bound = [&](int n) -> float {
@@ -459,7 +461,16 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     };
     // the tokens with from <= distance < below (infinities' NaN is 0)
     auto collect = [&](float from, float below) -> int {
-        return gather([&](const float (&y)[N]) { return !(distance(row.largest(y), top, r) >= below); },
+        return gather([&](const float (&y)[N]) {
+                          if (from == 0.0f) return !(distance(row.largest(y), top, r) >= below);
+                          bool any = false;
+#pragma unroll
+                          for (int i = 0; i < N; ++i) {
+                              const float d = distance(y[i], top, r);
+                              any = any || (d >= from && d < below);
+                          }
+                          return any;
+                      },
                       [&](float z) {
                           const float d = distance(z, top, r);
                           return !(d >= below || d < from);
@@ -503,13 +514,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     auto whole_key = [&](uint32_t key) { return !F32 && !(key >> 31) ? key | 0xFFFFu : key; };
     auto weight_at = [&](uint32_t key) -> uint64_t { return weight_of(value_of(key), top, r); };
 
-    bool few = false;                        // the kept tokens are all among the collected,
-    bool listed = false;                     // or at least those equal to kappa
+    bool few = false;                        // the kept tokens are all among the collected
     if (k > 0) {
         int n = k <= kThreads || p.V <= kCandidates ? collect(0.0f, bound(k)) : kCandidates + 1;
         uint64_t above;
         if (n <= kCandidates) {
-            few = listed = true;
+            few = true;
             k = k < n ? k : n;               // (fewer than k above -inf)
             own(n);
             kappa = whole_key(select(turn, 32, kStop, k, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t) { f(key, [] { return 1ull; }); }); }));
@@ -619,26 +629,21 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
                 const uint32_t entry = entry_at(q);
                 kappa = key_of(entry_value(entry));
                 above = sh.found_above;
-                // all kept tokens, or those equal to kappa alone (if not all of
-                // them are kept), or neither
+                // the kept tokens, if they are few
                 const float value = value_of(kappa);
                 const uint64_t w = weight_at(kappa);
                 take = (need - above + w - 1) / w;
-                int n = gather([&](const float (&y)[N]) { return row.largest(y) >= value; }, [&](float z) { return z >= value; });
-                few = listed = n <= kCandidates;
-                if (!few && take < sh.numbers[entry]) {
-                    gather_again();
-                    n = gather([&](const float (&y)[N]) {
-                        bool any = false;
-#pragma unroll
-                        for (int i = 0; i < N; ++i) any = any || y[i] == value;
-                        return any;
-                    }, [&](float z) { return z == value; });
-                    listed = n <= kCandidates;
-                } else if (!few) {
-                    take = ~uint64_t{0};     // (all: no ties to look at)
+                uint64_t kept = 0;
+#pragma unroll 1
+                for (int i = 0; i < kShare; ++i) {
+                    const uint32_t at = threadIdx.x * kShare + i;
+                    if (at < q && at != 0 && at != kTableHalf + 1) kept += sh.numbers[entry_at(at)];
                 }
-                if (listed) own(n);
+                if (turn.block_sum(kept) + take <= kCandidates) {
+                    const int n = gather([&](const float (&y)[N]) { return row.largest(y) >= value; }, [&](float z) { return z >= value; });
+                    few = n <= kCandidates;
+                    if (few) own(n);
+                }
             }
         }
         if (!counted) {
@@ -704,8 +709,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
                 gather_again();
                 n = collect(static_cast<float>(bin), static_cast<float>(bin + 1));
             }
-            listed = n <= kCandidates;
-            if (listed) {
+            if (n <= kCandidates) {
                 own(n);
                 const uint64_t skip = few ? 0 : before;
                 kappa = whole_key(select(turn, 32, kStop, need - skip, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t w) { f(key, [&] { return static_cast<unsigned long long>(w); }); }); }));
@@ -723,18 +727,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         few = n <= kCandidates;
         if (few) own(n);
     }
-    if (kappa && take != ~uint64_t{0}) {
+    if (few && kappa) {
         // the take-th of the tokens equal to kappa, by index, if not all are kept
         uint64_t ties = 0, above;
-        if (listed) collected([&](uint32_t key, uint32_t, uint32_t) { ties += key == kappa; });
-        else everything([&](uint32_t key, uint32_t, auto) { ties += key == kappa; });
+        collected([&](uint32_t key, uint32_t, uint32_t) { ties += key == kappa; });
         ties = turn.block_sum(ties);
-        if (take < ties) {
-            uint32_t at;
-            if (listed) at = select(turn, index_bits, 0, take, above, [&](auto f) { collected([&](uint32_t key, uint32_t i, uint32_t) { if (key == kappa) f(i ^ index_mask, [] { return 1ull; }); }); });
-            else at = select(turn, index_bits, 0, take, above, [&](auto f) { everything([&](uint32_t key, uint32_t i, auto) { if (key == kappa) f(i ^ index_mask, [] { return 1ull; }); }); });
-            iota = at ^ index_mask;
-        }
+        if (take < ties)
+            iota = select(turn, index_bits, 0, take, above, [&](auto f) { collected([&](uint32_t key, uint32_t i, uint32_t) { if (key == kappa) f(i ^ index_mask, [] { return 1ull; }); }); }) ^ index_mask;
     }
     auto keeps = [&](uint32_t key, uint32_t i) { return key > kappa || (key == kappa && i <= iota); };
     const uint64_t u_units = units_of_2_24(uniform, (1u << 24) - 1);
@@ -763,31 +762,42 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
 
     // Each wavefront takes a run of the row's vectors; the kept weight of its
     // segments of 4 x 64 vectors, then of the vectors and elements of the
-    // segment in which the target is reached.
+    // segment in which the target is reached.  How many tokens of a segment equal
+    // kappa is counted on the way (bits 48 and up): the first `take` are kept.
     const int turns = (row.count + 64 * kWaves - 1) / (64 * kWaves);   // of 64 vectors, a wavefront
     const int groups = (turns + kGroup - 1) / kGroup;
-    // values below this one are not kept: kappa's, or that of min_p less 2^-7 in the exponent
-    const float lowest = fmaxf(kappa ? value_of(kappa) : -INFINITY, least > 1 ? top + (logf(min_p) - 0.0078125f) * t : -INFINITY);
-    auto kept_weights = [&](const uint4& x, int v, uint32_t (&w)[N]) {
-        float y[N];
-        row.unpack(x, y);
-#pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = 0;
-        if (row.largest(y) < lowest) return;
-        weights(x, y, w);
-        if (kappa || least > 1)
-#pragma unroll
-            for (int i = 0; i < N; ++i) w[i] = keeps(key_of(y[i]), static_cast<uint32_t>(v * N + i - row.shift)) && w[i] >= least ? w[i] : 0u;
-    };
+    const float value = value_of(kappa);
+    constexpr uint64_t kSum = (uint64_t{1} << 48) - 1;
+    static_assert(kGroup * 64 * N < 1 << 16, "a segment's tokens fit 16 bits, their weights 48");
     if (!tabled) fill_table();
-    if (!F32 && kappa) {
+    if (!F32 && (kappa || least > 1)) {
         // values that are not kept have no weight
-        const float value = value_of(kappa);
         __syncthreads();
         for (uint32_t i = threadIdx.x; i < 2 * kTableHalf; i += kThreads)
-            if (entry_value(i) < value) sh.table[i] = 0;
+            if ((kappa && entry_value(i) < value) || sh.table[i] < least) sh.table[i] = 0;
         __syncthreads();
     }
+    // values below this one are not kept: kappa's, or that of min_p less 2^-7 in the exponent
+    const float lowest = fmaxf(kappa ? value : -INFINITY, least > 1 ? top + (logf(min_p) - 0.0078125f) * t : -INFINITY);
+    // the weights of a vector's tokens down to kappa, and which of them equal it
+    auto kept_weights = [&](const uint4& x, uint32_t (&w)[N]) -> uint32_t {
+        float y[N];
+        row.unpack(x, y);
+        if (F32) {                           // (an exponential each)
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = 0;
+            if (row.largest(y) < lowest) return 0;
+        }
+        if (weights(x, y, w)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = (kappa && !(y[i] >= value)) || w[i] < least ? 0u : w[i];
+        }
+        uint32_t ties = 0;
+        if (kappa)
+#pragma unroll
+            for (int i = 0; i < N; ++i) ties |= y[i] == value ? 1u << i : 0u;
+        return ties;
+    };
     auto segment_sum = [&](int w, int g) {   // this lane's part
         uint64_t sum = 0;
         uint4 x[kGroup];
@@ -797,9 +807,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
 #pragma unroll
         for (int j = 0; j < kGroup; ++j) {
             uint32_t kw[N];
-            kept_weights(x[j], first + 64 * j, kw);
+            const uint32_t ties = kept_weights(x[j], kw);
 #pragma unroll
             for (int i = 0; i < N; ++i) sum += kw[i];
+            sum += static_cast<uint64_t>(__popc(ties)) << 48;
         }
         return sum;
     };
@@ -810,8 +821,34 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     }
     __syncthreads();
     const int segments = kWaves * groups;
+    if (kappa) {
+        constexpr int kShare = (kSegments + kThreads - 1) / kThreads;
+        uint64_t mine_ties = 0;
+#pragma unroll
+        for (int i = 0; i < kShare; ++i) {
+            const int at = static_cast<int>(threadIdx.x) * kShare + i;
+            if (at < segments) mine_ties += sh.segments[at] >> 48;
+        }
+        const uint64_t upto = wave_scan64(mine_ties);
+        uint64_t* sums = sh.wave64[turn.sums++ & 1];
+        if (lane == 63) sums[wave] = upto;
+        __syncthreads();
+        uint64_t before = upto - mine_ties;
+        for (int i = 0; i < wave; ++i) before += sums[i];
+        const uint64_t one = weight_at(kappa) < least ? 0 : weight_at(kappa);
+#pragma unroll
+        for (int i = 0; i < kShare; ++i) {
+            const int at = static_cast<int>(threadIdx.x) * kShare + i;
+            if (at >= segments) continue;
+            const uint64_t all = sh.segments[at], ties = all >> 48;
+            const uint64_t left = before < take ? take - before : 0, kept = left < ties ? left : ties;
+            sh.segments[at] = (all & kSum) - (ties - kept) * one + (kept << 48);
+            before += ties;
+        }
+        __syncthreads();
+    }
     uint64_t total = 0;
-    for (int i = threadIdx.x; i < segments; i += kThreads) total += sh.segments[i];
+    for (int i = threadIdx.x; i < segments; i += kThreads) total += sh.segments[i] & kSum;
     total = turn.block_sum(total);
     if (total == 0) {
         if (threadIdx.x == 0) answer(-1, 0.0f);
@@ -822,19 +859,29 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     uint64_t before = 0, passed = 0;
     int segment = 0;
     for (;; segment += 64) {
-        const int at = reach<1>(target + 1 - before, passed, [&](int i) { return segment + i < segments ? sh.segments[segment + i] : uint64_t{0}; });
+        const int at = reach<1>(target + 1 - before, passed, [&](int i) { return segment + i < segments ? sh.segments[segment + i] & kSum : uint64_t{0}; });
         before += passed;
         if (at < 64) {
             segment += at;
             break;
         }
     }
+    uint64_t left = sh.segments[segment] >> 48;
     const int first = (segment / groups * turns + segment % groups * kGroup) * 64 + lane;
 #pragma unroll 1
     for (int j = 0; j < kGroup; ++j) {
         const int v = first + 64 * j;
         uint32_t w[N];
-        kept_weights(row.load(v), v, w);
+        const uint32_t ties = kept_weights(row.load(v), w);
+        if (kappa) {
+            const uint64_t upto = wave_scan64(static_cast<uint64_t>(__popc(ties)));
+            uint64_t rank = upto - __popc(ties);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if ((ties >> i) & 1 && rank++ >= left) w[i] = 0;
+            const uint64_t here = lane_value(upto, 63);
+            left = here < left ? left - here : 0;
+        }
         uint64_t sum = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) sum += w[i];
