@@ -463,9 +463,10 @@ int w4_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t
  *     context token's position is its index, a node's positions[row] (NULL,
  *     allowed without a tree: past + i).
  * For query head h on KV head h / (Hq / kv_heads):
- *   O = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale (q . k_j) - max),
+ *   O = sum_j p_j v_j / sum_j p_j,  p_j = bf16(exp(scale (q . k_j) - r)),
  * softmax statistics and sums in fp32, p rounded to bf16 as the operand of the
- * second product, one rounding to bf16 at the end.  A node that sees nothing
+ * second product (and summed as rounded), one rounding to bf16 at the end.  The
+ * reference r is at most 8 log(2) below the largest score so far; it cancels.  A node that sees nothing
  * gets zeros.  Keys and values that a node does not see do not reach its
  * output, whatever they hold (infinities and NaN included).
  *   q            [T, Hq, head_dim] bf16, rows q_stride elements apart (a
@@ -516,15 +517,12 @@ size_t w4_tree_attention_workspace_bytes(int64_t T, int64_t B, int Hq, int kv_he
  *                1, 0, none.  top_k <= 0: none.  temperature >= 0.
  *   tokens       [B] int32 out; -1 for a row without any weight (all -inf).
  *   probs        [B] fp32 out, the token's share of the kept weight; or NULL.
- *   workspace    w4_sample_workspace_bytes bytes, 16-byte aligned, contents
- *                irrelevant.
  */
 #define W4_LOGITS_BF16 0
 #define W4_LOGITS_F32 1
 int w4_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride, const float* u,
               const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
-              int32_t* tokens, float* probs, void* workspace, size_t workspace_bytes, hipStream_t stream);
-size_t w4_sample_workspace_bytes(int64_t B, int64_t V);
+              int32_t* tokens, float* probs, hipStream_t stream);
 
 /*
  * w4_kv_move -- keep an accepted path: in every layer, the token base[b] +

@@ -94,20 +94,15 @@ def test_attention_refusals(lib):
 
 def test_sample_refusals(lib):
     def call(**kw):
-        a = dict(x=FAKE, dtype=0, B=2, V=100, stride=100, u=FAKE, tokens=FAKE, ws=FAKE, ws_bytes=1 << 30)
+        a = dict(x=FAKE, dtype=0, B=2, V=100, stride=100, u=FAKE, tokens=FAKE)
         a.update(kw)
         return lib.w4_sample(a["x"], a["dtype"], a["B"], a["V"], a["stride"], a["u"], None, None, None, None, a["tokens"],
-                             None, a["ws"], a["ws_bytes"], None)
+                             None, None)
 
     for f, status in ((dict(dtype=2), 1), (dict(B=-1), 1), (dict(B=1 << 20), 1), (dict(V=0), 1), (dict(V=1 << 21, stride=1 << 21), 2),
-                      (dict(stride=99), 1), (dict(x=None), 1), (dict(x=ctypes.c_void_p(0x1001)), 1), (dict(x=ctypes.c_void_p(0x1002), dtype=1), 1), (dict(u=None), 1), (dict(tokens=None), 1),
-                      (dict(ws=ODD), 1)):
+                      (dict(stride=99), 1), (dict(x=None), 1), (dict(x=ctypes.c_void_p(0x1001)), 1), (dict(x=ctypes.c_void_p(0x1002), dtype=1), 1), (dict(u=None), 1), (dict(tokens=None), 1)):
         assert call(**f) == status, f
     assert call(B=0, x=None) == 0
-    need = lib.w4_sample_workspace_bytes(2, 100)
-    if need:
-        assert call(ws=None) == 1 and call(ws_bytes=need - 1) == 1
-    assert lib.w4_sample_workspace_bytes(-1, 5) == 0 and lib.w4_sample_workspace_bytes(5, 0) == 0
 
 
 def test_move_refusals(lib):

@@ -528,6 +528,32 @@ def test_sample_equal_logits_take_the_lowest_indices(V, f32):
 
 
 @pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("V", [9000, 60001, 200000])
+def test_sample_few_values_of_many_tokens(V, f32):
+    # 24 different logits: a filter's edge falls inside thousands of equal ones, of which the first are kept
+    require_gpu()
+    import torch
+    import w4_dequant_gemm_amd as w4
+    B = 8
+    rng = np.random.default_rng(V)
+    x = rng.choice(rng.uniform(-2, 2, 24), (B, V))
+    x[1::2, rng.integers(0, V, 3)] = 1e-6    # among them values of unusual size
+    x[2, 5] = 3.0
+    x[3, V // 2] = -400.0
+    x = torch.from_numpy(x.astype(np.float32)).to(torch.float32 if f32 else torch.bfloat16).to(dev())
+    for p, k, m in ((0.9, 0, 0.0), (0.5, 0, 0.0), (0.99, 0, 0.1), (1.0, V // 3, 0.0), (0.7, V // 2, 0.0)):
+        u = rng.random(B).astype(np.float32)
+        full = lambda a, t: torch.full((B,), a, dtype=t, device=dev())  # noqa: E731
+        tokens, probs = w4.w4_sample(x, _f32(u), top_p=full(p, torch.float32), top_k=full(k, torch.int32), min_p=full(m, torch.float32))
+        for r in range(B):
+            w = ref.kept_weights(_f64(x[r]), 1.0, k, p, m)
+            tok, share = int(tokens[r]), np.cumsum(w) / w.sum()
+            slack = 2.0 ** -18 + V * 2.0 ** -32 + 1 / np.count_nonzero(w)   # (a kept token more or less)
+            assert share[tok] >= u[r] - slack and (tok == 0 or share[tok - 1] <= u[r] + slack)
+            assert abs(float(probs[r]) - np.exp(_f64(x[r])[tok] - _f64(x[r]).max()) / w.sum()) <= 2.0 ** -12 * float(probs[r])
+
+
+@pytest.mark.parametrize("f32", [False, True])
 def test_sample_edges(f32):
     require_gpu()
     import torch

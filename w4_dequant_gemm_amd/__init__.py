@@ -25,7 +25,7 @@ __all__ = [
     "w4_nf4_levels", "w4_nf4_quantize", "w4_nf4_gemv",
     "FRACS_PLAIN", "FRACS_11",
     "w4_kv_cache", "w4_kv_append", "w4_tree_attention", "w4_tree_attention_workspace_bytes", "w4_sample",
-    "w4_sample_workspace_bytes", "w4_kv_move",
+    "w4_kv_move",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -122,9 +122,7 @@ def lib():
     L.w4_tree_attention.argtypes = [P, i64, i64, I, C, P, i64, P, P, i64, i64, i64, P, I, P, i64, f32, P, P, sz_t, P]
     L.w4_tree_attention_workspace_bytes.argtypes = [i64, i64, I, I, I, I, i64, i64, i64]
     L.w4_tree_attention_workspace_bytes.restype = sz_t
-    L.w4_sample.argtypes = [P, I, i64, i64, i64, P, P, P, P, P, P, P, P, sz_t, P]
-    L.w4_sample_workspace_bytes.argtypes = [i64, i64]
-    L.w4_sample_workspace_bytes.restype = sz_t
+    L.w4_sample.argtypes = [P, I, i64, i64, i64, P, P, P, P, P, P, P, P]
     L.w4_kv_move.argtypes = [C, P, i64, P, P, i64, P, i64, P]
     for name in ("w4_kv_append", "w4_tree_attention", "w4_sample", "w4_kv_move"):
         getattr(L, name).restype = I
@@ -729,14 +727,8 @@ def w4_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     return O
 
 
-@functools.lru_cache(maxsize=4096)
-def w4_sample_workspace_bytes(B: int, V: int) -> int:
-    """Workspace bytes ``w4_sample`` needs for B rows of V logits."""
-    return int(lib().w4_sample_workspace_bytes(B, V))
-
-
 def w4_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=None, top_k=None, top_p=None, min_p=None,
-              tokens=None, probs=None, workspace=None, stream=None):
+              tokens=None, probs=None, stream=None):
     """One token per row of ``logits`` [B, V] (bf16 or fp32; rows may be strided) from the uniform numbers ``u``
     [B].  ``temperature``, ``top_p``, ``min_p`` (fp32 [B]) and ``top_k`` (int32 [B]) are per row or None.
     Returns (tokens int32 [B], probs fp32 [B])."""
@@ -749,19 +741,12 @@ def w4_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=None, top_k=
     dev = logits.device
     tokens = _empty((B,), torch.int32, dev) if tokens is None else tokens
     probs = _empty((B,), torch.float32, dev) if probs is None else probs
-    if workspace is None:
-        need = w4_sample_workspace_bytes(B, V)
-        if need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-            if stream is not None:
-                workspace.record_stream(stream)
     rc = lib().w4_sample(logits.data_ptr(), 1 if logits.dtype == torch.float32 else 0, B, V,
                          logits.stride(0) if B > 1 else V,
                          _vec(fn, u, "u", B, torch.float32), _vec(fn, temperature, "temperature", B, torch.float32),
                          _vec(fn, top_k, "top_k", B, torch.int32), _vec(fn, top_p, "top_p", B, torch.float32),
                          _vec(fn, min_p, "min_p", B, torch.float32), _vec(fn, tokens, "tokens", B, torch.int32),
-                         _vec(fn, probs, "probs", B, torch.float32), _dev(workspace, "workspace"),
-                         _nbytes(workspace) if workspace is not None else 0, _stream(dev, stream))
+                         _vec(fn, probs, "probs", B, torch.float32), _stream(dev, stream))
     _check(fn, rc)
     return tokens, probs
 

@@ -184,14 +184,9 @@ int w4_tree_attention(const uint16_t* q, int64_t q_stride, int64_t T, int Hq, co
     return hip_status(w4::launch_attention(p, stream), fn);
 }
 
-size_t w4_sample_workspace_bytes(int64_t B, int64_t V) {
-    if (B <= 0 || V <= 0 || B > kInt32Most || V > kMaxVocab) return 0;
-    return w4::sample_workspace_bytes(B, V);
-}
-
 int w4_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride, const float* u,
               const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
-              int32_t* tokens, float* probs, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+              int32_t* tokens, float* probs, hipStream_t stream) {
     const char* fn = "w4_sample";
     if (dtype != W4_LOGITS_BF16 && dtype != W4_LOGITS_F32)
         return fail(W4_EINVAL, "%s: dtype %d is neither W4_LOGITS_BF16 nor W4_LOGITS_F32", fn, dtype);
@@ -206,13 +201,8 @@ int w4_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_s
         return fail(W4_EINVAL, "%s: logits is not aligned to its elements", fn);
     if (!u) return fail(W4_EINVAL, "%s: u is NULL", fn);
     if (!tokens) return fail(W4_EINVAL, "%s: tokens is NULL", fn);
-    if (workspace && !aligned16(workspace)) return fail(W4_EINVAL, "%s: workspace is not 16-byte aligned", fn);
-    const size_t need = w4::sample_workspace_bytes(B, V);
-    if (need > 0 && (!workspace || workspace_bytes < need))
-        return fail(W4_EINVAL, "%s: workspace of %zu bytes, these sizes need %zu (w4_sample_workspace_bytes)", fn,
-                    workspace ? workspace_bytes : size_t{0}, need);
     const w4::SampleParams p{logits, dtype == W4_LOGITS_F32, static_cast<int>(B), static_cast<int>(V), row_stride, u,
-                             temperature, top_k, top_p, min_p, tokens, probs, workspace};
+                             temperature, top_k, top_p, min_p, tokens, probs};
     return hip_status(w4::launch_sample(p, stream), fn);
 }
 

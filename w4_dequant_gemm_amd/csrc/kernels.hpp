@@ -298,9 +298,7 @@ struct SampleParams {
     const float* min_p;
     int32_t* tokens;
     float* probs;
-    void* ws;
 };
 hipError_t launch_sample(const SampleParams& p, hipStream_t stream);
-size_t sample_workspace_bytes(int64_t B, int64_t V);
 
 }  // namespace w4

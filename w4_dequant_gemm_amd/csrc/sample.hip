@@ -13,14 +13,24 @@
 //  - top-k: the k-th largest of the threads' own maxima bounds the k-th largest
 //    logit from below, so few tokens besides the top k lie above it: they are
 //    collected in shared memory and the filters and the draw work on them;
-//  - top-p alone: weights of the tokens near the top are summed in bins of the
-//    scaled distance to the maximum, all others together; the bin in which p of
-//    the total is reached is collected and searched;
+//  - top-p alone, bf16: how often each value occurs is counted, which gives the
+//    value at which p of the weight is reached;
+//  - top-p alone, fp32: weights of the tokens near the top are summed in bins of
+//    the scaled distance to the maximum, all others together; the bin in which p
+//    of the total is reached is collected and searched;
 //  - neither: nothing to search.
 // Searches are radix selections on the order-preserving key (or the index),
 // eight bits a level: by count for top-k, by weight for top-p and the draw.
-// Rows whose values crowd more tokens than shared memory holds (many equal
-// logits) take the same selections over the whole row.
+// Where more tokens are kept than shared memory collects, the draw goes over the
+// row once more; where a search's own tokens do not fit (many equal logits), it
+// goes over the row for each level.
+//
+// Measured, 200 rows of 131072 bf16 logits (52 MB: 10 us to read once): greedy
+// 16 us, top-k 50 30, top-p 0.5 44, top-p 0.95 of a flat row 49, no filter 29.
+// One row of 50001 fp32 logits: 11, 17, 31, 66, 22, of which launch and binding
+// are 9.  Bound by the row's one compute unit: each pass over a row from the
+// caches is 6 us, a table entry, count or comparison for each of its logits 8
+// to 13 more.
 #include <type_traits>
 
 #include "device.hpp"
@@ -909,8 +919,6 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
 }
 
 }  // namespace
-
-size_t sample_workspace_bytes(int64_t, int64_t) { return 0; }
 
 hipError_t launch_sample(const SampleParams& p, hipStream_t stream) {
     const dim3 grid(p.B), block(kThreads);
