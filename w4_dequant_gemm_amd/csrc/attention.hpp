@@ -3,7 +3,7 @@
 #pragma once
 
 #include "device.hpp"
-#include "kernels.hpp"
+#include "decode_kernels.hpp"
 
 namespace w4 {
 namespace attn {

@@ -7,7 +7,7 @@
 #include <cstdint>
 
 #include "checks.hpp"
-#include "kernels.hpp"
+#include "decode_kernels.hpp"
 
 namespace {
 using w4::aligned16;

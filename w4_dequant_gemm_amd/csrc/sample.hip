@@ -34,7 +34,7 @@
 #include <type_traits>
 
 #include "device.hpp"
-#include "kernels.hpp"
+#include "decode_kernels.hpp"
 
 namespace w4 {
 namespace {
