@@ -12,7 +12,20 @@
 // A wave has 32 rows and takes 64 tokens at a time.  The tokens' pieces go from
 // the cache straight to shared memory, in the order in which the operands are
 // read (one linear 1 KB a piece and wavefront: no bank is asked twice), the
-// next 64 tokens' while the present ones are used, one barrier a stage.
+// next 64 tokens' while the present ones are used, one barrier a stage.  (128
+// tokens a stage would halve the barriers but hold one workgroup a compute unit;
+// 32 tokens: 16 trees of 60 nodes, 4000 tokens 163 us against 124.)
+//
+// Bound by the matrix cores and the exponentials in turn: a stage is 1100 cycles
+// of products and 930 of VALU work a wave (32 exponentials of 16 cycles), and the
+// two waves of a SIMD overlap them only by chance (39 to 46 % MFMA, 40 % VALU).
+// Multiplying the next unit beside the exponentials of the present one, or 64 rows
+// a wave, needs more than 256 registers and was slower (chunk of 777 tokens at the
+// end of 6000: 430 to 510 us).  Measured (64 or 32 heads on 8 of 128):
+//   16 trees of 40 to 60 nodes, 2000 to 4000 tokens, bf16   112 .. 124 us, 590 .. 650 TFLOP/s
+//   3 chunks of 518 to 777, 3000 to 6000 tokens, bf16        212 .. 221 us, 800 .. 830 TFLOP/s
+//   8 tokens after 131000, E4M3 (WK = 2, 64 splits)          65 .. 68 us with the join, 4.0 TB/s
+// against 1230 TFLOP/s of a large library product.
 #include <type_traits>
 
 #include "attention.hpp"
