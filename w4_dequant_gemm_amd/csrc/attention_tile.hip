@@ -16,10 +16,13 @@
 // tokens a stage would halve the barriers but hold one workgroup a compute unit;
 // 32 tokens: 16 trees of 60 nodes, 4000 tokens 163 us against 124.)
 //
-// Bound by the matrix cores and the exponentials in turn: a stage is 1100 cycles
-// of products and 930 of VALU work a wave (32 exponentials of 16 cycles), and the
-// two waves of a SIMD overlap them only by chance (39 to 46 % MFMA, 40 % VALU).
-// Multiplying the next unit beside the exponentials of the present one, or 64 rows
+// A stage is 1100 cycles of products and 930 of VALU work a wave (32 exponentials
+// of 16 cycles); two waves a SIMD keep MFMA 39 to 46 % and VALU 40 % busy, at 1.5
+// to 1.6 GHz (2.0 where memory bounds).  Arranging the work otherwise changes
+// nothing measurable: one unit's products interleaved with the other's
+// exponentials inside a wave, long sequences first or paired with short ones, a
+// higher priority in the products (all within 2 %).  Multiplying the next unit
+// beside the exponentials of the present one, or 64 rows
 // a wave, needs more than 256 registers and was slower (chunk of 777 tokens at the
 // end of 6000: 430 to 510 us).  Measured (64 or 32 heads on 8 of 128):
 //   16 trees of 40 to 60 nodes, 2000 to 4000 tokens, bf16   112 .. 124 us, 590 .. 650 TFLOP/s
