@@ -19,15 +19,18 @@
 //    the scaled distance to the maximum, all others together; the bin in which p
 //    of the total is reached is collected and searched;
 //  - neither: nothing to search.
-// Searches are radix selections on the order-preserving key (or the index),
-// eight bits a level: by count for top-k, by weight for top-p and the draw.
+// Up to 128 collected tokens are compared each with each, which ranks them and
+// sums what precedes them at once (top-k 50 of 50001 fp32 logits 17 -> 13 us; 256
+// of them would take as long as the searches).  Other searches are radix
+// selections on the order-preserving key (or the index), eight bits a level: by
+// count for top-k, by weight for top-p and the draw.
 // Where more tokens are kept than shared memory collects, the draw goes over the
 // row once more; where a search's own tokens do not fit (many equal logits), it
 // goes over the row for each level.
 //
 // Measured, 200 rows of 131072 bf16 logits (52 MB: 10 us to read once): greedy
-// 16 us, top-k 50 30, top-p 0.5 44, top-p 0.95 of a flat row 49, no filter 29.
-// One row of 50001 fp32 logits: 11, 17, 31, 66, 22, of which launch and binding
+// 16 us, top-k 50 25, top-p 0.5 44, top-p 0.95 of a flat row 49, no filter 29.
+// One row of 50001 fp32 logits: 10, 13, 30, 66, 21, of which launch and binding
 // are 9.  Bound by the row's one compute unit: each pass over a row from the
 // caches is 6 us, a table entry, count or comparison for each of its logits 8
 // to 13 more.
@@ -42,6 +45,7 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kCandidates = 2048;            // tokens collected in shared memory, and vectors that hold them
+constexpr int kRanked = 128;                 // of those, few enough to compare each with each
 constexpr int kMine = kCandidates / kThreads;
 constexpr int kAhead = 8;                    // vectors a thread has on their way
 constexpr int kBins = 512;
@@ -524,11 +528,18 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     auto whole_key = [&](uint32_t key) { return !F32 && !(key >> 31) ? key | 0xFFFFu : key; };
     auto weight_at = [&](uint32_t key) -> uint64_t { return weight_of(value_of(key), top, r); };
 
+    // Few collected tokens: how many of them there are (0: more, or not collected)
+    // and are kept at most; top-p's weight is `ranked_need`, or p of theirs (0).
+    int ranked = 0;
+    uint64_t ranked_first = 0, ranked_need = 0;
     bool few = false;                        // the kept tokens are all among the collected
     if (k > 0) {
         int n = k <= kThreads || p.V <= kCandidates ? collect(0.0f, bound(k)) : kCandidates + 1;
-        uint64_t above;
-        if (n <= kCandidates) {
+        uint64_t above = 0;
+        if (n <= kRanked) {
+            ranked = n;
+            ranked_first = k;
+        } else if (n <= kCandidates) {
             few = true;
             k = k < n ? k : n;               // (fewer than k above -inf)
             own(n);
@@ -536,8 +547,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         } else {
             kappa = whole_key(select(turn, 32, kStop, k, above, [&](auto f) { everything([&](uint32_t key, uint32_t, auto) { f(key, [] { return 1ull; }); }); }));
         }
-        take = k - above;
-        if (cuts) {
+        if (!ranked) take = k - above;
+        if (!ranked && cuts) {
             uint64_t sum = 0;
             if (few) collected([&](uint32_t key, uint32_t, uint32_t w) { sum += key > kappa ? w : 0; });
             else everything([&](uint32_t key, uint32_t, auto w) { if (key > kappa) sum += w(); });
@@ -652,7 +663,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
                 if (turn.block_sum(kept) + take <= kCandidates) {
                     const int n = gather([&](const float (&y)[N]) { return row.largest(y) >= value; }, [&](float z) { return z >= value; });
                     few = n <= kCandidates;
-                    if (few) own(n);
+                    if (n <= kRanked) {
+                        ranked = n;
+                        ranked_first = n;
+                        ranked_need = need;
+                    } else if (few) {
+                        own(n);
+                    }
                 }
             }
         }
@@ -719,7 +736,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
                 gather_again();
                 n = collect(static_cast<float>(bin), static_cast<float>(bin + 1));
             }
-            if (n <= kCandidates) {
+            if (n <= kRanked && few) {
+                ranked = n;
+                ranked_first = n;
+                ranked_need = need;
+            } else if (n <= kCandidates) {
                 own(n);
                 const uint64_t skip = few ? 0 : before;
                 kappa = whole_key(select(turn, 32, kStop, need - skip, above, [&](auto f) { collected([&](uint32_t key, uint32_t, uint32_t w) { f(key, [&] { return static_cast<unsigned long long>(w); }); }); }));
@@ -737,6 +758,68 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         few = n <= kCandidates;
         if (few) own(n);
     }
+    const uint64_t u_units = units_of_2_24(uniform, (1u << 24) - 1);
+    bool more;
+    if (ranked) {
+        // A thread for each token and eighth of the others counts those that
+        // precede it and their weight, which answers every filter, then the kept
+        // weight of lower indices, which is the draw.
+        typedef unsigned long long ull;
+        auto& rank = sh.hist[0];             // (clear: no selection has run)
+        auto& before = sh.hist[1];
+        auto& lower = sh.hist[2];
+        auto& weight = sh.hist[3];
+        auto& kept = sh.hist[4];
+        const int c = threadIdx.x % kRanked, q = threadIdx.x / kRanked;
+        constexpr int kParts = kThreads / kRanked;
+        const bool is = c < ranked;
+        const uint32_t key = is ? sh.key[c] : 0, index = is ? sh.index[c] : 0;
+        const uint64_t w = is ? weight_at(key) : 0;
+        if (q == 0) weight[c] = w;
+        __syncthreads();
+        const uint64_t order = static_cast<uint64_t>(key) << 32 | ~index;
+        uint32_t count = 0;
+        uint64_t sum = 0;
+#pragma unroll 8
+        for (int j = q; j < ranked; j += kParts) {
+            const uint64_t other = static_cast<uint64_t>(sh.key[j]) << 32 | ~sh.index[j];
+            const uint64_t v = weight[j];
+            count += other > order;
+            sum += other > order ? v : 0;
+        }
+        if (is) {
+            atomicAdd(reinterpret_cast<ull*>(&rank[c]), static_cast<ull>(count));
+            atomicAdd(reinterpret_cast<ull*>(&before[c]), static_cast<ull>(sum));
+        }
+        __syncthreads();
+        const bool in = is && rank[c] < ranked_first;
+        uint64_t need = ranked_need;
+        if (cuts && need == 0) {
+            need = part_of(p_units, turn.block_sum(q == 0 && in ? w : 0), more);
+            need += more ? 1 : 0;
+            need = need < 1 ? 1 : need;
+        }
+        const bool keep = in && (!cuts || before[c] < need) && w >= least;
+        if (q == 0) kept[c] = keep ? w : 0;
+        const uint64_t total = turn.block_sum(q == 0 && keep ? w : 0);
+        if (total == 0) {                    // min_p above 1
+            if (threadIdx.x == 0) answer(-1, 0.0f);
+            return;
+        }
+        const uint64_t target = part_of(u_units, total, more);
+        sum = 0;
+#pragma unroll 8
+        for (int j = q; j < ranked; j += kParts) {
+            const uint32_t other = sh.index[j];
+            const uint64_t v = kept[j];
+            sum += other < index ? v : 0;
+        }
+        if (is) atomicAdd(reinterpret_cast<ull*>(&lower[c]), static_cast<ull>(sum));
+        __syncthreads();
+        if (q == 0 && keep && lower[c] <= target && target < lower[c] + w)
+            answer(static_cast<int>(index), static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
+        return;
+    }
     if (few && kappa) {
         // the take-th of the tokens equal to kappa, by index, if not all are kept
         uint64_t ties = 0, above;
@@ -746,8 +829,6 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
             iota = select(turn, index_bits, 0, take, above, [&](auto f) { collected([&](uint32_t key, uint32_t i, uint32_t) { if (key == kappa) f(i ^ index_mask, [] { return 1ull; }); }); }) ^ index_mask;
     }
     auto keeps = [&](uint32_t key, uint32_t i) { return key > kappa || (key == kappa && i <= iota); };
-    const uint64_t u_units = units_of_2_24(uniform, (1u << 24) - 1);
-    bool more;
 
     if (few) {
         uint64_t sum = 0;
