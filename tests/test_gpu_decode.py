@@ -665,6 +665,30 @@ def test_move_long_paths_and_places_outside(e4m3):
         assert np.array_equal(got, want, equal_nan=True)
 
 
+def test_results_of_another_stream_are_not_handed_out_early():
+    """Outputs allocated for a call on another stream keep their memory until that stream is through, even if the
+    caller drops them at once: what is allocated next on the current stream does not get it meanwhile."""
+    require_gpu()
+    import torch
+    import w4_dequant_gemm_amd as w4
+    side = torch.cuda.Stream()
+    x = torch.randn((8, 4099), device=dev())
+    u = torch.rand(8, device=dev())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        busy = torch.randn((4096, 4096), device=dev())
+        for _ in range(8):
+            busy = busy @ busy * 1e-4        # (keeps the stream occupied for a while)
+    tokens, probs = w4.w4_sample(x, u, stream=side)
+    places = {tokens.data_ptr(), probs.data_ptr()}
+    early = not side.query()
+    del tokens, probs
+    fresh = [torch.empty((8,), dtype=torch.int32, device=dev()) for _ in range(4)]
+    if early:
+        assert not places & {t.data_ptr() for t in fresh}
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------ graph capture
 
 def test_calls_replay_from_a_graph():

@@ -621,6 +621,14 @@ def _cache_arg(fn: str, k, v, k_scale, v_scale, layers: bool = False):
     return a, heads, geometry[3]
 
 
+def _result(shape, dtype, device, stream):
+    """Memory of the current stream that a call on ``stream`` uses (not handed out again before that is through)."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _rows_arg(fn: str, x, name: str, heads: int, dim: int, T=None):
     """Pointer and row stride of bf16 rows [T, heads, dim] whose heads are contiguous."""
     shape = x.shape
@@ -660,7 +668,7 @@ def w4_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, sl
         hq = q.shape[1] if q.dim() == 3 else 0
         qp, qs = _rows_arg(fn, q, "q", hq, dim, T)
         if Q is None:
-            Q = torch.empty((T, hq, dim), dtype=torch.bfloat16, device=q.device)
+            Q = _result((T, hq, dim), torch.bfloat16, q.device, stream)
         elif tuple(Q.shape) != (T, hq, dim):
             raise ValueError(f"{fn}: Q has shape {tuple(Q.shape)}, expected {(T, hq, dim)}")
         Qp = _dev(Q, "Q", torch.bfloat16)
@@ -706,15 +714,12 @@ def w4_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
             raise ValueError(f"{fn}: tree must be [{T}, words], got {tuple(tree.shape)}")
         words = tree.shape[1]
     if O is None:
-        O = torch.empty((T, Hq, dim), dtype=torch.bfloat16, device=q.device)
+        O = _result((T, Hq, dim), torch.bfloat16, q.device, stream)
     elif tuple(O.shape) != (T, Hq, dim):
         raise ValueError(f"{fn}: O has shape {tuple(O.shape)}, expected {(T, Hq, dim)}")
     if workspace is None:
         need = w4_tree_attention_workspace_bytes(T, B, Hq, hk, dim, cache.dtype == 1, max_q, max_kv, window)
-        if need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+        workspace = _result((need,), torch.uint8, q.device, stream) if need else None
     ws_bytes = _nbytes(workspace) if workspace is not None else 0
     rc = lib().w4_tree_attention(qp, qs, T, Hq, cache, _dev(page_table, "page_table", torch.int32), table_pages,
                                  _vec(fn, kv_len, "kv_len", B, torch.int32),
@@ -739,8 +744,8 @@ def w4_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=None, top_k=
         raise ValueError(f"{fn}: logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
     B, V = logits.shape
     dev = logits.device
-    tokens = _empty((B,), torch.int32, dev) if tokens is None else tokens
-    probs = _empty((B,), torch.float32, dev) if probs is None else probs
+    tokens = _result((B,), torch.int32, dev, stream) if tokens is None else tokens
+    probs = _result((B,), torch.float32, dev, stream) if probs is None else probs
     rc = lib().w4_sample(logits.data_ptr(), 1 if logits.dtype == torch.float32 else 0, B, V,
                          logits.stride(0) if B > 1 else V,
                          _vec(fn, u, "u", B, torch.float32), _vec(fn, temperature, "temperature", B, torch.float32),
