@@ -463,10 +463,11 @@ __global__ void __launch_bounds__(256, 2) attention_wide_kernel(AttentionParams 
             // As plain instructions: the compiler would wait for all of them
             // before any read of shared memory.  The wait is the explicit one
             // at the stage's end; a load the compiler does not know of only
-            // makes its own waits stricter.
+            // makes its own waits stricter.  (A load to shared memory may
+            // follow a write of M0 after one wait state.)
             const uint32_t m0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
                 reinterpret_cast<uintptr_t>(stage + ((values ? PER : 0) + x) * 64)));
-            asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(m0) : "memory", "m0");
+            asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(m0) : "memory", "m0");
         }
     };
     auto compute = [&](const uint4* stage, int k0) {

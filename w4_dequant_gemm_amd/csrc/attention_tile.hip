@@ -153,15 +153,16 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
         // before any read of shared memory.  Completion is the explicit
         // waits' matter; there is no register result.  The instruction's
         // offset counts in both places, so M0 makes up for the pieces' 512 B
-        // in the cache against 1 KB in shared memory.
+        // in the cache against 1 KB in shared memory.  (A load to shared
+        // memory may follow a write of M0 after one wait state.)
         const uint32_t to = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
             reinterpret_cast<uintptr_t>(ring + ((stage & 1) * STAGE + (my_unit * 2 + (values ? 1 : 0)) * KC) * 64)));
         auto pieces = [&](const uint8_t* from, uint32_t at, auto count) {
             constexpr int N = decltype(count)::value;
 #define W4_PIECE(x)                                                                                                        \
     if constexpr (x < N)                                                                                                   \
-        asm volatile("s_add_u32 m0, %1, %2\n\tglobal_load_lds_dwordx4 %0, off offset:%3" ::"v"(from), "s"(at),             \
-                     "n"((x) * 512), "n"((x) * 512) : "memory", "m0", "scc");
+        asm volatile("s_add_u32 m0, %1, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off offset:%3" ::"v"(from),          \
+                     "s"(at), "n"((x) * 512), "n"((x) * 512) : "memory", "m0", "scc");
             W4_PIECE(0) W4_PIECE(1) W4_PIECE(2) W4_PIECE(3) W4_PIECE(4) W4_PIECE(5) W4_PIECE(6) W4_PIECE(7)
 #undef W4_PIECE
         };

@@ -878,9 +878,10 @@ __global__ void __launch_bounds__(64 * NW) gemm256_breg_kernel(MulParams p) {
         // result (the data goes to LDS at M0 + 16 lane), and completion is
         // covered by the explicit wait at the end of each step.  Loads the
         // compiler does not know of only make its own vmcnt waits stricter.
+        // (A load to LDS may follow a write of M0 after one wait state.)
         const uint32_t m0 = __builtin_amdgcn_readfirstlane(
             static_cast<uint32_t>(reinterpret_cast<uintptr_t>(stage + (wave * ADMA + it) * 512)));
-        asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(m0) : "memory", "m0");
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(m0) : "memory", "m0");
     };
 
     // weights: column n_base + 64 wave + 32 jb + lane % 32 (PAIR: of the

@@ -262,12 +262,13 @@ __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(MulParams p) {
         // stages apart and would wait for every pending direct-to-LDS load
         // before any LDS read.  No register result (the data goes to LDS at
         // M0 + 16 lane); completion is covered by the wait at each step's end.
+        // (A load to LDS may follow a write of M0 after one wait state.)
         // the LDS byte address, as a uniform value (scalar arithmetic on the
         // stage's constant address)
         typedef __attribute__((address_space(3))) uint8_t lds_u8;
         const uint32_t m0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u8*)stage)) +
                             static_cast<uint32_t>((wave * ADMA + it) * 1024);
-        asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
                      ::"v"(voff), "s"(a_rsrc), "s"(m0), "s"(soff) : "memory", "m0");
     };
 
