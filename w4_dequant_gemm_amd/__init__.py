@@ -185,8 +185,24 @@ def _fracs(fracs: Sequence[float]):
     return arr, len(fracs)
 
 
-def _empty(shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device)
+def _scratch(nbytes: int, device, stream):
+    """Memory that only a call on ``stream`` uses.  It comes from that stream's own pool: what was freed on the
+    current stream may still be in use there."""
+    if stream is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+
+
+def _empty(shape, dtype, device, stream=None):
+    """Memory for a result of a call on ``stream``: from that stream's own pool (as ``_scratch``), and not handed
+    out again before what the current stream does with it is through."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _nbytes(t) -> int:
@@ -237,14 +253,12 @@ def _need_bytes(M: int, K: int, N: int, w4a8: bool) -> int:
 def _workspace(M: int, K: int, N: int, device, workspace, stream, w4a8=False):
     """(pointer, bytes) of the product's workspace: the caller's tensor, or a
     new byte tensor of the fastest schedule's size when the shape uses one
-    (kept alive on ``stream``)."""
+    (of ``stream``'s own memory)."""
     need = _need_bytes(M, K, N, w4a8)
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _scratch(need, device, stream)
     return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
 
 
@@ -263,14 +277,14 @@ def w4_quantize_blockwise(W: torch.Tensor, G: int, mode, fracs: Sequence[float] 
     N, K = W.shape
     dev = W.device
     ng = K // G if G else 0
-    packed = _empty((N, K // 2), torch.uint8, dev) if packed is None else packed
-    scale = _empty((N, ng), torch.float16, dev) if scale is None else scale
+    packed = _empty((N, K // 2), torch.uint8, dev, stream) if packed is None else packed
+    scale = _empty((N, ng), torch.float16, dev, stream) if scale is None else scale
     if m == ASYM and zero is None:
-        zero = _empty((N, ng), torch.float16, dev)
+        zero = _empty((N, ng), torch.float16, dev, stream)
     if m == SYM:
         zero = None
     if want_clip and clip_idx is None:
-        clip_idx = _empty((N, ng), torch.uint8, dev)
+        clip_idx = _empty((N, ng), torch.uint8, dev, stream)
     fr, nf = _fracs(fracs)
     rc = lib().w4_quantize_blockwise(_dev(W, "W", torch.float32), N, K, G, m, fr, nf,
                                      _dev(packed, "packed"), _dev(scale, "scale"), _dev(zero, "zero"),
@@ -286,9 +300,9 @@ def w4_mse_clip_search(W: torch.Tensor, G: int, mode, fracs: Sequence[float], *,
     N, K = W.shape
     dev = W.device
     ng = K // G if G else 0
-    clip_idx = _empty((N, ng), torch.uint8, dev) if clip_idx is None else clip_idx
+    clip_idx = _empty((N, ng), torch.uint8, dev, stream) if clip_idx is None else clip_idx
     if want_sse and sse is None:
-        sse = _empty((N, ng, len(fracs)), torch.float32, dev)
+        sse = _empty((N, ng, len(fracs)), torch.float32, dev, stream)
     fr, nf = _fracs(fracs)
     rc = lib().w4_mse_clip_search(_dev(W, "W", torch.float32), N, K, G, m, fr, nf,
                                   _dev(clip_idx, "clip_idx"), _dev(sse, "sse"), _stream(dev, stream))
@@ -303,8 +317,8 @@ def w4_prepack(packed: torch.Tensor, scale: torch.Tensor, zero: Optional[torch.T
     N, K2 = packed.shape
     K = 2 * K2
     dev = packed.device
-    wq = _empty((N, K // 8), torch.int32, dev) if wq is None else wq
-    sz = _empty((N, K // G if G else 0), torch.int32, dev) if sz is None else sz
+    wq = _empty((N, K // 8), torch.int32, dev, stream) if wq is None else wq
+    sz = _empty((N, K // G if G else 0), torch.int32, dev, stream) if sz is None else sz
     rc = lib().w4_prepack(_dev(packed, "packed"), _dev(scale, "scale"), _dev(zero if m == ASYM else None, "zero"),
                           N, K, G, m, _dev(wq, "wq"), _dev(sz, "sz"), _stream(dev, stream))
     _check("w4_prepack", rc)
@@ -392,8 +406,8 @@ def w4_quantize_rows_e4m3(X: torch.Tensor, *, xq=None, xscale=None, stream=None)
     """Per-row dynamic E4M3 of bf16 ``X[M, K]``: returns (xq uint8 [M, K], xscale fp32 [M])."""
     M, K = X.shape
     dev = X.device
-    xq = _empty((M, K), torch.uint8, dev) if xq is None else xq
-    xscale = _empty((M,), torch.float32, dev) if xscale is None else xscale
+    xq = _empty((M, K), torch.uint8, dev, stream) if xq is None else xq
+    xscale = _empty((M,), torch.float32, dev, stream) if xscale is None else xscale
     rc = lib().w4_quantize_rows_e4m3(_dev(X, "X", torch.bfloat16), M, K, _dev(xq, "xq"),
                                      _dev(xscale, "xscale", torch.float32), _stream(dev, stream))
     _check("w4_quantize_rows_e4m3", rc)
@@ -419,7 +433,7 @@ def w4a16_gemm(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *, Y
     bytes; allocated here when omitted and the shape needs one."""
     M, K, N = _check_product_shapes("w4a16_gemm", X, wq, sz, G, Y=Y)
     dev = X.device
-    Y = _empty((M, N), torch.bfloat16, dev) if Y is None else Y
+    Y = _empty((M, N), torch.bfloat16, dev, stream) if Y is None else Y
     ws, ws_bytes = _workspace(M, K, N, dev, workspace, stream)
     rc = lib().w4a16_gemm(_dev(X, "X", torch.bfloat16), M, K, _dev(wq, "wq"), _dev(sz, "sz"), N, G,
                           _dev(Y, "Y", torch.bfloat16), ws, ws_bytes, _stream(dev, stream))
@@ -445,9 +459,9 @@ def w4a8_gemm(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *, Y=
     """W4A8: per-row E4M3 of ``X`` then ``Y = bf16(xscale * Xq . W'^T)``; returns (Y, xq, xscale)."""
     M, K, N = _check_product_shapes("w4a8_gemm", X, wq, sz, G, Y=Y, xq=xq, xscale=xscale)
     dev = X.device
-    Y = _empty((M, N), torch.bfloat16, dev) if Y is None else Y
-    xq = _empty((M, K), torch.uint8, dev) if xq is None else xq
-    xscale = _empty((M,), torch.float32, dev) if xscale is None else xscale
+    Y = _empty((M, N), torch.bfloat16, dev, stream) if Y is None else Y
+    xq = _empty((M, K), torch.uint8, dev, stream) if xq is None else xq
+    xscale = _empty((M,), torch.float32, dev, stream) if xscale is None else xscale
     ws, ws_bytes = _workspace(M, K, N, dev, workspace, stream, w4a8=True)
     rc = lib().w4a8_gemm(_dev(X, "X", torch.bfloat16), M, K, _dev(wq, "wq"), _dev(sz, "sz"), N, G,
                          _dev(Y, "Y", torch.bfloat16), _dev(xq, "xq"), _dev(xscale, "xscale", torch.float32),
@@ -469,12 +483,10 @@ def w4a16_gate_up(X: torch.Tensor, gate: dict, up: dict, G: int, act="silu", *, 
     tensor (an empty one for none); by default one of ``w4a16_gate_up_workspace_bytes`` is allocated."""
     M, K, N = _check_product_shapes("w4a16_gate_up", X, gate["wq"], gate["sz"], G, Y=H, up=up)
     dev = X.device
-    H = _empty((M, N), torch.bfloat16, dev) if H is None else H
+    H = _empty((M, N), torch.bfloat16, dev, stream) if H is None else H
     if workspace is None:
         need = w4a16_gate_up_workspace_bytes(M, K, N)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-        if workspace is not None and stream is not None:
-            workspace.record_stream(stream)
+        workspace = _scratch(need, dev, stream) if need else None
     ws = _dev(workspace, "workspace") if workspace is not None and workspace.numel() else None
     ws_bytes = _nbytes(workspace) if ws is not None else 0
     rc = lib().w4a16_gate_up(_dev(X, "X", torch.bfloat16), M, K, _dev(gate["wq"], "gate wq"), _dev(gate["sz"], "gate sz"),
@@ -505,17 +517,15 @@ def w4a8_gate_up(X: torch.Tensor, gate: dict, up: dict, G: int, act="silu", *, H
             raise ValueError(f"w4a8_gate_up: hq must be one byte per element with shape ({M}, {N})")
         if hscale is not None and hscale.numel() != M:
             raise ValueError(f"w4a8_gate_up: hscale has {hscale.numel()} elements, expected {M}")
-    H = _empty((M, N), torch.bfloat16, dev) if H is None else H
-    xq = _empty((M, K), torch.uint8, dev) if xq is None else xq
-    xscale = _empty((M,), torch.float32, dev) if xscale is None else xscale
+    H = _empty((M, N), torch.bfloat16, dev, stream) if H is None else H
+    xq = _empty((M, K), torch.uint8, dev, stream) if xq is None else xq
+    xscale = _empty((M,), torch.float32, dev, stream) if xscale is None else xscale
     ws, ws_bytes = None, 0
     if emit:
-        hq = _empty((M, N), torch.uint8, dev) if hq is None else hq
-        hscale = _empty((M,), torch.float32, dev) if hscale is None else hscale
+        hq = _empty((M, N), torch.uint8, dev, stream) if hq is None else hq
+        hscale = _empty((M,), torch.float32, dev, stream) if hscale is None else hscale
         if workspace is None:
-            workspace = torch.empty((max(w4a8_gate_up_workspace_bytes(M, K, N), 16),), dtype=torch.uint8, device=dev)
-            if stream is not None:
-                workspace.record_stream(stream)
+            workspace = _scratch(max(w4a8_gate_up_workspace_bytes(M, K, N), 16), dev, stream)
         ws, ws_bytes = _dev(workspace, "workspace"), _nbytes(workspace)
     rc = lib().w4a8_gate_up(_dev(X, "X", torch.bfloat16), M, K, _dev(gate["wq"], "gate wq"), _dev(gate["sz"], "gate sz"),
                             _dev(up["wq"], "up wq"), _dev(up["sz"], "up sz"), N, G, _ACTS[act],
@@ -533,7 +543,7 @@ def w4a8_gemm_e4m3(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, sz:
         raise ValueError("w4a8_gemm_e4m3: xq must hold one byte per element")
     M, K, N = _check_product_shapes("w4a8_gemm_e4m3", xq, wq, sz, G, Y=Y, xscale=xscale)
     dev = xq.device
-    Y = _empty((M, N), torch.bfloat16, dev) if Y is None else Y
+    Y = _empty((M, N), torch.bfloat16, dev, stream) if Y is None else Y
     ws, ws_bytes = _workspace(M, K, N, dev, workspace, stream, w4a8=True)
     rc = lib().w4a8_gemm_e4m3(_dev(xq, "xq"), _dev(xscale, "xscale", torch.float32), M, K, _dev(wq, "wq"),
                               _dev(sz, "sz"), N, G, _dev(Y, "Y", torch.bfloat16), ws, ws_bytes, _stream(dev, stream))
@@ -557,9 +567,9 @@ def w4_nf4_quantize(W: torch.Tensor, *, stream=None) -> dict:
     N, K = W.shape
     dev = W.device
     nb = N * (K // 64)
-    packed = _empty((N, K // 2), torch.uint8, dev)
-    aq = _empty((nb,), torch.uint8, dev)
-    c2 = _empty(((nb + 255) // 256,), torch.float32, dev)
+    packed = _empty((N, K // 2), torch.uint8, dev, stream)
+    aq = _empty((nb,), torch.uint8, dev, stream)
+    c2 = _empty(((nb + 255) // 256,), torch.float32, dev, stream)
     rc = lib().w4_nf4_quantize(_dev(W, "W", torch.float32), N, K, _dev(packed, "packed"), _dev(aq, "absmax_q"),
                                _dev(c2, "absmax_c2", torch.float32), _stream(dev, stream))
     _check("w4_nf4_quantize", rc)
@@ -571,7 +581,7 @@ def w4_nf4_gemv(x: torch.Tensor, nf4: dict, *, y=None, stream=None):
     K = x.numel()
     N = nf4["packed"].shape[0]
     dev = x.device
-    y = _empty((N,), torch.bfloat16, dev) if y is None else y
+    y = _empty((N,), torch.bfloat16, dev, stream) if y is None else y
     rc = lib().w4_nf4_gemv(_dev(x, "x", torch.bfloat16), K, _dev(nf4["packed"], "packed"), _dev(nf4["absmax_q"], "absmax_q"),
                            _dev(nf4["absmax_c2"], "absmax_c2", torch.float32), N, _dev(y, "y", torch.bfloat16),
                            _stream(dev, stream))
@@ -621,14 +631,6 @@ def _cache_arg(fn: str, k, v, k_scale, v_scale, layers: bool = False):
     return a, heads, geometry[3]
 
 
-def _result(shape, dtype, device, stream):
-    """Memory of the current stream that a call on ``stream`` uses (not handed out again before that is through)."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 def _rows_arg(fn: str, x, name: str, heads: int, dim: int, T=None):
     """Pointer and row stride of bf16 rows [T, heads, dim] whose heads are contiguous."""
     shape = x.shape
@@ -668,7 +670,7 @@ def w4_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, sl
         hq = q.shape[1] if q.dim() == 3 else 0
         qp, qs = _rows_arg(fn, q, "q", hq, dim, T)
         if Q is None:
-            Q = _result((T, hq, dim), torch.bfloat16, q.device, stream)
+            Q = _empty((T, hq, dim), torch.bfloat16, q.device, stream)
         elif tuple(Q.shape) != (T, hq, dim):
             raise ValueError(f"{fn}: Q has shape {tuple(Q.shape)}, expected {(T, hq, dim)}")
         Qp = _dev(Q, "Q", torch.bfloat16)
@@ -714,12 +716,12 @@ def w4_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
             raise ValueError(f"{fn}: tree must be [{T}, words], got {tuple(tree.shape)}")
         words = tree.shape[1]
     if O is None:
-        O = _result((T, Hq, dim), torch.bfloat16, q.device, stream)
+        O = _empty((T, Hq, dim), torch.bfloat16, q.device, stream)
     elif tuple(O.shape) != (T, Hq, dim):
         raise ValueError(f"{fn}: O has shape {tuple(O.shape)}, expected {(T, Hq, dim)}")
     if workspace is None:
         need = w4_tree_attention_workspace_bytes(T, B, Hq, hk, dim, cache.dtype == 1, max_q, max_kv, window)
-        workspace = _result((need,), torch.uint8, q.device, stream) if need else None
+        workspace = _scratch(need, q.device, stream) if need else None
     ws_bytes = _nbytes(workspace) if workspace is not None else 0
     rc = lib().w4_tree_attention(qp, qs, T, Hq, cache, _dev(page_table, "page_table", torch.int32), table_pages,
                                  _vec(fn, kv_len, "kv_len", B, torch.int32),
@@ -744,8 +746,8 @@ def w4_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=None, top_k=
         raise ValueError(f"{fn}: logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
     B, V = logits.shape
     dev = logits.device
-    tokens = _result((B,), torch.int32, dev, stream) if tokens is None else tokens
-    probs = _result((B,), torch.float32, dev, stream) if probs is None else probs
+    tokens = _empty((B,), torch.int32, dev, stream) if tokens is None else tokens
+    probs = _empty((B,), torch.float32, dev, stream) if probs is None else probs
     rc = lib().w4_sample(logits.data_ptr(), 1 if logits.dtype == torch.float32 else 0, B, V,
                          logits.stride(0) if B > 1 else V,
                          _vec(fn, u, "u", B, torch.float32), _vec(fn, temperature, "temperature", B, torch.float32),
