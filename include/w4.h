@@ -502,7 +502,8 @@ size_t w4_tree_attention_workspace_bytes(int64_t T, int64_t B, int Hq, int kv_he
  * row.  With x the row (NaN counts as -inf), m its maximum and T its
  * temperature, tokens are ordered by x descending, then by index; each has the
  * whole-number weight
- *   w = rint(2^31 exp((x - m) (1 / T)))   (fp32; (x - m) rounded, then the product)
+ *   w = rint(2^31 exp((x - m) (1 / T)))   (fp32; (x - m) rounded, then the product;
+ *                                          2^31 where x = m, infinities included)
  * of which top_k keeps the first k, top_p the shortest prefix of those whose
  * weight reaches p of theirs (at least one token), min_p those with w >= min_p
  * 2^31.  The token is the first, in index order, up to which the kept weights

@@ -1,0 +1,39 @@
+"""w4_sample on numbers of unusual size: what is kept and drawn follows from whole numbers alone, so tokens are equal
+to the reference's, on every path of the kernel and in both types."""
+import numpy as np
+import pytest
+
+from helpers import dev, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+def _full(n, x):
+    import torch
+    return torch.full((n,), x, device=dev())
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("V", [50, 5003, 60000])
+def test_infinite_logits_share_everything(V, f32):
+    # whatever the temperature, an infinite one included: of n infinite logits the kept ones have equal weights
+    require_gpu()
+    import torch
+    import w4_dequant_gemm_amd as w4
+    rng = np.random.default_rng(V)
+    B, n = 16, 11
+    x = torch.randn((B, V), device=dev())
+    x[:, 3] = -float("inf")
+    at = np.stack([np.sort(rng.choice(np.arange(4, V), n, replace=False)) for _ in range(B)])
+    x.scatter_(1, torch.from_numpy(at).to(dev()), float("inf"))
+    x = x if f32 else x.to(torch.bfloat16)
+    u = rng.random(B).astype(np.float32)
+    units = np.floor(u.astype(np.float64) * 2 ** 24).astype(np.int64)
+    uu = torch.from_numpy(u).to(dev())
+    k = torch.full((B,), 4, dtype=torch.int32, device=dev())
+    for t in (0.5, 1.0, 2e37, float("inf")):
+        for kept, kw in ((n, {}), (6, {"top_p": _full(B, 0.5)}), (4, {"top_k": k}), (2, {"top_k": k, "top_p": _full(B, 0.5)}),
+                         (n, {"min_p": _full(B, 0.25)}), (6, {"top_p": _full(B, 0.5), "min_p": _full(B, 1.0)})):
+            tokens, probs = w4.w4_sample(x, uu, temperature=_full(B, t), **kw)
+            assert np.array_equal(tokens.cpu().numpy(), at[np.arange(B), units * kept >> 24]), (t, kept)
+            assert np.all(np.abs(probs.cpu().numpy() - 1 / kept) <= 2.0 ** -24), (t, kept)

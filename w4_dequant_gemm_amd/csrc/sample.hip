@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         sh.bins[threadIdx.x] = 0;
         sh.counts[threadIdx.x] = 0;
     }
-    if (threadIdx.x == 0) sh.candidates = sh.marked = 0;
+    if (threadIdx.x == 0) sh.candidates = sh.marked = sh.found = 0;
     if (threadIdx.x < 3) sh.outside[threadIdx.x] = 0;
 
     float mine = -INFINITY;
@@ -365,7 +365,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
 
     uint32_t kappa = 0, iota = 0xFFFFFFFFu;  // kept: keys above kappa, and equal ones up to index iota
     uint64_t take = 0;                       // how many equal ones
-    const float weightless = top - 22.5f / r;  // exp(-22.5) 2^31 < 1/2
+    // values below have no weight, exp(-22.5) 2^31 being less than 1/2 (an infinite top: all others;
+    // 22.5 / r may be infinite too)
+    const float weightless = top == INFINITY ? top : top - 22.5f / r;
     bool tabled = false;
     auto entry_value = [&](uint32_t i) {
         return __uint_as_float((i < kTableHalf ? kTableFrom + i : 0x8000u + kTableFrom + i - kTableHalf) << 16);
