@@ -1,0 +1,54 @@
+"""w4_tree_attention on values and scales of unusual size, in each of its forms: up to 16 and 32 rows a KV head, up
+to 64, more, and heads of 256 dims."""
+import numpy as np
+import pytest
+
+from helpers import dev, require_gpu
+from test_gpu_decode import _attend, _f64
+
+pytestmark = pytest.mark.gpu
+
+# n nodes, hq, hk, d: rows a KV head n hq / hk
+FORMS = [(6, 4, 2, 64), (6, 4, 2, 128), (12, 4, 2, 128), (12, 4, 2, 64), (25, 4, 2, 64), (25, 4, 2, 128), (45, 4, 2, 64),
+         (70, 4, 2, 128), (12, 8, 2, 256)]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("tree,window", [(True, 0), (False, 0), (False, 90), (True, 150)])
+@pytest.mark.parametrize("past", [401, 424])   # the context ends in the first and in the second half of 64 tokens
+@pytest.mark.parametrize("form", FORMS, ids=str)
+def test_infinities_and_nan_reach_the_rows_that_see_them(form, past, tree, window, e4m3):
+    """Values of one token in two dims are infinite or NaN: these dims of the rows that see the token show it, and
+    nothing else does, wherever the token lies beside the edges of what the rows see."""
+    require_gpu()
+    import torch
+    import w4_dequant_gemm_amd as w4
+    n, hq, hk, d = form
+    rng = np.random.default_rng(n + d + window)
+    args, kw, want, tol = _attend(rng, [n], [past + n], hq, hk, d, 16, e4m3, tree, window)
+    v_cache, table = args[2], args[3].cpu().numpy()[0]
+    c = 16 if e4m3 else 8
+    if tree:
+        words = kw["tree"].cpu().numpy().view(np.uint64)
+        bits = lambda i, j: bool(int(words[i, j // 64]) >> (j % 64) & 1)  # noqa: E731
+    else:
+        bits = lambda i, j: j <= i  # noqa: E731
+    at = kw["positions"].cpu().numpy() if "positions" in kw else past + np.arange(n)
+    position = lambda j: j if j < past else at[j - past]  # noqa: E731
+    low = past - window if window else 0
+    spots = {past - 1, past - 10, past - 20, past - 30, past - 45, past, past + n - 1, low + 1, low + 10, low + 30, low + 50,
+             low + n, low + n + 20, low + n + 40}
+    for j in sorted(s for s in spots if 0 <= s < past + n):
+        sees = np.array([(j < past or bits(i, j - past)) and (not window or position(j) > at[i] - window) for i in range(n)])
+        pg, blk, s = int(table[j // 16]), 0, j % 16
+        for value in ((0x7F,) if e4m3 else (float("nan"), float("inf"), -float("inf"))):
+            old = v_cache[pg, :, blk, s // c, :, s % c].clone()
+            v_cache[pg, :, blk, s // c, 3, s % c] = value
+            v_cache[pg, :, blk, s // c, d - 5, s % c] = value
+            got = _f64(w4.w4_tree_attention(*args, **kw))
+            v_cache[pg, :, blk, s // c, :, s % c] = old
+            special = np.zeros((n, hq, d), bool)
+            special[sees[:, None] & np.ones((1, hq), bool)] = np.isin(np.arange(d), (3, d - 5))
+            assert np.max(np.abs(got - want)[~special] / tol[~special]) <= 1, (j, value)
+            show = got[special]
+            assert np.all(np.isnan(show) if e4m3 or value != value else show == value), (j, value)

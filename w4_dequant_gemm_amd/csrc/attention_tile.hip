@@ -314,7 +314,8 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
 #pragma unroll 1
             for (int u = 0; u < units; ++u) {
                 const int k0 = from_token + 32 * u;
-                if (!needs_mask(k0, 32) || (WK == 2 && (u & 1) != unit0)) continue;
+                // (the units that a wave takes of a stage were checked, and cleaned, together)
+                if (!needs_mask(k0 - 32 * (u % UW), 32 * UW) || (WK == 2 && (u & 1) != unit0)) continue;
                 const uint32_t bits = mask_bits(k0);
 #pragma unroll
                 for (int db = 0; db < DB; ++db)
