@@ -37,3 +37,36 @@ def test_infinite_logits_share_everything(V, f32):
             tokens, probs = w4.w4_sample(x, uu, temperature=_full(B, t), **kw)
             assert np.array_equal(tokens.cpu().numpy(), at[np.arange(B), units * kept >> 24]), (t, kept)
             assert np.all(np.abs(probs.cpu().numpy() - 1 / kept) <= 2.0 ** -24), (t, kept)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("V,tail", [(1500, 600), (50000, 600), (50000, 5000)])
+@pytest.mark.parametrize("min_p,x,t", [(9e-10, -21.0, 1.0), (2.3e-9, -19.875, 19.875 / 19.95)])
+def test_small_min_p_keeps_weights_that_round_up(V, tail, f32, min_p, x, t):
+    # weights are whole numbers: one of 1.63 is 2 and passes a threshold of 1.93, which is 2 too
+    require_gpu()
+    import torch
+    import w4_dequant_gemm_amd as w4
+    rng = np.random.default_rng(V + tail)
+    logits = np.full(V, -400.0)
+    logits[0] = 0.0
+    at = np.sort(rng.choice(np.arange(1, V), tail, replace=False))
+    logits[at] = x
+    real = 2.0 ** 31 * np.exp(x / np.float32(t))
+    least = int(np.ceil(np.float32(min_p) * 2.0 ** 31))
+    weight = int(np.rint(real))
+    assert real < np.float32(min_p) * 2.0 ** 31 and weight >= least and abs(abs(real - weight) - 0.5) > 0.05
+    total = 2 ** 31 + weight * tail
+    units = 2 ** 24 - 1 - np.arange(12)
+    upto = np.concatenate([[2 ** 31], 2 ** 31 + weight * np.arange(1, tail + 1)])
+    want = np.concatenate([[0], at])[np.searchsorted(upto, units * total >> 24, side="right")]
+    assert np.count_nonzero(want) >= 3
+    B = len(units)
+    row = torch.from_numpy(logits.astype(np.float32)).to(torch.float32 if f32 else torch.bfloat16).to(dev())
+    u = torch.from_numpy((units / 2.0 ** 24).astype(np.float32)).to(dev())
+    many = torch.full((B,), tail + 100, dtype=torch.int32, device=dev())
+    for kw in ({}, {"top_k": many}):
+        tokens, probs = w4.w4_sample(row.expand(B, V), u, temperature=_full(B, t), min_p=_full(B, min_p), **kw)
+        assert np.array_equal(tokens.cpu().numpy(), want), kw
+        share = np.where(want == 0, 2.0 ** 31, weight) / total
+        assert np.all(np.abs(probs.cpu().numpy() - share) <= 2.0 ** -23 * share), kw

@@ -319,6 +319,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
         const float f = ceilf(min_p * 2147483648.0f);
         least = f >= 4294967040.0f ? 0xFFFFFFFFu : f > 1.0f ? static_cast<uint32_t>(f) : 1u;
     }
+    // a weight is kept from `least` less half a unit up: the logarithm of that (2^-7 more, for the
+    // exponential's and the distances' errors), in units of the scaled distance
+    const float least_log = logf((static_cast<float>(least) - 0.5f) * 0x1p-31f) - 0.0078125f;
     const float uniform = p.u[b];
     auto answer = [&](int token, float prob) {
         p.tokens[b] = token;
@@ -754,9 +757,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
             take = w ? (need - above + w - 1) / w : 1;
         }
     } else if (least > 1) {
-        // min_p alone: what it may keep (2^-7 more than that, in the exponent), if it fits
-        const float far = (0.0078125f - logf(min_p)) * kBinsPerUnit;
-        const int n = collect(0.0f, far);
+        // min_p alone: what it may keep, if it fits
+        const int n = collect(0.0f, -least_log * kBinsPerUnit);
         few = n <= kCandidates;
         if (few) own(n);
     }
@@ -870,8 +872,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
             if ((kappa && entry_value(i) < value) || sh.table[i] < least) sh.table[i] = 0;
         __syncthreads();
     }
-    // values below this one are not kept: kappa's, or that of min_p less 2^-7 in the exponent
-    const float lowest = fmaxf(kappa ? value : -INFINITY, least > 1 ? top + (logf(min_p) - 0.0078125f) * t : -INFINITY);
+    // values below this one are not kept: kappa's, or that of min_p
+    const float lowest = fmaxf(kappa ? value : -INFINITY, least > 1 ? top + least_log * t : -INFINITY);
     // the weights of a vector's tokens down to kappa, and which of them equal it
     auto kept_weights = [&](const uint4& x, uint32_t (&w)[N]) -> uint32_t {
         float y[N];
