@@ -70,3 +70,37 @@ def test_small_min_p_keeps_weights_that_round_up(V, tail, f32, min_p, x, t):
         assert np.array_equal(tokens.cpu().numpy(), want), kw
         share = np.where(want == 0, 2.0 ** 31, weight) / total
         assert np.all(np.abs(probs.cpu().numpy() - share) <= 2.0 ** -23 * share), kw
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("V", [40, 5003, 20000, 131072])
+def test_signalling_nan_count_as_nothing(V, f32):
+    # bit patterns of memory nobody wrote (a padded vocabulary): like -inf, wherever they stand beside the maximum
+    require_gpu()
+    import torch
+    import w4_dequant_gemm_amd as w4
+    rng = np.random.default_rng(V)
+    B = 24
+    x = torch.randn((B, V), device=dev())
+    for r in range(B):
+        x[r, r % V] = 6.0 + r / 8            # the maximum, in every place of a vector
+    bits = x.view(torch.int32) if f32 else (x := x.to(torch.bfloat16)).view(torch.int16)
+    patterns = [0x7F800001, 0x7FBFFFFF, -0x7FFFFF, -0x400001] if f32 else [0x7F81, 0x7FBF, -0x7F, -0x41]
+    spots = [s for s in range(0, V, 3)] + [s for s in range(V // 2, V)]
+    clean = x.clone()
+    for i, p in enumerate(patterns):
+        at = torch.tensor(spots[i::4], device=dev())
+        keep = bits[torch.arange(B), torch.arange(B) % V].clone()
+        bits[:, at] = p
+        clean[:, at] = -float("inf")
+        bits[torch.arange(B), torch.arange(B) % V] = keep
+        clean[torch.arange(B), torch.arange(B) % V] = x[torch.arange(B), torch.arange(B) % V]
+    assert bool(x.isnan().any())
+    u = torch.from_numpy(rng.random(B).astype(np.float32)).to(dev())
+    k = torch.full((B,), 7, dtype=torch.int32, device=dev())
+    tokens, _ = w4.w4_sample(x, u, temperature=_full(B, 0.0))
+    assert tokens.tolist() == [r % V for r in range(B)]
+    for kw in ({}, {"top_k": k}, {"top_p": _full(B, 0.8)}, {"min_p": _full(B, 0.05)}, {"top_k": k, "top_p": _full(B, 0.6)}):
+        got, want = w4.w4_sample(x, u, **kw), w4.w4_sample(clean, u, **kw)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), kw

@@ -74,11 +74,13 @@ __device__ __forceinline__ uint32_t weight_of(float x, float top, float r) {
 __device__ __forceinline__ float distance(float x, float top, float r) { return (top - x) * (r * kBinsPerUnit); }
 __device__ __forceinline__ int bin_of(float d) { return static_cast<int>(fminf(fmaxf(d, 0.0f), static_cast<float>(kBins))); }
 
-// (as an instruction: fmaxf first makes signalling NaN quiet, one more operation an element)
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float m;
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(c));
-    return m;
+// The larger of m (no NaN) and x, NaN left out, in one instruction (fmaxf: two).
+// A maximum with a signalling NaN is a quiet NaN and loses the other operand, so
+// x is first put beside itself: max(max(x, x), m).
+__device__ __forceinline__ float larger(float m, float x) {
+    float r;
+    asm("v_max3_f32 %0, %1, %1, %2" : "=v"(r) : "v"(x), "v"(m));
+    return r;
 }
 
 __device__ __forceinline__ uint64_t units_of_2_24(float x, uint64_t most) {
@@ -256,7 +258,7 @@ struct Row {
     // the largest of m and the values, NaN left out
     static __device__ __forceinline__ float largest(const float (&y)[N], float m = -INFINITY) {
 #pragma unroll
-        for (int i = 0; i < N; i += 2) m = max3(m, y[i], y[i + 1]);
+        for (int i = 0; i < N; ++i) m = larger(m, y[i]);
         return m;
     }
     // f(vector, its number, turn) for this thread's vectors, read ahead
