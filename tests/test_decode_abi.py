@@ -143,3 +143,23 @@ def test_binding_refusals():
         w4.w4_sample(torch.zeros(2, 8), torch.zeros(2))
     with pytest.raises(ValueError):
         w4.w4_kv_move(k, v, table, i[:1], table, i[:1])
+
+
+def test_binding_refuses_other_types_of_one_byte():
+    """An 8-bit cache holds OCP E4M3 codes: other types of that size would be read as them."""
+    import w4_dequant_gemm_amd as w4
+    k, v = w4.w4_kv_cache(4, 2, 64, 32, e4m3=True, device="cpu")
+    x = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    i = torch.zeros(3, dtype=torch.int32)
+    table = torch.zeros((1, 4), dtype=torch.int32)
+    for dtype in (torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e5m2fnuz, torch.int8, torch.bool):
+        bad = k.view(dtype), v.view(dtype)
+        with pytest.raises(ValueError, match="E4M3 codes"):
+            w4.w4_kv_append(None, x, x, i, *bad, k_scale=i, v_scale=i)
+        with pytest.raises(ValueError, match="E4M3 codes"):
+            w4.w4_tree_attention(x, *bad, table, i[:1], i[:2], 3, 50, k_scale=i, v_scale=i)
+        with pytest.raises(ValueError, match="E4M3 codes"):
+            w4.w4_kv_move(*bad, table, i[:1], table, i[:1])
+    for dtype in (torch.uint8, torch.float8_e4m3fn):     # these come as far as the pointers
+        with pytest.raises(ValueError, match="device tensor"):
+            w4.w4_kv_move(k.view(dtype), v.view(dtype), table, i[:1], table, i[:1])

@@ -615,8 +615,9 @@ def _cache_geometry(fn: str, shape, sv, dtype, dtype_v, layers: bool):
     if rows != 16 or c != (16 if one_byte else 8):
         raise ValueError(f"{fn}: k_cache of {dtype} must end in [head_dim/{16 if one_byte else 8}, 16, "
                          f"{16 if one_byte else 8}], got {tuple(shape)}")
-    if not one_byte and dtype != torch.bfloat16:
-        raise ValueError(f"{fn}: the cache must be bf16 or hold one byte per element, got {dtype}")
+    if dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
+        raise ValueError(f"{fn}: the cache must be torch.bfloat16 or hold E4M3 codes (torch.uint8 or torch.float8_e4m3fn), "
+                         f"got {dtype}")
     if dtype_v != dtype or tuple(sv) != (*shape[:-3], 16 // c, chunks * c, c):
         raise ValueError(f"{fn}: v_cache {tuple(sv)} of {dtype_v} does not belong to k_cache {tuple(shape)} of {dtype}")
     return pages, shape[0] if n == 7 else 1, heads, chunks * c, 16 * blocks, 1 if one_byte else 0
