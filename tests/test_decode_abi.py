@@ -163,3 +163,17 @@ def test_binding_refuses_other_types_of_one_byte():
     for dtype in (torch.uint8, torch.float8_e4m3fn):     # these come as far as the pointers
         with pytest.raises(ValueError, match="device tensor"):
             w4.w4_kv_move(k.view(dtype), v.view(dtype), table, i[:1], table, i[:1])
+
+
+def test_largest_integers_are_refused(lib):
+    """Sizes whose sums with other sizes would pass 64 bits."""
+    most = (1 << 63) - 1
+    for T in (most, most - 15, most - 16, 1 << 62, 1 << 32):
+        assert _append(lib, _cache(), T=T) == 1, T
+        assert _attend(lib, _cache(), T=T, max_q=3) in (1, 2), T
+    for window in (most, most - 66, most - 67, (1 << 29) + 1):
+        assert lib.w4_tree_attention_workspace_bytes(6, 2, 4, 2, 128, 0, 3, 100000, window) == 0, window
+        assert _attend(lib, _cache(), window=window, pos=FAKE) == 1, window
+    for f in (dict(B=most), dict(max_q=most), dict(max_kv=most), dict(pages=most)):
+        assert _attend(lib, _cache(), **f) in (1, 2), f
+    assert _append(lib, _cache(pages=most)) == 1

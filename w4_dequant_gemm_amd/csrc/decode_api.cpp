@@ -64,7 +64,7 @@ int check_table(const char* fn, const int32_t* page_table, int64_t table_pages, 
 
 bool attention_sizes_ok(int64_t T, int64_t B, int hq, int hk, int64_t max_q, int64_t max_kv, int64_t window) {
     return T > 0 && B > 0 && B <= 65535 && hq > 0 && hk > 0 && hq % hk == 0 && hq <= 65535 && T <= kInt32Most / hq && max_q > 0 &&
-           max_q <= T && max_kv > 0 && max_kv <= kMaxLength && window >= 0;
+           max_q <= T && max_kv > 0 && max_kv <= kMaxLength && window >= 0 && window <= kMaxLength;
 }
 }  // namespace
 
@@ -81,7 +81,7 @@ int w4_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t
     if (!q != !Q) return fail(W4_EINVAL, "%s: q and Q must both be given or both be NULL", fn);
     if (q && (Hq <= 0 || Hq > 65535)) return fail(W4_EINVAL, "%s: Hq = %d must be in 1..65535", fn, Hq);
     const int hq = q ? Hq : 0;
-    if (T < 0 || T + 16 > kInt32Most / (hq + 2 * hk) / (dim / 8))   // (a thread each 8 dims)
+    if (T < 0 || T > kInt32Most / (hq + 2 * hk) / (dim / 8) - 16)   // (a thread each 8 dims)
         return fail(W4_EINVAL, "%s: T = %lld outside 0..2^31 / (heads * head_dim / 8)", fn, ll(T));
     if (T == 0) return W4_OK;
     if (q) W4_TRY(check_rows(fn, "q", q, q_stride, hq, dim));
