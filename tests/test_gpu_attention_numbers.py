@@ -52,3 +52,16 @@ def test_infinities_and_nan_reach_the_rows_that_see_them(form, past, tree, windo
             assert np.max(np.abs(got - want)[~special] / tol[~special]) <= 1, (j, value)
             show = got[special]
             assert np.all(np.isnan(show) if e4m3 or value != value else show == value), (j, value)
+
+
+@pytest.mark.parametrize("form", FORMS, ids=str)
+def test_no_token_is_seen_where_the_bound_is_zero(form):
+    # lengths are cut to max_kv, to 0 too: rows that see nothing are zeros
+    require_gpu()
+    import torch
+    import w4_dequant_gemm_amd as w4
+    n, hq, hk, d = form
+    args, kw, _, _ = _attend(np.random.default_rng(n), [n, n], [n + 40, n], hq, hk, d, 16, False, False)
+    out = torch.full((2 * n, hq, d), 7.0, dtype=torch.bfloat16, device=dev())
+    args[7] = 0
+    assert bool((w4.w4_tree_attention(*args, **kw, O=out) == 0).all())

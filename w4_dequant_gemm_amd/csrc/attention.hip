@@ -650,7 +650,7 @@ size_t attention_workspace_bytes(int64_t T, int64_t B, int hq, int hk, int dim, 
 }
 
 hipError_t launch_attention(const AttentionParams& p, hipStream_t stream) {
-    AttentionPlan pl = make_plan(p.B, p.hq, p.cache.heads, p.cache.dim, p.max_q, p.max_kv, p.window);
+    AttentionPlan pl = make_plan(p.B, p.hq, p.cache.heads, p.cache.dim, p.max_q, p.max_kv > 0 ? p.max_kv : 1, p.window);
     const int pb = p.cache.page_blocks;
     pl.page_magic = pb > 1 ? static_cast<uint32_t>(((uint64_t{1} << 32) + pb - 1) / pb) : 0;
     if (p.cache.e4m3)

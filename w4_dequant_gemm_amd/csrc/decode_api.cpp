@@ -145,8 +145,8 @@ int w4_tree_attention(const uint16_t* q, int64_t q_stride, int64_t T, int Hq, co
     if (max_kv < 0 || max_kv > kMaxLength) return fail(W4_EINVAL, "%s: max_kv = %lld outside 0..2^29", fn, ll(max_kv));
     if (window < 0 || window > kMaxLength) return fail(W4_EINVAL, "%s: window = %lld outside 0..2^29", fn, ll(window));
     if (max_q == 0) return W4_OK;
-    if (max_kv == 0) max_kv = 1;             // every row is empty: zeros
-    if (!attention_sizes_ok(T, B, Hq, hk, max_q, max_kv, window))
+    const int64_t plan_kv = max_kv > 0 ? max_kv : 1;   // 0: every row is empty, zeros
+    if (!attention_sizes_ok(T, B, Hq, hk, max_q, plan_kv, window))
         return fail(W4_EUNSUPPORTED, "%s: T = %lld, B = %lld, Hq = %d: T Hq is limited to 2^31 - 1, B and Hq to 65535", fn, ll(T), ll(B), Hq);
     W4_TRY(check_rows(fn, "q", q, q_stride, Hq, dim));
     W4_REQUIRE_PTR(fn, O);
@@ -159,7 +159,7 @@ int w4_tree_attention(const uint16_t* q, int64_t q_stride, int64_t T, int Hq, co
     if (tree && window > 0 && !positions) return fail(W4_EINVAL, "%s: a window over a tree needs positions", fn);
     if (!std::isfinite(scale)) return fail(W4_EINVAL, "%s: scale is not finite", fn);
     if (workspace && !aligned16(workspace)) return fail(W4_EINVAL, "%s: workspace is not 16-byte aligned", fn);
-    const size_t need = w4::attention_workspace_bytes(T, B, Hq, hk, dim, p.cache.e4m3, max_q, max_kv, window);
+    const size_t need = w4::attention_workspace_bytes(T, B, Hq, hk, dim, p.cache.e4m3, max_q, plan_kv, window);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(W4_EINVAL, "%s: workspace of %zu bytes, these sizes need %zu (w4_tree_attention_workspace_bytes)", fn,
                     workspace ? workspace_bytes : size_t{0}, need);
