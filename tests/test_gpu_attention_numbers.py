@@ -65,3 +65,22 @@ def test_no_token_is_seen_where_the_bound_is_zero(form):
     out = torch.full((2 * n, hq, d), 7.0, dtype=torch.bfloat16, device=dev())
     args[7] = 0
     assert bool((w4.w4_tree_attention(*args, **kw, O=out) == 0).all())
+
+
+@pytest.mark.parametrize("stride", [1, 515, 1025])
+def test_a_single_row_has_any_stride(stride):
+    """The stride of a dimension of one row is arbitrary (of a slice, say): it is neither used nor checked."""
+    require_gpu()
+    import torch
+    import w4_dequant_gemm_amd as w4
+    rng = np.random.default_rng(stride)
+    args, kw, want, tol = _attend(rng, [1], [300], 8, 2, 64, 16, False, False)
+    odd = lambda x: x.as_strided(x.shape, (stride, x.stride(1), 1))  # noqa: E731
+    args[0] = odd(args[0])
+    assert np.max(np.abs(_f64(w4.w4_tree_attention(*args, **kw)) - want) / tol) <= 1
+    q, k = torch.randn((1, 8, 64), device=dev()).to(torch.bfloat16), torch.randn((1, 2, 64), device=dev()).to(torch.bfloat16)
+    slot = torch.tensor([5], dtype=torch.int32, device=dev())
+    caches = [w4.w4_kv_cache(1, 2, 64, 16, device=dev()) for _ in range(2)]
+    a = w4.w4_kv_append(q, k, k, slot, *caches[0])
+    b = w4.w4_kv_append(odd(q), odd(k), odd(k), slot, *caches[1])
+    assert torch.equal(a, b) and torch.equal(caches[0][0], caches[1][0]) and torch.equal(caches[0][1], caches[1][1])

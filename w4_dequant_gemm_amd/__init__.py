@@ -644,7 +644,7 @@ def _rows_arg(fn: str, x, name: str, heads: int, dim: int, T=None):
     st, sh, sd = x.stride()
     if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
         raise ValueError(f"{fn}: the heads of a row of {name} must be contiguous (strides {x.stride()})")
-    return x.data_ptr(), (st if shape[0] > 1 else max(st, heads * dim))
+    return x.data_ptr(), (st if shape[0] > 1 else heads * dim)   # (a single row's stride means nothing)
 
 
 def _vec(fn: str, x, name: str, n: int, dtype):
