@@ -177,3 +177,11 @@ def test_largest_integers_are_refused(lib):
     for f in (dict(B=most), dict(max_q=most), dict(max_kv=most), dict(pages=most)):
         assert _attend(lib, _cache(), **f) in (1, 2), f
     assert _append(lib, _cache(pages=most)) == 1
+
+
+def test_cache_sizes_are_not_rounded():
+    # a page of 24 tokens is not one of 16
+    import w4_dequant_gemm_amd as w4
+    for d, page, e4m3 in ((64, 24, False), (64, 0, False), (64, 8, True), (100, 16, False), (72, 16, True), (0, 16, False)):
+        with pytest.raises(ValueError, match="multiple"):
+            w4.w4_kv_cache(4, 2, d, page, e4m3=e4m3, device="cpu")

@@ -596,6 +596,8 @@ def w4_kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int, *, e4m
     """A zeroed paged cache ``(k, v)`` in the library's layout (``w4_kv_cache`` in ``w4.h``): bf16, or E4M3
     codes (uint8).  With ``layers`` the arrays hold that many layers; ``k[i]``, ``v[i]`` is one of them."""
     c = 16 if e4m3 else 8
+    if page_size <= 0 or page_size % 16 or head_dim <= 0 or head_dim % c:
+        raise ValueError(f"w4_kv_cache: page_size must be a multiple of 16 and head_dim of {c}, got {page_size} and {head_dim}")
     lead = (pages, kv_heads, page_size // 16)
     lead = lead if layers is None else (layers, *lead)
     dtype = torch.uint8 if e4m3 else torch.bfloat16
