@@ -84,3 +84,17 @@ def test_a_single_row_has_any_stride(stride):
     a = w4.w4_kv_append(q, k, k, slot, *caches[0])
     b = w4.w4_kv_append(odd(q), odd(k), odd(k), slot, *caches[1])
     assert torch.equal(a, b) and torch.equal(caches[0][0], caches[1][0]) and torch.equal(caches[0][1], caches[1][1])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 1.5])
+@pytest.mark.parametrize("form", FORMS, ids=str)
+def test_scales(form, scale, e4m3):
+    """Negative (the smallest product has the largest weight), zero (the mean of what a row sees), far above 1/sqrt(d)."""
+    require_gpu()
+    import w4_dequant_gemm_amd as w4
+    n, hq, hk, d = form
+    for tree, window in ((True, 0), (False, 150)):
+        args, kw, want, tol = _attend(np.random.default_rng(n + d), [n, n // 2], [n + 390, n // 2 + 7], hq, hk, d, 16, e4m3, tree, window, scale)
+        got = _f64(w4.w4_tree_attention(*args, **kw))
+        assert np.isfinite(got).all() and np.max(np.abs(got - want) / tol) <= 1, (tree, window)
