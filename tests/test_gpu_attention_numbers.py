@@ -98,3 +98,41 @@ def test_scales(form, scale, e4m3):
         args, kw, want, tol = _attend(np.random.default_rng(n + d), [n, n // 2], [n + 390, n // 2 + 7], hq, hk, d, 16, e4m3, tree, window, scale)
         got = _f64(w4.w4_tree_attention(*args, **kw))
         assert np.isfinite(got).all() and np.max(np.abs(got - want) / tol) <= 1, (tree, window)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("scale", [1e4, -1e4, 3e9, -3e9, 1e20, 1e30, -1e30])
+@pytest.mark.parametrize("form", FORMS, ids=str)
+def test_scores_far_apart(form, scale, e4m3):
+    """Products of small whole numbers are exact, so with a large scale a row's result is the mean of the values of its
+    largest products: equal weights for them and none for the others, whatever the size of the scores."""
+    require_gpu()
+    import torch
+    import w4_dequant_gemm_amd as w4
+    n, hq, hk, d = form
+    rng = np.random.default_rng(n + d)
+    past = 20000 if n < 8 else 390           # (the first forms with the tokens split over workgroups)
+    args, kw, _, _ = _attend(rng, [n], [past + n], hq, hk, d, 16, False, False)
+    q = torch.from_numpy(rng.integers(-2, 3, (n, hq, d)).astype(np.float32)).to(torch.bfloat16).to(dev())
+    # one KV head's keys and values [tokens, d] in the cache's places
+    keys, values = (rng.integers(-2, 3, (hk, past + n, d)).astype(np.float32) for _ in range(2))
+    c = 16 if e4m3 else 8
+    table = args[3].cpu().numpy()[0].astype(np.int64)
+    k_cache, v_cache = w4.w4_kv_cache(int(table.max()) + 1, hk, d, 16, device="cpu")
+    if e4m3:
+        k_cache, v_cache = (x.to(torch.float8_e4m3fn) for x in w4.w4_kv_cache(int(table.max()) + 1, hk, d, 16, e4m3=True, device="cpu"))
+        kw.update(k_scale=torch.full((hk,), 0.5, device=dev()), v_scale=torch.ones(hk, device=dev()))
+    t = np.arange(past + n)
+    for h in range(hk):
+        k_cache[table[t // 16], h, 0, :, t % 16] = torch.from_numpy(keys[h].reshape(-1, d // c, c)).to(k_cache.dtype)
+        v_cache[table[t // 16], h, 0, t % 16 // c, :, t % c] = torch.from_numpy(values[h]).to(v_cache.dtype)
+    args[:3] = q, *(x.view(torch.uint8 if e4m3 else x.dtype).to(dev()) for x in (k_cache, v_cache))
+    kw["scale"] = scale
+    got = _f64(w4.w4_tree_attention(*args, **kw))
+    qn = _f64(q)
+    for i in range(n):
+        for h in range(hq):
+            s = np.sign(scale) * (keys[h // (hq // hk), :past + i + 1].astype(np.float64) @ qn[i, h])
+            want = values[h // (hq // hk), :past + i + 1][s == s.max()].astype(np.float64).mean(0)
+            # one rounding to bf16, and the division's and the sums' to fp32
+            assert np.all(np.abs(got[i, h] - want) <= 1.01 * 2.0 ** -8 * np.abs(want) + 2.0 ** -20), (i, h)

@@ -150,15 +150,32 @@ struct Core {
                 for (int dt = 0; dt < DT; ++dt) O[r][dt] *= fade;
             }
         }
+        float base[R], by = scale;
+        bool far = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            base[r] = ref[r] == -INFINITY ? 0.0f : ref[r];
+            far = far || fabsf(base[r]) >= kFar;
+        }
+        if (__any(far)) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[r][t][j] = rounded_exponent(acc[r][t][j], scale, base[r]);
+                base[r] = 0.0f;
+            }
+            by = 1.0f;
+        }
         uint4 P[R][NP];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float base = ref[r] == -INFINITY ? 0.0f : ref[r];
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
                 float e[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) e[i] = exp2_fast(__builtin_fmaf(acc[r][2 * q + (i >> 2)][i & 3], scale, -base));
+                for (int i = 0; i < 8; ++i) e[i] = exp2_fast(__builtin_fmaf(acc[r][2 * q + (i >> 2)][i & 3], by, -base[r]));
                 P[r][q] = make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
                                      pack_bf16x2(e[6], e[7]));
             }
@@ -273,7 +290,7 @@ struct Core {
 // 8 of 128, bf16: 1.19 GB in 212 us, 5.6 TB/s, what a large copy moves; one
 // sequence of 517, 9 heads on 3 of 64: 8 us, of which most is the chain of a
 // launch's first reads (lengths, pages, keys, values).  D = 128, E4M3 and two row
-// tiles spill 24 bytes, outside the loop.
+// tiles spill 12 bytes, outside the loop.
 template <int D, int E, int R>
 __global__ void __launch_bounds__(256, 2) attention_stream_kernel(AttentionParams p, AttentionPlan pl) {
     using C = Core<D, E, R>;

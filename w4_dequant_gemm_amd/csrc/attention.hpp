@@ -18,6 +18,7 @@ struct AttentionPlan {
 };
 
 constexpr float kRaise = 8.0f;               // log2 of the largest p
+constexpr float kFar = 0x1p28f;              // references from here on: see rounded_exponent
 
 // whether any of a piece's values (8 bf16 or 16 E4M3) is infinite or NaN
 template <int E>
@@ -52,6 +53,15 @@ __device__ __forceinline__ float4_t mfma(const uint4& a, const uint4& b, const f
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The exponent of p for a score far from 0.  A fused x scale - ref keeps what
+// rounding the reference has lost, up to half a unit in its last place: the same
+// for all scores of a row, so it cancels, but from 2^31 on it may be 128, and
+// p infinite.  With the product rounded as the reference was, nothing is left.
+__device__ __forceinline__ float rounded_exponent(float x, float scale, float ref) {
+#pragma clang fp contract(off)
+    return x * scale - ref;
+}
 
 // maximum over the four lane groups (lanes m, m + 16, m + 32, m + 48)
 __device__ __forceinline__ float max_groups(float x) {

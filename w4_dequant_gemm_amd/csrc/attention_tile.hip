@@ -269,7 +269,15 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
 #pragma unroll
                 for (int db = 0; db < DB; ++db) O[db] *= fade;
             }
-            const float base = ref == -INFINITY ? 0.0f : ref;
+            float base = ref == -INFINITY ? 0.0f : ref, by = scale;
+            if (__any(fabsf(base) >= kFar)) {
+#pragma unroll
+                for (int u = 0; u < UW; ++u)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[u][i] = rounded_exponent(acc[u][i], scale, base);
+                base = 0.0f;
+                by = 1.0f;
+            }
             uint4 P[UW][2];
 #pragma unroll
             for (int u = 0; u < UW; ++u)
@@ -278,8 +286,8 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(AttentionParams 
                     uint32_t w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        w[i] = pack_bf16x2(exp2_fast(__builtin_fmaf(acc[u][8 * j + 2 * i], scale, -base)),
-                                           exp2_fast(__builtin_fmaf(acc[u][8 * j + 2 * i + 1], scale, -base)));
+                        w[i] = pack_bf16x2(exp2_fast(__builtin_fmaf(acc[u][8 * j + 2 * i], by, -base)),
+                                           exp2_fast(__builtin_fmaf(acc[u][8 * j + 2 * i + 1], by, -base)));
                         sum = dot2_bf16(w[i], 0x3F803F80u, sum);   // of the rounded p
                     }
                     P[u][j] = make_uint4(w[0], w[1], w[2], w[3]);
