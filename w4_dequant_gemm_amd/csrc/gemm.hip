@@ -871,17 +871,22 @@ __global__ void __launch_bounds__(64 * NW) gemm256_breg_kernel(MulParams p) {
         int64_t m = a_m + 8 * it;
         m = m < a_last ? m : a_last;
         const int chunk = (lane & 7) ^ swz(a_row0 + 8 * it);
-        const uint16_t* src = a_src + chunk * 8 + m * K + static_cast<int64_t>(kt) * BK;
+        const uint64_t row = reinterpret_cast<uintptr_t>(a_src + chunk * 8 + m * K);
+        const uint64_t k_bytes = static_cast<uint64_t>(kt) * (BK * 2);   // (uniform)
         // Issued as plain instructions: the compiler cannot tell the three
         // activation stages apart and would otherwise wait for every pending
         // direct-to-LDS load before any LDS read.  There is no register
         // result (the data goes to LDS at M0 + 16 lane), and completion is
         // covered by the explicit wait at the end of each step.  Loads the
         // compiler does not know of only make its own vmcnt waits stricter.
-        // (A load to LDS may follow a write of M0 after one wait state.)
+        // A load to LDS may follow a write of M0 after one wait state; the
+        // address is summed in it (with s_nop there: 830 against 809 us on the
+        // 70B shape).
         const uint32_t m0 = __builtin_amdgcn_readfirstlane(
             static_cast<uint32_t>(reinterpret_cast<uintptr_t>(stage + (wave * ADMA + it) * 512)));
-        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(m0) : "memory", "m0");
+        uint64_t src;
+        asm volatile("s_mov_b32 m0, %2\n\tv_lshl_add_u64 %0, %1, 0, %3\n\tglobal_load_lds_dwordx4 %0, off"
+                     : "=&v"(src) : "v"(row), "s"(m0), "s"(k_bytes) : "memory", "m0");
     };
 
     // weights: column n_base + 64 wave + 32 jb + lane % 32 (PAIR: of the
