@@ -5,6 +5,9 @@ arguments: torch tensors supply device memory and the current HIP stream,
 every step of the computation runs in the HIP library ``libw4.so``.  There is
 no CPU or PyTorch fallback: if the library is not built, or a call returns a
 non-zero status, the function raises.
+
+With ``stream=`` a call runs on that stream, and results and workspaces that it
+allocates come from that stream's memory; its inputs have to be ready there.
 """
 from __future__ import annotations
 
