@@ -91,9 +91,10 @@ def test_decoding_calls(monkeypatch):
     k = torch.randn((3, hk, d), device=dev()).to(torch.bfloat16)
     t = [i32(table), i32([length]), i32([0, 3]), i32([5, 70, 9])]
     assert w4.w4_tree_attention_workspace_bytes(3, 1, hq, hk, d, False, 3, length) > 0
-    given = [q, k, k_cache, v_cache, *t]
+    own = [(x.clone(), y.clone()) for x, y in [(k_cache, v_cache)] * 2]   # (appended to at the same time)
+    given = [q, k, k_cache, v_cache, *t, *own[0], *own[1]]
     _differ(w4, monkeypatch, "w4_tree_attention",
             lambda s: [w4.w4_tree_attention(q, k_cache, v_cache, t[0], t[1], t[2], 3, length, stream=s)], given)
-    _differ(w4, monkeypatch, "w4_kv_append", lambda s: [w4.w4_kv_append(q, k, k, t[3], k_cache, v_cache, stream=s)], given)
+    _differ(w4, monkeypatch, "w4_kv_append", lambda s: [w4.w4_kv_append(q, k, k, t[3], *own[s is None], stream=s)], given)
     x, u = torch.randn((9, 5000), device=dev()), torch.rand(9, device=dev())
     _differ(w4, monkeypatch, "w4_sample", lambda s: w4.w4_sample(x, u, stream=s), [x, u])
