@@ -348,6 +348,57 @@ int w4a8_gemm_e4m3(const uint8_t* xq, const float* xscale, int64_t M, int64_t K,
                    hipStream_t stream);
 
 /*
+ * Mixture-of-experts layer: w4_route chooses each token's experts, w4a16_moe runs
+ * their gated MLPs on 4-bit weights (the fused path of an expert model; gowda.ai
+ * "LLM fast inference", "Machete, with credit where it is due": model-specific
+ * fused paths; gsantana.dev "Quantizing LLMs Without Guesswork", "Production
+ * reality": small batches are bound by the weights they read).
+ *
+ * w4_route -- with l[t, e] = sum_h X[t, h] router[e, h] (fp32 sums) and the scores
+ *   s = softmax over the experts of l[t, .]   or   s = 1 / (1 + exp(-l))
+ * token t's choices are the top_k experts with the largest l, or with the
+ * largest s + bias[e] where a selection bias is given, in that order, ties to
+ * the lower index (NaN counts as -inf); their weights are s, divided by the sum
+ * over the choices if renormalize, then times scale.
+ *   X [T, H], router [E, H]  bf16;  H a multiple of 8;  E <= 1024, top_k <= 32.
+ *   bias       [E] fp32 or NULL.
+ *   ids        [T, top_k] int32 out;  weights [T, top_k] fp32 out.
+ *   workspace  w4_route_workspace_bytes(T, E) bytes, 16-byte aligned, its contents
+ *              irrelevant.
+ */
+#define W4_SCORE_SOFTMAX 0
+#define W4_SCORE_SIGMOID 1
+int w4_route(const uint16_t* X, int64_t T, int64_t H, const uint16_t* router, int64_t E, int top_k, int score,
+             const float* bias, int renormalize, float scale, int32_t* ids, float* weights, void* workspace,
+             size_t workspace_bytes, hipStream_t stream);
+size_t w4_route_workspace_bytes(int64_t T, int64_t E);
+
+/*
+ * w4a16_moe -- for token t with the experts e_j = ids[t, j] and weights w_j,
+ *   h_j  = w_j act(Wg'[e_j] . X[t]) * (Wu'[e_j] . X[t])
+ *   Y[t] = bf16(residual[t] + sum_j Wd'[e_j] . h_j)
+ * with W' = (q - z) s exact, fp32 accumulation, and h kept as the sum of two bf16
+ * numbers (16 bits of mantissa) between the products.  An id outside 0..E-1 is no
+ * expert (padding, or one that another process holds): its choice adds nothing,
+ * and a token without any gets its residual (or zeros).  A token may choose an
+ * expert twice.  Results do not depend on timing.
+ *   X          [T, H] bf16;  ids [T, top_k] int32;  weights [T, top_k] fp32.
+ *   wq_gate, sz_gate, wq_up, sz_up   the GPU layouts (w4_prepack) of the E experts'
+ *              [I, H] weights, one after the other; wq_down, sz_down of their [H, I]
+ *              weights.  H and I are multiples of G = 32, 64 or 128.
+ *   act        W4_ACT_SILU or W4_ACT_GELU_TANH.
+ *   residual   [T, H] bf16 or NULL; may be X or Y.
+ *   Y          [T, H] bf16 out, not X.
+ *   workspace  w4a16_moe_workspace_bytes bytes, 16-byte aligned, its contents
+ *              irrelevant; calls in flight together need separate ones.
+ */
+int w4a16_moe(const uint16_t* X, int64_t T, int64_t H, const int32_t* ids, const float* weights, int top_k,
+              const uint32_t* wq_gate, const uint32_t* sz_gate, const uint32_t* wq_up, const uint32_t* sz_up,
+              const uint32_t* wq_down, const uint32_t* sz_down, int64_t E, int64_t I, int G, int act,
+              const uint16_t* residual, uint16_t* Y, void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t w4a16_moe_workspace_bytes(int64_t T, int top_k, int64_t E, int64_t H, int64_t I, int G);
+
+/*
  * NF4 comparator (gsantana.dev "Quantizing LLMs Without Guesswork",
  * "Weight-only methods: GPTQ, AWQ and the file formats", the NF4 paragraph):
  * 16 levels that are normal quantiles (QLoRA's construction: 8 positive and 7
@@ -526,6 +577,43 @@ int w4_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_s
               int32_t* tokens, float* probs, hipStream_t stream);
 
 /*
+ * w4_adjust_logits -- what a serving loop does to logits before w4_sample:
+ * penalties for tokens that came before, biases of single tokens, and masks (a
+ * grammar's, say), in one pass.  For row b and token v, with c_all how often v is
+ * in the row's history and c how often behind its first prompt_len[b] tokens, in
+ * fp32 and in this order, rounded once to the logits' type:
+ *   x = logits[b, v]
+ *   c_all > 0:   x = x > 0 ? x / repetition[b] : x * repetition[b]
+ *   c > 0:       x = x - frequency[b] * c - presence[b]
+ *   a bias entry of v:  x = x + value   (of several entries of v the last one)
+ *   mask bit 0:  x = -inf
+ * NaN stays NaN unless masked.  A mask may leave a row nothing: all -inf.
+ *   logits       bf16 or fp32 (W4_LOGITS_*), [B, V], rows row_stride elements
+ *                apart (0: the same row for all); V <= 2^20.  No alignment
+ *                beyond the elements'.
+ *   history      [history_len] int32, row b's tokens are history_start[b] ..
+ *                history_start[b + 1] - 1 (history_start [B + 1] int32; cut to
+ *                the array); tokens outside 0..V-1 are not counted.  NULL: none.
+ *   prompt_len   [B] int32 or NULL: 0 (all of the history is penalised by
+ *                presence and frequency too).
+ *   repetition, presence, frequency   [B] fp32, each may be NULL: 1, 0, 0.
+ *                repetition > 0.
+ *   bias_ids, bias_values  [bias_len] int32 and fp32, row b's entries are
+ *                bias_start[b] .. bias_start[b + 1] - 1, as for the history;
+ *                entries outside 0..V-1 are left out.  All three NULL: none.
+ *   mask         uint32 words, bit v % 32 of word v / 32 allows v; rows
+ *                mask_stride words apart (0: one mask for all rows).  NULL: all
+ *                allowed.
+ *   out          as logits, rows out_stride >= V elements apart; may be logits
+ *                itself, with the same stride, but must not overlap it otherwise.
+ */
+int w4_adjust_logits(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride, const int32_t* history,
+                     int64_t history_len, const int32_t* history_start, const int32_t* prompt_len, const float* repetition,
+                     const float* presence, const float* frequency, const int32_t* bias_start, const int32_t* bias_ids,
+                     const float* bias_values, int64_t bias_len, const uint32_t* mask, int64_t mask_stride, void* out,
+                     int64_t out_stride, hipStream_t stream);
+
+/*
  * w4_kv_move -- keep an accepted path: in every layer, the token base[b] +
  * path[b, j] of sequence b moves to base[b] + j, for j < count[b], keys and
  * values alike.  path rows ascend strictly (path[b, j] >= j), so no token is
@@ -585,7 +673,7 @@ const char* w4_status_string(int status);
 const char* w4_last_error(void);
 
 /* Version of this ABI, currently 4; it counts changes of calls that were there,
- * so the decoding calls, added since, kept it (4: w4a16_gate_up takes an optional
+ * so the decoding and mixture-of-experts calls, added since, kept it (4: w4a16_gate_up takes an optional
  * workspace, w4a16_gate_up_workspace_bytes; 3: w4a8_gate_up emits the down
  * projection's E4M3 input; w4a8_gemm_e4m3; w4a16_gemm_noalloc). */
 int w4_abi_version(void);

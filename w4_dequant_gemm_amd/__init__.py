@@ -28,7 +28,8 @@ __all__ = [
     "w4_nf4_levels", "w4_nf4_quantize", "w4_nf4_gemv",
     "FRACS_PLAIN", "FRACS_11",
     "w4_kv_cache", "w4_kv_append", "w4_tree_attention", "w4_tree_attention_workspace_bytes", "w4_sample",
-    "w4_kv_move",
+    "w4_kv_move", "w4_adjust_logits",
+    "w4_route", "w4_route_workspace_bytes", "w4a16_moe", "w4a16_moe_workspace_bytes",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -127,7 +128,16 @@ def lib():
     L.w4_tree_attention_workspace_bytes.restype = sz_t
     L.w4_sample.argtypes = [P, I, i64, i64, i64, P, P, P, P, P, P, P, P]
     L.w4_kv_move.argtypes = [C, P, i64, P, P, i64, P, i64, P]
-    for name in ("w4_kv_append", "w4_tree_attention", "w4_sample", "w4_kv_move"):
+    L.w4_adjust_logits.argtypes = [P, I, i64, i64, i64, P, i64, P, P, P, P, P, P, P, P, i64, P, i64, P, i64, P]
+    for name in ("w4_kv_append", "w4_tree_attention", "w4_sample", "w4_kv_move", "w4_adjust_logits"):
+        getattr(L, name).restype = I
+    L.w4_route.argtypes = [P, i64, i64, P, i64, I, I, P, I, f32, P, P, P, sz_t, P]
+    L.w4_route_workspace_bytes.argtypes = [i64, i64]
+    L.w4_route_workspace_bytes.restype = sz_t
+    L.w4a16_moe.argtypes = [P, i64, i64, P, P, I, P, P, P, P, P, P, i64, i64, I, I, P, P, P, sz_t, P]
+    L.w4a16_moe_workspace_bytes.argtypes = [i64, I, i64, i64, i64, I]
+    L.w4a16_moe_workspace_bytes.restype = sz_t
+    for name in ("w4_route", "w4a16_moe"):
         getattr(L, name).restype = I
     L.w4_status_string.argtypes = [I]
     L.w4_status_string.restype = ctypes.c_char_p
@@ -554,6 +564,85 @@ def w4a8_gemm_e4m3(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, sz:
     return Y
 
 
+# -------------------------------------------------- mixture of experts
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+@functools.lru_cache(maxsize=4096)
+def w4_route_workspace_bytes(T: int, E: int) -> int:
+    """Workspace bytes ``w4_route`` needs."""
+    return int(lib().w4_route_workspace_bytes(T, E))
+
+
+def w4_route(X: torch.Tensor, router: torch.Tensor, top_k: int, *, score="softmax", bias=None, renormalize: bool = True,
+             scale: float = 1.0, ids=None, weights=None, workspace=None, stream=None):
+    """Each token's ``top_k`` experts by the bf16 ``router`` [E, H] for bf16 ``X`` [T, H]: (ids int32 [T, top_k],
+    weights fp32 [T, top_k]).  ``score`` is ``"softmax"`` or ``"sigmoid"``; ``bias`` (fp32 [E]) is added to the
+    scores to choose but not to weigh."""
+    fn = "w4_route"
+    if X.dim() != 2 or router.dim() != 2 or X.shape[1] != router.shape[1]:
+        raise ValueError(f"{fn}: X must be [T, H] and router [E, H], got {tuple(X.shape)} and {tuple(router.shape)}")
+    if score not in _SCORES:
+        raise ValueError(f"{fn}: score must be one of {sorted(_SCORES)}, got {score!r}")
+    (T, H), E, dev = X.shape, router.shape[0], X.device
+    ids = _empty((T, top_k), torch.int32, dev, stream) if ids is None else ids
+    weights = _empty((T, top_k), torch.float32, dev, stream) if weights is None else weights
+    if workspace is None:
+        workspace = _scratch(w4_route_workspace_bytes(T, E), dev, stream)
+    rc = lib().w4_route(_dev(X, "X", torch.bfloat16), T, H, _dev(router, "router", torch.bfloat16), E, top_k, _SCORES[score],
+                        _vec(fn, bias, "bias", E, torch.float32), renormalize, scale,
+                        _vec(fn, ids, "ids", T * top_k, torch.int32), _vec(fn, weights, "weights", T * top_k, torch.float32),
+                        _dev(workspace, "workspace"), _nbytes(workspace), _stream(dev, stream))
+    _check(fn, rc)
+    return ids, weights
+
+
+@functools.lru_cache(maxsize=4096)
+def w4a16_moe_workspace_bytes(T: int, top_k: int, E: int, H: int, I: int, G: int) -> int:
+    """Workspace bytes ``w4a16_moe`` needs."""
+    return int(lib().w4a16_moe_workspace_bytes(T, top_k, E, H, I, G))
+
+
+def _expert_weight(fn: str, w: dict, name: str, E: int, N: int, K: int, G: int):
+    """Pointers of E stacked GPU layouts of [N, K] weights."""
+    wq, sz = w["wq"], w["sz"]
+    if _nbytes(wq) != E * N * K // 2 or _nbytes(sz) != 4 * E * N * (K // G):
+        raise ValueError(f"{fn}: {name} holds {_nbytes(wq)} bytes of codes and {_nbytes(sz)} of scales; {E} experts of "
+                         f"[{N}, {K}] with G = {G} need {E * N * K // 2} and {4 * E * N * (K // G)}")
+    return _dev(wq, f"{name} wq"), _dev(sz, f"{name} sz")
+
+
+def w4a16_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: dict, up: dict, down: dict, G: int,
+              act="silu", *, residual=None, Y=None, workspace=None, stream=None):
+    """The experts' gated MLPs for bf16 ``X`` [T, H]: token t's choices are ``ids`` (int32 [T, top_k]; outside the
+    experts: none) with ``weights`` (fp32).  ``gate``, ``up`` and ``down`` are GPU layouts of ``w4_prepack`` stacked
+    over the experts (``wq`` [E, N, K/8], ``sz`` [E, N, K/G]).  Returns bf16 [T, H], ``residual`` (bf16 [T, H]) added."""
+    fn = "w4a16_moe"
+    if X.dim() != 2 or ids.dim() != 2 or ids.shape[0] != X.shape[0] or tuple(weights.shape) != tuple(ids.shape):
+        raise ValueError(f"{fn}: X must be [T, H], ids and weights [T, top_k], got {tuple(X.shape)}, {tuple(ids.shape)} and "
+                         f"{tuple(weights.shape)}")
+    if gate["wq"].dim() != 3:
+        raise ValueError(f"{fn}: gate wq must be [E, I, H/8], got {tuple(gate['wq'].shape)}")
+    (T, H), top_k, (E, I, _), dev = X.shape, ids.shape[1], gate["wq"].shape, X.device
+    if G <= 0 or H % G or I % G:
+        raise ValueError(f"{fn}: H = {H} and I = {I} must be multiples of the group size G = {G}")
+    pointers = (*_expert_weight(fn, gate, "gate", E, I, H, G), *_expert_weight(fn, up, "up", E, I, H, G),
+                *_expert_weight(fn, down, "down", E, H, I, G))
+    for t, name in ((Y, "Y"), (residual, "residual")):
+        if t is not None and tuple(t.shape) != (T, H):
+            raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {(T, H)}")
+    Y = _empty((T, H), torch.bfloat16, dev, stream) if Y is None else Y
+    if workspace is None:
+        workspace = _scratch(w4a16_moe_workspace_bytes(T, top_k, E, H, I, G), dev, stream)
+    rc = lib().w4a16_moe(_dev(X, "X", torch.bfloat16), T, H, _dev(ids, "ids", torch.int32),
+                         _dev(weights, "weights", torch.float32), top_k, *pointers, E, I, G, _ACTS[act],
+                         _dev(residual, "residual", torch.bfloat16), _dev(Y, "Y", torch.bfloat16),
+                         _dev(workspace, "workspace"), _nbytes(workspace), _stream(dev, stream))
+    _check(fn, rc)
+    return Y
+
+
 # -------------------------------------------------------- NF4 comparator
 
 def w4_nf4_levels():
@@ -762,6 +851,58 @@ def w4_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=None, top_k=
                          _vec(fn, probs, "probs", B, torch.float32), _stream(dev, stream))
     _check(fn, rc)
     return tokens, probs
+
+
+def _logits_arg(fn: str, x, name: str):
+    """Pointer, type and row stride of logits [B, V] whose rows are contiguous."""
+    if x.dim() != 2 or not x.is_cuda or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{fn}: {name} must be a device tensor [B, V] with contiguous rows")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{fn}: {name} must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    return x.data_ptr(), (1 if x.dtype == torch.float32 else 0), (x.stride(0) if x.shape[0] > 1 else x.shape[1])
+
+
+def w4_adjust_logits(logits: torch.Tensor, *, history=None, history_start=None, prompt_len=None, repetition=None,
+                     presence=None, frequency=None, bias_start=None, bias_ids=None, bias_values=None, mask=None,
+                     out=None, stream=None):
+    """Penalties for repeated tokens, biases and masks on ``logits`` [B, V] (bf16 or fp32; rows may be strided).
+    Row b's earlier tokens are ``history`` (int32) [history_start[b] : history_start[b + 1]], the first
+    ``prompt_len[b]`` of them its prompt, which only ``repetition`` counts; ``repetition``, ``presence`` and
+    ``frequency`` are fp32 [B].  ``bias_ids`` (int32) and ``bias_values`` (fp32) are split by ``bias_start`` alike.
+    ``mask``: int32 [B, ceil(V / 32)] or [1, ...] for all rows, a bit a token, 0 forbids it.  Returns ``out`` (new
+    by default; ``out=logits`` works in place)."""
+    fn = "w4_adjust_logits"
+    xp, f32, xs = _logits_arg(fn, logits, "logits")
+    B, V = logits.shape
+    dev = logits.device
+    if out is None:
+        out = _empty((B, V), logits.dtype, dev, stream)
+    elif tuple(out.shape) != (B, V) or out.dtype != logits.dtype:
+        raise ValueError(f"{fn}: out must be {logits.dtype} of shape {(B, V)}, got {out.dtype} of {tuple(out.shape)}")
+    op, _, os_ = _logits_arg(fn, out, "out")
+    if (history is None) != (history_start is None):
+        raise ValueError(f"{fn}: history and history_start must both be given or both be None")
+    if len({bias_start is None, bias_ids is None, bias_values is None}) > 1:
+        raise ValueError(f"{fn}: bias_start, bias_ids and bias_values must all be given or all be None")
+    nh = history.numel() if history is not None else 0
+    nb = bias_ids.numel() if bias_ids is not None else 0
+    words, ms = -(-V // 32), 0
+    if mask is not None:
+        if mask.dim() != 2 or mask.shape[1] != words or mask.shape[0] not in (1, B):
+            raise ValueError(f"{fn}: mask must be [{B} or 1, {words}], got {tuple(mask.shape)}")
+        ms = words if mask.shape[0] > 1 else 0
+    rc = lib().w4_adjust_logits(xp, f32, B, V, xs, _dev(history, "history", torch.int32), nh,
+                                _vec(fn, history_start, "history_start", B + 1, torch.int32),
+                                _vec(fn, prompt_len, "prompt_len", B, torch.int32),
+                                _vec(fn, repetition, "repetition", B, torch.float32),
+                                _vec(fn, presence, "presence", B, torch.float32),
+                                _vec(fn, frequency, "frequency", B, torch.float32),
+                                _vec(fn, bias_start, "bias_start", B + 1, torch.int32),
+                                _dev(bias_ids, "bias_ids", torch.int32),
+                                _vec(fn, bias_values, "bias_values", nb, torch.float32),
+                                nb, _dev(mask, "mask", torch.int32), ms, op, os_, _stream(dev, stream))
+    _check(fn, rc)
+    return out
 
 
 def w4_kv_move(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor, base: torch.Tensor,

@@ -1,8 +1,8 @@
 """Build the HIP library ``w4_dequant_gemm_amd/libw4.so`` for gfx950 with hipcc.
 
 Every kernel source is compiled for gfx950 only, with packed fp32 ops disabled
-and IEEE-correct fp32 division; the quantizer and the row quantizer are also
-built without FMA contraction so that their results are bit-reproducible.
+and IEEE-correct fp32 division; the quantizer, the row quantizer and the
+changes to logits are also built without FMA contraction so that their results are bit-reproducible.
 """
 from __future__ import annotations
 
@@ -23,11 +23,11 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 KERNELS = ["quantize.hip", "prepack.hip", "rowquant.hip", "skinny.hip", "gemm.hip", "nf4.hip", "noalloc.hip", "gemm_f8.hip",
-           "kvcache.hip", "attention.hip", "attention_tile.hip", "sample.hip"]
-NO_CONTRACT = {"quantize.hip", "rowquant.hip", "nf4.hip"}
+           "kvcache.hip", "attention.hip", "attention_tile.hip", "sample.hip", "adjust.hip", "route.hip", "moe.hip"]
+NO_CONTRACT = {"quantize.hip", "rowquant.hip", "nf4.hip", "adjust.hip"}
 # kernels whose MFMA results take VALU work: results in VGPRs, not AGPRs
-MFMA_VGPR = {"gemm_f8.hip", "attention.hip", "attention_tile.hip"}
-HOST_SOURCES = ["api.cpp", "decode_api.cpp", "portable.cpp"]   # host C++ (argument checks, file I/O)
+MFMA_VGPR = {"gemm_f8.hip", "attention.hip", "attention_tile.hip", "moe.hip"}
+HOST_SOURCES = ["api.cpp", "decode_api.cpp", "moe_api.cpp", "portable.cpp"]   # host C++ (argument checks, file I/O)
 
 HIP_FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
              "-fhip-fp32-correctly-rounded-divide-sqrt",

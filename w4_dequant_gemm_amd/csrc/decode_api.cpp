@@ -17,6 +17,7 @@ using w4::hip_status;
 constexpr int64_t kInt32Most = 0x7FFFFFFF;
 constexpr int64_t kMaxLength = int64_t{1} << 29;   // tokens of one sequence
 constexpr int64_t kMaxVocab = int64_t{1} << 20;
+constexpr int64_t kMaxStride = int64_t{1} << 40;   // elements between rows: 65535 of them stay within 64 bits
 
 long long ll(int64_t v) { return static_cast<long long>(v); }
 
@@ -204,6 +205,61 @@ int w4_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_s
     const w4::SampleParams p{logits, dtype == W4_LOGITS_F32, static_cast<int>(B), static_cast<int>(V), row_stride, u,
                              temperature, top_k, top_p, min_p, tokens, probs};
     return hip_status(w4::launch_sample(p, stream), fn);
+}
+
+int w4_adjust_logits(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride, const int32_t* history,
+                     int64_t history_len, const int32_t* history_start, const int32_t* prompt_len, const float* repetition,
+                     const float* presence, const float* frequency, const int32_t* bias_start, const int32_t* bias_ids,
+                     const float* bias_values, int64_t bias_len, const uint32_t* mask, int64_t mask_stride, void* out,
+                     int64_t out_stride, hipStream_t stream) {
+    const char* fn = "w4_adjust_logits";
+    if (dtype != W4_LOGITS_BF16 && dtype != W4_LOGITS_F32)
+        return fail(W4_EINVAL, "%s: dtype %d is neither W4_LOGITS_BF16 nor W4_LOGITS_F32", fn, dtype);
+    if (B < 0 || B > 65535) return fail(W4_EINVAL, "%s: B = %lld outside 0..65535", fn, ll(B));
+    if (V <= 0) return fail(W4_EINVAL, "%s: V = %lld must be > 0", fn, ll(V));
+    if (V > kMaxVocab) return fail(W4_EUNSUPPORTED, "%s: V = %lld above 2^20", fn, ll(V));
+    if (row_stride != 0 && (row_stride < V || row_stride > kMaxStride))
+        return fail(W4_EINVAL, "%s: row_stride = %lld is neither 0 (one row for all) nor V = %lld to 2^40", fn, ll(row_stride), ll(V));
+    if (out_stride < V || out_stride > kMaxStride)
+        return fail(W4_EINVAL, "%s: out_stride = %lld outside V = %lld .. 2^40", fn, ll(out_stride), ll(V));
+    if (history_len < 0 || history_len > kInt32Most || bias_len < 0 || bias_len > kInt32Most)
+        return fail(W4_EINVAL, "%s: history_len = %lld or bias_len = %lld outside 0..2^31 - 1", fn, ll(history_len), ll(bias_len));
+    if (mask && (mask_stride < 0 || mask_stride > kMaxStride || (mask_stride != 0 && mask_stride < (V + 31) / 32)))
+        return fail(W4_EINVAL, "%s: mask_stride = %lld is neither 0 (one mask for all rows) nor ceil(V / 32) to 2^40", fn, ll(mask_stride));
+    if (B == 0) return W4_OK;
+    if (!logits || !out) return fail(W4_EINVAL, "%s: logits or out is NULL", fn);
+    const uintptr_t size = dtype == W4_LOGITS_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(logits) % size != 0 || reinterpret_cast<uintptr_t>(out) % size != 0)
+        return fail(W4_EINVAL, "%s: logits or out is not aligned to its elements", fn);
+    if (logits == out && row_stride != out_stride && B > 1)
+        return fail(W4_EINVAL, "%s: in place, the rows of logits and out must be equally far apart", fn);
+    if (history && !history_start) return fail(W4_EINVAL, "%s: history without history_start", fn);
+    if (!history && history_len > 0) return fail(W4_EINVAL, "%s: history is NULL and history_len is not 0", fn);
+    if (!bias_ids != !bias_values || (bias_ids && !bias_start))
+        return fail(W4_EINVAL, "%s: bias_start, bias_ids and bias_values must all be given or all be NULL", fn);
+    if (!bias_ids && bias_len > 0) return fail(W4_EINVAL, "%s: bias_ids is NULL and bias_len is not 0", fn);
+    w4::AdjustParams p{};
+    p.logits = logits;
+    p.f32 = dtype == W4_LOGITS_F32;
+    p.B = static_cast<int>(B);
+    p.V = static_cast<int>(V);
+    p.row_stride = row_stride;
+    p.history = history_len > 0 ? history : nullptr;
+    p.history_len = history_len;
+    p.history_start = history_start;
+    p.prompt_len = prompt_len;
+    p.repetition = repetition;
+    p.presence = presence;
+    p.frequency = frequency;
+    p.bias_start = bias_start;
+    p.bias_ids = bias_len > 0 ? bias_ids : nullptr;
+    p.bias_values = bias_values;
+    p.bias_len = bias_len;
+    p.mask = mask;
+    p.mask_stride = mask_stride;
+    p.out = out;
+    p.out_stride = out_stride;
+    return hip_status(w4::launch_adjust(p, stream), fn);
 }
 
 int w4_kv_move(const w4_kv_cache* cache, const int32_t* page_table, int64_t table_pages, const int32_t* base,

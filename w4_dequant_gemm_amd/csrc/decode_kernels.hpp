@@ -87,4 +87,27 @@ struct SampleParams {
 };
 hipError_t launch_sample(const SampleParams& p, hipStream_t stream);
 
+struct AdjustParams {
+    const void* logits;
+    bool f32;
+    int B, V;
+    int64_t row_stride;
+    const int32_t* history;        // or null; [history_len], row b has history_start[b] .. history_start[b + 1] - 1
+    int64_t history_len;
+    const int32_t* history_start;
+    const int32_t* prompt_len;
+    const float* repetition;
+    const float* presence;
+    const float* frequency;
+    const int32_t* bias_start;     // bias entries alike, or null
+    const int32_t* bias_ids;
+    const float* bias_values;
+    int64_t bias_len;
+    const uint32_t* mask;          // or null
+    int64_t mask_stride;
+    void* out;
+    int64_t out_stride;
+};
+hipError_t launch_adjust(const AdjustParams& p, hipStream_t stream);
+
 }  // namespace w4
