@@ -348,6 +348,36 @@ int w4a8_gemm_e4m3(const uint8_t* xq, const float* xscale, int64_t M, int64_t K,
                    hipStream_t stream);
 
 /*
+ * w4a16_linear, w4a8_linear, w4a8_linear_e4m3 -- w4a16_gemm, w4a8_gemm and
+ * w4a8_gemm_e4m3 with bias, activation and residual in the epilogue:
+ *   Y[m, n] = bf16(act(sum + bias[n]) + residual[m, n])
+ * with `sum` the product's fp32 sum (row scale applied), everything in fp32 and
+ * one rounding at the end: the products of a served layer (queries, keys and
+ * values with a bias, attention's and the MLP's output added to the stream, an
+ * MLP without a gate) in one pass over the output (gowda.ai "LLM fast
+ * inference", "Machete, with credit where it is due": model-specific fused
+ * paths).
+ *   bias       [N] fp32 or NULL.
+ *   act        W4_ACT_NONE, _SILU, _GELU_TANH, _RELU or _GELU (the erf form).
+ *   residual   [M, N] bf16, 16-byte aligned, or NULL; may be Y itself.
+ *   Without any of the three the results are those of the plain products.
+ *   Workspaces (w4_gemm_workspace_bytes, w4a8_gemm_workspace_bytes) and the other
+ *   arguments as for those.
+ */
+#define W4_ACT_NONE 0
+#define W4_ACT_RELU 3
+#define W4_ACT_GELU 4
+int w4a16_linear(const uint16_t* X, int64_t M, int64_t K, const uint32_t* wq, const uint32_t* sz, int64_t N, int G,
+                 const float* bias, int act, const uint16_t* residual, uint16_t* Y, void* workspace,
+                 size_t workspace_bytes, hipStream_t stream);
+int w4a8_linear(const uint16_t* X, int64_t M, int64_t K, const uint32_t* wq, const uint32_t* sz, int64_t N, int G,
+                const float* bias, int act, const uint16_t* residual, uint16_t* Y, uint8_t* xq, float* xscale,
+                void* workspace, size_t workspace_bytes, hipStream_t stream);
+int w4a8_linear_e4m3(const uint8_t* xq, const float* xscale, int64_t M, int64_t K, const uint32_t* wq,
+                     const uint32_t* sz, int64_t N, int G, const float* bias, int act, const uint16_t* residual,
+                     uint16_t* Y, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Mixture-of-experts layer: w4_route chooses each token's experts, w4a16_moe runs
  * their gated MLPs on 4-bit weights (the fused path of an expert model; gowda.ai
  * "LLM fast inference", "Machete, with credit where it is due": model-specific
@@ -673,7 +703,7 @@ const char* w4_status_string(int status);
 const char* w4_last_error(void);
 
 /* Version of this ABI, currently 4; it counts changes of calls that were there,
- * so the decoding and mixture-of-experts calls, added since, kept it (4: w4a16_gate_up takes an optional
+ * so calls added since kept it (4: w4a16_gate_up takes an optional
  * workspace, w4a16_gate_up_workspace_bytes; 3: w4a8_gate_up emits the down
  * projection's E4M3 input; w4a8_gemm_e4m3; w4a16_gemm_noalloc). */
 int w4_abi_version(void);

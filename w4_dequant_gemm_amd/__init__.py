@@ -29,7 +29,7 @@ __all__ = [
     "FRACS_PLAIN", "FRACS_11",
     "w4_kv_cache", "w4_kv_append", "w4_tree_attention", "w4_tree_attention_workspace_bytes", "w4_sample",
     "w4_kv_move", "w4_adjust_logits",
-    "w4_route", "w4_route_workspace_bytes", "w4a16_moe", "w4a16_moe_workspace_bytes",
+    "w4a16_linear", "w4a8_linear", "w4a8_linear_e4m3", "w4_route", "w4_route_workspace_bytes", "w4a16_moe", "w4a16_moe_workspace_bytes",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -130,6 +130,11 @@ def lib():
     L.w4_kv_move.argtypes = [C, P, i64, P, P, i64, P, i64, P]
     L.w4_adjust_logits.argtypes = [P, I, i64, i64, i64, P, i64, P, P, P, P, P, P, P, P, i64, P, i64, P, i64, P]
     for name in ("w4_kv_append", "w4_tree_attention", "w4_sample", "w4_kv_move", "w4_adjust_logits"):
+        getattr(L, name).restype = I
+    L.w4a16_linear.argtypes = [P, i64, i64, P, P, i64, I, P, I, P, P, P, sz_t, P]
+    L.w4a8_linear.argtypes = [P, i64, i64, P, P, i64, I, P, I, P, P, P, P, P, sz_t, P]
+    L.w4a8_linear_e4m3.argtypes = [P, P, i64, i64, P, P, i64, I, P, I, P, P, P, sz_t, P]
+    for name in ("w4a16_linear", "w4a8_linear", "w4a8_linear_e4m3"):
         getattr(L, name).restype = I
     L.w4_route.argtypes = [P, i64, i64, P, i64, I, I, P, I, f32, P, P, P, sz_t, P]
     L.w4_route_workspace_bytes.argtypes = [i64, i64]
@@ -483,6 +488,71 @@ def w4a8_gemm(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *, Y=
     return Y, xq, xscale
 
 
+# activations of the products with an epilogue (gate and up take the gated two)
+_LINEAR_ACTS = {None: 0, "none": 0, "silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH, "relu": 3, "gelu": 4}
+
+
+def _epilogue_args(fn: str, M: int, N: int, bias, act, residual):
+    if act not in _LINEAR_ACTS:
+        raise ValueError(f"{fn}: act must be None, 'none', 'silu', 'gelu_tanh', 'relu' or 'gelu', got {act!r}")
+    if residual is not None and tuple(residual.shape) != (M, N):
+        raise ValueError(f"{fn}: residual has shape {tuple(residual.shape)}, expected ({M}, {N})")
+    return _vec(fn, bias, "bias", N, torch.float32), _LINEAR_ACTS[act], _dev(residual, "residual", torch.bfloat16)
+
+
+def w4a16_linear(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *, bias=None, act=None, residual=None,
+                 Y=None, workspace=None, stream=None):
+    """``w4a16_gemm`` with its epilogue: ``Y[M, N] = bf16(act(X . W'^T + bias) + residual)``.  ``bias`` is fp32 [N],
+    ``act`` None, ``"silu"``, ``"gelu_tanh"``, ``"gelu"`` (erf) or ``"relu"``, ``residual`` bf16 [M, N] (may be ``Y``)."""
+    fn = "w4a16_linear"
+    M, K, N = _check_product_shapes(fn, X, wq, sz, G, Y=Y)
+    dev = X.device
+    epilogue = _epilogue_args(fn, M, N, bias, act, residual)
+    Y = _empty((M, N), torch.bfloat16, dev, stream) if Y is None else Y
+    ws, ws_bytes = _workspace(M, K, N, dev, workspace, stream)
+    rc = lib().w4a16_linear(_dev(X, "X", torch.bfloat16), M, K, _dev(wq, "wq"), _dev(sz, "sz"), N, G, *epilogue,
+                            _dev(Y, "Y", torch.bfloat16), ws, ws_bytes, _stream(dev, stream))
+    _check(fn, rc)
+    return Y
+
+
+def w4a8_linear(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *, bias=None, act=None, residual=None,
+                Y=None, xq=None, xscale=None, workspace=None, stream=None):
+    """``w4a8_gemm`` with the epilogue of ``w4a16_linear``; returns (Y, xq, xscale)."""
+    fn = "w4a8_linear"
+    M, K, N = _check_product_shapes(fn, X, wq, sz, G, Y=Y, xq=xq, xscale=xscale)
+    dev = X.device
+    epilogue = _epilogue_args(fn, M, N, bias, act, residual)
+    Y = _empty((M, N), torch.bfloat16, dev, stream) if Y is None else Y
+    xq = _empty((M, K), torch.uint8, dev, stream) if xq is None else xq
+    xscale = _empty((M,), torch.float32, dev, stream) if xscale is None else xscale
+    ws, ws_bytes = _workspace(M, K, N, dev, workspace, stream, w4a8=True)
+    rc = lib().w4a8_linear(_dev(X, "X", torch.bfloat16), M, K, _dev(wq, "wq"), _dev(sz, "sz"), N, G, *epilogue,
+                           _dev(Y, "Y", torch.bfloat16), _dev(xq, "xq"), _dev(xscale, "xscale", torch.float32),
+                           ws, ws_bytes, _stream(dev, stream))
+    _check(fn, rc)
+    return Y, xq, xscale
+
+
+def w4a8_linear_e4m3(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *, bias=None,
+                     act=None, residual=None, Y=None, workspace=None, stream=None):
+    """``w4a8_gemm_e4m3`` with the epilogue of ``w4a16_linear``: a down projection on ``w4a8_gate_up``'s E4M3 rows added
+    to the residual stream, say."""
+    fn = "w4a8_linear_e4m3"
+    if xq.element_size() != 1:
+        raise ValueError(f"{fn}: xq must hold one byte per element")
+    M, K, N = _check_product_shapes(fn, xq, wq, sz, G, Y=Y, xscale=xscale)
+    dev = xq.device
+    epilogue = _epilogue_args(fn, M, N, bias, act, residual)
+    Y = _empty((M, N), torch.bfloat16, dev, stream) if Y is None else Y
+    ws, ws_bytes = _workspace(M, K, N, dev, workspace, stream, w4a8=True)
+    rc = lib().w4a8_linear_e4m3(_dev(xq, "xq"), _dev(xscale, "xscale", torch.float32), M, K, _dev(wq, "wq"),
+                                _dev(sz, "sz"), N, G, *epilogue, _dev(Y, "Y", torch.bfloat16), ws, ws_bytes,
+                                _stream(dev, stream))
+    _check(fn, rc)
+    return Y
+
+
 def w4a16_gate_up_workspace_bytes(M: int, K: int, N: int) -> int:
     """Workspace bytes that let ``w4a16_gate_up`` split K in its last round (0: no split)."""
     return int(lib().w4a16_gate_up_workspace_bytes(M, K, N))
@@ -604,13 +674,11 @@ def w4a16_moe_workspace_bytes(T: int, top_k: int, E: int, H: int, I: int, G: int
     return int(lib().w4a16_moe_workspace_bytes(T, top_k, E, H, I, G))
 
 
-def _expert_weight(fn: str, w: dict, name: str, E: int, N: int, K: int, G: int):
-    """Pointers of E stacked GPU layouts of [N, K] weights."""
-    wq, sz = w["wq"], w["sz"]
-    if _nbytes(wq) != E * N * K // 2 or _nbytes(sz) != 4 * E * N * (K // G):
-        raise ValueError(f"{fn}: {name} holds {_nbytes(wq)} bytes of codes and {_nbytes(sz)} of scales; {E} experts of "
-                         f"[{N}, {K}] with G = {G} need {E * N * K // 2} and {4 * E * N * (K // G)}")
-    return _dev(wq, f"{name} wq"), _dev(sz, f"{name} sz")
+def _check_experts(fn: str, w: dict, name: str, E: int, N: int, K: int, G: int):
+    """E stacked GPU layouts of [N, K] weights."""
+    if _nbytes(w["wq"]) != E * N * K // 2 or _nbytes(w["sz"]) != 4 * E * N * (K // G):
+        raise ValueError(f"{fn}: {name} holds {_nbytes(w['wq'])} bytes of codes and {_nbytes(w['sz'])} of scales; {E} experts "
+                         f"of [{N}, {K}] with G = {G} need {E * N * K // 2} and {4 * E * N * (K // G)}")
 
 
 def w4a16_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: dict, up: dict, down: dict, G: int,
@@ -627,14 +695,15 @@ def w4a16_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: d
     (T, H), top_k, (E, I, _), dev = X.shape, ids.shape[1], gate["wq"].shape, X.device
     if G <= 0 or H % G or I % G:
         raise ValueError(f"{fn}: H = {H} and I = {I} must be multiples of the group size G = {G}")
-    pointers = (*_expert_weight(fn, gate, "gate", E, I, H, G), *_expert_weight(fn, up, "up", E, I, H, G),
-                *_expert_weight(fn, down, "down", E, H, I, G))
+    for w, name, N, K in ((gate, "gate", I, H), (up, "up", I, H), (down, "down", H, I)):
+        _check_experts(fn, w, name, E, N, K, G)
     for t, name in ((Y, "Y"), (residual, "residual")):
         if t is not None and tuple(t.shape) != (T, H):
             raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {(T, H)}")
     Y = _empty((T, H), torch.bfloat16, dev, stream) if Y is None else Y
     if workspace is None:
         workspace = _scratch(w4a16_moe_workspace_bytes(T, top_k, E, H, I, G), dev, stream)
+    pointers = [_dev(w[key], f"{name} {key}") for w, name in ((gate, "gate"), (up, "up"), (down, "down")) for key in ("wq", "sz")]
     rc = lib().w4a16_moe(_dev(X, "X", torch.bfloat16), T, H, _dev(ids, "ids", torch.int32),
                          _dev(weights, "weights", torch.float32), top_k, *pointers, E, I, G, _ACTS[act],
                          _dev(residual, "residual", torch.bfloat16), _dev(Y, "Y", torch.bfloat16),

@@ -318,12 +318,86 @@ bool w4a16_tiled(int64_t M, int64_t K, int64_t N, const void* workspace, size_t 
     return need == 0 || (workspace && aligned16(workspace) && workspace_bytes >= need);
 }
 
+// what a product does to its sums before they are rounded (w4.h: w4a16_linear)
+struct Epilogue {
+    const float* bias;
+    int act;
+    const uint16_t* residual;
+};
+int check_epilogue(const char* fn, const Epilogue* epi) {
+    if (!epi) return W4_OK;
+    if (epi->act < W4_ACT_NONE || epi->act > W4_ACT_GELU)
+        return fail(W4_EINVAL, "%s: act = %d is none of W4_ACT_NONE, _SILU, _GELU_TANH, _RELU, _GELU", fn, epi->act);
+    if (reinterpret_cast<uintptr_t>(epi->bias) % sizeof(float) != 0)
+        return fail(W4_EINVAL, "%s: bias is not aligned to its elements", fn);
+    if (epi->residual && !aligned16(epi->residual)) return fail(W4_EINVAL, "%s: residual is not 16-byte aligned", fn);
+    return W4_OK;
+}
+void set_epilogue(w4::MulParams& p, const Epilogue* epi) {
+    // with nothing to do the plain kernels run
+    if (!epi || (!epi->bias && epi->act == W4_ACT_NONE && !epi->residual)) return;
+    p.epi = true;
+    p.bias = epi->bias;
+    p.residual = epi->residual;
+    p.out_act = epi->act;
+}
+
 int w4a16_run(const char* fn, const uint16_t* X, int64_t M, int64_t K, const uint32_t* wq, const uint32_t* sz,
-              int64_t N, int G, uint16_t* Y, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+              int64_t N, int G, const Epilogue* epi, uint16_t* Y, void* workspace, size_t workspace_bytes,
+              hipStream_t stream) {
+    W4_TRY(check_epilogue(fn, epi));
     W4_TRY(mul_common(fn, X, M, K, wq, sz, N, G, Y, workspace, workspace_bytes, false));
     if (M == 0 || N == 0) return W4_OK;
     w4::MulParams p{X, nullptr, M, K, N, G, wq, sz, Y, false};
+    set_epilogue(p, epi);
     if (!w4a16_tiled(M, K, N, workspace, workspace_bytes))
+        return hip_status(w4::launch_skinny(with_skinny_split(p, workspace, workspace_bytes), stream), fn);
+    return hip_status(w4::launch_gemm(with_split(p, workspace), stream), fn);
+}
+
+int w4a8_run(const char* fn, const uint16_t* X, int64_t M, int64_t K, const uint32_t* wq, const uint32_t* sz, int64_t N,
+             int G, const Epilogue* epi, uint16_t* Y, uint8_t* xq, float* xscale, void* workspace, size_t workspace_bytes,
+             hipStream_t stream) {
+    W4_TRY(check_epilogue(fn, epi));
+    W4_TRY(mul_common(fn, X, M, K, wq, sz, N, G, Y, workspace, workspace_bytes, true));
+    if (M == 0 || N == 0) return W4_OK;
+    W4_REQUIRE_PTR(fn, xq);
+    if (!xscale) return fail(W4_EINVAL, "%s: xscale is NULL", fn);
+    if (w4::skinny_quantizes_rows(M, K)) {
+        // one kernel: row quantization (same arithmetic) and product
+        w4::MulParams p{X, nullptr, M, K, N, G, wq, sz, Y, true, xq, xscale};
+        set_epilogue(p, epi);
+        return hip_status(w4::launch_skinny(p, stream), fn);
+    }
+    // above 128 rows, a workspace that also holds the widened activations
+    // (w4a8_gemm_workspace_bytes) lets the row quantizer write them and the
+    // bf16 tiled kernel run on them
+    uint16_t* xw = nullptr;
+    const size_t xw_bytes = M > w4::kSkinnyMaxM && !f8_product(M, K, N, G) ? w4::gemm_xw_bytes(M, K, N) : 0;
+    if (xw_bytes && workspace && workspace_bytes >= w4::gemm_xw_offset(M, K, N) + xw_bytes)
+        xw = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + w4::gemm_xw_offset(M, K, N));
+    w4::RowQuantParams rq{X, M, K, xq, xscale, xw};
+    W4_TRY(hip_status(w4::launch_rowquant(rq, stream), fn));
+    w4::MulParams p{xq, xscale, M, K, N, G, wq, sz, Y, true};
+    p.xw = xw;
+    set_epilogue(p, epi);
+    if (M <= w4::kSkinnyMaxM && !f8_product(M, K, N, G))
+        return hip_status(w4::launch_skinny(with_skinny_split(p, workspace, workspace_bytes), stream), fn);
+    return hip_status(w4::launch_gemm(with_split(p, workspace), stream), fn);
+}
+
+int w4a8_e4m3_run(const char* fn, const uint8_t* xq, const float* xscale, int64_t M, int64_t K, const uint32_t* wq,
+                  const uint32_t* sz, int64_t N, int G, const Epilogue* epi, uint16_t* Y, void* workspace,
+                  size_t workspace_bytes, hipStream_t stream) {
+    W4_TRY(check_epilogue(fn, epi));
+    W4_TRY(mul_common(fn, reinterpret_cast<const uint16_t*>(xq), M, K, wq, sz, N, G, Y, workspace, workspace_bytes,
+                      true));
+    if (M == 0 || N == 0) return W4_OK;
+    if (K % 16 != 0) return fail(W4_EINVAL, "%s: K = %lld must be a multiple of 16", fn, static_cast<long long>(K));
+    if (!xscale) return fail(W4_EINVAL, "%s: xscale is NULL", fn);
+    w4::MulParams p{xq, xscale, M, K, N, G, wq, sz, Y, true};
+    set_epilogue(p, epi);
+    if (M <= w4::kSkinnyMaxM && !f8_product(M, K, N, G))
         return hip_status(w4::launch_skinny(with_skinny_split(p, workspace, workspace_bytes), stream), fn);
     return hip_status(w4::launch_gemm(with_split(p, workspace), stream), fn);
 }
@@ -331,7 +405,21 @@ int w4a16_run(const char* fn, const uint16_t* X, int64_t M, int64_t K, const uin
 
 int w4a16_gemm(const uint16_t* X, int64_t M, int64_t K, const uint32_t* wq, const uint32_t* sz, int64_t N,
                int G, uint16_t* Y, void* workspace, size_t workspace_bytes, hipStream_t stream) {
-    return w4a16_run("w4a16_gemm", X, M, K, wq, sz, N, G, Y, workspace, workspace_bytes, stream);
+    return w4a16_run("w4a16_gemm", X, M, K, wq, sz, N, G, nullptr, Y, workspace, workspace_bytes, stream);
+}
+
+int w4a16_linear(const uint16_t* X, int64_t M, int64_t K, const uint32_t* wq, const uint32_t* sz, int64_t N, int G,
+                 const float* bias, int act, const uint16_t* residual, uint16_t* Y, void* workspace,
+                 size_t workspace_bytes, hipStream_t stream) {
+    const Epilogue epi{bias, act, residual};
+    return w4a16_run("w4a16_linear", X, M, K, wq, sz, N, G, &epi, Y, workspace, workspace_bytes, stream);
+}
+
+int w4a8_linear(const uint16_t* X, int64_t M, int64_t K, const uint32_t* wq, const uint32_t* sz, int64_t N, int G,
+                const float* bias, int act, const uint16_t* residual, uint16_t* Y, uint8_t* xq, float* xscale,
+                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const Epilogue epi{bias, act, residual};
+    return w4a8_run("w4a8_linear", X, M, K, wq, sz, N, G, &epi, Y, xq, xscale, workspace, workspace_bytes, stream);
 }
 
 int w4a16_gemm_noalloc(const uint16_t* X, int64_t M, int64_t K, const uint32_t* wq, const uint32_t* sz,
@@ -346,36 +434,13 @@ int w4a16_gemm_noalloc(const uint16_t* X, int64_t M, int64_t K, const uint32_t* 
                     static_cast<size_t>(W4_NOALLOC_SCRATCH_BYTES));
     void* scratch = nullptr;
     W4_TRY(hip_status(w4::noalloc_scratch(&scratch), fn));
-    return w4a16_run(fn, X, M, K, wq, sz, N, G, Y, scratch, W4_NOALLOC_SCRATCH_BYTES, stream);
+    return w4a16_run(fn, X, M, K, wq, sz, N, G, nullptr, Y, scratch, W4_NOALLOC_SCRATCH_BYTES, stream);
 }
 
 int w4a8_gemm(const uint16_t* X, int64_t M, int64_t K, const uint32_t* wq, const uint32_t* sz, int64_t N,
               int G, uint16_t* Y, uint8_t* xq, float* xscale, void* workspace, size_t workspace_bytes,
               hipStream_t stream) {
-    const char* fn = "w4a8_gemm";
-    W4_TRY(mul_common(fn, X, M, K, wq, sz, N, G, Y, workspace, workspace_bytes, true));
-    if (M == 0 || N == 0) return W4_OK;
-    W4_REQUIRE_PTR(fn, xq);
-    if (!xscale) return fail(W4_EINVAL, "%s: xscale is NULL", fn);
-    if (w4::skinny_quantizes_rows(M, K)) {
-        // one kernel: row quantization (same arithmetic) and product
-        w4::MulParams p{X, nullptr, M, K, N, G, wq, sz, Y, true, xq, xscale};
-        return hip_status(w4::launch_skinny(p, stream), fn);
-    }
-    // above 128 rows, a workspace that also holds the widened activations
-    // (w4a8_gemm_workspace_bytes) lets the row quantizer write them and the
-    // bf16 tiled kernel run on them
-    uint16_t* xw = nullptr;
-    const size_t xw_bytes = M > w4::kSkinnyMaxM && !f8_product(M, K, N, G) ? w4::gemm_xw_bytes(M, K, N) : 0;
-    if (xw_bytes && workspace && workspace_bytes >= w4::gemm_xw_offset(M, K, N) + xw_bytes)
-        xw = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + w4::gemm_xw_offset(M, K, N));
-    w4::RowQuantParams rq{X, M, K, xq, xscale, xw};
-    W4_TRY(hip_status(w4::launch_rowquant(rq, stream), fn));
-    w4::MulParams p{xq, xscale, M, K, N, G, wq, sz, Y, true};
-    p.xw = xw;
-    if (M <= w4::kSkinnyMaxM && !f8_product(M, K, N, G))
-        return hip_status(w4::launch_skinny(with_skinny_split(p, workspace, workspace_bytes), stream), fn);
-    return hip_status(w4::launch_gemm(with_split(p, workspace), stream), fn);
+    return w4a8_run("w4a8_gemm", X, M, K, wq, sz, N, G, nullptr, Y, xq, xscale, workspace, workspace_bytes, stream);
 }
 
 
@@ -463,16 +528,14 @@ int w4a8_gate_up(const uint16_t* X, int64_t M, int64_t K, const uint32_t* wq_gat
 int w4a8_gemm_e4m3(const uint8_t* xq, const float* xscale, int64_t M, int64_t K, const uint32_t* wq,
                    const uint32_t* sz, int64_t N, int G, uint16_t* Y, void* workspace, size_t workspace_bytes,
                    hipStream_t stream) {
-    const char* fn = "w4a8_gemm_e4m3";
-    W4_TRY(mul_common(fn, reinterpret_cast<const uint16_t*>(xq), M, K, wq, sz, N, G, Y, workspace, workspace_bytes,
-                      true));
-    if (M == 0 || N == 0) return W4_OK;
-    if (K % 16 != 0) return fail(W4_EINVAL, "%s: K = %lld must be a multiple of 16", fn, static_cast<long long>(K));
-    if (!xscale) return fail(W4_EINVAL, "%s: xscale is NULL", fn);
-    w4::MulParams p{xq, xscale, M, K, N, G, wq, sz, Y, true};
-    if (M <= w4::kSkinnyMaxM && !f8_product(M, K, N, G))
-        return hip_status(w4::launch_skinny(with_skinny_split(p, workspace, workspace_bytes), stream), fn);
-    return hip_status(w4::launch_gemm(with_split(p, workspace), stream), fn);
+    return w4a8_e4m3_run("w4a8_gemm_e4m3", xq, xscale, M, K, wq, sz, N, G, nullptr, Y, workspace, workspace_bytes, stream);
+}
+
+int w4a8_linear_e4m3(const uint8_t* xq, const float* xscale, int64_t M, int64_t K, const uint32_t* wq,
+                     const uint32_t* sz, int64_t N, int G, const float* bias, int act, const uint16_t* residual,
+                     uint16_t* Y, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const Epilogue epi{bias, act, residual};
+    return w4a8_e4m3_run("w4a8_linear_e4m3", xq, xscale, M, K, wq, sz, N, G, &epi, Y, workspace, workspace_bytes, stream);
 }
 
 int w4_nf4_levels(float* levels) {

@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "device.hpp"
+#include "epilogue.hpp"
 #include "kernels.hpp"
 
 namespace w4 {
@@ -67,7 +68,7 @@ constexpr int BM = 128, BN = 128, BK = 32;
 constexpr int LDS_STRIDE = BK + 8;   // bf16 elements per LDS row (16 bytes of padding)
 }  // namespace small
 
-template <bool XF8>
+template <bool XF8, bool EPI>
 __global__ void __launch_bounds__(256) gemm_kernel(MulParams p) {
     using namespace small;
     __shared__ __attribute__((aligned(16))) uint16_t As[BM * LDS_STRIDE];
@@ -178,6 +179,25 @@ __global__ void __launch_bounds__(256) gemm_kernel(MulParams p) {
     }
 
     // epilogue: register r of lane l holds row (r%4) + 4(l/32) + 8(r/4), column l%32
+    if constexpr (EPI) {
+        // a 32-row block of both wave rows a round
+        __shared__ __attribute__((aligned(16))) float sums[64 * BN];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int lr = wm * 32 + (r & 3) + 4 * (lane >> 5) + 8 * (r >> 2);
+                    sums[lr * BN + ((wn * 64 + j * 32 + (lane & 31)) ^ epi_swizzle(lr))] = acc[i][j][r];
+                }
+            __syncthreads();
+            epilogue_rows<256, BN, XF8>(p, sums, 64, n_base, threadIdx.x,
+                                        [&](int r) { return m_base + (r >> 5) * 64 + i * 32 + (r & 31); });
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -273,7 +293,7 @@ __device__ __forceinline__ TileJob tile_job(const MulParams& p) {
 }
 }  // namespace big
 
-template <int WM, int WN, bool XF8>
+template <int WM, int WN, bool XF8, bool EPI>
 __global__ void __launch_bounds__(64 * WM * WN) gemm256_kernel(MulParams p) {
     using namespace big;
     constexpr int NT = 64 * WM * WN;         // threads
@@ -472,6 +492,28 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm256_kernel(MulParams p) {
     if (kt < KT) step(kt, r0, r1);
 
     // epilogue: register r of lane l holds row (r%4) + 4(l/32) + 8(r/4), column l%32
+    if (EPI && job.part < 0) {
+        // a 32-row block of one wave row a round
+        float* const sums = reinterpret_cast<float*>(lds);
+        static_assert(!EPI || 32 * BN * 4 <= sizeof(lds), "a round fits the operand stages");
+#pragma unroll
+        for (int i = 0; i < FI; ++i)
+            for (int w = 0; w < WM; ++w) {
+                __syncthreads();
+                if (wm == w) {
+#pragma unroll
+                    for (int j = 0; j < FJ; ++j)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const int lr = (r & 3) + 4 * (lane >> 5) + 8 * (r >> 2);
+                            sums[lr * BN + ((wn * TN + j * 32 + (lane & 31)) ^ epi_swizzle(lr))] = acc[i][j][r];
+                        }
+                }
+                __syncthreads();
+                epilogue_rows<NT, BN, XF8>(p, sums, 32, n_base, tid, [&](int r) { return m_base + w * TM + i * 32 + r; });
+            }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < FI; ++i)
 #pragma unroll
@@ -538,7 +580,7 @@ __device__ __forceinline__ big::TileJob tile_job_t(const MulParams& p) {
 // (rows TBN/2 ..), so with two wave columns the waves of column 0 sum
 // gate products and those of column 1 up products for the same outputs; at
 // the end the up sums go through LDS and H = bf16(act(gate) * up).
-template <int TBM, int TBN, int WM, int WN, bool XF8, bool PAIR = false>
+template <int TBM, int TBN, int WM, int WN, bool XF8, bool PAIR = false, bool EPI = false>
 __global__ void __launch_bounds__(64 * WM * WN) gemm_mid_kernel(MulParams p) {
     using big::BK;
     using big::lds_off;
@@ -755,6 +797,26 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_mid_kernel(MulParams p) {
         return;
     }
 
+    if (EPI && job.part < 0) {
+        // a 32-row block of every wave row a round
+        float* const sums = reinterpret_cast<float*>(lds);
+        static_assert(!EPI || 32 * WM * TBN * 4 <= sizeof(lds), "a round fits the operand stages");
+#pragma unroll
+        for (int i = 0; i < FI; ++i) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < FJ; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int lr = wm * 32 + (r & 3) + 4 * (lane >> 5) + 8 * (r >> 2);
+                    sums[lr * TBN + ((wn * TN + j * 32 + (lane & 31)) ^ epi_swizzle(lr))] = acc[i][j][r];
+                }
+            __syncthreads();
+            epilogue_rows<NT, TBN, XF8>(p, sums, 32 * WM, n_base, tid,
+                                        [&](int r) { return m_base + (r >> 5) * TM + i * 32 + (r & 31); });
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < FI; ++i)
 #pragma unroll
@@ -829,7 +891,7 @@ struct Geom {
 __device__ __forceinline__ int swz(int row) { return big::swizzle_fn(W4_DSWZ, row); }
 }  // namespace breg
 
-template <bool PAIR, int NW = 4>
+template <bool PAIR, int NW = 4, bool EPI = false>
 __global__ void __launch_bounds__(64 * NW) gemm256_breg_kernel(MulParams p) {
     using namespace breg;
     static_assert(!PAIR || NW % 2 == 0, "the pair form pairs waves w and w + NW / 2");
@@ -1112,6 +1174,25 @@ __global__ void __launch_bounds__(64 * NW) gemm256_breg_kernel(MulParams p) {
             }
         return;
     }
+    if (EPI && job.part < 0) {
+        // a 32-row block of all waves a round, in the free activation stage
+        float* const sums = reinterpret_cast<float*>(lds_a0);
+        static_assert(32 * BN * 4 <= sizeof(lds_a0), "a round fits a stage");
+#pragma unroll
+        for (int i = 0; i < FI; ++i) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < FJ; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int lr = (r & 3) + 4 * (lane >> 5) + 8 * (r >> 2);
+                    sums[lr * BN + ((WNC * wave + 32 * j + (lane & 31)) ^ epi_swizzle(lr))] = acc[i][j][r];
+                }
+            __syncthreads();
+            epilogue_rows<NT, BN, true>(p, sums, 32, n_base, tid, [&](int r) { return m_base + i * 32 + r; });
+        }
+        return;
+    }
     // W4A8 (widened E4M3 activations, whole tiles): the row scales of a row
     // block are loaded together before its stores
     const bool scale_rows = p.x_fp8 && job.part < 0;
@@ -1142,7 +1223,7 @@ __global__ void __launch_bounds__(64 * NW) gemm256_breg_kernel(MulParams p) {
 // fp32 sum of its `splits` partials in split order, times the row scale
 // (W4A8), rounded to bf16.  A thread takes four consecutive columns of one
 // tile row (16-byte loads; consecutive lanes read consecutive addresses).
-template <int BM, int BN>
+template <int BM, int BN, bool EPI>
 __global__ void __launch_bounds__(256) splitk_reduce_kernel(MulParams p) {
     const int64_t e4 = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;   // element of the split tiles
     const int64_t j = e4 / (BM * BN);
@@ -1163,15 +1244,7 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(MulParams p) {
         const float r = p.xscale[row];
         y.x *= r; y.y *= r; y.z *= r; y.w *= r;
     }
-    const float yv[4] = {y.x, y.y, y.z, y.w};
-    uint16_t* dst = p.Y + row * p.N + col;
-    if (col + 3 < p.N && p.N % 4 == 0) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(
-            float_to_bf16_bits(yv[0]) | (static_cast<uint32_t>(float_to_bf16_bits(yv[1])) << 16),
-            float_to_bf16_bits(yv[2]) | (static_cast<uint32_t>(float_to_bf16_bits(yv[3])) << 16));
-    } else {
-        for (int e = 0; e < 4 && col + e < p.N; ++e) dst[e] = float_to_bf16_bits(yv[e]);
-    }
+    finish4<EPI>(p, row, col, y);
 }
 
 // Sum of the K-split partials of the W4A16 gate and up pair on 256 x 128
@@ -1352,12 +1425,14 @@ hipError_t launch_mid(const MulParams& p, hipStream_t stream) {
     if (q.splits > q.K / big::BK || q.split_t0 < 0 || q.split_t0 > tiles || (q.splits > 1 && !q.ws))
         return hipErrorInvalidValue;
     const int64_t wgs = q.split_t0 + (tiles - q.split_t0) * q.splits;
-    hipLaunchKernelGGL((gemm_mid_kernel<TBM, TBN, 2, 2, XF8>), dim3(static_cast<unsigned>(wgs)), dim3(256), 0, stream, q);
+    if (q.epi)
+        hipLaunchKernelGGL((gemm_mid_kernel<TBM, TBN, 2, 2, XF8, false, true>), dim3(static_cast<unsigned>(wgs)), dim3(256), 0, stream, q);
+    else
+        hipLaunchKernelGGL((gemm_mid_kernel<TBM, TBN, 2, 2, XF8>), dim3(static_cast<unsigned>(wgs)), dim3(256), 0, stream, q);
     if (q.splits > 1 && q.split_t0 < tiles) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        const int64_t blocks = (tiles - q.split_t0) * (TBM * TBN / 1024);
-        hipLaunchKernelGGL((splitk_reduce_kernel<TBM, TBN>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, q);
+        return launch_split_sum(q, TBM, TBN, tiles, stream);
     }
     return hipGetLastError();
 }
@@ -1456,29 +1531,28 @@ size_t pair_workspace_bytes(int64_t M, int64_t K, int64_t N) {
 
 int64_t gate_up_amax_tiles(int64_t M, int64_t N) { return M <= kGateUpMaxM ? (N + 15) / 16 : (N + 127) / 128; }
 
-hipError_t launch_split_sum(const MulParams& q, int bm, int bn, int64_t tiles, hipStream_t stream) {
+namespace {
+template <bool EPI>
+hipError_t launch_split_sum_e(const MulParams& q, int bm, int bn, int64_t tiles, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>((tiles - q.split_t0) * (static_cast<int64_t>(bm) * bn / 1024)));
-    if (bm == 256 && bn == 256)
-        hipLaunchKernelGGL((splitk_reduce_kernel<256, 256>), grid, dim3(256), 0, stream, q);
-    else if (bm == 128 && bn == 256)
-        hipLaunchKernelGGL((splitk_reduce_kernel<128, 256>), grid, dim3(256), 0, stream, q);
-    else if (bm == 64 && bn == 256)
-        hipLaunchKernelGGL((splitk_reduce_kernel<64, 256>), grid, dim3(256), 0, stream, q);
-    else if (bm == 64 && bn == 128)
-        hipLaunchKernelGGL((splitk_reduce_kernel<64, 128>), grid, dim3(256), 0, stream, q);
-    else if (bm == 256 && bn == 128)
-        hipLaunchKernelGGL((splitk_reduce_kernel<256, 128>), grid, dim3(256), 0, stream, q);
-    else if (bm == 256 && bn == 64)
-        hipLaunchKernelGGL((splitk_reduce_kernel<256, 64>), grid, dim3(256), 0, stream, q);
-    else if (bm == 128 && bn == 128)
-        hipLaunchKernelGGL((splitk_reduce_kernel<128, 128>), grid, dim3(256), 0, stream, q);
-    else if (bm == 64 && bn == 64)
-        hipLaunchKernelGGL((splitk_reduce_kernel<64, 64>), grid, dim3(256), 0, stream, q);
-    else if (bm == 128 && bn == 64)
-        hipLaunchKernelGGL((splitk_reduce_kernel<128, 64>), grid, dim3(256), 0, stream, q);
-    else
-        return hipErrorInvalidValue;
+    auto is = [&](int m, int n) { return bm == m && bn == n; };
+#define W4_SPLIT_SUM(BM, BN) hipLaunchKernelGGL((splitk_reduce_kernel<BM, BN, EPI>), grid, dim3(256), 0, stream, q)
+    if (is(256, 256)) W4_SPLIT_SUM(256, 256);
+    else if (is(128, 256)) W4_SPLIT_SUM(128, 256);
+    else if (is(64, 256)) W4_SPLIT_SUM(64, 256);
+    else if (is(64, 128)) W4_SPLIT_SUM(64, 128);
+    else if (is(256, 128)) W4_SPLIT_SUM(256, 128);
+    else if (is(256, 64)) W4_SPLIT_SUM(256, 64);
+    else if (is(128, 128)) W4_SPLIT_SUM(128, 128);
+    else if (is(64, 64)) W4_SPLIT_SUM(64, 64);
+    else if (is(128, 64)) W4_SPLIT_SUM(128, 64);
+    else return hipErrorInvalidValue;
+#undef W4_SPLIT_SUM
     return hipGetLastError();
+}
+}  // namespace
+hipError_t launch_split_sum(const MulParams& q, int bm, int bn, int64_t tiles, hipStream_t stream) {
+    return q.epi ? launch_split_sum_e<true>(q, bm, bn, tiles, stream) : launch_split_sum_e<false>(q, bm, bn, tiles, stream);
 }
 
 hipError_t launch_gemm(const MulParams& p, hipStream_t stream) {
@@ -1505,30 +1579,33 @@ hipError_t launch_gemm(const MulParams& p, hipStream_t stream) {
             return hipErrorInvalidValue;
         const int64_t wgs = q.split_t0 + (tiles - q.split_t0) * q.splits;
         const dim3 grid(static_cast<unsigned>(wgs));
-        if (q.x_fp8 && q.xw) {
-            // W4A8 on the widened activations: the bf16 kernel, row scales in
-            // its epilogue (or in the split sum)
-            q.X = q.xw;
-            hipLaunchKernelGGL((gemm256_breg_kernel<false, 8>), grid, dim3(breg::Geom<8>::NT), 0, stream, q);
-        } else if (q.x_fp8) {
-            hipLaunchKernelGGL((gemm256_kernel<kBigWM, kBigWN, true>), grid, dim3(64 * kBigWM * kBigWN), 0, stream, q);
-        } else {
-            hipLaunchKernelGGL((gemm256_breg_kernel<false, 8>), grid, dim3(breg::Geom<8>::NT), 0, stream, q);
-        }
+        // W4A8 on the widened activations runs the bf16 kernel, row scales in
+        // its epilogue (or in the split sum)
+        const bool widened = q.x_fp8 && q.xw;
+        if (widened) q.X = q.xw;
+        auto launch = [&](auto epi) {
+            constexpr bool EPI = decltype(epi)::value;
+            if (q.x_fp8 && !widened)
+                hipLaunchKernelGGL((gemm256_kernel<kBigWM, kBigWN, true, EPI>), grid, dim3(64 * kBigWM * kBigWN), 0, stream, q);
+            else
+                hipLaunchKernelGGL((gemm256_breg_kernel<false, 8, EPI>), grid, dim3(breg::Geom<8>::NT), 0, stream, q);
+        };
+        if (q.epi) launch(std::true_type{});
+        else launch(std::false_type{});
         if (q.splits > 1 && q.split_t0 < tiles) {
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
-            const int64_t blocks = (tiles - q.split_t0) * (big::BM * big::BN / 1024);
-            hipLaunchKernelGGL((splitk_reduce_kernel<big::BM, big::BN>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, q);
+            return launch_split_sum(q, big::BM, big::BN, tiles, stream);
         }
         return hipGetLastError();
     }
     const dim3 grid(static_cast<unsigned>((p.N + small::BN - 1) / small::BN),
                     static_cast<unsigned>((p.M + small::BM - 1) / small::BM));
-    if (p.x_fp8)
-        hipLaunchKernelGGL((gemm_kernel<true>), grid, dim3(256), 0, stream, p);
-    else
-        hipLaunchKernelGGL((gemm_kernel<false>), grid, dim3(256), 0, stream, p);
+    auto launch = [&](auto xf8, auto epi) {
+        hipLaunchKernelGGL((gemm_kernel<decltype(xf8)::value, decltype(epi)::value>), grid, dim3(256), 0, stream, p);
+    };
+    if (p.x_fp8) p.epi ? launch(std::true_type{}, std::true_type{}) : launch(std::true_type{}, std::false_type{});
+    else p.epi ? launch(std::false_type{}, std::true_type{}) : launch(std::false_type{}, std::false_type{});
     return hipGetLastError();
 }
 

@@ -41,6 +41,7 @@
 #include <utility>
 
 #include "device.hpp"
+#include "epilogue.hpp"
 #include "kernels.hpp"
 
 namespace w4 {
@@ -185,7 +186,7 @@ __device__ __forceinline__ float4_t mfma_f8_16x16x128(const int8x_t& a, const in
 // the same k), the row sums of the step's activations from four more MFMAs
 // against ones, and per group and output acc += s (T - (128 + z) X1): exact
 // weights, any zero point.
-template <int BM_, int BN_, int WR_, int WC_, bool PAIR = false, int SA_ = 3, int DW_ = 2, bool A16 = false>
+template <int BM_, int BN_, int WR_, int WC_, bool PAIR = false, int SA_ = 3, int DW_ = 2, bool A16 = false, bool EPI = false>
 __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(MulParams p) {
     using namespace f8;
     using Gm = Geom<BM_, BN_, WR_, WC_>;
@@ -666,6 +667,32 @@ __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(MulParams p) {
         return;
     }
     const bool whole = job.part < 0;
+    if (EPI && whole) {
+        // as many row blocks of every wave as fit an activation stage a round
+        constexpr int FIT = STAGE / (16 * WR_ * BN * 4), RPR = FIT < RB ? FIT : RB;
+        static_assert(!EPI || (RPR >= 1 && RB % RPR == 0), "whole rounds");
+        float* const sums = reinterpret_cast<float*>(lds_a0);
+#pragma unroll
+        for (int r0 = 0; r0 < RB; r0 += RPR) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < RPR; ++i)
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int lr = 16 * (RPR * wr + i) + 4 * q + e;
+                        // (row scales here, where they lie in LDS)
+                        sums[lr * BN + ((wcol + 16 * cb + c) ^ epi_swizzle(lr))] =
+                            acc[r0 + i][cb][e] * lds_xs[row0 + 16 * (r0 + i) + 4 * q + e];
+                    }
+            __syncthreads();
+            epilogue_rows<Gm::NT, BN, false>(p, sums, 16 * RPR * WR_, n_base, tid, [&](int r) {
+                return m_base + r / (16 * RPR) * (16 * RB) + 16 * r0 + r % (16 * RPR);
+            });
+        }
+        return;
+    }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         float rsc[4];
@@ -806,19 +833,24 @@ hipError_t launch_gemm_f8(const MulParams& p, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(q.split_t0 + (g.tiles - q.split_t0) * q.splits));
     const int t = f8_tile(p.M, p.K, p.N);
     const dim3 block(static_cast<unsigned>(64 * kF8Tiles[t].wr * kF8Tiles[t].wc));
-    switch (t) {
-        case 0: hipLaunchKernelGGL((gemm_f8_kernel<256, 256, 1, 8>), grid, block, 0, stream, q); break;
+    auto launch = [&](auto epi) {
+        constexpr bool EPI = decltype(epi)::value;
+        switch (t) {
 #define W4_F8_LAUNCH(T)                                                                                         \
     hipLaunchKernelGGL((gemm_f8_kernel<kF8Tiles[T].bm, kF8Tiles[T].bn, kF8Tiles[T].wr, kF8Tiles[T].wc, false,      \
-                                       kF8Tiles[T].sa, kF8Tiles[T].dw>),                                           \
+                                       kF8Tiles[T].sa, kF8Tiles[T].dw, false, EPI>),                               \
                        grid, block, 0, stream, q)
-        case 1: W4_F8_LAUNCH(1); break;
-        case 2: W4_F8_LAUNCH(2); break;
-        case 3: W4_F8_LAUNCH(3); break;
-        case 4: W4_F8_LAUNCH(4); break;
-        default: W4_F8_LAUNCH(5); break;
+            case 0: W4_F8_LAUNCH(0); break;
+            case 1: W4_F8_LAUNCH(1); break;
+            case 2: W4_F8_LAUNCH(2); break;
+            case 3: W4_F8_LAUNCH(3); break;
+            case 4: W4_F8_LAUNCH(4); break;
+            default: W4_F8_LAUNCH(5); break;
 #undef W4_F8_LAUNCH
-    }
+        }
+    };
+    if (q.epi) launch(std::true_type{});
+    else launch(std::false_type{});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || q.splits == 1) return e;
     return launch_split_sum(q, g.bm, g.bn, g.tiles, stream);
@@ -851,10 +883,15 @@ hipError_t launch_gemm_a16(const MulParams& p, hipStream_t stream) {
     if (q.splits > q.K / f8::BK || q.split_t0 < 0 || q.split_t0 > tiles || (q.splits > 1 && !q.ws))
         return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(q.split_t0 + (tiles - q.split_t0) * q.splits));
-    if (BM == 128)
-        hipLaunchKernelGGL((gemm_f8_kernel<128, BN, 1, 8, false, 3, 3, true>), grid, dim3(512), 0, stream, q);
-    else
-        hipLaunchKernelGGL((gemm_f8_kernel<64, BN, 1, 8, false, 3, 3, true>), grid, dim3(512), 0, stream, q);
+    auto launch = [&](auto epi) {
+        constexpr bool EPI = decltype(epi)::value;
+        if (BM == 128)
+            hipLaunchKernelGGL((gemm_f8_kernel<128, BN, 1, 8, false, 3, 3, true, EPI>), grid, dim3(512), 0, stream, q);
+        else
+            hipLaunchKernelGGL((gemm_f8_kernel<64, BN, 1, 8, false, 3, 3, true, EPI>), grid, dim3(512), 0, stream, q);
+    };
+    if (q.epi) launch(std::true_type{});
+    else launch(std::false_type{});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || q.splits == 1) return e;
     return launch_split_sum(q, BM, BN, tiles, stream);

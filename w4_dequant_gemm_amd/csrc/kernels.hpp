@@ -93,6 +93,12 @@ struct MulParams {
     // column tile), for the row quantization of H that follows
     float* amax_part = nullptr;
     int64_t amax_tiles = 0;
+    // product with an epilogue (never with wq2): Y = bf16(act(y + bias) +
+    // residual); out_act 0 none, 1 SiLU, 2 GELU (tanh), 3 ReLU, 4 GELU (erf)
+    bool epi = false;
+    const float* bias = nullptr;          // [N] or null
+    const uint16_t* residual = nullptr;   // [M, N] or null
+    int out_act = 0;
 };
 // largest M of the streaming kernel's gate and up pass; above it the tiled
 // pair GEMM (K a multiple of 64) takes the fused product

@@ -39,6 +39,7 @@
 #include <type_traits>
 
 #include "device.hpp"
+#include "epilogue.hpp"
 #include "kernels.hpp"
 
 namespace w4 {
@@ -91,7 +92,7 @@ constexpr int kDotMaxM = 2;
 template <int MB, int MODE>
 constexpr int skinny_max_threads() { return MODE == kDotLds || MODE == kDotLdsQ ? 1024 : 512; }
 
-template <int MB, int FJ, bool XF8, int MODE>
+template <int MB, int FJ, bool XF8, int MODE, bool EPI>
 __global__ void __launch_bounds__((skinny_max_threads<MB, MODE>())) gemm_skinny_kernel(MulParams p, int wk) {
     constexpr bool CORR = MODE == kCorr, QX = MODE == kDotLdsQ, DOTL = MODE == kDotLds || QX,
                    DOT = MODE == kDot || DOTL;
@@ -416,6 +417,26 @@ __global__ void __launch_bounds__((skinny_max_threads<MB, MODE>())) gemm_skinny_
             }
         }
     }
+    // an epilogue's bias and residual of the thread's first output, ahead of
+    // the weights: they would otherwise be waited for at the end
+    [[maybe_unused]] float bias0 = 0.0f, res0 = 0.0f;
+    if constexpr (EPI) {
+        const int64_t row = threadIdx.x / (16 * FJ), n = n0 + threadIdx.x % (16 * FJ);
+        if (row < M && n < N && !ksplit) {
+            if (p.bias) bias0 = p.bias[n];
+            if (p.residual) res0 = bf16_lo(p.residual[row * N + n]);
+        }
+    }
+    // output o of the workgroup (row, n): the first of a thread on what was loaded ahead
+    auto store = [&](int o, int64_t row, int64_t n, float y) {
+        if constexpr (EPI) {
+            if (o == static_cast<int>(threadIdx.x)) {
+                p.Y[row * N + n] = float_to_bf16_bits(linear_activation(p.out_act, y + bias0) + res0);
+                return;
+            }
+        }
+        p.Y[row * N + n] = finish<EPI>(p, row, n, y);
+    };
     issue(step);
     if constexpr (DOTL) {
         // stage the activations while the first weights are in flight:
@@ -648,7 +669,7 @@ __global__ void __launch_bounds__((skinny_max_threads<MB, MODE>())) gemm_skinny_
             const int64_t n = n0 + col;
             if (row < M && n < N) {
                 if constexpr (QX || XF8) y *= row_factor(row);
-                p.Y[static_cast<int64_t>(row) * N + n] = float_to_bf16_bits(y);
+                store(o, row, n, y);
             }
         }
         return;
@@ -699,7 +720,7 @@ __global__ void __launch_bounds__((skinny_max_threads<MB, MODE>())) gemm_skinny_
                 p.ws[(static_cast<int64_t>(kr) * M + row) * N + n] = y;
             } else {
                 if constexpr (XF8) y *= p.xscale[row];
-                p.Y[static_cast<int64_t>(row) * N + n] = float_to_bf16_bits(y);
+                store(o, row, n, y);
             }
         }
     }
@@ -707,6 +728,7 @@ __global__ void __launch_bounds__((skinny_max_threads<MB, MODE>())) gemm_skinny_
 
 // Sum of the K-split partials of the streaming kernel: Y = bf16(sum over the
 // ranges in order, times the row scale for W4A8).
+template <bool EPI>
 __global__ void __launch_bounds__(256) skinny_reduce_kernel(MulParams p) {
     const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int64_t mn = p.M * p.N;
@@ -714,30 +736,35 @@ __global__ void __launch_bounds__(256) skinny_reduce_kernel(MulParams p) {
     float y = p.ws[e];
     for (int z = 1; z < p.splits; ++z) y += p.ws[z * mn + e];
     if (p.x_fp8) y *= p.xscale[e / p.N];
-    p.Y[e] = float_to_bf16_bits(y);
+    p.Y[e] = finish<EPI>(p, e / p.N, e % p.N, y);
 }
 
 // LDS words of one staged activation row: 16 bf16 pairs and one sum per
 // 32-k quarter, quarters padded to a whole 128-k step
 int64_t staged_words_row(int64_t K) { return 17 * (((K / 32) + 3) & ~int64_t{3}); }
 
-template <int MB, int FJ, bool XF8, int MODE>
-hipError_t launch_skinny_c(const MulParams& p, int wk, hipStream_t stream) {
+template <int MB, int FJ, bool XF8, int MODE, bool EPI>
+hipError_t launch_skinny_e(const MulParams& p, int wk, hipStream_t stream) {
     const int64_t cols = p.wq2 ? 16 : 16 * FJ;       // output columns per workgroup
     if (p.wq2 && FJ != 2) return hipErrorInvalidValue;
     const bool split = MODE < kDot && p.splits > 1;
     const int64_t blocks = (p.N + cols - 1) / cols * (split ? p.splits : 1);
     size_t lds = static_cast<size_t>(wk) * (MODE >= kDot ? 16 : 256) * MB * FJ * sizeof(float);
     if (MODE == kDotLds || MODE == kDotLdsQ) lds += static_cast<size_t>(MB) * staged_words_row(p.K) * sizeof(uint32_t);
-    hipLaunchKernelGGL((gemm_skinny_kernel<MB, FJ, XF8, MODE>), dim3(static_cast<unsigned>(blocks)), dim3(64 * wk), lds,
+    hipLaunchKernelGGL((gemm_skinny_kernel<MB, FJ, XF8, MODE, EPI>), dim3(static_cast<unsigned>(blocks)), dim3(64 * wk), lds,
                        stream, p, wk);
     if (split) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(skinny_reduce_kernel, dim3(static_cast<unsigned>((p.M * p.N + 255) / 256)), dim3(256), 0,
+        hipLaunchKernelGGL((skinny_reduce_kernel<EPI>), dim3(static_cast<unsigned>((p.M * p.N + 255) / 256)), dim3(256), 0,
                            stream, p);
     }
     return hipGetLastError();
+}
+template <int MB, int FJ, bool XF8, int MODE>
+hipError_t launch_skinny_c(const MulParams& p, int wk, hipStream_t stream) {
+    return p.epi ? launch_skinny_e<MB, FJ, XF8, MODE, true>(p, wk, stream)
+                 : launch_skinny_e<MB, FJ, XF8, MODE, false>(p, wk, stream);
 }
 
 // groups of 128 or more (a K step lies in one group; per-channel included)
