@@ -393,22 +393,24 @@ int w4a8_linear_e4m3(const uint8_t* xq, const float* xscale, int64_t M, int64_t 
  *   X [T, H], router [E, H]  bf16;  H a multiple of 8;  E <= 1024, top_k <= 32.
  *   bias       [E] fp32 or NULL.
  *   ids        [T, top_k] int32 out;  weights [T, top_k] fp32 out.
- *   workspace  w4_route_workspace_bytes(T, E) bytes, 16-byte aligned, its contents
- *              irrelevant.
+ *   workspace  w4_route_workspace_bytes(T, H, E) bytes, 16-byte aligned, its
+ *              contents irrelevant.
  */
 #define W4_SCORE_SOFTMAX 0
 #define W4_SCORE_SIGMOID 1
 int w4_route(const uint16_t* X, int64_t T, int64_t H, const uint16_t* router, int64_t E, int top_k, int score,
              const float* bias, int renormalize, float scale, int32_t* ids, float* weights, void* workspace,
              size_t workspace_bytes, hipStream_t stream);
-size_t w4_route_workspace_bytes(int64_t T, int64_t E);
+size_t w4_route_workspace_bytes(int64_t T, int64_t H, int64_t E);
 
 /*
  * w4a16_moe -- for token t with the experts e_j = ids[t, j] and weights w_j,
  *   h_j  = w_j act(Wg'[e_j] . X[t]) * (Wu'[e_j] . X[t])
  *   Y[t] = bf16(residual[t] + sum_j Wd'[e_j] . h_j)
- * with W' = (q - z) s exact, fp32 accumulation, and h kept as the sum of two bf16
- * numbers (16 bits of mantissa) between the products.  An id outside 0..E-1 is no
+ * with W' = (q - z) s exact, fp32 accumulation, and h kept between the products as
+ * the sum of two bf16 numbers (16 bits of mantissa), or, where groups of 128 and
+ * 24 rows an expert or more (T top_k >= 24 E, T > 16) take the tiled kernels,
+ * rounded to bf16.  An id outside 0..E-1 is no
  * expert (padding, or one that another process holds): its choice adds nothing,
  * and a token without any gets its residual (or zeros).  A token may choose an
  * expert twice.  Results do not depend on timing.

@@ -73,8 +73,9 @@ def test_route_refusals(lib):
                       (dict(ids=None), 1), (dict(w=None), 1), (dict(ws=None), 1), (dict(ws=ODD), 1), (dict(n=95), 1)):
         assert call(**f) == status, f
     assert call(T=0, X=None, ws=None) == 0
-    assert lib.w4_route_workspace_bytes(3, 8) == 96
-    for bad in ((0, 8), (-1, 8), (3, 0), (3, MOST), (MOST, 8)):
+    assert lib.w4_route_workspace_bytes(3, 64, 8) == 96
+    assert lib.w4_route_workspace_bytes(3, 4096, 8) == 8 * 96          # eight ranges of 512 k
+    for bad in ((0, 64, 8), (-1, 64, 8), (3, 64, 0), (3, 64, MOST), (MOST, 64, 8), (3, 0, 8), (3, 60, 8), (3, MOST - 7, 8)):
         assert lib.w4_route_workspace_bytes(*bad) == 0, bad
 
 

@@ -137,7 +137,7 @@ def lib():
     for name in ("w4a16_linear", "w4a8_linear", "w4a8_linear_e4m3"):
         getattr(L, name).restype = I
     L.w4_route.argtypes = [P, i64, i64, P, i64, I, I, P, I, f32, P, P, P, sz_t, P]
-    L.w4_route_workspace_bytes.argtypes = [i64, i64]
+    L.w4_route_workspace_bytes.argtypes = [i64, i64, i64]
     L.w4_route_workspace_bytes.restype = sz_t
     L.w4a16_moe.argtypes = [P, i64, i64, P, P, I, P, P, P, P, P, P, i64, i64, I, I, P, P, P, sz_t, P]
     L.w4a16_moe_workspace_bytes.argtypes = [i64, I, i64, i64, i64, I]
@@ -640,9 +640,9 @@ _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 @functools.lru_cache(maxsize=4096)
-def w4_route_workspace_bytes(T: int, E: int) -> int:
+def w4_route_workspace_bytes(T: int, H: int, E: int) -> int:
     """Workspace bytes ``w4_route`` needs."""
-    return int(lib().w4_route_workspace_bytes(T, E))
+    return int(lib().w4_route_workspace_bytes(T, H, E))
 
 
 def w4_route(X: torch.Tensor, router: torch.Tensor, top_k: int, *, score="softmax", bias=None, renormalize: bool = True,
@@ -659,7 +659,7 @@ def w4_route(X: torch.Tensor, router: torch.Tensor, top_k: int, *, score="softma
     ids = _empty((T, top_k), torch.int32, dev, stream) if ids is None else ids
     weights = _empty((T, top_k), torch.float32, dev, stream) if weights is None else weights
     if workspace is None:
-        workspace = _scratch(w4_route_workspace_bytes(T, E), dev, stream)
+        workspace = _scratch(w4_route_workspace_bytes(T, H, E), dev, stream)
     rc = lib().w4_route(_dev(X, "X", torch.bfloat16), T, H, _dev(router, "router", torch.bfloat16), E, top_k, _SCORES[score],
                         _vec(fn, bias, "bias", E, torch.float32), renormalize, scale,
                         _vec(fn, ids, "ids", T * top_k, torch.int32), _vec(fn, weights, "weights", T * top_k, torch.float32),

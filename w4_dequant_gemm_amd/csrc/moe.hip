@@ -26,6 +26,7 @@
 // h rounded to bf16 once the result was 1.4 times as far from the exact one
 // as its own rounding to bf16 leaves it.
 #include "device.hpp"
+#include "kernels.hpp"
 #include "moe_kernels.hpp"
 
 namespace w4 {
@@ -33,56 +34,176 @@ namespace {
 
 // ------------------------------------------------------------------- lists
 
-// Slots ordered by expert, and the experts that have any.  One workgroup:
-// counts in LDS, a running sum over the experts, then every slot takes a place
-// behind its expert's start.  (Which place inside an expert's run is up to the
-// order of the atomics; every row's result is the same at any place.)
-constexpr int kListThreads = 1024;
-__global__ void __launch_bounds__(kListThreads) moe_lists_kernel(MoeParams p) {
-    __shared__ int count[kMaxExperts], sums[2][kListThreads];
-    const int tid = threadIdx.x;
-    for (int e = tid; e < p.E; e += kListThreads) count[e] = 0;
+// Which slots belong together: found by one workgroup, in a launch of its own
+// where there are more slots than a wavefront has lanes; with fewer the gate
+// and up kernel looks its rows up among the ids, and one more workgroup of it
+// makes the lists that the down product needs.
+
+// Runs: the slots ordered by expert, and (expert, first, rows) of each expert
+// that has any; runs behind the last one have no rows.  (Which place inside an
+// expert's run a slot gets is up to the order of the atomics; every row's
+// result is the same at any place.)
+struct RunMem {
+    int count[kMaxExperts];
+};
+// TILES: also the runs cut into tiles of `tile_rows` rows, for the tiled products.
+template <bool TILES>
+__device__ __forceinline__ void build_runs(const MoeParams& p, RunMem& m, int tid, int threads, int tile_rows = 64) {
+    for (int e = tid; e < p.E; e += threads) m.count[e] = 0;
     __syncthreads();
     const int slots = static_cast<int>(p.T * p.k);
-    for (int s = tid; s < slots; s += kListThreads) {
+    for (int s = tid; s < slots; s += threads) {
         const uint32_t e = static_cast<uint32_t>(p.ids[s]);
-        if (e < static_cast<uint32_t>(p.E)) atomicAdd(&count[e], 1);
+        if (e < static_cast<uint32_t>(p.E)) atomicAdd(&m.count[e], 1);
     }
     __syncthreads();
-    // inclusive sums over the experts (kMaxExperts threads), of the counts
-    // (low 31 bits would do) and of the experts that have rows
-    const int mine = tid < p.E ? count[tid] : 0;
-    sums[0][tid] = mine;
-    sums[1][tid] = mine > 0;
-    __syncthreads();
-    for (int off = 1; off < kListThreads; off <<= 1) {
-        const int a = tid >= off ? sums[0][tid - off] : 0, b = tid >= off ? sums[1][tid - off] : 0;
-        __syncthreads();
-        sums[0][tid] += a;
-        sums[1][tid] += b;
-        __syncthreads();
+    if (tid < kWave) {
+        // the first wavefront sums over the experts, 64 at a time
+        int rows = 0, active = 0, tiles = 0;
+        for (int e0 = 0; e0 < p.E; e0 += kWave) {
+            const int e = e0 + tid;
+            const int mine = e < p.E ? m.count[e] : 0;
+            int upto = mine;
+#pragma unroll
+            for (int off = 1; off < kWave; off <<= 1) {
+                const int o = __shfl_up(upto, off, kWave);
+                upto += tid >= off ? o : 0;
+            }
+            const uint64_t some = __builtin_amdgcn_ballot_w64(mine > 0);
+            const int first = rows + upto - mine;
+            if (e < p.E) m.count[e] = first;
+            if (mine > 0) p.runs[active + __builtin_popcountll(some & ((uint64_t{1} << tid) - 1))] = make_int4(e, first, mine, 0);
+            if constexpr (TILES) {
+                const int own = (mine + tile_rows - 1) / tile_rows;
+                int before = own;
+#pragma unroll
+                for (int off = 1; off < kWave; off <<= 1) {
+                    const int o = __shfl_up(before, off, kWave);
+                    before += tid >= off ? o : 0;
+                }
+                for (int i = 0; i < own; ++i)
+                    p.tiles[tiles + before - own + i] =
+                        make_int4(e, first + i * tile_rows, mine - i * tile_rows < tile_rows ? mine - i * tile_rows : tile_rows, 0);
+                tiles += __shfl(before, kWave - 1, kWave);
+            }
+            rows += __shfl(upto, kWave - 1, kWave);
+            active += __builtin_popcountll(some);
+        }
+        if (TILES && tid == 0) *p.tile_count = tiles;
+        for (int i = active + tid; i < p.E; i += kWave) p.runs[i] = make_int4(0, 0, 0, 0);
     }
-    if (tid < p.E) {
-        const int start = sums[0][tid] - mine;
-        p.offset[tid] = start;
-        count[tid] = start;
-        if (mine > 0) p.active[sums[1][tid] - 1] = tid;
-        if (tid == p.E - 1) {
-            p.offset[p.E] = sums[0][tid];
-            p.active[p.E] = sums[1][tid];
+    __syncthreads();
+    for (int s = tid; s < slots; s += threads) {
+        const uint32_t e = static_cast<uint32_t>(p.ids[s]);
+        if (e < static_cast<uint32_t>(p.E)) p.order[atomicAdd(&m.count[e], 1)] = s;
+    }
+}
+
+// For at most 16 tokens: units of one expert and, for every token, its slot
+// with that expert.  A token without one has the row behind the slots' rows,
+// which is cleared here.  A token's second choice of the same expert is another
+// unit.
+constexpr int kUnitTokens = 16;
+constexpr int kMaxUnits = kUnitTokens * kMaxTopK;
+struct UnitMem {
+    int key[kMaxUnits], lead[kMaxUnits], rank[kMaxUnits], tokens[kMaxUnits], units;
+};
+__device__ __forceinline__ void build_units(const MoeParams& p, UnitMem& m, int tid, int threads) {
+    const int slots = static_cast<int>(p.T * p.k);
+    for (int s = tid; s < slots; s += threads) {
+        const int e = p.ids[s];
+        m.key[s] = static_cast<uint32_t>(e) < static_cast<uint32_t>(p.E) ? e * kMaxTopK : -1;
+        m.tokens[s] = 0;
+    }
+    __syncthreads();
+    // (the experts are compared without what is added here)
+    int extra[kMaxUnits / kWave];
+    int n = 0;
+    for (int s = tid; s < slots; s += threads, ++n) {
+        int same = 0;
+        for (int j = s - s % p.k; j < s; ++j) same += m.key[j] == m.key[s];
+        extra[n] = same;
+    }
+    __syncthreads();
+    n = 0;
+    for (int s = tid; s < slots; s += threads, ++n)
+        if (m.key[s] >= 0) m.key[s] += extra[n];
+    __syncthreads();
+    for (int s = tid; s < slots; s += threads) {
+        int first = s;
+        for (int j = s - 1; j >= 0; --j) first = m.key[j] == m.key[s] ? j : first;
+        m.lead[s] = m.key[s] < 0 ? -1 : first;
+    }
+    __syncthreads();
+    if (tid < kWave) {
+        int units = 0;
+        for (int s0 = 0; s0 < slots; s0 += kWave) {
+            const int s = s0 + tid;
+            const bool leads = s < slots && m.lead[s] == s;
+            const uint64_t some = __builtin_amdgcn_ballot_w64(leads);
+            if (leads) {
+                const int u = units + __builtin_popcountll(some & ((uint64_t{1} << tid) - 1));
+                m.rank[s] = u;
+                p.unit_expert[u] = m.key[s] / kMaxTopK;
+            }
+            units += __builtin_popcountll(some);
+        }
+        if (tid == 0) {
+            m.units = units;
+            p.unit_expert[slots] = units;
         }
     }
     __syncthreads();
-    for (int s = tid; s < slots; s += kListThreads) {
-        const uint32_t e = static_cast<uint32_t>(p.ids[s]);
-        if (e < static_cast<uint32_t>(p.E)) p.order[atomicAdd(&count[e], 1)] = s;
+    for (int s = tid; s < slots; s += threads)
+        if (m.lead[s] >= 0) {
+            const int u = m.rank[m.lead[s]], t = s / p.k;
+            p.unit_slot[u * kUnitTokens + t] = s;
+            atomicOr(&m.tokens[u], 1 << t);
+        }
+    __syncthreads();
+    for (int i = tid; i < m.units * kUnitTokens; i += threads)
+        if (!(m.tokens[i / kUnitTokens] >> (i % kUnitTokens) & 1)) p.unit_slot[i] = slots;
+    const u32x4_t zero = {0u, 0u, 0u, 0u};
+    for (int i = tid; i < p.I / 8; i += threads) {
+        reinterpret_cast<u32x4_t*>(p.hi + static_cast<int64_t>(slots) * p.I)[i] = zero;
+        reinterpret_cast<u32x4_t*>(p.lo + static_cast<int64_t>(slots) * p.I)[i] = zero;
     }
+}
+
+constexpr int kListThreads = 1024;
+__global__ void __launch_bounds__(kListThreads) moe_lists_kernel(MoeParams p) {
+    __shared__ union {
+        RunMem runs;
+        UnitMem units;
+    } mem;
+    build_runs<false>(p, mem.runs, threadIdx.x, kListThreads);
+    if (p.T > kUnitTokens) return;
+    __syncthreads();
+    build_units(p, mem.units, threadIdx.x, kListThreads);
+}
+
+// For the tiled products: workgroup 0 makes the runs and tiles, the others the
+// tokens' row sums over each 128 k (16 lanes a sum).
+__global__ void __launch_bounds__(kListThreads) moe_tiles_kernel(MoeParams p, int tile_rows) {
+    __shared__ RunMem mem;
+    if (blockIdx.x == 0) {
+        build_runs<true>(p, mem, threadIdx.x, kListThreads, tile_rows);
+        return;
+    }
+    const int64_t i = (static_cast<int64_t>(blockIdx.x - 1) * kListThreads + threadIdx.x) / 16;
+    const int64_t sums = p.T * (p.H / 128);
+    const u32x4_t v = reinterpret_cast<const u32x4_t*>(p.X)[(i < sums ? i : 0) * 16 + threadIdx.x % 16];
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s += bf16_lo(v[e]) + bf16_hi(v[e]);
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) s += __shfl_xor(s, off, 16);
+    if (i < sums && threadIdx.x % 16 == 0) p.x_sums[i] = s;
 }
 
 // ------------------------------------------------------------------ products
 
 constexpr int kStepK = 128;
-constexpr int kDepth = 2;        // steps in flight a wave
 
 // 4 x 4 transposition of words over the quarters: w[t] of quarter q becomes
 // w[q] of quarter t
@@ -94,50 +215,184 @@ __device__ __forceinline__ void transpose_quarters(u32x4_t& w) {
     w = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
 }
 
-// UP: gate and up (FJ = 2: block 0 the gate weight, block 1 the up weight, at
-// the same 16 columns), rows gathered from X; else the down product on the
-// rows hi + lo.
-template <int MB, int FJ, int G, bool UP>
+// One 128-k step of up to 16 MB rows by 16 FJ columns; AP parts of every
+// activation (hi and lo).  The weights' blocks and the rows are given by
+// pointers that already include the lane's column c or row.
+template <int FJ, int G>
+struct StepB {
+    u32x4_t w[FJ];
+    uint32_t s[FJ][kStepK / G];
+};
+template <int MB, int AP>
+struct StepA {
+    u32x4_t a[MB][AP][4];
+};
+template <int FJ, int G>
+__device__ __forceinline__ void load_b(StepB<FJ, G>& b, const uint32_t* const (&wb)[FJ], const uint32_t* const (&sb)[FJ], int step,
+                                       int K, int q) {
+    constexpr int NG = kStepK / G;
+    int t = 4 * step + q;
+    t = t < K / 32 ? t : K / 32 - 1;
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) {
+        b.w[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wb[j] + 64 * t));
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            int gg = NG * step + g;
+            gg = gg < K / G ? gg : K / G - 1;
+            b.s[j][g] = sb[j][16 * gg];
+        }
+    }
+}
+// fragment f: the 8 k at 32 q + 8 f of the step (groups of 128), or at 32 f + 8 q
+template <int MB, int AP, int G>
+__device__ __forceinline__ void load_a(StepA<MB, AP>& a, const uint16_t* const (&arow)[MB][AP], int step, int K, int q) {
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+        int t = 4 * step + (G == kStepK ? q : f);
+        t = t < K / 32 ? t : K / 32 - 1;
+        const int k = 32 * t + 8 * (G == kStepK ? f : q);
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int v = 0; v < AP; ++v) a.a[i][v][f] = *reinterpret_cast<const u32x4_t*>(arow[i][v] + k);
+    }
+}
+template <int MB, int AP, int FJ, int G>
+__device__ __forceinline__ void multiply(float4_t (&acc)[MB][FJ], StepB<FJ, G>& b, const StepA<MB, AP>& a, int step, int K,
+                                         uint32_t bias) {
+    constexpr int NG = kStepK / G, PER = 4 / NG;     // groups in a step, fragments in a group
+    const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+    const u32x4_t zero = {0u, 0u, 0u, 0u};
+    if constexpr (NG > 1) {
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) transpose_quarters(b.w[j]);
+    }
+    float4_t ps[MB][FJ], x1[MB];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+        if (f % PER == 0) {
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                x1[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < FJ; ++j) ps[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+        }
+        // K may end inside the last step of groups below 128
+        const bool in = NG == 1 || 4 * step + f < K / 32;
+        bf16x8_t bp[FJ];
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) {
+            const uint32_t w = b.w[j][f];
+            bp[j] = __builtin_bit_cast(bf16x8_t, u32x4_t{nibble_pair_bf16(w, 0, bias), nibble_pair_bf16(w, 1, bias),
+                                                         nibble_pair_bf16(w, 2, bias), nibble_pair_bf16(w, 3, bias)});
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int v = 0; v < AP; ++v) {
+                const bf16x8_t ap = __builtin_bit_cast(bf16x8_t, in ? a.a[i][v][f] : zero);
+                x1[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ap, ones, x1[i], 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < FJ; ++j) ps[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ap, bp[j], ps[i][j], 0, 0, 0);
+            }
+        if (f % PER == PER - 1) {
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) {
+                const uint32_t sz = b.s[j][f / PER];
+                const float sc = half_bits_to_float(sz), zc = 128.0f + half_bits_to_float(sz >> 16);
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(sc, fmaf(-zc, x1[i][e], ps[i][j][e]), acc[i][j][e]);
+            }
+        }
+    }
+}
+
+// h as two bf16 numbers (an infinite upper part has no rest)
+__device__ __forceinline__ void store_h(const MoeParams& p, int64_t at, float h) {
+    const uint16_t hi = float_to_bf16_bits(h);
+    p.hi[at] = hi;
+    p.lo[at] = (hi & 0x7FFFu) == 0x7F80u ? 0 : float_to_bf16_bits(h - bf16_lo(hi));
+}
+
+// UP: gate and up (blocks 0 .. FJ / 2 - 1 of the gate weight, the others of the
+// up weight, at the same columns), rows gathered from X; else the down product
+// on the rows hi + lo.  SCAN (UP only, at most 64 slots): the expert's rows from
+// the ids, with blockIdx.y the expert or, where there are fewer slots than
+// experts, a slot, whose expert it takes if no slot before has the same; the
+// last blockIdx.y makes the lists for the kernels behind.
+template <int MB, int FJ, int G, bool UP, bool SCAN>
 __global__ void __launch_bounds__(512) moe_stream_kernel(MoeParams p, int wk) {
-    static_assert(!UP || FJ == 2, "a block for each weight");
-    constexpr int NG = kStepK / G;                 // groups in a step
+    static_assert(!UP || FJ % 2 == 0, "as many blocks of each weight");
+    static_assert(UP || !SCAN, "the lists are made by then");
     constexpr int AP = UP ? 1 : 2;                 // parts of an activation
-    constexpr int COLS = UP ? 16 : 16 * FJ;
+    constexpr int DEPTH = MB * AP <= 2 ? 2 : 1;    // steps in flight a wave
+    constexpr int COLS = UP ? 8 * FJ : 16 * FJ;
+    constexpr int TILE = 256 * MB * FJ;
     extern __shared__ float red[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
-    if (static_cast<int>(blockIdx.y) >= p.active[p.E]) return;
-    const int expert = p.active[blockIdx.y];
-    const int first = p.offset[expert], rows = p.offset[expert + 1] - first;
+    int expert, rows;
+    const int* list;
+    __shared__ int scanned[SCAN ? kWave : 1];
+    if constexpr (SCAN) {
+        const int slots = static_cast<int>(p.T * p.k);
+        if (blockIdx.y == gridDim.y - 1) {
+            if (blockIdx.x > 0) return;
+            __shared__ union {
+                RunMem runs;
+                UnitMem units;
+            } mem;
+            if (p.T <= kUnitTokens) build_units(p, mem.units, threadIdx.x, 64 * wk);
+            else build_runs<false>(p, mem.runs, threadIdx.x, 64 * wk);
+            return;
+        }
+        const int id = lane < slots ? p.ids[lane] : -1;
+        expert = slots < p.E ? __builtin_amdgcn_readlane(id, blockIdx.y) : static_cast<int>(blockIdx.y);
+        if (static_cast<uint32_t>(expert) >= static_cast<uint32_t>(p.E)) return;
+        const uint64_t some = __builtin_amdgcn_ballot_w64(id == expert);
+        rows = __builtin_popcountll(some);
+        if (rows == 0 || (slots < p.E && __builtin_ctzll(some) < static_cast<int>(blockIdx.y))) return;
+        // every wavefront writes the same list and reads what it wrote
+        if (id == expert) scanned[__builtin_popcountll(some & ((uint64_t{1} << lane) - 1))] = lane;
+        list = scanned;
+    } else {
+        const int4 run = p.runs[blockIdx.y];
+        expert = run.x;
+        rows = run.z;
+        if (rows == 0) return;
+        list = p.order + run.y;
+    }
     const int K = UP ? p.H : p.I, N = UP ? p.I : p.H;
-    const int KS = (K + kStepK - 1) / kStepK, KQ = K / 32;
+    const int KS = (K + kStepK - 1) / kStepK;
     const int n0 = COLS * blockIdx.x;
     const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * (K / G);
 
-    // the blocks' first words; N is a multiple of 16, so every block has 16 rows
+    // the blocks' first words; N is a multiple of 16, so every block has 16
+    // rows (a block past N repeats the last one and is not stored)
     const uint32_t* wb[FJ];
     const uint32_t* sb[FJ];
 #pragma unroll
     for (int j = 0; j < FJ; ++j) {
-        const MoeWeight& w = UP ? (j == 0 ? p.gate : p.up) : p.down;
-        int r0 = UP ? n0 : n0 + 16 * j;
+        const MoeWeight& w = UP ? (j < FJ / 2 ? p.gate : p.up) : p.down;
+        int r0 = n0 + 16 * (UP ? j % (FJ / 2) : j);
         r0 = r0 < N ? r0 : N - 16;
         wb[j] = w.wq + expert * words + static_cast<int64_t>(r0) * (K / 8) + 4 * c;
         sb[j] = w.sz + expert * groups + static_cast<int64_t>(r0) * (K / G) + c;
     }
     const uint32_t bias = opaque_vgpr(kBf16Bias128x2);
-    const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
-    const u32x4_t zero = {0u, 0u, 0u, 0u};
 
     for (int m0 = 0; m0 < rows; m0 += 16 * MB) {
         // the lane's row in each block (past the last: the last, never stored)
         const uint16_t* arow[MB][AP];
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
-            int m = m0 + 16 * i + c;
-            m = m < rows ? m : rows - 1;
-            const int slot = p.order[first + m];
+            const int m = m0 + 16 * i + c;
+            const int slot = list[m < rows ? m : rows - 1];
             if constexpr (UP) {
                 arow[i][0] = p.X + static_cast<int64_t>(slot / p.k) * K;
             } else {
@@ -150,112 +405,26 @@ __global__ void __launch_bounds__(512) moe_stream_kernel(MoeParams p, int wk) {
         for (int i = 0; i < MB; ++i)
 #pragma unroll
             for (int j = 0; j < FJ; ++j) acc[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-
-        struct B {
-            u32x4_t w[FJ];
-            uint32_t s[FJ][NG];
-        };
-        struct A {
-            u32x4_t a[MB][AP][4];
-        };
-        auto load_b = [&](int step, B& b) {
-            int t = 4 * step + q;
-            t = t < KQ ? t : KQ - 1;
-#pragma unroll
-            for (int j = 0; j < FJ; ++j) {
-                b.w[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wb[j] + 64 * t));
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    int gg = NG * step + g;
-                    gg = gg < K / G ? gg : K / G - 1;
-                    b.s[j][g] = sb[j][16 * gg];
-                }
-            }
-        };
-        // fragment f: the 8 k at 32 q + 8 f of the step (groups of 128), or at
-        // 32 f + 8 q
-        auto load_a = [&](int step, A& a) {
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                int t = 4 * step + (NG == 1 ? q : f);
-                t = t < KQ ? t : KQ - 1;
-                const int k = 32 * t + 8 * (NG == 1 ? f : q);
-#pragma unroll
-                for (int i = 0; i < MB; ++i)
-#pragma unroll
-                    for (int v = 0; v < AP; ++v) a.a[i][v][f] = *reinterpret_cast<const u32x4_t*>(arow[i][v] + k);
-            }
-        };
-        auto multiply = [&](int step, B& b, const A& a) {
-            if constexpr (NG > 1) {
-#pragma unroll
-                for (int j = 0; j < FJ; ++j) transpose_quarters(b.w[j]);
-            }
-            float4_t ps[MB][FJ], x1[MB];
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                if (f % (4 / NG) == 0) {
-#pragma unroll
-                    for (int i = 0; i < MB; ++i) {
-                        x1[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int j = 0; j < FJ; ++j) ps[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-                    }
-                }
-                // K ends inside the last step of groups below 128
-                const bool in = NG == 1 || 4 * step + f < KQ;
-                bf16x8_t bp[FJ];
-#pragma unroll
-                for (int j = 0; j < FJ; ++j) {
-                    const uint32_t w = b.w[j][f];
-                    bp[j] = __builtin_bit_cast(bf16x8_t, u32x4_t{nibble_pair_bf16(w, 0, bias), nibble_pair_bf16(w, 1, bias),
-                                                                 nibble_pair_bf16(w, 2, bias), nibble_pair_bf16(w, 3, bias)});
-                }
-#pragma unroll
-                for (int i = 0; i < MB; ++i)
-#pragma unroll
-                    for (int v = 0; v < AP; ++v) {
-                        const bf16x8_t ap = __builtin_bit_cast(bf16x8_t, in ? a.a[i][v][f] : zero);
-                        x1[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ap, ones, x1[i], 0, 0, 0);
-#pragma unroll
-                        for (int j = 0; j < FJ; ++j)
-                            ps[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ap, bp[j], ps[i][j], 0, 0, 0);
-                    }
-                if (f % (4 / NG) == 4 / NG - 1) {
-#pragma unroll
-                    for (int j = 0; j < FJ; ++j) {
-                        const uint32_t sz = b.s[j][f / (4 / NG)];
-                        const float sc = half_bits_to_float(sz), zc = 128.0f + half_bits_to_float(sz >> 16);
-#pragma unroll
-                        for (int i = 0; i < MB; ++i)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc[i][j][e] = fmaf(sc, fmaf(-zc, x1[i][e], ps[i][j][e]), acc[i][j][e]);
-                    }
-                }
-            }
-        };
-        // rounds of kDepth steps: their loads together, then their products;
+        // rounds of DEPTH steps: their loads together, then their products;
         // the other waves on the compute unit cover the latency
-        for (int step = wave; step < KS; step += kDepth * wk) {
-            B b[kDepth];
-            A a[kDepth];
+        for (int step = wave; step < KS; step += DEPTH * wk) {
+            StepB<FJ, G> b[DEPTH];
+            StepA<MB, AP> a[DEPTH];
 #pragma unroll
-            for (int d = 0; d < kDepth; ++d)
+            for (int d = 0; d < DEPTH; ++d)
                 if (step + d * wk < KS) {
-                    load_b(step + d * wk, b[d]);
-                    load_a(step + d * wk, a[d]);
+                    load_b<FJ, G>(b[d], wb, sb, step + d * wk, K, q);
+                    load_a<MB, AP, G>(a[d], arow, step + d * wk, K, q);
                 }
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int d = 0; d < kDepth; ++d)
-                if (step + d * wk < KS) multiply(step + d * wk, b[d], a[d]);
+            for (int d = 0; d < DEPTH; ++d)
+                if (step + d * wk < KS) multiply<MB, AP, FJ, G>(acc, b[d], a[d], step + d * wk, K, bias);
         }
 
         // the waves' sums through LDS, in wave order: register e of lane (c, q)
         // is row 4 q + e of its block, column c
-        constexpr int TILE = 256 * MB * FJ;
         __syncthreads();                           // (the last rows' sums are read)
 #pragma unroll
         for (int i = 0; i < MB; ++i)
@@ -265,86 +434,498 @@ __global__ void __launch_bounds__(512) moe_stream_kernel(MoeParams p, int wk) {
                 for (int e = 0; e < 4; ++e)
                     red[wave * TILE + (16 * i + 4 * q + e) * (16 * FJ) + 16 * j + c] = acc[i][j][e];
         __syncthreads();
-        for (int o = threadIdx.x; o < 16 * MB * COLS; o += blockDim.x) {
+        const int some = rows - m0 < 16 * MB ? rows - m0 : 16 * MB;
+        for (int o = threadIdx.x; o < some * COLS; o += blockDim.x) {
             const int row = o / COLS, col = o % COLS;
-            if (m0 + row >= rows || n0 + col >= N) continue;
-            const int slot = p.order[first + m0 + row];
+            if (n0 + col >= N) continue;
+            const int slot = list[m0 + row];
+            const int64_t at = static_cast<int64_t>(slot) * N + n0 + col;
             if constexpr (UP) {
+                const float weight = p.weights[slot];
                 float g = 0.0f, u = 0.0f;
                 for (int w = 0; w < wk; ++w) {
-                    g += red[w * TILE + row * 32 + col];
-                    u += red[w * TILE + row * 32 + 16 + col];
+                    g += red[w * TILE + row * (16 * FJ) + col];
+                    u += red[w * TILE + row * (16 * FJ) + COLS + col];
                 }
-                const float h = activation(p.act, g) * u * p.weights[slot];
-                const uint16_t hi = float_to_bf16_bits(h);
-                const float rest = h - bf16_lo(hi);
-                const int64_t at = static_cast<int64_t>(slot) * N + n0 + col;
-                p.hi[at] = hi;
-                // (an infinite upper part has no rest)
-                p.lo[at] = (hi & 0x7FFFu) == 0x7F80u ? 0 : float_to_bf16_bits(rest);
+                store_h(p, at, activation(p.act, g) * u * weight);
             } else {
                 float y = 0.0f;
                 for (int w = 0; w < wk; ++w) y += red[w * TILE + row * COLS + col];
-                p.part[static_cast<int64_t>(slot) * N + n0 + col] = y;
+                p.part[at] = y;
             }
         }
     }
 }
 
-// Y = bf16(residual + the slots' shares in the order of the choices), eight
+// The down product of at most 16 tokens with the join: a workgroup owns 16 FJ
+// columns of all tokens and goes through every unit; row t of a unit's rows is
+// token t's h, or the row of zeros.  Its waves take equal runs of the (unit, step) pairs.
+template <int FJ, int G>
+__global__ void __launch_bounds__(1024) moe_down_kernel(MoeParams p, int wk) {
+    constexpr int COLS = 16 * FJ, DEPTH = 2, TILE = 256 * FJ;
+    __shared__ int16_t unit_slot[kMaxUnits * kUnitTokens], unit_expert[kMaxUnits];
+    extern __shared__ float red[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int K = p.I, N = p.H, KS = (K + kStepK - 1) / kStepK;
+    const int n0 = COLS * blockIdx.x;
+    const int T = static_cast<int>(p.T), slots = T * p.k;
+    // (past the units there are whatever numbers, which nothing reads)
+    const int units = p.unit_expert[slots];
+    for (int i = tid; i < slots; i += blockDim.x) unit_expert[i] = static_cast<int16_t>(p.unit_expert[i]);
+    for (int i = tid; i < slots * kUnitTokens; i += blockDim.x) unit_slot[i] = static_cast<int16_t>(p.unit_slot[i]);
+    // the residual of the thread's first output, ahead of the weights
+    float first = 0.0f;
+    if (p.residual && tid / COLS < T && n0 + tid % COLS < N)
+        first = bf16_lo(p.residual[static_cast<int64_t>(tid / COLS) * N + n0 + tid % COLS]);
+    __syncthreads();
+
+    const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * (K / G);
+    const uint32_t bias = opaque_vgpr(kBf16Bias128x2);
+    float4_t acc[1][FJ];
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) acc[0][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const int all = units * KS, begin = static_cast<int>(static_cast<int64_t>(all) * wave / wk),
+              end = static_cast<int>(static_cast<int64_t>(all) * (wave + 1) / wk);
+    for (int at = begin; at < end; at += DEPTH) {
+        StepB<FJ, G> b[DEPTH];
+        StepA<1, 2> a[DEPTH];
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            if (at + d < end) {
+                const int u = (at + d) / KS, step = (at + d) % KS;
+                const int expert = __builtin_amdgcn_readfirstlane(unit_expert[u]);
+                const uint32_t* wb[FJ];
+                const uint32_t* sb[FJ];
+#pragma unroll
+                for (int j = 0; j < FJ; ++j) {
+                    int r0 = n0 + 16 * j;
+                    r0 = r0 < N ? r0 : N - 16;
+                    wb[j] = p.down.wq + expert * words + static_cast<int64_t>(r0) * (K / 8) + 4 * c;
+                    sb[j] = p.down.sz + expert * groups + static_cast<int64_t>(r0) * (K / G) + c;
+                }
+                const int slot = unit_slot[u * kUnitTokens + c];
+                const uint16_t* const arow[1][2] = {{p.hi + static_cast<int64_t>(slot) * K, p.lo + static_cast<int64_t>(slot) * K}};
+                load_b<FJ, G>(b[d], wb, sb, step, K, q);
+                load_a<1, 2, G>(a[d], arow, step, K, q);
+            }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            if (at + d < end) multiply<1, 2, FJ, G>(acc, b[d], a[d], (at + d) % KS, K, bias);
+    }
+#pragma unroll
+    for (int j = 0; j < FJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) red[wave * TILE + (4 * q + e) * COLS + 16 * j + c] = acc[0][j][e];
+    __syncthreads();
+    for (int o = tid; o < T * COLS; o += blockDim.x) {
+        const int row = o / COLS, col = o % COLS;
+        if (n0 + col >= N) continue;
+        const int64_t at = static_cast<int64_t>(row) * N + n0 + col;
+        float y = 0.0f;
+        for (int w = 0; w < wk; ++w) y += red[w * TILE + o];
+        if (p.residual) y += o == tid ? first : bf16_lo(p.residual[at]);
+        p.Y[at] = float_to_bf16_bits(y);
+    }
+}
+
+// One or two tokens: every slot by itself.  The matrix cores would multiply 16
+// rows where there is one, and each wave would load every row 16 times over;
+// here the rows lie in LDS, each lane multiplies the 32 codes it loads by the 32
+// activations of its tile (v_dot2_f32_bf16 on the exact 128 + u), and the
+// group's scale and zero point are applied per lane, whose 32 k lie in one group
+// of any size.
+constexpr int kDotTokens = 2;
+// bf16 pairs of a row and the sums of its tiles, in LDS words
+constexpr int dot_words(int K, int parts) { return parts * (K / 2) + K / 32; }
+constexpr int kDotWords = 12288;                   // most of them: 48 KB
+
+// a tile's 32 products: the codes of one lane against `x` (16 words, 16 more of
+// the second part), whose sum is xs
+template <int AP>
+__device__ __forceinline__ float dot_tile(const u32x4_t& w, uint32_t sz, const uint32_t* hi, const uint32_t* lo, float xs, uint32_t bias) {
+    const float sc = half_bits_to_float(sz), zc = 128.0f + half_bits_to_float(sz >> 16);
+    float d[2] = {-zc * xs, 0.0f};
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const u32x4_t h = *reinterpret_cast<const u32x4_t*>(hi + 4 * b);
+        u32x4_t l = {0u, 0u, 0u, 0u};
+        if constexpr (AP == 2) l = *reinterpret_cast<const u32x4_t*>(lo + 4 * b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t pr = nibble_pair_bf16(w[b], i, bias);
+            d[0] = dot2_bf16(pr, h[i], d[0]);
+            if constexpr (AP == 2) d[1] = dot2_bf16(pr, l[i], d[1]);
+        }
+    }
+    return sc * (d[0] + d[1]);
+}
+// tile t of a row into LDS: its 32 values as they are, and their sum
+__device__ __forceinline__ float put_tile(uint32_t* to, const u32x4_t (&v)[4]) {
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        *reinterpret_cast<u32x4_t*>(to + 4 * b) = v[b];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[b] = dot2_bf16(v[b][i], 0x3F803F80u, sum[b]);
+    }
+    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+__global__ void __launch_bounds__(512) moe_up_dot_kernel(MoeParams p, int wk) {
+    constexpr int DEPTH = 4;
+    extern __shared__ uint32_t x_lds[];            // the row's pairs, then its tiles' sums
+    __shared__ float red[8][32];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int slot = blockIdx.y, n0 = 16 * blockIdx.x;
+    const int expert = p.ids[slot];
+    const float weight = p.weights[slot];
+    const int K = p.H, N = p.I, KQ = K / 32, KS = (KQ + 3) / 4;
+    const u32x4_t* const x = reinterpret_cast<const u32x4_t*>(p.X + static_cast<int64_t>(slot / p.k) * K);
+    float* const xs = reinterpret_cast<float*>(x_lds + K / 2);
+    u32x4_t xv[4];
+    if (tid < KQ) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) xv[b] = x[4 * tid + b];
+    }
+    if (static_cast<uint32_t>(expert) >= static_cast<uint32_t>(p.E)) return;
+    const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * (K / p.G);
+    const int per = p.G / 32;                      // tiles of a group
+    const uint32_t* wb[2];
+    const uint32_t* sb[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const MoeWeight& w = j == 0 ? p.gate : p.up;
+        wb[j] = w.wq + expert * words + static_cast<int64_t>(n0) * (K / 8) + 4 * c;
+        sb[j] = w.sz + expert * groups + static_cast<int64_t>(n0) * (K / p.G) + c;
+    }
+    u32x4_t w[DEPTH][2];
+    uint32_t sz[DEPTH][2];
+    auto load = [&](int step, int d) {
+        int t = 4 * step + q;
+        t = t < KQ ? t : KQ - 1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            w[d][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wb[j] + 64 * t));
+            sz[d][j] = sb[j][16 * (t / per)];
+        }
+    };
+    // the first steps' weights are on their way while the row is put into LDS
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(wave + d * wk, d);
+    asm volatile("" ::: "memory");
+    if (tid < KQ) xs[tid] = put_tile(x_lds + 16 * tid, xv);
+    for (int t = tid + blockDim.x; t < KQ; t += blockDim.x) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) xv[b] = x[4 * t + b];
+        xs[t] = put_tile(x_lds + 16 * t, xv);
+    }
+    __syncthreads();
+    const uint32_t bias = opaque_vgpr(kBf16Bias128x2);
+    float acc[2] = {0.0f, 0.0f};
+    for (int step = wave; step < KS; step += DEPTH * wk) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            const int t = 4 * (step + d * wk) + q;
+            if (t < KQ)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[j] += dot_tile<1>(w[d][j], sz[d][j], x_lds + 16 * t, nullptr, xs[t], bias);
+            load(step + (DEPTH + d) * wk, d);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        acc[j] += __shfl_xor(acc[j], 16, kWave);
+        acc[j] += __shfl_xor(acc[j], 32, kWave);
+        if (q == 0) red[wave][16 * j + c] = acc[j];
+    }
+    __syncthreads();
+    if (tid < 16) {
+        float g = 0.0f, u = 0.0f;
+        for (int v = 0; v < wk; ++v) {
+            g += red[v][tid];
+            u += red[v][16 + tid];
+        }
+        store_h(p, static_cast<int64_t>(slot) * N + n0 + tid, activation(p.act, g) * u * weight);
+    }
+}
+
+// The waves take equal runs of the (slot, step) pairs.
+__global__ void __launch_bounds__(1024) moe_down_dot_kernel(MoeParams p, int wk) {
+    constexpr int DEPTH = 4;
+    extern __shared__ uint32_t h_lds[];            // [slot] pairs of hi, then of lo; then [slot] the tiles' sums
+    __shared__ float red[16][kDotTokens][16];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int n0 = 16 * blockIdx.x;
+    const int K = p.I, N = p.H, KQ = K / 32, KS = (KQ + 3) / 4;
+    const int T = static_cast<int>(p.T), slots = T * p.k, tiles = slots * KQ;
+    float* const hs = reinterpret_cast<float*>(h_lds + slots * K);
+    // lane s: slot s's expert
+    const int ids = lane < slots ? p.ids[lane] : -1;
+    const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * (K / p.G);
+    const int per = p.G / 32;
+    const int all = slots * KS, begin = all * wave / wk, end = all * (wave + 1) / wk;
+    u32x4_t w[DEPTH];
+    uint32_t sz[DEPTH];
+    int where[DEPTH];                              // slot and step of the codes in flight, -1: none
+    int slot = begin / KS, step = begin % KS;
+    auto load = [&](int at, int d) {
+        where[d] = -1;
+        if (at >= end) return;
+        const int expert = __builtin_amdgcn_readlane(ids, slot);
+        if (static_cast<uint32_t>(expert) < static_cast<uint32_t>(p.E)) {
+            where[d] = slot << 16 | step;
+            int t = 4 * step + q;
+            t = t < KQ ? t : KQ - 1;
+            w[d] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(
+                p.down.wq + expert * words + static_cast<int64_t>(n0) * (K / 8) + 4 * c + 64 * t));
+            sz[d] = p.down.sz[expert * groups + static_cast<int64_t>(n0) * (K / p.G) + c + 16 * (t / per)];
+        }
+        if (++step == KS) {
+            step = 0;
+            ++slot;
+        }
+    };
+    // h's first tiles, then the first steps' weights
+    u32x4_t hv[2][4];
+    auto take = [&](int i) {
+        const int64_t at = static_cast<int64_t>(i) * 4;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            hv[0][b] = reinterpret_cast<const u32x4_t*>(p.hi)[at + b];
+            hv[1][b] = reinterpret_cast<const u32x4_t*>(p.lo)[at + b];
+        }
+    };
+    auto put = [&](int i) {
+        // (rows of slots without an expert hold whatever was there; nothing reads them)
+        const int s = i / KQ, t = i % KQ;
+        uint32_t* const to = h_lds + s * K + 16 * t;
+        hs[i] = put_tile(to, hv[0]) + put_tile(to + K / 2, hv[1]);
+    };
+    if (tid < tiles) take(tid);
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(begin + d, d);
+    float first = 0.0f;
+    if (p.residual && tid < 16 * T) first = bf16_lo(p.residual[static_cast<int64_t>(tid / 16) * N + n0 + tid % 16]);
+    asm volatile("" ::: "memory");
+    if (tid < tiles) put(tid);
+    for (int i = tid + blockDim.x; i < tiles; i += blockDim.x) {
+        take(i);
+        put(i);
+    }
+    __syncthreads();
+    const uint32_t bias = opaque_vgpr(kBf16Bias128x2);
+    float acc[kDotTokens] = {0.0f, 0.0f};
+    for (int at = begin; at < end; at += DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            if (where[d] >= 0) {
+                const int s = where[d] >> 16, t = 4 * (where[d] & 0xFFFF) + q;
+                float y = 0.0f;
+                if (t < KQ) {
+                    const uint32_t* const h = h_lds + s * K + 16 * t;
+                    y = dot_tile<2>(w[d], sz[d], h, h + K / 2, hs[s * KQ + t], bias);
+                }
+                if (s < p.k) acc[0] += y;
+                else acc[1] += y;
+            }
+            load(at + DEPTH + d, d);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kDotTokens; ++t) {
+        acc[t] += __shfl_xor(acc[t], 16, kWave);
+        acc[t] += __shfl_xor(acc[t], 32, kWave);
+        if (q == 0) red[wave][t][c] = acc[t];
+    }
+    __syncthreads();
+    if (tid < 16 * T) {
+        float y = 0.0f;
+        for (int v = 0; v < wk; ++v) y += red[v][tid / 16][tid % 16];
+        p.Y[static_cast<int64_t>(tid / 16) * N + n0 + tid % 16] = float_to_bf16_bits(y + first);
+    }
+}
+
+// Y = bf16(residual + the slots' shares in the order of the choices), four
 // columns a thread
 __global__ void __launch_bounds__(256) moe_join_kernel(MoeParams p) {
-    const int per = p.H / 8;
+    const int per = p.H / 4;
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= p.T * per) return;
     const int64_t t = i / per;
-    const int n = static_cast<int>(i % per) * 8;
-    float y[8];
+    const int n = static_cast<int>(i % per) * 4;
+    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    u32x2_t r = {0u, 0u};
+    if (p.residual) r = *reinterpret_cast<const u32x2_t*>(p.residual + t * p.H + n);
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+        // eight choices' shares in flight; one that is no expert has none
+        float4 v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-    for (int j = 0; j < p.k; ++j) {
-        const int64_t slot = t * p.k + j;
-        if (static_cast<uint32_t>(p.ids[slot]) >= static_cast<uint32_t>(p.E)) continue;
-        const float4* src = reinterpret_cast<const float4*>(p.part + slot * p.H + n);
-        const float4 a = src[0], b = src[1];
-        y[0] += a.x; y[1] += a.y; y[2] += a.z; y[3] += a.w;
-        y[4] += b.x; y[5] += b.y; y[6] += b.z; y[7] += b.w;
-    }
-    if (p.residual) {
-        const u32x4_t r = *reinterpret_cast<const u32x4_t*>(p.residual + t * p.H + n);
+        for (int j = 0; j < 8; ++j) {
+            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const int64_t slot = t * p.k + j0 + j;
+            if (j0 + j < p.k && static_cast<uint32_t>(p.ids[slot]) < static_cast<uint32_t>(p.E))
+                v[j] = *reinterpret_cast<const float4*>(p.part + slot * p.H + n);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            y[2 * e] += bf16_lo(r[e]);
-            y[2 * e + 1] += bf16_hi(r[e]);
+        for (int j = 0; j < 8; ++j) {
+            y[0] += v[j].x;
+            y[1] += v[j].y;
+            y[2] += v[j].z;
+            y[3] += v[j].w;
         }
     }
-    *reinterpret_cast<u32x4_t*>(p.Y + t * p.H + n) = u32x4_t{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                            pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])};
+    y[0] += bf16_lo(r[0]);
+    y[1] += bf16_hi(r[0]);
+    y[2] += bf16_lo(r[1]);
+    y[3] += bf16_hi(r[1]);
+    *reinterpret_cast<u32x2_t*>(p.Y + t * p.H + n) = u32x2_t{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
 }
 
 template <int MB, int FJ, int G, bool UP>
 hipError_t launch_stream(const MoeParams& p, hipStream_t stream) {
-    const int K = UP ? p.H : p.I, N = UP ? p.I : p.H, cols = UP ? 16 : 16 * FJ;
+    const int K = UP ? p.H : p.I, N = UP ? p.I : p.H, cols = UP ? 8 * FJ : 16 * FJ;
     const int64_t slots = p.T * p.k;
     const int experts = slots < p.E ? static_cast<int>(slots) : p.E;
     const int nb = (N + cols - 1) / cols, steps = (K + kStepK - 1) / kStepK;
     int64_t wk = 4096 / (static_cast<int64_t>(nb) * experts);
     wk = wk > 8 ? 8 : wk;
+    wk = wk < 4 ? 4 : wk;
     wk = wk > steps / 2 ? steps / 2 : wk;
     wk = wk < 1 ? 1 : wk;
-    hipLaunchKernelGGL((moe_stream_kernel<MB, FJ, G, UP>), dim3(static_cast<unsigned>(nb), static_cast<unsigned>(experts)),
-                       dim3(static_cast<unsigned>(64 * wk)), static_cast<size_t>(wk) * 256 * MB * FJ * sizeof(float), stream, p,
-                       static_cast<int>(wk));
+    const size_t lds = static_cast<size_t>(wk) * 256 * MB * FJ * sizeof(float);
+    const dim3 block(static_cast<unsigned>(64 * wk));
+    if constexpr (UP) {
+        if (slots <= kWave) {
+            hipLaunchKernelGGL((moe_stream_kernel<MB, FJ, G, true, true>),
+                               dim3(static_cast<unsigned>(nb), static_cast<unsigned>(experts + 1)), block, lds, stream, p,
+                               static_cast<int>(wk));
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((moe_stream_kernel<MB, FJ, G, UP, false>), dim3(static_cast<unsigned>(nb), static_cast<unsigned>(experts)),
+                       block, lds, stream, p, static_cast<int>(wk));
     return hipGetLastError();
 }
 
-template <int MB, bool UP>
-hipError_t launch_stream_g(const MoeParams& p, hipStream_t stream) {
-    switch (p.G) {
-        case 32: return launch_stream<MB, 2, 32, UP>(p, stream);
-        case 64: return launch_stream<MB, 2, 64, UP>(p, stream);
-        default: return launch_stream<MB, 2, 128, UP>(p, stream);
+template <int FJ, int G>
+hipError_t launch_down(const MoeParams& p, hipStream_t stream) {
+    const int nb = (p.H + 16 * FJ - 1) / (16 * FJ);
+    const int wk = 16 / FJ;
+    hipLaunchKernelGGL((moe_down_kernel<FJ, G>), dim3(static_cast<unsigned>(nb)), dim3(static_cast<unsigned>(64 * wk)),
+                       static_cast<size_t>(wk) * 256 * FJ * sizeof(float), stream, p, wk);
+    return hipGetLastError();
+}
+
+// one or two tokens, their rows within LDS
+bool dot_form(const MoeParams& p) {
+    const int64_t slots = p.T * p.k;
+    return p.T <= kDotTokens && slots <= kWave && dot_words(p.H, 1) <= kDotWords && slots * dot_words(p.I, 2) <= kDotWords;
+}
+hipError_t launch_dot(const MoeParams& p, hipStream_t stream) {
+    const int slots = static_cast<int>(p.T * p.k);
+    const int up_steps = (p.H + kStepK - 1) / kStepK;
+    int wk = up_steps < 8 ? up_steps : 8;
+    hipLaunchKernelGGL(moe_up_dot_kernel, dim3(static_cast<unsigned>(p.I / 16), static_cast<unsigned>(slots)),
+                       dim3(static_cast<unsigned>(64 * wk)), 4 * dot_words(p.H, 1), stream, p, wk);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    wk = slots * ((p.I + kStepK - 1) / kStepK);
+    wk = wk > 16 ? 16 : wk;
+    hipLaunchKernelGGL(moe_down_dot_kernel, dim3(static_cast<unsigned>(p.H / 16)), dim3(static_cast<unsigned>(64 * wk)),
+                       4 * slots * dot_words(p.I, 2), stream, p, wk);
+    return hipGetLastError();
+}
+
+// The rows of an expert in tiles on the matrix cores (gemm_f8.hip), where groups
+// are of 128 and an expert has enough of them.
+#ifndef W4_MOE_TILE_FROM
+#define W4_MOE_TILE_FROM 24
+#endif
+#ifndef W4_MOE_TILE_ROWS
+#define W4_MOE_TILE_ROWS 64
+#endif
+bool tile_form(const MoeParams& p) {
+    constexpr int64_t kMost = (int64_t{1} << 31) - 1;
+    const int64_t slots = p.T * p.k, wide = p.H > p.I ? p.H : p.I;
+    return p.G == 128 && p.T > kUnitTokens && slots >= static_cast<int64_t>(W4_MOE_TILE_FROM) * p.E &&
+           wide / 128 * W4_MOE_TILE_ROWS <= kGroupSums && 2 * slots * wide <= kMost &&
+           static_cast<int64_t>(p.H) * p.I / 2 <= kMost;
+}
+hipError_t launch_tiles(const MoeParams& p, hipStream_t stream) {
+    const int rows = W4_MOE_TILE_ROWS;
+    const int64_t slots = p.T * p.k, tiles = group_tiles(slots, p.E, rows);
+    const int64_t sums = p.T * (p.H / 128);
+    hipLaunchKernelGGL(moe_tiles_kernel, dim3(static_cast<unsigned>(1 + (sums * 16 + kListThreads - 1) / kListThreads)),
+                       dim3(kListThreads), 0, stream, p, rows);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    GroupParams g{};
+    g.X = p.X;
+    g.M = p.T;
+    g.K = p.H;
+    g.N = p.I;
+    g.G = p.G;
+    g.wq = p.gate.wq;
+    g.sz = p.gate.sz;
+    g.wq2 = p.up.wq;
+    g.sz2 = p.up.sz;
+    g.act = p.act;
+    g.Y = p.hi;
+    g.tiles = p.tiles;
+    g.tile_count = p.tile_count;
+    g.order = p.order;
+    g.weights = p.weights;
+    g.k = p.k;
+    g.sums = p.x_sums;
+    g.sums_out = p.h_sums;
+    e = launch_gemm_group(g, rows, tiles, stream);
+    if (e != hipSuccess) return e;
+    g.X = p.hi;
+    g.M = slots;
+    g.K = p.I;
+    g.N = p.H;
+    g.wq = p.down.wq;
+    g.sz = p.down.sz;
+    g.wq2 = nullptr;
+    g.sz2 = nullptr;
+    g.sums = p.h_sums;
+    g.part = p.part;
+    return launch_gemm_group(g, rows, tiles, stream);
+}
+
+hipError_t launch_join(const MoeParams& p, hipStream_t stream) {
+    hipLaunchKernelGGL(moe_join_kernel, dim3(static_cast<unsigned>((p.T * (p.H / 4) + 255) / 256)), dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <int G>
+hipError_t launch_moe_g(const MoeParams& p, hipStream_t stream) {
+    const int64_t slots = p.T * p.k;
+    hipError_t e;
+    if (slots > kWave) {
+        hipLaunchKernelGGL(moe_lists_kernel, dim3(1), dim3(kListThreads), 0, stream, p);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
+    const int64_t each = slots / p.E;             // an expert's rows, were the choices even
+    if (p.T <= kUnitTokens || each <= 12) e = launch_stream<1, 2, G, true>(p, stream);
+    else if (each <= 24) e = launch_stream<2, 2, G, true>(p, stream);
+    else e = launch_stream<4, 2, G, true>(p, stream);
+    if (e != hipSuccess) return e;
+    if (p.T <= kUnitTokens) return launch_down<1, G>(p, stream);
+    if (each <= 12) e = launch_stream<1, 2, G, false>(p, stream);
+    else if (each <= 24) e = launch_stream<2, 2, G, false>(p, stream);
+    else e = launch_stream<4, 2, G, false>(p, stream);
+    if (e != hipSuccess) return e;
+    return launch_join(p, stream);
 }
 
 }  // namespace
@@ -357,25 +938,36 @@ size_t moe_workspace(MoeParams& p, void* base) {
         at += (bytes + 255) & ~size_t{255};
         return q;
     };
-    p.offset = static_cast<int32_t*>(take(4 * (p.E + 1)));
-    p.active = static_cast<int32_t*>(take(4 * (p.E + 1)));
+    p.hi = static_cast<uint16_t*>(take(2 * (slots + 1) * p.I));
+    if (!tile_form(p)) p.lo = static_cast<uint16_t*>(take(2 * (slots + 1) * p.I));
+    p.runs = static_cast<int4*>(take(16 * p.E));
     p.order = static_cast<int32_t*>(take(4 * slots));
-    p.hi = static_cast<uint16_t*>(take(2 * slots * p.I));
-    p.lo = static_cast<uint16_t*>(take(2 * slots * p.I));
-    p.part = static_cast<float*>(take(4 * slots * p.H));
+    if (p.T <= kUnitTokens) {
+        p.unit_expert = static_cast<int32_t*>(take(4 * (slots + 1)));
+        p.unit_slot = static_cast<int32_t*>(take(4 * slots * kUnitTokens));
+    } else {
+        p.part = static_cast<float*>(take(4 * slots * p.H));
+        if (tile_form(p)) {
+            p.tiles = static_cast<int4*>(take(16 * group_tiles(static_cast<int64_t>(slots), p.E, W4_MOE_TILE_ROWS)));
+            p.tile_count = static_cast<int32_t*>(take(4));
+            p.x_sums = static_cast<float*>(take(4 * p.T * (p.H / 128)));
+            p.h_sums = static_cast<float*>(take(4 * slots * (p.I / 128)));
+        }
+    }
     return at;
 }
 
 hipError_t launch_moe(const MoeParams& p, hipStream_t stream) {
-    hipLaunchKernelGGL(moe_lists_kernel, dim3(1), dim3(kListThreads), 0, stream, p);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    e = launch_stream_g<1, true>(p, stream);
-    if (e != hipSuccess) return e;
-    e = launch_stream_g<1, false>(p, stream);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(moe_join_kernel, dim3(static_cast<unsigned>((p.T * (p.H / 8) + 255) / 256)), dim3(256), 0, stream, p);
-    return hipGetLastError();
+    if (dot_form(p)) return launch_dot(p, stream);
+    if (tile_form(p)) {
+        const hipError_t e = launch_tiles(p, stream);
+        return e != hipSuccess ? e : launch_join(p, stream);
+    }
+    switch (p.G) {
+        case 32: return launch_moe_g<32>(p, stream);
+        case 64: return launch_moe_g<64>(p, stream);
+        default: return launch_moe_g<128>(p, stream);
+    }
 }
 
 }  // namespace w4

@@ -16,11 +16,11 @@ using w4::hip_status;
 
 long long ll(int64_t v) { return static_cast<long long>(v); }
 
-constexpr int64_t kMaxTokens = int64_t{1} << 20;
+constexpr int64_t kMaxTokens = 1000000;
 constexpr int64_t kMaxWidth = 65536;      // hidden and inner sizes
 
 int check_sizes(const char* fn, int64_t T, int64_t E, int top_k) {
-    if (T < 0 || T > kMaxTokens) return fail(W4_EINVAL, "%s: T = %lld outside 0..2^20", fn, ll(T));
+    if (T < 0 || T > kMaxTokens) return fail(W4_EINVAL, "%s: T = %lld outside 0..%lld", fn, ll(T), ll(kMaxTokens));
     if (E <= 0) return fail(W4_EINVAL, "%s: E = %lld must be > 0", fn, ll(E));
     if (E > w4::kMaxExperts) return fail(W4_EUNSUPPORTED, "%s: E = %lld above %d", fn, ll(E), w4::kMaxExperts);
     if (top_k <= 0) return fail(W4_EINVAL, "%s: top_k = %d must be > 0", fn, top_k);
@@ -35,9 +35,10 @@ bool widths_ok(int64_t H, int64_t I, int G) {
 
 extern "C" {
 
-size_t w4_route_workspace_bytes(int64_t T, int64_t E) {
-    if (T <= 0 || T > kMaxTokens || E <= 0 || E > w4::kMaxExperts) return 0;
-    return static_cast<size_t>(T) * static_cast<size_t>(E) * sizeof(float);
+size_t w4_route_workspace_bytes(int64_t T, int64_t H, int64_t E) {
+    if (T <= 0 || T > kMaxTokens || E <= 0 || E > w4::kMaxExperts || H <= 0 || H > kMaxWidth || H % 8 != 0) return 0;
+    return static_cast<size_t>(w4::route_splits(T, static_cast<int>(E), static_cast<int>(H))) * static_cast<size_t>(T) *
+           static_cast<size_t>(E) * sizeof(float);
 }
 
 int w4_route(const uint16_t* X, int64_t T, int64_t H, const uint16_t* router, int64_t E, int top_k, int score,
@@ -56,11 +57,12 @@ int w4_route(const uint16_t* X, int64_t T, int64_t H, const uint16_t* router, in
     W4_REQUIRE_PTR(fn, router);
     if (!ids || !weights) return fail(W4_EINVAL, "%s: ids or weights is NULL", fn);
     W4_REQUIRE_PTR(fn, workspace);
-    const size_t need = w4_route_workspace_bytes(T, E);
+    const size_t need = w4_route_workspace_bytes(T, H, E);
     if (workspace_bytes < need)
         return fail(W4_EINVAL, "%s: workspace of %zu bytes, these sizes need %zu (w4_route_workspace_bytes)", fn, workspace_bytes, need);
     const w4::RouteParams p{X, T, static_cast<int>(H), router, static_cast<int>(E), top_k, score == W4_SCORE_SIGMOID, bias,
-                            renormalize != 0, scale, ids, weights, static_cast<float*>(workspace)};
+                            renormalize != 0, scale, ids, weights, static_cast<float*>(workspace),
+                            w4::route_splits(T, static_cast<int>(E), static_cast<int>(H))};
     return hip_status(w4::launch_route(p, stream), fn);
 }
 

@@ -23,8 +23,11 @@ struct RouteParams {
     float scale;
     int32_t* ids;            // [T, k]
     float* weights;          // [T, k]
-    float* logits;           // [T, E] workspace
+    float* logits;           // [splits, T, E] workspace: partial logits of the K ranges
+    int splits;
 };
+// K ranges that the logits of these sizes are split into
+int route_splits(int64_t T, int E, int H);
 hipError_t launch_route(const RouteParams& p, hipStream_t stream);
 
 struct MoeWeight {
@@ -42,12 +45,20 @@ struct MoeParams {
     const uint16_t* residual;   // [T, H] or null
     uint16_t* Y;             // [T, H]
     // workspace, see moe_workspace
-    int32_t* offset;         // [E + 1] first place of each expert's rows in `order`
-    int32_t* active;         // [E] experts with rows, then at [E] their number
-    int32_t* order;          // [T k] slots (t k + j) by expert
-    uint16_t* hi;            // [T k, I] rows of act(gate) up weight, upper and lower part
+    uint16_t* hi;            // [T k + 1, I] rows of act(gate) up weight by slot t k + j, upper and lower part
     uint16_t* lo;
+    int4* runs;              // [E] expert, first place in `order`, rows
+    int32_t* order;          // [T k] slots by expert
+    // up to 16 tokens: units of an expert and the tokens' slots with it
+    int32_t* unit_expert;    // [T k], their number at [T k]
+    int32_t* unit_slot;      // [T k, 16]; T k: the row of zeros
+    // more
     float* part;             // [T k, H] each slot's share of the result
+    // tiled products
+    int4* tiles;             // expert, first place in `order`, rows
+    int32_t* tile_count;
+    float* x_sums;           // [T, H / 128] row sums of X
+    float* h_sums;           // [T k, I / 128] of h, in the order of `order`
 };
 // bytes of the workspace, and the pointers into it
 size_t moe_workspace(MoeParams& p, void* base);
