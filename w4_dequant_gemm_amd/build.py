@@ -23,10 +23,11 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 KERNELS = ["quantize.hip", "prepack.hip", "rowquant.hip", "skinny.hip", "gemm.hip", "nf4.hip", "noalloc.hip", "gemm_f8.hip",
-           "kvcache.hip", "attention.hip", "attention_tile.hip", "sample.hip", "adjust.hip", "route.hip", "moe.hip"]
+           "kvcache.hip", "attention.hip", "attention_tile.hip", "sample.hip", "adjust.hip", "route.hip", "moe.hip",
+           "moe_tile.hip"]
 NO_CONTRACT = {"quantize.hip", "rowquant.hip", "nf4.hip", "adjust.hip"}
 # kernels whose MFMA results take VALU work: results in VGPRs, not AGPRs
-MFMA_VGPR = {"gemm_f8.hip", "attention.hip", "attention_tile.hip", "moe.hip"}
+MFMA_VGPR = {"gemm_f8.hip", "attention.hip", "attention_tile.hip", "moe.hip", "moe_tile.hip"}
 HOST_SOURCES = ["api.cpp", "decode_api.cpp", "moe_api.cpp", "portable.cpp"]   # host C++ (argument checks, file I/O)
 
 HIP_FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

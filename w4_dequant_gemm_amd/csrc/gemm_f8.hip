@@ -186,16 +186,8 @@ __device__ __forceinline__ float4_t mfma_f8_16x16x128(const int8x_t& a, const in
 // the same k), the row sums of the step's activations from four more MFMAs
 // against ones, and per group and output acc += s (T - (128 + z) X1): exact
 // weights, any zero point.
-//
-// GROUP (with A16): the rows of a mixture of experts, a tile of one expert's
-// rows.  The row sums are not made here but read (they lie in LDS, [step][row]):
-// with two column blocks a wave their MFMAs were a third of all.  PAIR gathers
-// the tokens' rows and leaves h = act(g) u weight in the order of the rows, with
-// its row sums (the tile's 128 columns are one group of the down product);
-// the down product leaves each slot's fp32 result.
-template <int BM_, int BN_, int WR_, int WC_, bool PAIR = false, int SA_ = 3, int DW_ = 2, bool A16 = false, bool EPI = false,
-          bool GROUP = false>
-__global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(std::conditional_t<GROUP, GroupParams, MulParams> p) {
+template <int BM_, int BN_, int WR_, int WC_, bool PAIR = false, int SA_ = 3, int DW_ = 2, bool A16 = false, bool EPI = false>
+__global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(MulParams p) {
     using namespace f8;
     using Gm = Geom<BM_, BN_, WR_, WC_>;
     constexpr int AB = A16 ? 2 : 1;               // bytes per activation
@@ -231,33 +223,10 @@ __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(std::conditiona
     const int row0 = 16 * RB * wr;   // the wave's first tile row
     static_assert(!PAIR || (WR_ == 1 && WC_ % 2 == 0 && (BN_ / 2) % 64 == 0), "pair tiles");
     constexpr int BNO = PAIR ? BN / 2 : BN;      // output columns of the tile
-    static_assert(!GROUP || (A16 && !EPI), "the grouped form is the bf16-activation form's");
-    F8Job job;
-    int64_t M = p.M;
-    const int64_t N = p.N, K = p.K;
-    int64_t expert = 0;
-    int first = 0;                               // GROUP: the tile's first place in the order of the rows
-    if constexpr (GROUP) {
-        const int nt = static_cast<int>((N + BNO - 1) / BNO);
-        const int total = *p.tile_count * nt;
-        if (static_cast<int>(blockIdx.x) >= total) return;
-        const int j = static_cast<int>(xcd_tile(blockIdx.x, total));
-        const int4 t = p.tiles[j / nt];
-        expert = __builtin_amdgcn_readfirstlane(t.x);
-        first = __builtin_amdgcn_readfirstlane(t.y);
-        M = __builtin_amdgcn_readfirstlane(t.z);
-        job = F8Job{0, static_cast<int64_t>(j % nt) * BNO, 0, static_cast<int>(K / BK), -1};
-    } else {
-        job = f8_job<BM, BNO>(p);
-    }
+    const F8Job job = f8_job<BM, BNO>(p);
     const int64_t m_base = job.m_base, n_base = job.n_base;
+    const int64_t M = p.M, N = p.N, K = p.K;
     __shared__ float lds_xs[BM];
-    extern __shared__ __attribute__((aligned(16))) float lds_x1[];   // GROUP: [step][row]
-    __shared__ int lds_slot[GROUP ? BM : 1];
-    if constexpr (GROUP) {
-        for (int r = tid; r < BM; r += Gm::NT) lds_slot[r] = p.order[first + (r < M ? r : 0)];
-        __syncthreads();
-    }
     const int kb = job.kb, KT = job.KT;
     const int g_shift = group_shift(p.G);
 
@@ -275,27 +244,15 @@ __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(std::conditiona
     // buffer's end and read as zeros (their outputs are never stored).
     const int a_row0 = 8 * wave * ADMA + (lane >> 3);
     const int a_chunk = (lane & 7) ^ (lane >> 4) ^ ((wave * ADMA) & 1 ? 4 : 0);
-    const u32x4_t a_rsrc = buffer_rsrc(p.X, static_cast<uint32_t>((GROUP ? p.M : M) * K * AB));
+    const u32x4_t a_rsrc = buffer_rsrc(p.X, static_cast<uint32_t>(M * K * AB));
     const uint32_t a_voff = static_cast<uint32_t>((m_base + a_row0) * K + a_chunk * 16);
     // A16: a 256-byte stage row of 16 chunks, chunk ch of row r at position
     // ch ^ (r & 15); load `it` fills rows 4 (wave ADMA + it) .. + 3, lane l
     // row 4 (wave ADMA + it) + l / 16 at position l % 16
-    // GROUP: the rows of the lane's loads (past the tile's: its first, never stored)
-    [[maybe_unused]] uint32_t g_voff[GROUP ? ADMA : 1];
-    if constexpr (GROUP) {
-#pragma unroll
-        for (int it = 0; it < ADMA; ++it) {
-            const int r = 4 * (wave * ADMA + it) + (lane >> 4);
-            const int64_t row = PAIR ? lds_slot[r] / p.k : first + (r < M ? r : 0);
-            g_voff[it] = static_cast<uint32_t>(row * (2 * K) + 16 * ((lane & 15) ^ (r & 15)));
-        }
-    }
     auto dma_item = [&](int kt, uint8_t* stage, int it) {
         kt = (kt < KT ? kt : KT - 1) + kb;
         uint32_t voff;
-        if constexpr (GROUP) {
-            voff = g_voff[it];
-        } else if constexpr (A16) {
+        if constexpr (A16) {
             const int r = 4 * (wave * ADMA + it) + (lane >> 4);
             voff = static_cast<uint32_t>((m_base + r) * (2 * K) + 16 * ((lane & 15) ^ (r & 15)));
         } else {
@@ -326,10 +283,8 @@ __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(std::conditiona
     // (PAIR: the up weight for waves wc >= WC / 2, at the same columns)
     const bool up_wave = PAIR && wc >= WC / 2;
     const int wcol = WN * (PAIR ? wc % (WC / 2) : wc);   // the wave's first column in the tile
-    const uint32_t* const wq_base = (up_wave ? p.wq2 : p.wq) + (GROUP ? expert * (N * (K / 8)) : 0);
-    const uint32_t* const sz_base = (up_wave ? p.sz2 : p.sz) + (GROUP ? expert * (N * (K / p.G)) : 0);
-    const u32x4_t q_rsrc = buffer_rsrc(wq_base, static_cast<uint32_t>(N * K / 2));
-    const u32x4_t s_rsrc = buffer_rsrc(sz_base, static_cast<uint32_t>(N * (K / p.G) * 4));
+    const u32x4_t q_rsrc = buffer_rsrc(up_wave ? p.wq2 : p.wq, static_cast<uint32_t>(N * K / 2));
+    const u32x4_t s_rsrc = buffer_rsrc(up_wave ? p.sz2 : p.sz, static_cast<uint32_t>(N * (K / p.G) * 4));
     uint32_t qblk[CB], sblk[CB], nrb[CB];      // uniform: block byte offsets, rows in the block
     uint32_t qoff[CB], soff[CB];               // the lane's byte offsets in the block
     const int64_t nblk_last = ((N - 1) / 16) * 16;
@@ -512,9 +467,7 @@ __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(std::conditiona
             for (int u = 0; u < NSLOT; ++u) {
                 const int rb = u / CB, cb = u % CB;
                 __builtin_amdgcn_sched_barrier(0);
-                if constexpr (GROUP) {
-                    if (cb == 0) X1[rb] = *reinterpret_cast<const float4_t*>(lds_x1 + kt * BM + 16 * rb + 4 * q);
-                } else if (cb == 0) {
+                if (cb == 0) {
                     // the step's row sums of the block's 16 rows (every column alike)
                     X1[rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[0], ones, float4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
 #pragma unroll
@@ -609,15 +562,6 @@ __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(std::conditiona
     for (int it = 0; it < NCONV; ++it) conv_item(it, rr[0], oo[0]);
     // the tile's row scales for the epilogue of a whole tile (a partial tile
     // leaves them to the split sum), fetched under the first steps' loads
-    if constexpr (GROUP) {
-        // (GROUP: the rows' weights in their place)
-        for (int r = tid; r < BM; r += Gm::NT) lds_xs[r] = PAIR ? p.weights[lds_slot[r]] : 1.0f;
-        for (int i = tid; i < KT * BM; i += Gm::NT) {
-            const int g = i / BM, r = i % BM;
-            const int64_t row = PAIR ? lds_slot[r] / p.k : first + (r < M ? r : 0);
-            lds_x1[i] = p.sums[row * KT + g];
-        }
-    } else
     for (int r = tid; r < BM; r += Gm::NT) lds_xs[r] = !A16 && job.part < 0 && m_base + r < M ? p.xscale[m_base + r] : 1.0f;
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0);
@@ -682,7 +626,7 @@ __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(std::conditiona
             if (!up_wave) {
 #pragma unroll
                 for (int rb = hh * RB / 2; rb < (hh + 1) * RB / 2; ++rb) {
-                    float hmax[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // (GROUP: sums)
+                    float hmax[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int cb = 0; cb < CB; ++cb) {
                         const int oc = wcol + 16 * cb + c;
@@ -693,29 +637,14 @@ __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(std::conditiona
                             const int64_t row = m_base + lr;
                             const float r = lds_xs[lr];
                             const float u = su(oc, lr - hh * (BM / 2));
-                            if constexpr (GROUP) {
-                                // (N is a multiple of the tile's columns)
-                                if (row < M) {
-                                    const uint16_t hb = float_to_bf16_bits(activation(p.act, acc[rb][cb][e]) * u * r);
-                                    p.Y[(first + row) * N + col] = hb;
-                                    hmax[e] += bf16_lo(hb);
-                                }
-                            } else if (row < M && col < N) {
+                            if (row < M && col < N) {
                                 const uint16_t hb = float_to_bf16_bits(activation(p.act, acc[rb][cb][e] * r) * (u * r));
                                 p.Y[row * N + col] = hb;
                                 hmax[e] = fmaxf(hmax[e], fabsf(bf16_lo(hb)));
                             }
                         }
                     }
-                    if constexpr (GROUP) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float v = hmax[e];
-#pragma unroll
-                            for (int off = 8; off >= 1; off >>= 1) v += __shfl_xor(v, off, 16);
-                            if (c == 0) lds_amax[wc][16 * rb + 4 * q + e] = v;
-                        }
-                    } else if (p.amax_part) {
+                    if (p.amax_part) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float v = max16(hmax[e]);
@@ -725,15 +654,7 @@ __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(std::conditiona
                 }
             }
         }
-        if constexpr (GROUP) {
-            __syncthreads();
-            for (int r = tid; r < BM; r += Gm::NT) {
-                float v = 0.0f;
-#pragma unroll
-                for (int w = 0; w < WC / 2; ++w) v += lds_amax[w][r];
-                if (r < M) p.sums_out[(first + r) * (N / BNO) + n_base / BNO] = v;
-            }
-        } else if (p.amax_part) {
+        if (p.amax_part) {
             __syncthreads();
             const int64_t tcol = n_base / BNO;
             for (int r = tid; r < BM; r += Gm::NT) {
@@ -743,20 +664,6 @@ __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(std::conditiona
                 if (m_base + r < M) p.amax_part[(m_base + r) * p.amax_tiles + tcol] = v;
             }
         }
-        return;
-    }
-    if constexpr (GROUP) {
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int lr = 16 * rb + 4 * q + e;
-                if (lr >= M) continue;
-                float* const dst = p.part + static_cast<int64_t>(lds_slot[lr]) * N + n_base + wcol + c;
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb)
-                    if (n_base + wcol + 16 * cb + c < N) dst[16 * cb] = acc[rb][cb][e];
-            }
         return;
     }
     const bool whole = job.part < 0;
@@ -1017,25 +924,6 @@ hipError_t launch_gemm_a16_pair(const MulParams& p, hipStream_t stream) {
     else
         hipLaunchKernelGGL((gemm_f8_kernel<64, 256, 1, 8, true, 3, 3, true>), dim3(static_cast<unsigned>(tiles)), dim3(512),
                            0, stream, q);
-    return hipGetLastError();
-}
-
-hipError_t launch_gemm_group(const GroupParams& p, int tile_rows, int64_t tiles, hipStream_t stream) {
-    const bool pair = p.wq2 != nullptr;
-    if (p.x_fp8 || p.G != f8::BK || p.K % f8::BK != 0 || p.N % (pair ? 128 : 16) != 0 || !f8_fits_buffers(2 * p.M, p.K, p.N) ||
-        p.K / f8::BK * tile_rows > kGroupSums || (tile_rows != 64 && tile_rows != 128))
-        return hipErrorInvalidValue;
-    const int64_t grid = tiles * (pair ? (p.N + 127) / 128 : (p.N + 255) / 256);
-    if (grid <= 0 || grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    const size_t lds = static_cast<size_t>(p.K / f8::BK) * tile_rows * sizeof(float);
-    auto launch = [&](auto rows, auto is_pair) {
-        hipLaunchKernelGGL((gemm_f8_kernel<decltype(rows)::value, 256, 1, 8, decltype(is_pair)::value, 3, 3, true, false, true>),
-                           dim3(static_cast<unsigned>(grid)), dim3(512), lds, stream, p);
-    };
-    using r64 = std::integral_constant<int, 64>;
-    using r128 = std::integral_constant<int, 128>;
-    if (tile_rows == 64) pair ? launch(r64{}, std::true_type{}) : launch(r64{}, std::false_type{});
-    else pair ? launch(r128{}, std::true_type{}) : launch(r128{}, std::false_type{});
     return hipGetLastError();
 }
 

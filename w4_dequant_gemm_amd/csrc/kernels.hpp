@@ -100,29 +100,6 @@ struct MulParams {
     const uint16_t* residual = nullptr;   // [M, N] or null
     int out_act = 0;
 };
-// One product of every expert's rows (the bf16-activation form of the fp8
-// kernel, groups of 128): p.wq, p.sz (and the up weight's p.wq2, p.sz2) hold the
-// experts' weights one after the other, and a workgroup's tile is 64 or 128 of
-// one expert's rows in the order of `order`.
-struct GroupParams : MulParams {
-    const int4* tiles;        // expert, first place in `order`, rows
-    const int32_t* tile_count;
-    const int32_t* order;     // slots t k + j by expert
-    const float* weights;     // [slots]
-    int k;
-    // row sums over each 128 k of X: [T, K / 128] with wq2 (X holds the tokens'
-    // rows), else [slots, K / 128] in the order of `order`, as X's rows are
-    const float* sums;
-    float* sums_out;          // with wq2: the same of Y, [slots, N / 128]
-    float* part;              // without wq2: fp32 results by slot, [slots, N]
-};
-// most row sums of a tile (they lie in LDS): K / 128 times its rows
-constexpr int64_t kGroupSums = 8192;
-// row tiles of at most `rows` rows that `slots` slots of E experts come to
-constexpr int64_t group_tiles(int64_t slots, int64_t E, int rows) { return slots / rows + (slots < E ? slots : E); }
-// `tile_rows` 64 or 128; at most `tiles` row tiles
-hipError_t launch_gemm_group(const GroupParams& p, int tile_rows, int64_t tiles, hipStream_t stream);
-
 // largest M of the streaming kernel's gate and up pass; above it the tiled
 // pair GEMM (K a multiple of 64) takes the fused product
 constexpr int64_t kGateUpMaxM = 32;

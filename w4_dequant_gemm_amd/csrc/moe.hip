@@ -26,7 +26,6 @@
 // h rounded to bf16 once the result was 1.4 times as far from the exact one
 // as its own rounding to bf16 leaves it.
 #include "device.hpp"
-#include "kernels.hpp"
 #include "moe_kernels.hpp"
 
 namespace w4 {
@@ -46,9 +45,9 @@ namespace {
 struct RunMem {
     int count[kMaxExperts];
 };
-// TILES: also the runs cut into tiles of `tile_rows` rows, for the tiled products.
+// TILES: also the runs cut into tiles, for the tiled products.
 template <bool TILES>
-__device__ __forceinline__ void build_runs(const MoeParams& p, RunMem& m, int tid, int threads, int tile_rows = 64) {
+__device__ __forceinline__ void build_runs(const MoeParams& p, RunMem& m, int tid, int threads) {
     for (int e = tid; e < p.E; e += threads) m.count[e] = 0;
     __syncthreads();
     const int slots = static_cast<int>(p.T * p.k);
@@ -74,7 +73,8 @@ __device__ __forceinline__ void build_runs(const MoeParams& p, RunMem& m, int ti
             if (e < p.E) m.count[e] = first;
             if (mine > 0) p.runs[active + __builtin_popcountll(some & ((uint64_t{1} << tid) - 1))] = make_int4(e, first, mine, 0);
             if constexpr (TILES) {
-                const int own = (mine + tile_rows - 1) / tile_rows;
+                constexpr int kRows = kMoeTileRows;
+                const int own = (mine + kRows - 1) / kRows;
                 int before = own;
 #pragma unroll
                 for (int off = 1; off < kWave; off <<= 1) {
@@ -83,7 +83,7 @@ __device__ __forceinline__ void build_runs(const MoeParams& p, RunMem& m, int ti
                 }
                 for (int i = 0; i < own; ++i)
                     p.tiles[tiles + before - own + i] =
-                        make_int4(e, first + i * tile_rows, mine - i * tile_rows < tile_rows ? mine - i * tile_rows : tile_rows, 0);
+                        make_int4(e, first + i * kRows, mine - i * kRows < kRows ? mine - i * kRows : kRows, 0);
                 tiles += __shfl(before, kWave - 1, kWave);
             }
             rows += __shfl(upto, kWave - 1, kWave);
@@ -184,10 +184,10 @@ __global__ void __launch_bounds__(kListThreads) moe_lists_kernel(MoeParams p) {
 
 // For the tiled products: workgroup 0 makes the runs and tiles, the others the
 // tokens' row sums over each 128 k (16 lanes a sum).
-__global__ void __launch_bounds__(kListThreads) moe_tiles_kernel(MoeParams p, int tile_rows) {
+__global__ void __launch_bounds__(kListThreads) moe_tiles_kernel(MoeParams p) {
     __shared__ RunMem mem;
     if (blockIdx.x == 0) {
-        build_runs<true>(p, mem, threadIdx.x, kListThreads, tile_rows);
+        build_runs<true>(p, mem, threadIdx.x, kListThreads);
         return;
     }
     const int64_t i = (static_cast<int64_t>(blockIdx.x - 1) * kListThreads + threadIdx.x) / 16;
@@ -844,61 +844,30 @@ hipError_t launch_dot(const MoeParams& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The rows of an expert in tiles on the matrix cores (gemm_f8.hip), where groups
+// The rows of an expert in tiles on the matrix cores (moe_tile.hip), where groups
 // are of 128 and an expert has enough of them.
 #ifndef W4_MOE_TILE_FROM
 #define W4_MOE_TILE_FROM 24
 #endif
-#ifndef W4_MOE_TILE_ROWS
-#define W4_MOE_TILE_ROWS 64
-#endif
+int64_t tile_count(const MoeParams& p) {
+    const int64_t slots = p.T * p.k;
+    return slots / kMoeTileRows + (slots < p.E ? slots : p.E);
+}
 bool tile_form(const MoeParams& p) {
+    // (the activations are addressed with 31-bit byte offsets)
     constexpr int64_t kMost = (int64_t{1} << 31) - 1;
     const int64_t slots = p.T * p.k, wide = p.H > p.I ? p.H : p.I;
     return p.G == 128 && p.T > kUnitTokens && slots >= static_cast<int64_t>(W4_MOE_TILE_FROM) * p.E &&
-           wide / 128 * W4_MOE_TILE_ROWS <= kGroupSums && 2 * slots * wide <= kMost &&
-           static_cast<int64_t>(p.H) * p.I / 2 <= kMost;
+           wide / 128 * kMoeTileRows <= kMoeTileSums && 2 * slots * wide <= kMost;
 }
 hipError_t launch_tiles(const MoeParams& p, hipStream_t stream) {
-    const int rows = W4_MOE_TILE_ROWS;
-    const int64_t slots = p.T * p.k, tiles = group_tiles(slots, p.E, rows);
     const int64_t sums = p.T * (p.H / 128);
     hipLaunchKernelGGL(moe_tiles_kernel, dim3(static_cast<unsigned>(1 + (sums * 16 + kListThreads - 1) / kListThreads)),
-                       dim3(kListThreads), 0, stream, p, rows);
+                       dim3(kListThreads), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    GroupParams g{};
-    g.X = p.X;
-    g.M = p.T;
-    g.K = p.H;
-    g.N = p.I;
-    g.G = p.G;
-    g.wq = p.gate.wq;
-    g.sz = p.gate.sz;
-    g.wq2 = p.up.wq;
-    g.sz2 = p.up.sz;
-    g.act = p.act;
-    g.Y = p.hi;
-    g.tiles = p.tiles;
-    g.tile_count = p.tile_count;
-    g.order = p.order;
-    g.weights = p.weights;
-    g.k = p.k;
-    g.sums = p.x_sums;
-    g.sums_out = p.h_sums;
-    e = launch_gemm_group(g, rows, tiles, stream);
-    if (e != hipSuccess) return e;
-    g.X = p.hi;
-    g.M = slots;
-    g.K = p.I;
-    g.N = p.H;
-    g.wq = p.down.wq;
-    g.sz = p.down.sz;
-    g.wq2 = nullptr;
-    g.sz2 = nullptr;
-    g.sums = p.h_sums;
-    g.part = p.part;
-    return launch_gemm_group(g, rows, tiles, stream);
+    e = launch_moe_tile(p, true, tile_count(p), stream);
+    return e != hipSuccess ? e : launch_moe_tile(p, false, tile_count(p), stream);
 }
 
 hipError_t launch_join(const MoeParams& p, hipStream_t stream) {
@@ -948,7 +917,7 @@ size_t moe_workspace(MoeParams& p, void* base) {
     } else {
         p.part = static_cast<float*>(take(4 * slots * p.H));
         if (tile_form(p)) {
-            p.tiles = static_cast<int4*>(take(16 * group_tiles(static_cast<int64_t>(slots), p.E, W4_MOE_TILE_ROWS)));
+            p.tiles = static_cast<int4*>(take(16 * tile_count(p)));
             p.tile_count = static_cast<int32_t*>(take(4));
             p.x_sums = static_cast<float*>(take(4 * p.T * (p.H / 128)));
             p.h_sums = static_cast<float*>(take(4 * slots * (p.I / 128)));

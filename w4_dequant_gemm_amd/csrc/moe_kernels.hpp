@@ -64,4 +64,10 @@ struct MoeParams {
 size_t moe_workspace(MoeParams& p, void* base);
 hipError_t launch_moe(const MoeParams& p, hipStream_t stream);
 
+// the tiled products (moe_tile.hip): rows of a tile, the most row sums of one
+// (they lie in LDS), and the launch for at most `tiles` tiles
+constexpr int kMoeTileRows = 64;
+constexpr int kMoeTileSums = 8192;
+hipError_t launch_moe_tile(const MoeParams& p, bool up, int64_t tiles, hipStream_t stream);
+
 }  // namespace w4

@@ -1,0 +1,289 @@
+// The products of a mixture of experts with many tokens, on gfx950's matrix
+// cores (groups of 128): tiles of 64 of one expert's rows.
+//
+//   up:    h = bf16(w act(Wg x) * (Wu x)) of every slot, in the order of the
+//          experts' rows, and h's sums over each group of 128
+//   down:  part[slot] = Wd h, fp32
+//
+// A workgroup of four waves computes 64 rows by 128 columns of h (or 256
+// columns of the down product); a wave owns all 64 rows of 64 weight columns,
+// in two blocks of 32: the same 32 columns of the gate and of the up weight, so
+// that a lane holds both sums of its outputs, or 64 columns of the down weight.
+// Four 32 x 32 x 16 MFMAs then share two fragments of activations and two of
+// weights: with 32 columns a wave (four 16 x 16 MFMAs to four fragments) the
+// reads of the activations from LDS took as long as the matrix cores, and the
+// up product of 1999 tokens by 64 experts 206 us.
+//
+// The activations go straight from global memory into LDS, two steps of 128 k
+// ahead in three stages of 64 x 256 bytes; chunk ch (16 bytes) of row r lies at
+// ch ^ (r & 15).  The weights never pass through LDS: half h of the lanes loads
+// the 16 bytes of every second 32-k tile, a step ahead, and a code word becomes
+// the four registers of an MFMA operand (the exact bf16 values 128 + u) right
+// before its MFMAs; MFMA j of a 64-k half takes the 8 k at 32 h + 8 j.  With x1
+// the row sum of the group's activations, which a kernel before has made,
+//   acc += s (T - (128 + z) x1)
+// per group, exact in the weights.
+#include "device.hpp"
+#include "moe_kernels.hpp"
+
+namespace w4 {
+namespace {
+
+constexpr int kRows = kMoeTileRows, kThreads = 256, kStepK = 128;
+constexpr int kStage = kRows * kStepK * 2;          // bytes
+constexpr int kDma = kStage / (1024 * 4);           // loads to LDS a wave and step
+static_assert(kRows == 64, "two row blocks of 32");
+
+__device__ __forceinline__ u32x4_t tile_rsrc(const void* base, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    return u32x4_t{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a))),
+                   static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32))) & 0xFFFFu,
+                   static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
+}
+
+template <bool UP>
+__global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds_a0[kStage];
+    __shared__ __attribute__((aligned(16))) uint8_t lds_a1[kStage];
+    __shared__ __attribute__((aligned(16))) uint8_t lds_a2[kStage];
+    __shared__ int lds_slot[kRows];
+    __shared__ float lds_weight[kRows];
+    extern __shared__ __attribute__((aligned(16))) float lds_x1[];   // [step][row]
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 31, h = lane >> 5;
+    const int K = UP ? p.H : p.I, N = UP ? p.I : p.H, KT = K / kStepK;
+    constexpr int COLS = UP ? 128 : 256;             // the workgroup's columns of the result
+    const int nt = (N + COLS - 1) / COLS;
+    const int total = *p.tile_count * nt;
+    if (static_cast<int>(blockIdx.x) >= total) return;
+    const int job = static_cast<int>(xcd_tile(blockIdx.x, total));
+    const int4 t4 = p.tiles[job / nt];
+    const int expert = __builtin_amdgcn_readfirstlane(t4.x);
+    const int first = __builtin_amdgcn_readfirstlane(t4.y);
+    const int rows = __builtin_amdgcn_readfirstlane(t4.z);
+    const int n0 = (job % nt) * COLS;
+    if (tid < kRows) {
+        const int slot = p.order[first + (tid < rows ? tid : 0)];
+        lds_slot[tid] = slot;
+        if constexpr (UP) lds_weight[tid] = p.weights[slot];
+    }
+    __syncthreads();
+
+    // activations: load `it` of the wave fills stage rows 4 (4 wave + it) .. + 3,
+    // lane l row 4 (4 wave + it) + l / 16 at position l % 16 (rows past the
+    // tile's: its first, never stored)
+    const u32x4_t a_rsrc = tile_rsrc(UP ? p.X : p.hi, static_cast<uint32_t>((UP ? p.T : p.T * p.k) * K * 2));
+    uint32_t a_voff[kDma];
+#pragma unroll
+    for (int it = 0; it < kDma; ++it) {
+        const int r = 4 * (kDma * wave + it) + (lane >> 4);
+        const int row = UP ? lds_slot[r] / p.k : first + (r < rows ? r : 0);
+        a_voff[it] = static_cast<uint32_t>(row) * static_cast<uint32_t>(2 * K) + 16u * ((lane & 15) ^ (r & 15));
+    }
+    auto dma = [&](int kt, uint8_t* stage) {
+        kt = kt < KT ? kt : KT - 1;
+        const uint32_t soff = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kt * kStepK * 2));
+        typedef __attribute__((address_space(3))) uint8_t lds_u8;
+#pragma unroll
+        for (int it = 0; it < kDma; ++it) {
+            const uint32_t m0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u8*)stage)) +
+                                static_cast<uint32_t>((kDma * wave + it) * 1024);
+            // (a load to LDS may follow a write of M0 after one wait state; it
+            // has no register result, and the wait at a step's start covers it)
+            asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
+                         ::"v"(a_voff[it]), "s"(a_rsrc), "s"(m0), "s"(soff) : "memory", "m0");
+        }
+    };
+
+    // weights: block j's 32 columns are two 16-row blocks of the layout (N is a
+    // multiple of 32); lane (c, h) reads tile 4 kt + 2 m + h of its column
+    const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * KT;
+    const uint32_t* wb[2];
+    const uint32_t* sb[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const MoeWeight& w = UP ? (j == 0 ? p.gate : p.up) : p.down;
+        int r0 = n0 + (UP ? 32 * wave : 64 * wave + 32 * j);
+        r0 = r0 < N ? r0 : N - 32;                   // (columns past N are not stored)
+        r0 += c & 16;
+        wb[j] = w.wq + expert * words + static_cast<int64_t>(r0) * (K / 8) + 4 * (c & 15) + 64 * h;
+        sb[j] = w.sz + expert * groups + static_cast<int64_t>(r0) * KT + (c & 15);
+    }
+    struct Regs {
+        u32x4_t q[2][2];     // [block][64-k half]
+        uint32_t s[2];
+    };
+    auto load_w = [&](int kt, Regs& r) {
+        kt = kt < KT ? kt : KT - 1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) r.q[j][m] = *reinterpret_cast<const u32x4_t*>(wb[j] + 64 * (4 * kt + 2 * m));
+            r.s[j] = sb[j][16 * kt];
+        }
+    };
+    constexpr int kWLoads = 6;
+
+    Regs rr[2];
+    load_w(0, rr[0]);
+    asm volatile("" ::: "memory");
+    dma(0, lds_a0);
+    dma(1, lds_a1);
+    for (int i = tid; i < KT * kRows; i += kThreads) {
+        const int g = i / kRows, r = i % kRows;
+        const int64_t row = UP ? lds_slot[r] / p.k : first + (r < rows ? r : 0);
+        lds_x1[i] = (UP ? p.x_sums : p.h_sums)[row * KT + g];
+    }
+
+    float16_t acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    const uint32_t bias = opaque_vgpr(kBf16Bias128x2);
+
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    auto step = [&](int kt, const uint8_t* A, uint8_t* Ad, const Regs& cur, Regs& next) __attribute__((always_inline)) {
+        load_w(kt + 1, next);
+        asm volatile("" ::: "memory");
+        dma(kt + 2, Ad);
+        float16_t T[2][2];
+        // fragments a slot ahead; the barriers keep the scheduler from fetching
+        // more of them than there are registers
+        auto frag = [&](int i, int f) {
+            return *reinterpret_cast<const bf16x8_t*>(A + (32 * i + c) * 256 + 16 * ((8 * (f >> 2) + 4 * h + (f & 3)) ^ (c & 15)));
+        };
+        bf16x8_t a[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) a[0][i] = frag(i, 0);
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (f < 7) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) a[(f + 1) & 1][i] = frag(i, f + 1);
+            }
+            bf16x8_t b[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t w = cur.q[j][f >> 2][f & 3];
+                b[j] = __builtin_bit_cast(bf16x8_t, u32x4_t{nibble_pair_bf16(w, 0, bias), nibble_pair_bf16(w, 1, bias),
+                                                            nibble_pair_bf16(w, 2, bias), nibble_pair_bf16(w, 3, bias)});
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float16_t zero = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                    T[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[f & 1][i], b[j], f == 0 ? zero : T[i][j], 0, 0, 0);
+                }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // register e of lane (c, h): row 8 (e / 4) + 4 h + e % 4 of its block, column c
+        float sc[2], zc[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            sc[j] = half_bits_to_float(cur.s[j]);
+            zc[j] = 128.0f + half_bits_to_float(cur.s[j] >> 16);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float4_t x1 = *reinterpret_cast<const float4_t*>(lds_x1 + kt * kRows + 32 * i + 8 * g + 4 * h);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 4 * g; e < 4 * g + 4; ++e)
+                        acc[i][j][e] = fmaf(sc[j], fmaf(-zc[j], x1[e % 4], T[i][j][e]), acc[i][j][e]);
+            }
+        }
+        // the next step's activations are in LDS: all loads done but the last
+        // step's and this one's weights and activations
+        asm volatile("" ::: "memory");
+        constexpr int kLeft = kWLoads + kDma;
+        __builtin_amdgcn_s_waitcnt((kLeft & 15) | (7 << 4) | ((kLeft >> 4) << 14));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    int kt = 0;
+    for (; kt + 6 <= KT; kt += 6) {
+        step(kt, lds_a0, lds_a2, rr[0], rr[1]);
+        step(kt + 1, lds_a1, lds_a0, rr[1], rr[0]);
+        step(kt + 2, lds_a2, lds_a1, rr[0], rr[1]);
+        step(kt + 3, lds_a0, lds_a2, rr[1], rr[0]);
+        step(kt + 4, lds_a1, lds_a0, rr[0], rr[1]);
+        step(kt + 5, lds_a2, lds_a1, rr[1], rr[0]);
+    }
+    if (kt < KT) step(kt, lds_a0, lds_a2, rr[0], rr[1]);
+    if (kt + 1 < KT) step(kt + 1, lds_a1, lds_a0, rr[1], rr[0]);
+    if (kt + 2 < KT) step(kt + 2, lds_a2, lds_a1, rr[0], rr[1]);
+    if (kt + 3 < KT) step(kt + 3, lds_a0, lds_a2, rr[1], rr[0]);
+    if (kt + 4 < KT) step(kt + 4, lds_a1, lds_a0, rr[0], rr[1]);
+    __builtin_amdgcn_s_waitcnt(0);                   // nothing is on its way into LDS any more
+    asm volatile("" ::: "memory");
+    __syncthreads();
+
+    if constexpr (UP) {
+        // h through LDS, [row][128] bf16 (chunk ch of row r at ch ^ (r & 15)),
+        // out in 16-byte pieces with the rows' sums
+        uint16_t* const hl = reinterpret_cast<uint16_t*>(lds_a0);
+        const int col = 32 * wave + c;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int r = 32 * i + 8 * (e / 4) + 4 * h + e % 4;
+                const float v = activation(p.act, acc[i][0][e]) * acc[i][1][e] * lds_weight[r];
+                hl[r * 128 + 8 * ((col >> 3) ^ (r & 15)) + (col & 7)] = float_to_bf16_bits(v);
+            }
+        __syncthreads();
+        const int r = tid >> 2, part = tid & 3;      // a row's quarter of 32 columns
+        float sum = 0.0f;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(hl + r * 128 + 8 * ((4 * part + b) ^ (r & 15)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += bf16_lo(v[e]) + bf16_hi(v[e]);
+            if (r < rows) *reinterpret_cast<u32x4_t*>(p.hi + static_cast<int64_t>(first + r) * N + n0 + 32 * part + 8 * b) = v;
+        }
+        sum += __shfl_xor(sum, 1, kWave);
+        sum += __shfl_xor(sum, 2, kWave);
+        if (r < rows && part == 0) p.h_sums[static_cast<int64_t>(first + r) * (N / 128) + n0 / 128] = sum;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int r = 32 * i + 8 * (e / 4) + 4 * h + e % 4;
+                if (r >= rows) continue;
+                float* const dst = p.part + static_cast<int64_t>(lds_slot[r]) * N;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int n = n0 + 64 * wave + 32 * j + c;
+                    if (n < N) dst[n] = acc[i][j][e];
+                }
+            }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_moe_tile(const MoeParams& p, bool up, int64_t tiles, hipStream_t stream) {
+    const int K = up ? p.H : p.I, N = up ? p.I : p.H, cols = up ? 128 : 256;
+    const int64_t grid = tiles * ((N + cols - 1) / cols);
+    const size_t lds = static_cast<size_t>(K / kStepK) * kRows * sizeof(float);
+    if (p.G != kStepK || K % kStepK != 0 || N % 128 != 0 || lds > 4 * kMoeTileSums || grid <= 0 || grid > 0x7FFFFFFF)
+        return hipErrorInvalidValue;
+    if (up) hipLaunchKernelGGL((moe_tile_kernel<true>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, stream, p);
+    else hipLaunchKernelGGL((moe_tile_kernel<false>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace w4
