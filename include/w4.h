@@ -393,8 +393,8 @@ int w4a8_linear_e4m3(const uint8_t* xq, const float* xscale, int64_t M, int64_t 
  *   X [T, H], router [E, H]  bf16;  H a multiple of 8;  E <= 1024, top_k <= 32.
  *   bias       [E] fp32 or NULL.
  *   ids        [T, top_k] int32 out;  weights [T, top_k] fp32 out.
- *   workspace  w4_route_workspace_bytes(T, H, E) bytes, 16-byte aligned, its
- *              contents irrelevant.
+ *   workspace  w4_route_workspace_bytes(T, H, E) bytes (0: none), 16-byte aligned,
+ *              its contents irrelevant.
  */
 #define W4_SCORE_SOFTMAX 0
 #define W4_SCORE_SIGMOID 1

@@ -62,18 +62,19 @@ def test_linear_refusals(lib):
 
 def test_route_refusals(lib):
     def call(**kw):
-        a = dict(X=FAKE, T=3, H=64, R=FAKE, E=8, k=2, score=0, bias=None, re=1, scale=1.0, ids=FAKE, w=FAKE, ws=FAKE, n=96)
+        a = dict(X=FAKE, T=3, H=64, R=FAKE, E=20, k=2, score=0, bias=None, re=1, scale=1.0, ids=FAKE, w=FAKE, ws=FAKE, n=240)
         a.update(kw)
         return lib.w4_route(a["X"], a["T"], a["H"], a["R"], a["E"], a["k"], a["score"], a["bias"], a["re"], a["scale"],
                             a["ids"], a["w"], a["ws"], a["n"], None)
 
     for f, status in ((dict(T=-1), 1), (dict(T=MOST), 1), (dict(H=0), 1), (dict(H=60), 1), (dict(H=MOST - 7), 1), (dict(E=0), 1),
-                      (dict(E=2000), 2), (dict(E=MOST), 2), (dict(k=0), 1), (dict(k=9), 1), (dict(E=64, k=33), 2), (dict(score=2), 1),
+                      (dict(E=2000), 2), (dict(E=MOST), 2), (dict(k=0), 1), (dict(k=21), 1), (dict(E=64, k=33), 2), (dict(score=2), 1),
                       (dict(scale=float("nan")), 1), (dict(X=None), 1), (dict(X=ODD), 1), (dict(R=None), 1), (dict(R=ODD), 1),
-                      (dict(ids=None), 1), (dict(w=None), 1), (dict(ws=None), 1), (dict(ws=ODD), 1), (dict(n=95), 1)):
+                      (dict(ids=None), 1), (dict(w=None), 1), (dict(ws=None), 1), (dict(ws=ODD), 1), (dict(n=239), 1)):
         assert call(**f) == status, f
     assert call(T=0, X=None, ws=None) == 0
-    assert lib.w4_route_workspace_bytes(3, 64, 8) == 96
+    assert lib.w4_route_workspace_bytes(3, 64, 20) == 240
+    assert lib.w4_route_workspace_bytes(3, 64, 8) == 0                 # one kernel
     assert lib.w4_route_workspace_bytes(3, 4096, 8) == 8 * 96          # eight ranges of 512 k
     for bad in ((0, 64, 8), (-1, 64, 8), (3, 64, 0), (3, 64, MOST), (MOST, 64, 8), (3, 0, 8), (3, 60, 8), (3, MOST - 7, 8)):
         assert lib.w4_route_workspace_bytes(*bad) == 0, bad
@@ -147,7 +148,7 @@ def test_binding_refusals():
         with pytest.raises(ValueError, match="device tensor"):
             f(X, wq, sz, G)
     r = torch.zeros((8, K), dtype=bf)
-    for bad in (dict(X=X[0]), dict(router=r[:, :8]), dict(score="relu"), dict(bias=torch.zeros(7))):
+    for bad in (dict(X=X[0]), dict(router=r[:, :8]), dict(score="relu"), dict(bias=torch.zeros(7)), dict(router=r.float())):
         a = dict(X=X, router=r, top_k=2)
         a.update(bad)
         with pytest.raises(ValueError):

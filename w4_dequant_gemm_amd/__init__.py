@@ -185,6 +185,41 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None):
     return t.data_ptr()
 
 
+def _ptr(fn: str, t: torch.Tensor, name: str, dtype, device: int):
+    """Address of a contiguous tensor of ``dtype`` on GPU ``device`` (the checks of ``_dev`` in half their time: a
+    mixture-of-experts call makes a dozen of them, as long as a launch takes)."""
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    if not t.is_cuda:
+        raise ValueError(f"{fn}: {name} must be a device tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on cuda:{device} as the others are")
+    raise ValueError(f"{fn}: {name} must be contiguous")
+
+
+def _vec_ptr(fn: str, t, name: str, n: int, dtype, device: int):
+    if t is None:
+        return None
+    if t.numel() != n:
+        raise ValueError(f"{fn}: {name} has {t.numel()} elements, expected {n}")
+    return _ptr(fn, t, name, dtype, device)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _gpu(fn: str, t: torch.Tensor, name: str) -> int:
+    """The index of the GPU that holds ``t``, which has to be the current one: the kernels run there."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{fn}: {name} must be a device tensor")
+    if device != _current_device():
+        raise ValueError(f"{fn}: {name} is on cuda:{device}, and the current device is cuda:{_current_device()}")
+    return device
+
+
 # the current stream's handle as an integer, without building a Stream object
 # (about 2 us of host time per call otherwise, as much as a launch)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -492,12 +527,27 @@ def w4a8_gemm(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *, Y=
 _LINEAR_ACTS = {None: 0, "none": 0, "silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH, "relu": 3, "gelu": 4}
 
 
-def _epilogue_args(fn: str, M: int, N: int, bias, act, residual):
+def _linear_shapes(fn: str, X, wq, sz, G: int, Y, xq=None, xscale=None):
+    """(M, K, N), as ``_check_product_shapes``."""
+    xs, ws = X.shape, wq.shape
+    if len(xs) == 2 and len(ws) == 2 and G > 0 and Y is None and xq is None:
+        (M, K), N = xs, ws[0]
+        if K % G == 0 and K % 8 == 0 and wq.nbytes == N * K // 2 and sz.nbytes == 4 * N * (K // G) and (
+                xscale is None or xscale.numel() == M):
+            return M, K, N
+    return _check_product_shapes(fn, X, wq, sz, G, Y=Y, xq=xq, xscale=xscale)
+
+
+def _epilogue_args(fn: str, M: int, N: int, bias, act, residual, gpu: int):
     if act not in _LINEAR_ACTS:
         raise ValueError(f"{fn}: act must be None, 'none', 'silu', 'gelu_tanh', 'relu' or 'gelu', got {act!r}")
-    if residual is not None and tuple(residual.shape) != (M, N):
+    if residual is None:
+        r = None
+    elif tuple(residual.shape) != (M, N):
         raise ValueError(f"{fn}: residual has shape {tuple(residual.shape)}, expected ({M}, {N})")
-    return _vec(fn, bias, "bias", N, torch.float32), _LINEAR_ACTS[act], _dev(residual, "residual", torch.bfloat16)
+    else:
+        r = _ptr(fn, residual, "residual", torch.bfloat16, gpu)
+    return _vec_ptr(fn, bias, "bias", N, torch.float32, gpu), _LINEAR_ACTS[act], r
 
 
 def w4a16_linear(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *, bias=None, act=None, residual=None,
@@ -505,14 +555,17 @@ def w4a16_linear(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *,
     """``w4a16_gemm`` with its epilogue: ``Y[M, N] = bf16(act(X . W'^T + bias) + residual)``.  ``bias`` is fp32 [N],
     ``act`` None, ``"silu"``, ``"gelu_tanh"``, ``"gelu"`` (erf) or ``"relu"``, ``residual`` bf16 [M, N] (may be ``Y``)."""
     fn = "w4a16_linear"
-    M, K, N = _check_product_shapes(fn, X, wq, sz, G, Y=Y)
+    M, K, N = _linear_shapes(fn, X, wq, sz, G, Y)
     dev = X.device
-    epilogue = _epilogue_args(fn, M, N, bias, act, residual)
+    b, a, r = _epilogue_args(fn, M, N, bias, act, residual, X.get_device())
+    gpu = _gpu(fn, X, "X")
     Y = _empty((M, N), torch.bfloat16, dev, stream) if Y is None else Y
     ws, ws_bytes = _workspace(M, K, N, dev, workspace, stream)
-    rc = lib().w4a16_linear(_dev(X, "X", torch.bfloat16), M, K, _dev(wq, "wq"), _dev(sz, "sz"), N, G, *epilogue,
-                            _dev(Y, "Y", torch.bfloat16), ws, ws_bytes, _stream(dev, stream))
-    _check(fn, rc)
+    rc = lib().w4a16_linear(_ptr(fn, X, "X", torch.bfloat16, gpu), M, K, _ptr(fn, wq, "wq", torch.int32, gpu),
+                            _ptr(fn, sz, "sz", torch.int32, gpu), N, G, b, a, r, _ptr(fn, Y, "Y", torch.bfloat16, gpu),
+                            ws, ws_bytes, _stream(dev, stream))
+    if rc:
+        _check(fn, rc)
     return Y
 
 
@@ -520,17 +573,20 @@ def w4a8_linear(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *, 
                 Y=None, xq=None, xscale=None, workspace=None, stream=None):
     """``w4a8_gemm`` with the epilogue of ``w4a16_linear``; returns (Y, xq, xscale)."""
     fn = "w4a8_linear"
-    M, K, N = _check_product_shapes(fn, X, wq, sz, G, Y=Y, xq=xq, xscale=xscale)
+    M, K, N = _linear_shapes(fn, X, wq, sz, G, Y, xq, xscale)
     dev = X.device
-    epilogue = _epilogue_args(fn, M, N, bias, act, residual)
+    b, a, r = _epilogue_args(fn, M, N, bias, act, residual, X.get_device())
+    gpu = _gpu(fn, X, "X")
     Y = _empty((M, N), torch.bfloat16, dev, stream) if Y is None else Y
     xq = _empty((M, K), torch.uint8, dev, stream) if xq is None else xq
     xscale = _empty((M,), torch.float32, dev, stream) if xscale is None else xscale
     ws, ws_bytes = _workspace(M, K, N, dev, workspace, stream, w4a8=True)
-    rc = lib().w4a8_linear(_dev(X, "X", torch.bfloat16), M, K, _dev(wq, "wq"), _dev(sz, "sz"), N, G, *epilogue,
-                           _dev(Y, "Y", torch.bfloat16), _dev(xq, "xq"), _dev(xscale, "xscale", torch.float32),
-                           ws, ws_bytes, _stream(dev, stream))
-    _check(fn, rc)
+    rc = lib().w4a8_linear(_ptr(fn, X, "X", torch.bfloat16, gpu), M, K, _ptr(fn, wq, "wq", torch.int32, gpu),
+                           _ptr(fn, sz, "sz", torch.int32, gpu), N, G, b, a, r, _ptr(fn, Y, "Y", torch.bfloat16, gpu),
+                           _dev(xq, "xq"), _ptr(fn, xscale, "xscale", torch.float32, gpu), ws, ws_bytes,
+                           _stream(dev, stream))
+    if rc:
+        _check(fn, rc)
     return Y, xq, xscale
 
 
@@ -539,17 +595,19 @@ def w4a8_linear_e4m3(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, s
     """``w4a8_gemm_e4m3`` with the epilogue of ``w4a16_linear``: a down projection on ``w4a8_gate_up``'s E4M3 rows added
     to the residual stream, say."""
     fn = "w4a8_linear_e4m3"
-    if xq.element_size() != 1:
-        raise ValueError(f"{fn}: xq must hold one byte per element")
-    M, K, N = _check_product_shapes(fn, xq, wq, sz, G, Y=Y, xscale=xscale)
+    if xq.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise ValueError(f"{fn}: xq must hold E4M3 codes (torch.uint8 or torch.float8_e4m3fn), got {xq.dtype}")
+    M, K, N = _linear_shapes(fn, xq, wq, sz, G, Y, None, xscale)
     dev = xq.device
-    epilogue = _epilogue_args(fn, M, N, bias, act, residual)
+    b, a, r = _epilogue_args(fn, M, N, bias, act, residual, xq.get_device())
+    gpu = _gpu(fn, xq, "xq")
     Y = _empty((M, N), torch.bfloat16, dev, stream) if Y is None else Y
     ws, ws_bytes = _workspace(M, K, N, dev, workspace, stream, w4a8=True)
-    rc = lib().w4a8_linear_e4m3(_dev(xq, "xq"), _dev(xscale, "xscale", torch.float32), M, K, _dev(wq, "wq"),
-                                _dev(sz, "sz"), N, G, *epilogue, _dev(Y, "Y", torch.bfloat16), ws, ws_bytes,
-                                _stream(dev, stream))
-    _check(fn, rc)
+    rc = lib().w4a8_linear_e4m3(_ptr(fn, xq, "xq", xq.dtype, gpu), _ptr(fn, xscale, "xscale", torch.float32, gpu), M, K,
+                                _ptr(fn, wq, "wq", torch.int32, gpu), _ptr(fn, sz, "sz", torch.int32, gpu), N, G, b, a, r,
+                                _ptr(fn, Y, "Y", torch.bfloat16, gpu), ws, ws_bytes, _stream(dev, stream))
+    if rc:
+        _check(fn, rc)
     return Y
 
 
@@ -651,20 +709,26 @@ def w4_route(X: torch.Tensor, router: torch.Tensor, top_k: int, *, score="softma
     weights fp32 [T, top_k]).  ``score`` is ``"softmax"`` or ``"sigmoid"``; ``bias`` (fp32 [E]) is added to the
     scores to choose but not to weigh."""
     fn = "w4_route"
-    if X.dim() != 2 or router.dim() != 2 or X.shape[1] != router.shape[1]:
-        raise ValueError(f"{fn}: X must be [T, H] and router [E, H], got {tuple(X.shape)} and {tuple(router.shape)}")
+    xs, rs = X.shape, router.shape
+    if len(xs) != 2 or len(rs) != 2 or xs[1] != rs[1]:
+        raise ValueError(f"{fn}: X must be [T, H] and router [E, H], got {tuple(xs)} and {tuple(rs)}")
     if score not in _SCORES:
         raise ValueError(f"{fn}: score must be one of {sorted(_SCORES)}, got {score!r}")
-    (T, H), E, dev = X.shape, router.shape[0], X.device
+    (T, H), E, dev = xs, rs[0], X.device
+    b = _vec_ptr(fn, bias, "bias", E, torch.float32, X.get_device())
+    gpu = _gpu(fn, X, "X")
     ids = _empty((T, top_k), torch.int32, dev, stream) if ids is None else ids
     weights = _empty((T, top_k), torch.float32, dev, stream) if weights is None else weights
-    if workspace is None:
-        workspace = _scratch(w4_route_workspace_bytes(T, H, E), dev, stream)
-    rc = lib().w4_route(_dev(X, "X", torch.bfloat16), T, H, _dev(router, "router", torch.bfloat16), E, top_k, _SCORES[score],
-                        _vec(fn, bias, "bias", E, torch.float32), renormalize, scale,
-                        _vec(fn, ids, "ids", T * top_k, torch.int32), _vec(fn, weights, "weights", T * top_k, torch.float32),
-                        _dev(workspace, "workspace"), _nbytes(workspace), _stream(dev, stream))
-    _check(fn, rc)
+    ws, ws_bytes = None, 0
+    need = w4_route_workspace_bytes(T, H, E)
+    if need:
+        workspace = _scratch(need, dev, stream) if workspace is None else workspace
+        ws, ws_bytes = _dev(workspace, "workspace"), workspace.nbytes
+    rc = lib().w4_route(_ptr(fn, X, "X", torch.bfloat16, gpu), T, H, _ptr(fn, router, "router", torch.bfloat16, gpu), E, top_k,
+                        _SCORES[score], b, renormalize, scale, _vec_ptr(fn, ids, "ids", T * top_k, torch.int32, gpu),
+                        _vec_ptr(fn, weights, "weights", T * top_k, torch.float32, gpu), ws, ws_bytes, _stream(dev, stream))
+    if rc:
+        _check(fn, rc)
     return ids, weights
 
 
@@ -674,11 +738,13 @@ def w4a16_moe_workspace_bytes(T: int, top_k: int, E: int, H: int, I: int, G: int
     return int(lib().w4a16_moe_workspace_bytes(T, top_k, E, H, I, G))
 
 
-def _check_experts(fn: str, w: dict, name: str, E: int, N: int, K: int, G: int):
-    """E stacked GPU layouts of [N, K] weights."""
-    if _nbytes(w["wq"]) != E * N * K // 2 or _nbytes(w["sz"]) != 4 * E * N * (K // G):
-        raise ValueError(f"{fn}: {name} holds {_nbytes(w['wq'])} bytes of codes and {_nbytes(w['sz'])} of scales; {E} experts "
+def _experts(fn: str, w: dict, name: str, E: int, N: int, K: int, G: int, gpu: int):
+    """Addresses of E stacked GPU layouts of [N, K] weights."""
+    wq, sz = w["wq"], w["sz"]
+    if wq.nbytes != E * N * K // 2 or sz.nbytes != 4 * E * N * (K // G):
+        raise ValueError(f"{fn}: {name} holds {wq.nbytes} bytes of codes and {sz.nbytes} of scales; {E} experts "
                          f"of [{N}, {K}] with G = {G} need {E * N * K // 2} and {4 * E * N * (K // G)}")
+    return _ptr(fn, wq, name, torch.int32, gpu), _ptr(fn, sz, name, torch.int32, gpu)
 
 
 def w4a16_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: dict, up: dict, down: dict, G: int,
@@ -687,28 +753,32 @@ def w4a16_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: d
     experts: none) with ``weights`` (fp32).  ``gate``, ``up`` and ``down`` are GPU layouts of ``w4_prepack`` stacked
     over the experts (``wq`` [E, N, K/8], ``sz`` [E, N, K/G]).  Returns bf16 [T, H], ``residual`` (bf16 [T, H]) added."""
     fn = "w4a16_moe"
-    if X.dim() != 2 or ids.dim() != 2 or ids.shape[0] != X.shape[0] or tuple(weights.shape) != tuple(ids.shape):
-        raise ValueError(f"{fn}: X must be [T, H], ids and weights [T, top_k], got {tuple(X.shape)}, {tuple(ids.shape)} and "
+    xs, js, gs = X.shape, ids.shape, gate["wq"].shape
+    if len(xs) != 2 or len(js) != 2 or js[0] != xs[0] or weights.shape != js:
+        raise ValueError(f"{fn}: X must be [T, H], ids and weights [T, top_k], got {tuple(xs)}, {tuple(js)} and "
                          f"{tuple(weights.shape)}")
-    if gate["wq"].dim() != 3:
-        raise ValueError(f"{fn}: gate wq must be [E, I, H/8], got {tuple(gate['wq'].shape)}")
-    (T, H), top_k, (E, I, _), dev = X.shape, ids.shape[1], gate["wq"].shape, X.device
+    if len(gs) != 3:
+        raise ValueError(f"{fn}: gate wq must be [E, I, H/8], got {tuple(gs)}")
+    (T, H), top_k, (E, I, _), dev = xs, js[1], gs, X.device
     if G <= 0 or H % G or I % G:
         raise ValueError(f"{fn}: H = {H} and I = {I} must be multiples of the group size G = {G}")
-    for w, name, N, K in ((gate, "gate", I, H), (up, "up", I, H), (down, "down", H, I)):
-        _check_experts(fn, w, name, E, N, K, G)
-    for t, name in ((Y, "Y"), (residual, "residual")):
-        if t is not None and tuple(t.shape) != (T, H):
-            raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {(T, H)}")
+    if (residual is not None and residual.shape != xs) or (Y is not None and Y.shape != xs):
+        t, name = (residual, "residual") if residual is not None and residual.shape != xs else (Y, "Y")
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {(T, H)}")
+    gpu = X.get_device()
+    g, u, d = (_experts(fn, gate, "gate", E, I, H, G, gpu), _experts(fn, up, "up", E, I, H, G, gpu),
+               _experts(fn, down, "down", E, H, I, G, gpu))
+    _gpu(fn, X, "X")
     Y = _empty((T, H), torch.bfloat16, dev, stream) if Y is None else Y
     if workspace is None:
         workspace = _scratch(w4a16_moe_workspace_bytes(T, top_k, E, H, I, G), dev, stream)
-    pointers = [_dev(w[key], f"{name} {key}") for w, name in ((gate, "gate"), (up, "up"), (down, "down")) for key in ("wq", "sz")]
-    rc = lib().w4a16_moe(_dev(X, "X", torch.bfloat16), T, H, _dev(ids, "ids", torch.int32),
-                         _dev(weights, "weights", torch.float32), top_k, *pointers, E, I, G, _ACTS[act],
-                         _dev(residual, "residual", torch.bfloat16), _dev(Y, "Y", torch.bfloat16),
-                         _dev(workspace, "workspace"), _nbytes(workspace), _stream(dev, stream))
-    _check(fn, rc)
+    rc = lib().w4a16_moe(_ptr(fn, X, "X", torch.bfloat16, gpu), T, H, _ptr(fn, ids, "ids", torch.int32, gpu),
+                         _ptr(fn, weights, "weights", torch.float32, gpu), top_k, g[0], g[1], u[0], u[1], d[0], d[1], E, I, G,
+                         _ACTS[act], None if residual is None else _ptr(fn, residual, "residual", torch.bfloat16, gpu),
+                         _ptr(fn, Y, "Y", torch.bfloat16, gpu), _dev(workspace, "workspace"), workspace.nbytes,
+                         _stream(dev, stream))
+    if rc:
+        _check(fn, rc)
     return Y
 
 
@@ -942,35 +1012,40 @@ def w4_adjust_logits(logits: torch.Tensor, *, history=None, history_start=None, 
     by default; ``out=logits`` works in place)."""
     fn = "w4_adjust_logits"
     xp, f32, xs = _logits_arg(fn, logits, "logits")
-    B, V = logits.shape
-    dev = logits.device
+    (B, V), dev, gpu = logits.shape, logits.device, _gpu(fn, logits, "logits")
     if out is None:
         out = _empty((B, V), logits.dtype, dev, stream)
-    elif tuple(out.shape) != (B, V) or out.dtype != logits.dtype:
-        raise ValueError(f"{fn}: out must be {logits.dtype} of shape {(B, V)}, got {out.dtype} of {tuple(out.shape)}")
-    op, _, os_ = _logits_arg(fn, out, "out")
-    if (history is None) != (history_start is None):
-        raise ValueError(f"{fn}: history and history_start must both be given or both be None")
-    if len({bias_start is None, bias_ids is None, bias_values is None}) > 1:
-        raise ValueError(f"{fn}: bias_start, bias_ids and bias_values must all be given or all be None")
-    nh = history.numel() if history is not None else 0
-    nb = bias_ids.numel() if bias_ids is not None else 0
-    words, ms = -(-V // 32), 0
+        op, os_ = out.data_ptr(), V
+    else:
+        if out.shape != logits.shape or out.dtype != logits.dtype:
+            raise ValueError(f"{fn}: out must be {logits.dtype} of shape {(B, V)}, got {out.dtype} of {tuple(out.shape)}")
+        op, _, os_ = _logits_arg(fn, out, "out")
+        if out.get_device() != gpu:
+            raise ValueError(f"{fn}: out is on {out.device}, not on cuda:{gpu} as the logits are")
+    hp, nh, hs, bi, bv, bs, nb, mp, ms = None, 0, None, None, None, None, 0, None, 0
+    if history is not None or history_start is not None:
+        if history is None or history_start is None:
+            raise ValueError(f"{fn}: history and history_start must both be given or both be None")
+        nh, hp = history.numel(), _ptr(fn, history, "history", torch.int32, gpu)
+        hs = _vec_ptr(fn, history_start, "history_start", B + 1, torch.int32, gpu)
+    if bias_ids is not None or bias_start is not None or bias_values is not None:
+        if bias_ids is None or bias_start is None or bias_values is None:
+            raise ValueError(f"{fn}: bias_start, bias_ids and bias_values must all be given or all be None")
+        nb, bi = bias_ids.numel(), _ptr(fn, bias_ids, "bias_ids", torch.int32, gpu)
+        bv = _vec_ptr(fn, bias_values, "bias_values", nb, torch.float32, gpu)
+        bs = _vec_ptr(fn, bias_start, "bias_start", B + 1, torch.int32, gpu)
     if mask is not None:
+        words = -(-V // 32)
         if mask.dim() != 2 or mask.shape[1] != words or mask.shape[0] not in (1, B):
             raise ValueError(f"{fn}: mask must be [{B} or 1, {words}], got {tuple(mask.shape)}")
-        ms = words if mask.shape[0] > 1 else 0
-    rc = lib().w4_adjust_logits(xp, f32, B, V, xs, _dev(history, "history", torch.int32), nh,
-                                _vec(fn, history_start, "history_start", B + 1, torch.int32),
-                                _vec(fn, prompt_len, "prompt_len", B, torch.int32),
-                                _vec(fn, repetition, "repetition", B, torch.float32),
-                                _vec(fn, presence, "presence", B, torch.float32),
-                                _vec(fn, frequency, "frequency", B, torch.float32),
-                                _vec(fn, bias_start, "bias_start", B + 1, torch.int32),
-                                _dev(bias_ids, "bias_ids", torch.int32),
-                                _vec(fn, bias_values, "bias_values", nb, torch.float32),
-                                nb, _dev(mask, "mask", torch.int32), ms, op, os_, _stream(dev, stream))
-    _check(fn, rc)
+        mp, ms = _ptr(fn, mask, "mask", torch.int32, gpu), (words if mask.shape[0] > 1 else 0)
+    f = torch.float32
+    rc = lib().w4_adjust_logits(xp, f32, B, V, xs, hp, nh, hs, _vec_ptr(fn, prompt_len, "prompt_len", B, torch.int32, gpu),
+                                _vec_ptr(fn, repetition, "repetition", B, f, gpu), _vec_ptr(fn, presence, "presence", B, f, gpu),
+                                _vec_ptr(fn, frequency, "frequency", B, f, gpu), bs, bi, bv, nb, mp, ms, op, os_,
+                                _stream(dev, stream))
+    if rc:
+        _check(fn, rc)
     return out
 
 

@@ -37,6 +37,7 @@ extern "C" {
 
 size_t w4_route_workspace_bytes(int64_t T, int64_t H, int64_t E) {
     if (T <= 0 || T > kMaxTokens || E <= 0 || E > w4::kMaxExperts || H <= 0 || H > kMaxWidth || H % 8 != 0) return 0;
+    if (w4::route_in_one(static_cast<int>(E), static_cast<int>(H))) return 0;
     return static_cast<size_t>(w4::route_splits(T, static_cast<int>(E), static_cast<int>(H))) * static_cast<size_t>(T) *
            static_cast<size_t>(E) * sizeof(float);
 }
@@ -56,8 +57,8 @@ int w4_route(const uint16_t* X, int64_t T, int64_t H, const uint16_t* router, in
     W4_REQUIRE_PTR(fn, X);
     W4_REQUIRE_PTR(fn, router);
     if (!ids || !weights) return fail(W4_EINVAL, "%s: ids or weights is NULL", fn);
-    W4_REQUIRE_PTR(fn, workspace);
     const size_t need = w4_route_workspace_bytes(T, H, E);
+    if (need > 0) W4_REQUIRE_PTR(fn, workspace);
     if (workspace_bytes < need)
         return fail(W4_EINVAL, "%s: workspace of %zu bytes, these sizes need %zu (w4_route_workspace_bytes)", fn, workspace_bytes, need);
     const w4::RouteParams p{X, T, static_cast<int>(H), router, static_cast<int>(E), top_k, score == W4_SCORE_SIGMOID, bias,

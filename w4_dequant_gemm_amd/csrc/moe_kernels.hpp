@@ -26,6 +26,8 @@ struct RouteParams {
     float* logits;           // [splits, T, E] workspace: partial logits of the K ranges
     int splits;
 };
+// one kernel makes the logits and chooses (no workspace)
+constexpr bool route_in_one(int E, int H) { return E <= 16 && H <= 1024; }
 // K ranges that the logits of these sizes are split into
 int route_splits(int64_t T, int E, int H);
 hipError_t launch_route(const RouteParams& p, hipStream_t stream);

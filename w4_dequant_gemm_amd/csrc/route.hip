@@ -234,7 +234,7 @@ int route_splits(int64_t T, int E, int H) {
 
 hipError_t launch_route(const RouteParams& p, hipStream_t stream) {
     const int steps = (p.H + kStep - 1) / kStep;
-    if (p.E <= 16 && p.H <= 1024) {
+    if (route_in_one(p.E, p.H)) {
         const int wk = steps / 2 < 1 ? 1 : (steps / 2 > 16 ? 16 : steps / 2);
         hipLaunchKernelGGL(route_kernel, dim3(static_cast<unsigned>((p.T + 15) / 16)), dim3(64 * wk), 0, stream, p, wk);
         return hipGetLastError();
