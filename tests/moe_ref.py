@@ -62,7 +62,7 @@ def moe(x, ids, weights, gate, up, down, act, residual=None):
         # h is kept as hi + lo, the rest of a rounding to bf16 rounded to bf16, or, from 24 rows an expert on with groups
         # of 128, as bf16
         G = gate["W"].shape[2] // gate["sz"].shape[2]
-        dh = dh + (BF16 if G == 128 and x.shape[0] > 16 and ids.numel() >= 24 * E else 2.0 ** -16) * (h.abs() + dh)
+        dh = dh + (BF16 if G == 128 and ids.numel() > 64 and ids.numel() >= 24 * E else 2.0 ** -16) * (h.abs() + dh)
         for j in range(ids.shape[1]):
             w = share[:, j:j + 1]
             o, do = product(w * h, w.abs() * dh, down, e)

@@ -38,14 +38,14 @@ namespace {
 // and up kernel looks its rows up among the ids, and one more workgroup of it
 // makes the lists that the down product needs.
 
-// Runs: the slots ordered by expert, and (expert, first, rows) of each expert
-// that has any; runs behind the last one have no rows.  (Which place inside an
+// The slots ordered by expert, and the runs of equal ones: (expert, first, rows)
+// of each expert that has any; runs behind the last one have no rows.  (Which place inside an
 // expert's run a slot gets is up to the order of the atomics; every row's
 // result is the same at any place.)
 struct RunMem {
     int count[kMaxExperts];
 };
-// TILES: also the runs cut into tiles, for the tiled products.
+// TILES: the runs cut into tiles instead, for the tiled products.
 template <bool TILES>
 __device__ __forceinline__ void build_runs(const MoeParams& p, RunMem& m, int tid, int threads) {
     for (int e = tid; e < p.E; e += threads) m.count[e] = 0;
@@ -71,7 +71,7 @@ __device__ __forceinline__ void build_runs(const MoeParams& p, RunMem& m, int ti
             const uint64_t some = __builtin_amdgcn_ballot_w64(mine > 0);
             const int first = rows + upto - mine;
             if (e < p.E) m.count[e] = first;
-            if (mine > 0) p.runs[active + __builtin_popcountll(some & ((uint64_t{1} << tid) - 1))] = make_int4(e, first, mine, 0);
+            if (!TILES && mine > 0) p.runs[active + __builtin_popcountll(some & ((uint64_t{1} << tid) - 1))] = make_int4(e, first, mine, 0);
             if constexpr (TILES) {
                 constexpr int kRows = kMoeTileRows;
                 const int own = (mine + kRows - 1) / kRows;
@@ -90,7 +90,8 @@ __device__ __forceinline__ void build_runs(const MoeParams& p, RunMem& m, int ti
             active += __builtin_popcountll(some);
         }
         if (TILES && tid == 0) *p.tile_count = tiles;
-        for (int i = active + tid; i < p.E; i += kWave) p.runs[i] = make_int4(0, 0, 0, 0);
+        if constexpr (!TILES)
+            for (int i = active + tid; i < p.E; i += kWave) p.runs[i] = make_int4(0, 0, 0, 0);
     }
     __syncthreads();
     for (int s = tid; s < slots; s += threads) {
@@ -99,87 +100,10 @@ __device__ __forceinline__ void build_runs(const MoeParams& p, RunMem& m, int ti
     }
 }
 
-// For at most 16 tokens: units of one expert and, for every token, its slot
-// with that expert.  A token without one has the row behind the slots' rows,
-// which is cleared here.  A token's second choice of the same expert is another
-// unit.
-constexpr int kUnitTokens = 16;
-constexpr int kMaxUnits = kUnitTokens * kMaxTopK;
-struct UnitMem {
-    int key[kMaxUnits], lead[kMaxUnits], rank[kMaxUnits], tokens[kMaxUnits], units;
-};
-__device__ __forceinline__ void build_units(const MoeParams& p, UnitMem& m, int tid, int threads) {
-    const int slots = static_cast<int>(p.T * p.k);
-    for (int s = tid; s < slots; s += threads) {
-        const int e = p.ids[s];
-        m.key[s] = static_cast<uint32_t>(e) < static_cast<uint32_t>(p.E) ? e * kMaxTopK : -1;
-        m.tokens[s] = 0;
-    }
-    __syncthreads();
-    // (the experts are compared without what is added here)
-    int extra[kMaxUnits / kWave];
-    int n = 0;
-    for (int s = tid; s < slots; s += threads, ++n) {
-        int same = 0;
-        for (int j = s - s % p.k; j < s; ++j) same += m.key[j] == m.key[s];
-        extra[n] = same;
-    }
-    __syncthreads();
-    n = 0;
-    for (int s = tid; s < slots; s += threads, ++n)
-        if (m.key[s] >= 0) m.key[s] += extra[n];
-    __syncthreads();
-    for (int s = tid; s < slots; s += threads) {
-        int first = s;
-        for (int j = s - 1; j >= 0; --j) first = m.key[j] == m.key[s] ? j : first;
-        m.lead[s] = m.key[s] < 0 ? -1 : first;
-    }
-    __syncthreads();
-    if (tid < kWave) {
-        int units = 0;
-        for (int s0 = 0; s0 < slots; s0 += kWave) {
-            const int s = s0 + tid;
-            const bool leads = s < slots && m.lead[s] == s;
-            const uint64_t some = __builtin_amdgcn_ballot_w64(leads);
-            if (leads) {
-                const int u = units + __builtin_popcountll(some & ((uint64_t{1} << tid) - 1));
-                m.rank[s] = u;
-                p.unit_expert[u] = m.key[s] / kMaxTopK;
-            }
-            units += __builtin_popcountll(some);
-        }
-        if (tid == 0) {
-            m.units = units;
-            p.unit_expert[slots] = units;
-        }
-    }
-    __syncthreads();
-    for (int s = tid; s < slots; s += threads)
-        if (m.lead[s] >= 0) {
-            const int u = m.rank[m.lead[s]], t = s / p.k;
-            p.unit_slot[u * kUnitTokens + t] = s;
-            atomicOr(&m.tokens[u], 1 << t);
-        }
-    __syncthreads();
-    for (int i = tid; i < m.units * kUnitTokens; i += threads)
-        if (!(m.tokens[i / kUnitTokens] >> (i % kUnitTokens) & 1)) p.unit_slot[i] = slots;
-    const u32x4_t zero = {0u, 0u, 0u, 0u};
-    for (int i = tid; i < p.I / 8; i += threads) {
-        reinterpret_cast<u32x4_t*>(p.hi + static_cast<int64_t>(slots) * p.I)[i] = zero;
-        reinterpret_cast<u32x4_t*>(p.lo + static_cast<int64_t>(slots) * p.I)[i] = zero;
-    }
-}
-
 constexpr int kListThreads = 1024;
 __global__ void __launch_bounds__(kListThreads) moe_lists_kernel(MoeParams p) {
-    __shared__ union {
-        RunMem runs;
-        UnitMem units;
-    } mem;
-    build_runs<false>(p, mem.runs, threadIdx.x, kListThreads);
-    if (p.T > kUnitTokens) return;
-    __syncthreads();
-    build_units(p, mem.units, threadIdx.x, kListThreads);
+    __shared__ RunMem mem;
+    build_runs<false>(p, mem, threadIdx.x, kListThreads);
 }
 
 // For the tiled products: workgroup 0 makes the runs and tiles, the others the
@@ -223,54 +147,56 @@ struct StepB {
     u32x4_t w[FJ];
     uint32_t s[FJ][kStepK / G];
 };
-template <int MB, int AP>
-struct StepA {
-    u32x4_t a[MB][AP][4];
-};
+// From the blocks' first words: a step's address is uniform, the lane's offset in
+// it the same for all steps.  (The step passes through an empty asm: the
+// compiler would otherwise keep a pointer of its own in registers for each of the
+// loads in flight.)
 template <int FJ, int G>
 __device__ __forceinline__ void load_b(StepB<FJ, G>& b, const uint32_t* const (&wb)[FJ], const uint32_t* const (&sb)[FJ], int step,
-                                       int K, int q) {
+                                       int K, int c, int q) {
     constexpr int NG = kStepK / G;
-    int t = 4 * step + q;
-    t = t < K / 32 ? t : K / 32 - 1;
+    step = __builtin_amdgcn_readfirstlane(step);
+    asm volatile("" : "+s"(step));
+    uint32_t tile = q;
+    if constexpr (NG > 1) {
+        // K may end inside the last step of groups below 128
+        const uint32_t tiles = K / 32 - 4 * step;
+        tile = tile < tiles ? tile : tiles - 1;
+    }
 #pragma unroll
     for (int j = 0; j < FJ; ++j) {
-        b.w[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wb[j] + 64 * t));
+        const uint8_t* const w = reinterpret_cast<const uint8_t*>(wb[j]) + static_cast<int64_t>(step) * 1024;
+        b.w[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(w + (256u * tile + 16u * c)));
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             int gg = NG * step + g;
-            gg = gg < K / G ? gg : K / G - 1;
-            b.s[j][g] = sb[j][16 * gg];
+            if constexpr (NG > 1) gg = gg < K / G ? gg : K / G - 1;
+            const uint8_t* const s = reinterpret_cast<const uint8_t*>(sb[j]) + static_cast<int64_t>(gg) * 64;
+            b.s[j][g] = *reinterpret_cast<const uint32_t*>(s + 4u * c);
         }
     }
 }
-// fragment f: the 8 k at 32 q + 8 f of the step (groups of 128), or at 32 f + 8 q
-template <int MB, int AP, int G>
-__device__ __forceinline__ void load_a(StepA<MB, AP>& a, const uint16_t* const (&arow)[MB][AP], int step, int K, int q) {
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-        int t = 4 * step + (G == kStepK ? q : f);
-        t = t < K / 32 ? t : K / 32 - 1;
-        const int k = 32 * t + 8 * (G == kStepK ? f : q);
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-            for (int v = 0; v < AP; ++v) a.a[i][v][f] = *reinterpret_cast<const u32x4_t*>(arow[i][v] + k);
-    }
-}
-template <int MB, int AP, int FJ, int G>
-__device__ __forceinline__ void multiply(float4_t (&acc)[MB][FJ], StepB<FJ, G>& b, const StepA<MB, AP>& a, int step, int K,
-                                         uint32_t bias) {
+// `frag(i, v, f)`: fragment f of part v of the rows' block i: the 8 k at 32 q +
+// 8 f of the step (groups of 128), or at 32 f + 8 q.  Blocks of rows from
+// `blocks` on are left out.
+template <int MB, int AP, int FJ, int G, typename Frag>
+__device__ __forceinline__ void multiply(float4_t (&acc)[MB][FJ], const StepB<FJ, G>& b, Frag frag, int step, int K, uint32_t bias,
+                                         int blocks = MB) {
     constexpr int NG = kStepK / G, PER = 4 / NG;     // groups in a step, fragments in a group
     const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
     const u32x4_t zero = {0u, 0u, 0u, 0u};
-    if constexpr (NG > 1) {
+    u32x4_t word[FJ];
 #pragma unroll
-        for (int j = 0; j < FJ; ++j) transpose_quarters(b.w[j]);
+    for (int j = 0; j < FJ; ++j) {
+        word[j] = b.w[j];
+        if constexpr (NG > 1) transpose_quarters(word[j]);
     }
     float4_t ps[MB][FJ], x1[MB];
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
+        // (the scheduler would otherwise fetch fragments ahead until the
+        // registers are full, and fewer waves fit a compute unit)
+        __builtin_amdgcn_sched_barrier(0);
         if (f % PER == 0) {
 #pragma unroll
             for (int i = 0; i < MB; ++i) {
@@ -284,19 +210,22 @@ __device__ __forceinline__ void multiply(float4_t (&acc)[MB][FJ], StepB<FJ, G>& 
         bf16x8_t bp[FJ];
 #pragma unroll
         for (int j = 0; j < FJ; ++j) {
-            const uint32_t w = b.w[j][f];
+            const uint32_t w = word[j][f];
             bp[j] = __builtin_bit_cast(bf16x8_t, u32x4_t{nibble_pair_bf16(w, 0, bias), nibble_pair_bf16(w, 1, bias),
                                                          nibble_pair_bf16(w, 2, bias), nibble_pair_bf16(w, 3, bias)});
         }
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
+        for (int i = 0; i < MB; ++i) {
+            if (MB > 1 && i >= blocks) continue;
 #pragma unroll
             for (int v = 0; v < AP; ++v) {
-                const bf16x8_t ap = __builtin_bit_cast(bf16x8_t, in ? a.a[i][v][f] : zero);
+                const u32x4_t x = frag(i, v, f);
+                const bf16x8_t ap = __builtin_bit_cast(bf16x8_t, in ? x : zero);
                 x1[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ap, ones, x1[i], 0, 0, 0);
 #pragma unroll
                 for (int j = 0; j < FJ; ++j) ps[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ap, bp[j], ps[i][j], 0, 0, 0);
             }
+        }
         if (f % PER == PER - 1) {
 #pragma unroll
             for (int j = 0; j < FJ; ++j) {
@@ -318,23 +247,41 @@ __device__ __forceinline__ void store_h(const MoeParams& p, int64_t at, float h)
     p.lo[at] = (hi & 0x7FFFu) == 0x7F80u ? 0 : float_to_bf16_bits(h - bf16_lo(hi));
 }
 
-// UP: gate and up (blocks 0 .. FJ / 2 - 1 of the gate weight, the others of the
-// up weight, at the same columns), rows gathered from X; else the down product
-// on the rows hi + lo.  SCAN (UP only, at most 64 slots): the expert's rows from
-// the ids, with blockIdx.y the expert or, where there are fewer slots than
-// experts, a slot, whose expert it takes if no slot before has the same; the
-// last blockIdx.y makes the lists for the kernels behind.
-template <int MB, int FJ, int G, bool UP, bool SCAN>
-__global__ void __launch_bounds__(512) moe_stream_kernel(MoeParams p, int wk) {
-    static_assert(!UP || FJ % 2 == 0, "as many blocks of each weight");
+// UP: gate and up (block 0 of the gate weight, block 1 of the up weight, at the
+// same 16 columns), rows gathered from X; else the down product on the rows
+// hi + lo.  SCAN (UP only, at most 64 slots): the expert's rows from the ids,
+// with blockIdx.y the expert or, where there are fewer slots than experts, a
+// slot, whose expert it takes if no slot before has the same; the last
+// blockIdx.y makes the lists for the kernels behind.
+//
+// A wave streams the weights of its own columns, two 128-k steps ahead, and all
+// of the workgroup's waves multiply them by the same rows, which go straight from
+// global memory into LDS a piece of CS steps ahead (waves that split the k
+// instead read the rows from L2 for every 32 columns anew, four times the bytes
+// of the weights: 8 experts of 14336 x 4096, 24 tokens, down product 78 us).
+// With blockIdx.z the down product's k are split over workgroups.
+template <int MB, int G, bool UP, bool SCAN>
+__global__ void __launch_bounds__(512, 2) moe_stream_kernel(MoeParams p) {
     static_assert(UP || !SCAN, "the lists are made by then");
+    constexpr int FJ = 2, NG = kStepK / G;
     constexpr int AP = UP ? 1 : 2;                 // parts of an activation
-    constexpr int DEPTH = MB * AP <= 2 ? 2 : 1;    // steps in flight a wave
-    constexpr int COLS = UP ? 8 * FJ : 16 * FJ;
-    constexpr int TILE = 256 * MB * FJ;
-    extern __shared__ float red[];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int RM = 16 * MB;                    // rows at a time
+    // steps of weights in flight, and steps of a piece of the rows: with two of
+    // each, two workgroups of 8 waves share a compute unit and cover each other's
+    // waits (four of each: 138 registers and 64 KB of LDS, one workgroup, down
+    // products 5 to 10 us slower)
+    constexpr int DEPTH = 2;
+    constexpr int CS = MB * AP <= 4 ? 2 : 1;
+    constexpr int ROW = CS * kStepK * 2;           // its bytes in a row
+    constexpr int RPD = 1024 / ROW;                // rows of a load to LDS
+    constexpr int LOADS = FJ * (1 + NG);           // loads of one
+    constexpr int COLS = UP ? 16 : 32;             // columns of a wave
+    static_assert(CS * LOADS < 64, "vmcnt range");
+    __shared__ __attribute__((aligned(16))) uint8_t lds_a[2][AP * RM * ROW];
+    __shared__ int row_at[RM];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int waves = blockDim.x >> 6;
     const int c = lane & 15, q = lane >> 4;
     int expert, rows;
     const int* list;
@@ -343,16 +290,12 @@ __global__ void __launch_bounds__(512) moe_stream_kernel(MoeParams p, int wk) {
         const int slots = static_cast<int>(p.T * p.k);
         if (blockIdx.y == gridDim.y - 1) {
             if (blockIdx.x > 0) return;
-            __shared__ union {
-                RunMem runs;
-                UnitMem units;
-            } mem;
-            if (p.T <= kUnitTokens) build_units(p, mem.units, threadIdx.x, 64 * wk);
-            else build_runs<false>(p, mem.runs, threadIdx.x, 64 * wk);
+            __shared__ RunMem mem;
+            build_runs<false>(p, mem, tid, blockDim.x);
             return;
         }
         const int id = lane < slots ? p.ids[lane] : -1;
-        expert = slots < p.E ? __builtin_amdgcn_readlane(id, blockIdx.y) : static_cast<int>(blockIdx.y);
+        expert = __builtin_amdgcn_readfirstlane(slots < p.E ? __builtin_amdgcn_readlane(id, blockIdx.y) : static_cast<int>(blockIdx.y));
         if (static_cast<uint32_t>(expert) >= static_cast<uint32_t>(p.E)) return;
         const uint64_t some = __builtin_amdgcn_ballot_w64(id == expert);
         rows = __builtin_popcountll(some);
@@ -362,173 +305,143 @@ __global__ void __launch_bounds__(512) moe_stream_kernel(MoeParams p, int wk) {
         list = scanned;
     } else {
         const int4 run = p.runs[blockIdx.y];
-        expert = run.x;
-        rows = run.z;
+        expert = __builtin_amdgcn_readfirstlane(run.x);
+        rows = __builtin_amdgcn_readfirstlane(run.z);
         if (rows == 0) return;
-        list = p.order + run.y;
+        list = p.order + __builtin_amdgcn_readfirstlane(run.y);
     }
     const int K = UP ? p.H : p.I, N = UP ? p.I : p.H;
     const int KS = (K + kStepK - 1) / kStepK;
-    const int n0 = COLS * blockIdx.x;
+    const int z = blockIdx.z, zs = gridDim.z;
+    const int first = z * KS / zs, n = (z + 1) * KS / zs - first;    // the workgroup's steps
+    const int n0 = COLS * (blockIdx.x * waves + wave);
     const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * (K / G);
 
-    // the blocks' first words; N is a multiple of 16, so every block has 16
-    // rows (a block past N repeats the last one and is not stored)
+    // the blocks' first words; N is a multiple of 32, so every block has 16
+    // rows (a wave past N repeats the last columns and stores nothing)
     const uint32_t* wb[FJ];
     const uint32_t* sb[FJ];
 #pragma unroll
     for (int j = 0; j < FJ; ++j) {
-        const MoeWeight& w = UP ? (j < FJ / 2 ? p.gate : p.up) : p.down;
-        int r0 = n0 + 16 * (UP ? j % (FJ / 2) : j);
-        r0 = r0 < N ? r0 : N - 16;
-        wb[j] = w.wq + expert * words + static_cast<int64_t>(r0) * (K / 8) + 4 * c;
-        sb[j] = w.sz + expert * groups + static_cast<int64_t>(r0) * (K / G) + c;
+        const MoeWeight& w = UP ? (j == 0 ? p.gate : p.up) : p.down;
+        const int r0 = (n0 < N ? n0 : N - COLS) + (UP ? 0 : 16 * j);
+        wb[j] = w.wq + expert * words + static_cast<int64_t>(r0) * (K / 8);
+        sb[j] = w.sz + expert * groups + static_cast<int64_t>(r0) * (K / G);
     }
     const uint32_t bias = opaque_vgpr(kBf16Bias128x2);
+    StepB<FJ, G> b[DEPTH];
+    auto load = [&](int i, int d) { load_b<FJ, G>(b[d], wb, sb, first + i, K, c, q); };
 
-    for (int m0 = 0; m0 < rows; m0 += 16 * MB) {
-        // the lane's row in each block (past the last: the last, never stored)
-        const uint16_t* arow[MB][AP];
+    for (int m0 = 0; m0 < rows; m0 += RM) {
+        const int some = rows - m0 < RM ? rows - m0 : RM;
+        // the first steps' weights need no list; the rows of m0 in LDS
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            if (d < n) load(d, d);
+        __syncthreads();                            // (the rows before are multiplied)
+        if (tid < some) {
+            const int slot = list[m0 + tid];
+            row_at[tid] = UP ? slot / p.k : slot;
+        }
+        __syncthreads();
+        // piece j of the rows (its steps first + CS j ..): 16-byte chunk ch of
+        // row r at ch ^ (r & 15); a lane past K reads the row's last chunk, which
+        // meets zeros or nothing
+        auto dma = [&](int j) {
+            const int per = (some + RPD - 1) / RPD;          // loads of one part
+            for (int d = wave; d < AP * per; d += waves) {
+                const int v = d / per, r0 = d % per * RPD;
+                int r = r0 + lane / (ROW / 16);
+                const int ch = (lane % (ROW / 16)) ^ (r & 15);
+                r = r < some ? r : some - 1;
+                int k = (first + CS * j) * kStepK + 8 * ch;
+                k = k < K ? k : K - 8;
+                const uint16_t* const from = (UP ? p.X : v == 0 ? p.hi : p.lo) + static_cast<int64_t>(row_at[r]) * K + k;
+                typedef __attribute__((address_space(3))) uint8_t lds_u8;
+                const uint32_t m0_ = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
+                    reinterpret_cast<uintptr_t>((lds_u8*)(lds_a[j & 1] + (v * RM + r0) * ROW))));
+                asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(m0_) : "memory", "m0");
+            }
+        };
+        dma(0);
+        const int blocks = (some + 15) / 16;
+        // where the lane's fragment f lies in a step of its row in each block (past
+        // the last row: the last): f moves it among the step's 16 chunks only
+        uint32_t at[MB][4];
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
-            const int m = m0 + 16 * i + c;
-            const int slot = list[m < rows ? m : rows - 1];
-            if constexpr (UP) {
-                arow[i][0] = p.X + static_cast<int64_t>(slot / p.k) * K;
-            } else {
-                arow[i][0] = p.hi + static_cast<int64_t>(slot) * K;
-                arow[i][1] = p.lo + static_cast<int64_t>(slot) * K;
-            }
+            const int r = 16 * i + c < some ? 16 * i + c : some - 1;
+#pragma unroll
+            for (int f = 0; f < 4; ++f) at[i][f] = static_cast<uint32_t>(r * ROW + 16 * ((NG == 1 ? 4 * q + f : 4 * f + q) ^ (r & 15)));
         }
         float4_t acc[MB][FJ];
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
             for (int j = 0; j < FJ; ++j) acc[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        // rounds of DEPTH steps: their loads together, then their products;
-        // the other waves on the compute unit cover the latency
-        for (int step = wave; step < KS; step += DEPTH * wk) {
-            StepB<FJ, G> b[DEPTH];
-            StepA<MB, AP> a[DEPTH];
-#pragma unroll
-            for (int d = 0; d < DEPTH; ++d)
-                if (step + d * wk < KS) {
-                    load_b<FJ, G>(b[d], wb, sb, step + d * wk, K, q);
-                    load_a<MB, AP, G>(a[d], arow, step + d * wk, K, q);
-                }
+        // the piece that step i begins is in LDS for all waves (`behind`: loads
+        // issued after it that may be under way), and the next one on its way
+        auto piece = [&](int i, bool all) {
             asm volatile("" ::: "memory");
-            __builtin_amdgcn_sched_barrier(0);
+            constexpr int kBehind = CS * LOADS;
+            if (all) __builtin_amdgcn_s_waitcnt((kBehind & 15) | (7 << 4) | (0 << 8) | ((kBehind >> 4) << 14));
+            else __builtin_amdgcn_s_waitcnt(0);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (i + CS < n) dma(i / CS + 1);
+        };
+        auto one = [&](int i, int s) {
+            const uint8_t* const from = lds_a[(i / CS) & 1];
+            multiply<MB, AP, FJ, G>(
+                acc, b[s],
+                [&](int rb, int v, int f) {
+                    return *reinterpret_cast<const u32x4_t*>(from + at[rb][f] + (v * (RM * ROW) + 256 * (s % CS)));
+                },
+                first + i, K, bias, blocks);
+        };
+        int i = 0;
+        // whole groups of DEPTH steps whose refills are all real: no branch
+        // around a load, so that a step waits for its own weights only
+        for (; i + 2 * DEPTH <= n; i += DEPTH) {
 #pragma unroll
-            for (int d = 0; d < DEPTH; ++d)
-                if (step + d * wk < KS) multiply<MB, AP, FJ, G>(acc, b[d], a[d], step + d * wk, K, bias);
-        }
-
-        // the waves' sums through LDS, in wave order: register e of lane (c, q)
-        // is row 4 q + e of its block, column c
-        __syncthreads();                           // (the last rows' sums are read)
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-            for (int j = 0; j < FJ; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    red[wave * TILE + (16 * i + 4 * q + e) * (16 * FJ) + 16 * j + c] = acc[i][j][e];
-        __syncthreads();
-        const int some = rows - m0 < 16 * MB ? rows - m0 : 16 * MB;
-        for (int o = threadIdx.x; o < some * COLS; o += blockDim.x) {
-            const int row = o / COLS, col = o % COLS;
-            if (n0 + col >= N) continue;
-            const int slot = list[m0 + row];
-            const int64_t at = static_cast<int64_t>(slot) * N + n0 + col;
-            if constexpr (UP) {
-                const float weight = p.weights[slot];
-                float g = 0.0f, u = 0.0f;
-                for (int w = 0; w < wk; ++w) {
-                    g += red[w * TILE + row * (16 * FJ) + col];
-                    u += red[w * TILE + row * (16 * FJ) + COLS + col];
-                }
-                store_h(p, at, activation(p.act, g) * u * weight);
-            } else {
-                float y = 0.0f;
-                for (int w = 0; w < wk; ++w) y += red[w * TILE + row * COLS + col];
-                p.part[at] = y;
+            for (int s = 0; s < DEPTH; ++s) {
+                // (before the first group nothing was issued behind its piece)
+                if (s % CS == 0) piece(i + s, i + s >= CS);
+                one(i + s, s);
+                load(i + DEPTH + s, s);
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-    }
-}
-
-// The down product of at most 16 tokens with the join: a workgroup owns 16 FJ
-// columns of all tokens and goes through every unit; row t of a unit's rows is
-// token t's h, or the row of zeros.  Its waves take equal runs of the (unit, step) pairs.
-template <int FJ, int G>
-__global__ void __launch_bounds__(1024) moe_down_kernel(MoeParams p, int wk) {
-    constexpr int COLS = 16 * FJ, DEPTH = 2, TILE = 256 * FJ;
-    __shared__ int16_t unit_slot[kMaxUnits * kUnitTokens], unit_expert[kMaxUnits];
-    extern __shared__ float red[];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int c = lane & 15, q = lane >> 4;
-    const int K = p.I, N = p.H, KS = (K + kStepK - 1) / kStepK;
-    const int n0 = COLS * blockIdx.x;
-    const int T = static_cast<int>(p.T), slots = T * p.k;
-    // (past the units there are whatever numbers, which nothing reads)
-    const int units = p.unit_expert[slots];
-    for (int i = tid; i < slots; i += blockDim.x) unit_expert[i] = static_cast<int16_t>(p.unit_expert[i]);
-    for (int i = tid; i < slots * kUnitTokens; i += blockDim.x) unit_slot[i] = static_cast<int16_t>(p.unit_slot[i]);
-    // the residual of the thread's first output, ahead of the weights
-    float first = 0.0f;
-    if (p.residual && tid / COLS < T && n0 + tid % COLS < N)
-        first = bf16_lo(p.residual[static_cast<int64_t>(tid / COLS) * N + n0 + tid % COLS]);
-    __syncthreads();
-
-    const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * (K / G);
-    const uint32_t bias = opaque_vgpr(kBf16Bias128x2);
-    float4_t acc[1][FJ];
+        for (; i < n; i += DEPTH) {
 #pragma unroll
-    for (int j = 0; j < FJ; ++j) acc[0][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const int all = units * KS, begin = static_cast<int>(static_cast<int64_t>(all) * wave / wk),
-              end = static_cast<int>(static_cast<int64_t>(all) * (wave + 1) / wk);
-    for (int at = begin; at < end; at += DEPTH) {
-        StepB<FJ, G> b[DEPTH];
-        StepA<1, 2> a[DEPTH];
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            if (at + d < end) {
-                const int u = (at + d) / KS, step = (at + d) % KS;
-                const int expert = __builtin_amdgcn_readfirstlane(unit_expert[u]);
-                const uint32_t* wb[FJ];
-                const uint32_t* sb[FJ];
-#pragma unroll
-                for (int j = 0; j < FJ; ++j) {
-                    int r0 = n0 + 16 * j;
-                    r0 = r0 < N ? r0 : N - 16;
-                    wb[j] = p.down.wq + expert * words + static_cast<int64_t>(r0) * (K / 8) + 4 * c;
-                    sb[j] = p.down.sz + expert * groups + static_cast<int64_t>(r0) * (K / G) + c;
+            for (int s = 0; s < DEPTH; ++s) {
+                if (i + s < n) {
+                    if (s % CS == 0) piece(i + s, false);
+                    one(i + s, s);
+                    if (i + DEPTH + s < n) load(i + DEPTH + s, s);
                 }
-                const int slot = unit_slot[u * kUnitTokens + c];
-                const uint16_t* const arow[1][2] = {{p.hi + static_cast<int64_t>(slot) * K, p.lo + static_cast<int64_t>(slot) * K}};
-                load_b<FJ, G>(b[d], wb, sb, step, K, q);
-                load_a<1, 2, G>(a[d], arow, step, K, q);
             }
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
+        }
+
+        // register e of lane (c, q): row 4 q + e of its block, column c
+        if (n0 >= N) continue;
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            if (at + d < end) multiply<1, 2, FJ, G>(acc, b[d], a[d], (at + d) % KS, K, bias);
-    }
+        for (int rb = 0; rb < MB; ++rb)
 #pragma unroll
-    for (int j = 0; j < FJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) red[wave * TILE + (4 * q + e) * COLS + 16 * j + c] = acc[0][j][e];
-    __syncthreads();
-    for (int o = tid; o < T * COLS; o += blockDim.x) {
-        const int row = o / COLS, col = o % COLS;
-        if (n0 + col >= N) continue;
-        const int64_t at = static_cast<int64_t>(row) * N + n0 + col;
-        float y = 0.0f;
-        for (int w = 0; w < wk; ++w) y += red[w * TILE + o];
-        if (p.residual) y += o == tid ? first : bf16_lo(p.residual[at]);
-        p.Y[at] = float_to_bf16_bits(y);
+            for (int e = 0; e < 4; ++e) {
+                const int r = 16 * rb + 4 * q + e;
+                if (r >= some) continue;
+                const int slot = UP ? list[m0 + r] : row_at[r];
+                const int64_t at = static_cast<int64_t>(slot) * N + n0 + c;
+                if constexpr (UP) {
+                    store_h(p, at, activation(p.act, acc[rb][0][e]) * acc[rb][1][e] * p.weights[slot]);
+                } else {
+                    float* const dst = p.part + z * p.T * p.k * N + at;
+                    dst[0] = acc[rb][0][e];
+                    dst[16] = acc[rb][1][e];
+                }
+            }
     }
 }
 
@@ -771,8 +684,16 @@ __global__ void __launch_bounds__(256) moe_join_kernel(MoeParams p) {
         for (int j = 0; j < 8; ++j) {
             v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             const int64_t slot = t * p.k + j0 + j;
-            if (j0 + j < p.k && static_cast<uint32_t>(p.ids[slot]) < static_cast<uint32_t>(p.E))
+            if (j0 + j < p.k && static_cast<uint32_t>(p.ids[slot]) < static_cast<uint32_t>(p.E)) {
                 v[j] = *reinterpret_cast<const float4*>(p.part + slot * p.H + n);
+                for (int z = 1; z < p.splits; ++z) {
+                    const float4 u = *reinterpret_cast<const float4*>(p.part + (z * p.T * p.k + slot) * p.H + n);
+                    v[j].x += u.x;
+                    v[j].y += u.y;
+                    v[j].z += u.z;
+                    v[j].w += u.w;
+                }
+            }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -789,38 +710,28 @@ __global__ void __launch_bounds__(256) moe_join_kernel(MoeParams p) {
     *reinterpret_cast<u32x2_t*>(p.Y + t * p.H + n) = u32x2_t{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
 }
 
-template <int MB, int FJ, int G, bool UP>
+// Waves of a workgroup: as many columns as give two workgroups a compute unit,
+// from 8 waves down to 2.
+int stream_waves(int64_t columns, int per_wave, int64_t experts) {
+    int w = 8;
+    while (w > 2 && (columns + w * per_wave - 1) / (w * per_wave) * experts < 512) w /= 2;
+    return w;
+}
+template <int MB, int G, bool UP>
 hipError_t launch_stream(const MoeParams& p, hipStream_t stream) {
-    const int K = UP ? p.H : p.I, N = UP ? p.I : p.H, cols = UP ? 8 * FJ : 16 * FJ;
-    const int64_t slots = p.T * p.k;
-    const int experts = slots < p.E ? static_cast<int>(slots) : p.E;
-    const int nb = (N + cols - 1) / cols, steps = (K + kStepK - 1) / kStepK;
-    int64_t wk = 4096 / (static_cast<int64_t>(nb) * experts);
-    wk = wk > 8 ? 8 : wk;
-    wk = wk < 4 ? 4 : wk;
-    wk = wk > steps / 2 ? steps / 2 : wk;
-    wk = wk < 1 ? 1 : wk;
-    const size_t lds = static_cast<size_t>(wk) * 256 * MB * FJ * sizeof(float);
-    const dim3 block(static_cast<unsigned>(64 * wk));
+    const int N = UP ? p.I : p.H, per = UP ? 16 : 32;
+    const int64_t slots = p.T * p.k, experts = slots < p.E ? slots : p.E;
+    const int w = stream_waves(N, per, experts * (UP ? 1 : p.splits));
+    dim3 grid(static_cast<unsigned>((N + w * per - 1) / (w * per)), static_cast<unsigned>(experts), UP ? 1u : static_cast<unsigned>(p.splits));
+    const dim3 block(static_cast<unsigned>(64 * w));
     if constexpr (UP) {
         if (slots <= kWave) {
-            hipLaunchKernelGGL((moe_stream_kernel<MB, FJ, G, true, true>),
-                               dim3(static_cast<unsigned>(nb), static_cast<unsigned>(experts + 1)), block, lds, stream, p,
-                               static_cast<int>(wk));
+            grid.y += 1;
+            hipLaunchKernelGGL((moe_stream_kernel<MB, G, true, true>), grid, block, 0, stream, p);
             return hipGetLastError();
         }
     }
-    hipLaunchKernelGGL((moe_stream_kernel<MB, FJ, G, UP, false>), dim3(static_cast<unsigned>(nb), static_cast<unsigned>(experts)),
-                       block, lds, stream, p, static_cast<int>(wk));
-    return hipGetLastError();
-}
-
-template <int FJ, int G>
-hipError_t launch_down(const MoeParams& p, hipStream_t stream) {
-    const int nb = (p.H + 16 * FJ - 1) / (16 * FJ);
-    const int wk = 16 / FJ;
-    hipLaunchKernelGGL((moe_down_kernel<FJ, G>), dim3(static_cast<unsigned>(nb)), dim3(static_cast<unsigned>(64 * wk)),
-                       static_cast<size_t>(wk) * 256 * FJ * sizeof(float), stream, p, wk);
+    hipLaunchKernelGGL((moe_stream_kernel<MB, G, UP, false>), grid, block, 0, stream, p);
     return hipGetLastError();
 }
 
@@ -857,7 +768,7 @@ bool tile_form(const MoeParams& p) {
     // (the activations are addressed with 31-bit byte offsets)
     constexpr int64_t kMost = (int64_t{1} << 31) - 1;
     const int64_t slots = p.T * p.k, wide = p.H > p.I ? p.H : p.I;
-    return p.G == 128 && p.T > kUnitTokens && slots >= static_cast<int64_t>(W4_MOE_TILE_FROM) * p.E &&
+    return p.G == 128 && slots > kWave && slots >= static_cast<int64_t>(W4_MOE_TILE_FROM) * p.E &&
            wide / 128 * kMoeTileRows <= kMoeTileSums && 2 * slots * wide <= kMost;
 }
 hipError_t launch_tiles(const MoeParams& p, hipStream_t stream) {
@@ -875,6 +786,14 @@ hipError_t launch_join(const MoeParams& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// K ranges of the down product, towards two workgroups of 256 columns a compute
+// unit, each of at least eight steps (`parts`: experts, or tiles)
+int down_splits(const MoeParams& p, int64_t parts) {
+    int64_t z = 512 / ((p.H + 255) / 256 * parts);
+    if (z > p.I / kStepK / 8) z = p.I / kStepK / 8;
+    return z < 1 ? 1 : (z > 8 ? 8 : static_cast<int>(z));
+}
+
 template <int G>
 hipError_t launch_moe_g(const MoeParams& p, hipStream_t stream) {
     const int64_t slots = p.T * p.k;
@@ -885,14 +804,13 @@ hipError_t launch_moe_g(const MoeParams& p, hipStream_t stream) {
         if (e != hipSuccess) return e;
     }
     const int64_t each = slots / p.E;             // an expert's rows, were the choices even
-    if (p.T <= kUnitTokens || each <= 12) e = launch_stream<1, 2, G, true>(p, stream);
-    else if (each <= 24) e = launch_stream<2, 2, G, true>(p, stream);
-    else e = launch_stream<4, 2, G, true>(p, stream);
+    if (each <= 12) e = launch_stream<1, G, true>(p, stream);
+    else if (each <= 24) e = launch_stream<2, G, true>(p, stream);
+    else e = launch_stream<4, G, true>(p, stream);
     if (e != hipSuccess) return e;
-    if (p.T <= kUnitTokens) return launch_down<1, G>(p, stream);
-    if (each <= 12) e = launch_stream<1, 2, G, false>(p, stream);
-    else if (each <= 24) e = launch_stream<2, 2, G, false>(p, stream);
-    else e = launch_stream<4, 2, G, false>(p, stream);
+    if (each <= 12) e = launch_stream<1, G, false>(p, stream);
+    else if (each <= 24) e = launch_stream<2, G, false>(p, stream);
+    else e = launch_stream<4, G, false>(p, stream);
     if (e != hipSuccess) return e;
     return launch_join(p, stream);
 }
@@ -907,21 +825,21 @@ size_t moe_workspace(MoeParams& p, void* base) {
         at += (bytes + 255) & ~size_t{255};
         return q;
     };
-    p.hi = static_cast<uint16_t*>(take(2 * (slots + 1) * p.I));
-    if (!tile_form(p)) p.lo = static_cast<uint16_t*>(take(2 * (slots + 1) * p.I));
-    p.runs = static_cast<int4*>(take(16 * p.E));
+    const bool dot = dot_form(p), tile = !dot && tile_form(p);
+    p.hi = static_cast<uint16_t*>(take(2 * slots * p.I));
+    if (!tile) p.lo = static_cast<uint16_t*>(take(2 * slots * p.I));
+    if (dot) return at;
     p.order = static_cast<int32_t*>(take(4 * slots));
-    if (p.T <= kUnitTokens) {
-        p.unit_expert = static_cast<int32_t*>(take(4 * (slots + 1)));
-        p.unit_slot = static_cast<int32_t*>(take(4 * slots * kUnitTokens));
+    const int64_t experts = static_cast<int64_t>(slots) < p.E ? slots : p.E;
+    p.splits = down_splits(p, tile ? static_cast<int64_t>(slots) / kMoeTileRows + experts / 2 : experts);
+    p.part = static_cast<float*>(take(4 * slots * p.H * p.splits));
+    if (tile) {
+        p.tiles = static_cast<int4*>(take(16 * tile_count(p)));
+        p.tile_count = static_cast<int32_t*>(take(4));
+        p.x_sums = static_cast<float*>(take(4 * p.T * (p.H / 128)));
+        p.h_sums = static_cast<float*>(take(4 * slots * (p.I / 128)));
     } else {
-        p.part = static_cast<float*>(take(4 * slots * p.H));
-        if (tile_form(p)) {
-            p.tiles = static_cast<int4*>(take(16 * tile_count(p)));
-            p.tile_count = static_cast<int32_t*>(take(4));
-            p.x_sums = static_cast<float*>(take(4 * p.T * (p.H / 128)));
-            p.h_sums = static_cast<float*>(take(4 * slots * (p.I / 128)));
-        }
+        p.runs = static_cast<int4*>(take(16 * p.E));
     }
     return at;
 }

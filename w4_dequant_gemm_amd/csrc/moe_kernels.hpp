@@ -47,15 +47,12 @@ struct MoeParams {
     const uint16_t* residual;   // [T, H] or null
     uint16_t* Y;             // [T, H]
     // workspace, see moe_workspace
-    uint16_t* hi;            // [T k + 1, I] rows of act(gate) up weight by slot t k + j, upper and lower part
-    uint16_t* lo;
+    uint16_t* hi;            // [T k, I] rows of act(gate) up weight by slot t k + j, upper and lower part
+    uint16_t* lo;            // (tiled: rounded to bf16 in `hi`, in the order of `order`)
     int4* runs;              // [E] expert, first place in `order`, rows
     int32_t* order;          // [T k] slots by expert
-    // up to 16 tokens: units of an expert and the tokens' slots with it
-    int32_t* unit_expert;    // [T k], their number at [T k]
-    int32_t* unit_slot;      // [T k, 16]; T k: the row of zeros
-    // more
-    float* part;             // [T k, H] each slot's share of the result
+    float* part;             // [splits, T k, H] each slot's share of the result, by ranges of the inner k
+    int splits;
     // tiled products
     int4* tiles;             // expert, first place in `order`, rows
     int32_t* tile_count;

@@ -41,6 +41,16 @@ __device__ __forceinline__ u32x4_t tile_rsrc(const void* base, uint32_t bytes) {
                    static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
 }
 
+// activation() with the hardware's exponential and reciprocal (a few units of
+// 2^-24; what is made of it is rounded to bf16).  1 + tanh(t) = 2 / (1 + e^-2t):
+// both forms are x / (1 + 2^-y), y = x (a + b x^2).  (x^2 kept finite: 0 times an
+// infinity is NaN.)
+__device__ __forceinline__ float quick_activation(int act, float x) {
+    const float a = act == 1 ? 1.4426950408889634f : 2.3022081986685205f, b = act == 1 ? 0.0f : 0.10294324003185554f;
+    const float y = x * fmaf(b, fminf(x * x, 3.0e38f), a);
+    return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-y));
+}
+
 template <bool UP>
 __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     __shared__ __attribute__((aligned(16))) uint8_t lds_a0[kStage];
@@ -52,12 +62,16 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 31, h = lane >> 5;
-    const int K = UP ? p.H : p.I, N = UP ? p.I : p.H, KT = K / kStepK;
+    const int K = UP ? p.H : p.I, N = UP ? p.I : p.H;
     constexpr int COLS = UP ? 128 : 256;             // the workgroup's columns of the result
     const int nt = (N + COLS - 1) / COLS;
-    const int total = *p.tile_count * nt;
+    const int zs = UP ? 1 : p.splits;                // ranges of the down product's k
+    const int total = *p.tile_count * nt * zs;
     if (static_cast<int>(blockIdx.x) >= total) return;
-    const int job = static_cast<int>(xcd_tile(blockIdx.x, total));
+    int job = static_cast<int>(xcd_tile(blockIdx.x, total));
+    const int z = job % zs;
+    job /= zs;
+    const int kb = z * (K / kStepK) / zs, KT = (z + 1) * (K / kStepK) / zs - kb;
     const int4 t4 = p.tiles[job / nt];
     const int expert = __builtin_amdgcn_readfirstlane(t4.x);
     const int first = __builtin_amdgcn_readfirstlane(t4.y);
@@ -83,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     }
     auto dma = [&](int kt, uint8_t* stage) {
         kt = kt < KT ? kt : KT - 1;
-        const uint32_t soff = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kt * kStepK * 2));
+        const uint32_t soff = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>((kb + kt) * kStepK * 2));
         typedef __attribute__((address_space(3))) uint8_t lds_u8;
 #pragma unroll
         for (int it = 0; it < kDma; ++it) {
@@ -98,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
 
     // weights: block j's 32 columns are two 16-row blocks of the layout (N is a
     // multiple of 32); lane (c, h) reads tile 4 kt + 2 m + h of its column
-    const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * KT;
+    const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * (K / kStepK);
     const uint32_t* wb[2];
     const uint32_t* sb[2];
 #pragma unroll
@@ -108,14 +122,14 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
         r0 = r0 < N ? r0 : N - 32;                   // (columns past N are not stored)
         r0 += c & 16;
         wb[j] = w.wq + expert * words + static_cast<int64_t>(r0) * (K / 8) + 4 * (c & 15) + 64 * h;
-        sb[j] = w.sz + expert * groups + static_cast<int64_t>(r0) * KT + (c & 15);
+        sb[j] = w.sz + expert * groups + static_cast<int64_t>(r0) * (K / kStepK) + (c & 15);
     }
     struct Regs {
         u32x4_t q[2][2];     // [block][64-k half]
         uint32_t s[2];
     };
     auto load_w = [&](int kt, Regs& r) {
-        kt = kt < KT ? kt : KT - 1;
+        kt = kb + (kt < KT ? kt : KT - 1);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -133,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     for (int i = tid; i < KT * kRows; i += kThreads) {
         const int g = i / kRows, r = i % kRows;
         const int64_t row = UP ? lds_slot[r] / p.k : first + (r < rows ? r : 0);
-        lds_x1[i] = (UP ? p.x_sums : p.h_sums)[row * KT + g];
+        lds_x1[i] = (UP ? p.x_sums : p.h_sums)[row * (K / kStepK) + kb + g];
     }
 
     float16_t acc[2][2];
@@ -240,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int r = 32 * i + 8 * (e / 4) + 4 * h + e % 4;
-                const float v = activation(p.act, acc[i][0][e]) * acc[i][1][e] * lds_weight[r];
+                const float v = quick_activation(p.act, acc[i][0][e]) * acc[i][1][e] * lds_weight[r];
                 hl[r * 128 + 8 * ((col >> 3) ^ (r & 15)) + (col & 7)] = float_to_bf16_bits(v);
             }
         __syncthreads();
@@ -263,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
             for (int e = 0; e < 16; ++e) {
                 const int r = 32 * i + 8 * (e / 4) + 4 * h + e % 4;
                 if (r >= rows) continue;
-                float* const dst = p.part + static_cast<int64_t>(lds_slot[r]) * N;
+                float* const dst = p.part + (z * p.T * p.k + lds_slot[r]) * N;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int n = n0 + 64 * wave + 32 * j + c;
@@ -277,8 +291,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
 
 hipError_t launch_moe_tile(const MoeParams& p, bool up, int64_t tiles, hipStream_t stream) {
     const int K = up ? p.H : p.I, N = up ? p.I : p.H, cols = up ? 128 : 256;
-    const int64_t grid = tiles * ((N + cols - 1) / cols);
-    const size_t lds = static_cast<size_t>(K / kStepK) * kRows * sizeof(float);
+    const int zs = up ? 1 : p.splits;
+    const int64_t grid = tiles * ((N + cols - 1) / cols) * zs;
+    const size_t lds = static_cast<size_t>((K / kStepK + zs - 1) / zs) * kRows * sizeof(float);
     if (p.G != kStepK || K % kStepK != 0 || N % 128 != 0 || lds > 4 * kMoeTileSums || grid <= 0 || grid > 0x7FFFFFFF)
         return hipErrorInvalidValue;
     if (up) hipLaunchKernelGGL((moe_tile_kernel<true>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, stream, p);
