@@ -163,13 +163,23 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     __builtin_amdgcn_s_waitcnt(0);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    // code word f of a step's two columns as MFMA operands
+    auto convert = [&](const Regs& r, int f, bf16x8_t (&o)[2]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t w = r.q[j][f >> 2][f & 3];
+            o[j] = __builtin_bit_cast(bf16x8_t, u32x4_t{nibble_pair_bf16(w, 0, bias), nibble_pair_bf16(w, 1, bias),
+                                                        nibble_pair_bf16(w, 2, bias), nibble_pair_bf16(w, 3, bias)});
+        }
+    };
+    // operands of slot f in b[f & 1]; slot 0 of a step is converted in slot 7 of
+    // the one before
+    bf16x8_t b[2][2];
+    convert(rr[0], 0, b[0]);
     auto step = [&](int kt, const uint8_t* A, uint8_t* Ad, const Regs& cur, Regs& next) __attribute__((always_inline)) {
         load_w(kt + 1, next);
         asm volatile("" ::: "memory");
-        dma(kt + 2, Ad);
         float16_t T[2][2];
-        // fragments a slot ahead; the barriers keep the scheduler from fetching
-        // more of them than there are registers
         auto frag = [&](int i, int f) {
             return *reinterpret_cast<const bf16x8_t*>(A + (32 * i + c) * 256 + 16 * ((8 * (f >> 2) + 4 * h + (f & 3)) ^ (c & 15)));
         };
@@ -178,27 +188,34 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
         for (int i = 0; i < 2; ++i) a[0][i] = frag(i, 0);
 #pragma unroll
         for (int f = 0; f < 8; ++f) {
+            // A slot: the fragments of the next one are fetched and its code words
+            // converted between this one's MFMAs.
             __builtin_amdgcn_sched_barrier(0);
             if (f < 7) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) a[(f + 1) & 1][i] = frag(i, f + 1);
-            }
-            bf16x8_t b[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t w = cur.q[j][f >> 2][f & 3];
-                b[j] = __builtin_bit_cast(bf16x8_t, u32x4_t{nibble_pair_bf16(w, 0, bias), nibble_pair_bf16(w, 1, bias),
-                                                            nibble_pair_bf16(w, 2, bias), nibble_pair_bf16(w, 3, bias)});
+                convert(cur, f + 1, b[(f + 1) & 1]);
+            } else {
+                convert(next, 0, b[0]);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float16_t zero = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-                    T[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[f & 1][i], b[j], f == 0 ? zero : T[i][j], 0, 0, 0);
+                    T[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[f & 1][i], b[f & 1][j], f == 0 ? zero : T[i][j], 0, 0, 0);
                 }
+            if (f < 7) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // LDS reads
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // an MFMA
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);          // VALU
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
+        // (behind the use of the next step's first code words: the compiler's wait
+        // for those, which does not know these loads, would wait for them as well)
+        dma(kt + 2, Ad);
         // register e of lane (c, h): row 8 (e / 4) + 4 h + e % 4 of its block, column c
         float sc[2], zc[2];
 #pragma unroll
