@@ -51,10 +51,18 @@ __device__ __forceinline__ void build_runs(const MoeParams& p, RunMem& m, int ti
     for (int e = tid; e < p.E; e += threads) m.count[e] = 0;
     __syncthreads();
     const int slots = static_cast<int>(p.T * p.k);
-    for (int s = tid; s < slots; s += threads) {
-        const uint32_t e = static_cast<uint32_t>(p.ids[s]);
-        if (e < static_cast<uint32_t>(p.E)) atomicAdd(&m.count[e], 1);
-    }
+    // (four ids a thread in flight)
+    auto each = [&](auto take) {
+        for (int s0 = tid; s0 < slots; s0 += 4 * threads) {
+            uint32_t e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = s0 + i * threads < slots ? static_cast<uint32_t>(p.ids[s0 + i * threads]) : ~0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (e[i] < static_cast<uint32_t>(p.E)) take(s0 + i * threads, e[i]);
+        }
+    };
+    each([&](int, uint32_t e) { atomicAdd(&m.count[e], 1); });
     __syncthreads();
     if (tid < kWave) {
         // the first wavefront sums over the experts, 64 at a time
@@ -94,10 +102,7 @@ __device__ __forceinline__ void build_runs(const MoeParams& p, RunMem& m, int ti
             for (int i = active + tid; i < p.E; i += kWave) p.runs[i] = make_int4(0, 0, 0, 0);
     }
     __syncthreads();
-    for (int s = tid; s < slots; s += threads) {
-        const uint32_t e = static_cast<uint32_t>(p.ids[s]);
-        if (e < static_cast<uint32_t>(p.E)) p.order[atomicAdd(&m.count[e], 1)] = s;
-    }
+    each([&](int s, uint32_t e) { p.order[atomicAdd(&m.count[e], 1)] = s; });
 }
 
 constexpr int kListThreads = 1024;

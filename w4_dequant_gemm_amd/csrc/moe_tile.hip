@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     __shared__ __attribute__((aligned(16))) uint8_t lds_a0[kStage];
     __shared__ __attribute__((aligned(16))) uint8_t lds_a1[kStage];
     __shared__ __attribute__((aligned(16))) uint8_t lds_a2[kStage];
-    __shared__ int lds_slot[kRows];
+    __shared__ int lds_slot[kRows], lds_row[kRows];
     __shared__ float lds_weight[kRows];
     extern __shared__ __attribute__((aligned(16))) float lds_x1[];   // [step][row]
     const int tid = threadIdx.x, lane = tid & 63;
@@ -77,39 +77,6 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     const int first = __builtin_amdgcn_readfirstlane(t4.y);
     const int rows = __builtin_amdgcn_readfirstlane(t4.z);
     const int n0 = (job % nt) * COLS;
-    if (tid < kRows) {
-        const int slot = p.order[first + (tid < rows ? tid : 0)];
-        lds_slot[tid] = slot;
-        if constexpr (UP) lds_weight[tid] = p.weights[slot];
-    }
-    __syncthreads();
-
-    // activations: load `it` of the wave fills stage rows 4 (4 wave + it) .. + 3,
-    // lane l row 4 (4 wave + it) + l / 16 at position l % 16 (rows past the
-    // tile's: its first, never stored)
-    const u32x4_t a_rsrc = tile_rsrc(UP ? p.X : p.hi, static_cast<uint32_t>((UP ? p.T : p.T * p.k) * K * 2));
-    uint32_t a_voff[kDma];
-#pragma unroll
-    for (int it = 0; it < kDma; ++it) {
-        const int r = 4 * (kDma * wave + it) + (lane >> 4);
-        const int row = UP ? lds_slot[r] / p.k : first + (r < rows ? r : 0);
-        a_voff[it] = static_cast<uint32_t>(row) * static_cast<uint32_t>(2 * K) + 16u * ((lane & 15) ^ (r & 15));
-    }
-    auto dma = [&](int kt, uint8_t* stage) {
-        kt = kt < KT ? kt : KT - 1;
-        const uint32_t soff = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>((kb + kt) * kStepK * 2));
-        typedef __attribute__((address_space(3))) uint8_t lds_u8;
-#pragma unroll
-        for (int it = 0; it < kDma; ++it) {
-            const uint32_t m0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u8*)stage)) +
-                                static_cast<uint32_t>((kDma * wave + it) * 1024);
-            // (a load to LDS may follow a write of M0 after one wait state; it
-            // has no register result, and the wait at a step's start covers it)
-            asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
-                         ::"v"(a_voff[it]), "s"(a_rsrc), "s"(m0), "s"(soff) : "memory", "m0");
-        }
-    };
-
     // weights: block j's 32 columns are two 16-row blocks of the layout (N is a
     // multiple of 32); lane (c, h) reads tile 4 kt + 2 m + h of its column
     const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * (K / kStepK);
@@ -138,16 +105,51 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
         }
     };
     constexpr int kWLoads = 6;
-
+    // the first weights need no list of rows
     Regs rr[2];
     load_w(0, rr[0]);
     asm volatile("" ::: "memory");
+
+    if (tid < kRows) {
+        const int slot = p.order[first + (tid < rows ? tid : 0)];
+        lds_slot[tid] = slot;
+        // the row of X, or of h, which is in the order of the rows
+        lds_row[tid] = UP ? slot / p.k : first + (tid < rows ? tid : 0);
+        if constexpr (UP) lds_weight[tid] = p.weights[slot];
+    }
+    __syncthreads();
+
+    // activations: load `it` of the wave fills stage rows 4 (4 wave + it) .. + 3,
+    // lane l row 4 (4 wave + it) + l / 16 at position l % 16 (rows past the
+    // tile's: its first, never stored)
+    const u32x4_t a_rsrc = tile_rsrc(UP ? p.X : p.hi, static_cast<uint32_t>((UP ? p.T : p.T * p.k) * K * 2));
+    uint32_t a_voff[kDma];
+#pragma unroll
+    for (int it = 0; it < kDma; ++it) {
+        const int r = 4 * (kDma * wave + it) + (lane >> 4);
+        a_voff[it] = static_cast<uint32_t>(lds_row[r]) * static_cast<uint32_t>(2 * K) + 16u * ((lane & 15) ^ (r & 15));
+    }
+    auto dma = [&](int kt, uint8_t* stage) {
+        kt = kt < KT ? kt : KT - 1;
+        const uint32_t soff = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>((kb + kt) * kStepK * 2));
+        typedef __attribute__((address_space(3))) uint8_t lds_u8;
+#pragma unroll
+        for (int it = 0; it < kDma; ++it) {
+            const uint32_t m0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u8*)stage)) +
+                                static_cast<uint32_t>((kDma * wave + it) * 1024);
+            // (a load to LDS may follow a write of M0 after one wait state; it
+            // has no register result, and the wait at a step's start covers it)
+            asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
+                         ::"v"(a_voff[it]), "s"(a_rsrc), "s"(m0), "s"(soff) : "memory", "m0");
+        }
+    };
+
     dma(0, lds_a0);
     dma(1, lds_a1);
-    for (int i = tid; i < KT * kRows; i += kThreads) {
-        const int g = i / kRows, r = i % kRows;
-        const int64_t row = UP ? lds_slot[r] / p.k : first + (r < rows ? r : 0);
-        lds_x1[i] = (UP ? p.x_sums : p.h_sums)[row * (K / kStepK) + kb + g];
+    {
+        const int r = tid % kRows;
+        const float* const from = (UP ? p.x_sums : p.h_sums) + static_cast<int64_t>(lds_row[r]) * (K / kStepK) + kb;
+        for (int g = tid / kRows; g < KT; g += kThreads / kRows) lds_x1[g * kRows + r] = from[g];
     }
 
     float16_t acc[2][2];
