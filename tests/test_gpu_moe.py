@@ -39,6 +39,8 @@ def _check(got, want, bound, what):
     # rows in tiles: ragged, one tile and several an expert, columns past the last tile's, long inner sums
     (100, 2, 4, 128, 128, 128), (200, 6, 16, 384, 640, 128), (700, 4, 32, 640, 256, 128), (90, 3, 3, 256, 4096, 128),
     (65, 1, 1, 4096, 256, 128), (1000, 8, 64, 256, 384, 128),
+    (100, 2, 4, 64, 192, 64), (300, 4, 8, 320, 448, 64), (130, 1, 2, 576, 1536, 64), (200, 3, 5, 96, 160, 32),
+    (90, 2, 2, 576, 1536, 32), (150, 2, 3, 288, 32, 32), (77, 1, 1, 2048, 4096, 32), (100, 2, 4, 128, 14336, 64),
 ])
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 def test_moe(T, k, E, H, I, G, act):

@@ -112,22 +112,24 @@ __global__ void __launch_bounds__(kListThreads) moe_lists_kernel(MoeParams p) {
 }
 
 // For the tiled products: workgroup 0 makes the runs and tiles, the others the
-// tokens' row sums over each 128 k (16 lanes a sum).
+// tokens' row sums over each group (an eighth as many lanes as it has k).
+template <int G>
 __global__ void __launch_bounds__(kListThreads) moe_tiles_kernel(MoeParams p) {
+    constexpr int LANES = G / 8;
     __shared__ RunMem mem;
     if (blockIdx.x == 0) {
         build_runs<true>(p, mem, threadIdx.x, kListThreads);
         return;
     }
-    const int64_t i = (static_cast<int64_t>(blockIdx.x - 1) * kListThreads + threadIdx.x) / 16;
-    const int64_t sums = p.T * (p.H / 128);
-    const u32x4_t v = reinterpret_cast<const u32x4_t*>(p.X)[(i < sums ? i : 0) * 16 + threadIdx.x % 16];
+    const int64_t i = (static_cast<int64_t>(blockIdx.x - 1) * kListThreads + threadIdx.x) / LANES;
+    const int64_t sums = p.T * (p.H / G);
+    const u32x4_t v = reinterpret_cast<const u32x4_t*>(p.X)[(i < sums ? i : 0) * LANES + threadIdx.x % LANES];
     float s = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) s += bf16_lo(v[e]) + bf16_hi(v[e]);
 #pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) s += __shfl_xor(s, off, 16);
-    if (i < sums && threadIdx.x % 16 == 0) p.x_sums[i] = s;
+    for (int off = LANES / 2; off >= 1; off >>= 1) s += __shfl_xor(s, off, LANES);
+    if (i < sums && threadIdx.x % LANES == 0) p.x_sums[i] = s;
 }
 
 // ------------------------------------------------------------------ products
@@ -760,11 +762,9 @@ hipError_t launch_dot(const MoeParams& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The rows of an expert in tiles on the matrix cores (moe_tile.hip), where groups
-// are of 128 and an expert has enough of them.
-#ifndef W4_MOE_TILE_FROM
-#define W4_MOE_TILE_FROM 24
-#endif
+// The rows of an expert in tiles on the matrix cores (moe_tile.hip), where an
+// expert has enough of them.
+constexpr int64_t kTileFrom = 24;
 int64_t tile_count(const MoeParams& p) {
     const int64_t slots = p.T * p.k;
     return slots / kMoeTileRows + (slots < p.E ? slots : p.E);
@@ -773,12 +773,13 @@ bool tile_form(const MoeParams& p) {
     // (the activations are addressed with 31-bit byte offsets)
     constexpr int64_t kMost = (int64_t{1} << 31) - 1;
     const int64_t slots = p.T * p.k, wide = p.H > p.I ? p.H : p.I;
-    return p.G == 128 && slots > kWave && slots >= static_cast<int64_t>(W4_MOE_TILE_FROM) * p.E &&
-           wide / 128 * kMoeTileRows <= kMoeTileSums && 2 * slots * wide <= kMost;
+    return slots > kWave && slots >= kTileFrom * p.E &&
+           (wide + 127) / 128 * (128 / p.G) * kMoeTileRows <= kMoeTileSums && 2 * slots * wide <= kMost;
 }
+template <int G>
 hipError_t launch_tiles(const MoeParams& p, hipStream_t stream) {
-    const int64_t sums = p.T * (p.H / 128);
-    hipLaunchKernelGGL(moe_tiles_kernel, dim3(static_cast<unsigned>(1 + (sums * 16 + kListThreads - 1) / kListThreads)),
+    const int64_t lanes = p.T * (p.H / 8);
+    hipLaunchKernelGGL((moe_tiles_kernel<G>), dim3(static_cast<unsigned>(1 + (lanes + kListThreads - 1) / kListThreads)),
                        dim3(kListThreads), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -803,19 +804,21 @@ template <int G>
 hipError_t launch_moe_g(const MoeParams& p, hipStream_t stream) {
     const int64_t slots = p.T * p.k;
     hipError_t e;
+    if (tile_form(p)) {
+        e = launch_tiles<G>(p, stream);
+        return e != hipSuccess ? e : launch_join(p, stream);
+    }
     if (slots > kWave) {
         hipLaunchKernelGGL(moe_lists_kernel, dim3(1), dim3(kListThreads), 0, stream, p);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const int64_t each = slots / p.E;             // an expert's rows, were the choices even
-    if (each <= 12) e = launch_stream<1, G, true>(p, stream);
-    else if (each <= 24) e = launch_stream<2, G, true>(p, stream);
-    else e = launch_stream<4, G, true>(p, stream);
+    // an expert's rows, were the choices even: 16 at a time, or 32 (each read of
+    // the weights then serves twice as many)
+    const bool few = slots <= 12 * static_cast<int64_t>(p.E);
+    e = few ? launch_stream<1, G, true>(p, stream) : launch_stream<2, G, true>(p, stream);
     if (e != hipSuccess) return e;
-    if (each <= 12) e = launch_stream<1, G, false>(p, stream);
-    else if (each <= 24) e = launch_stream<2, G, false>(p, stream);
-    else e = launch_stream<4, G, false>(p, stream);
+    e = few ? launch_stream<1, G, false>(p, stream) : launch_stream<2, G, false>(p, stream);
     if (e != hipSuccess) return e;
     return launch_join(p, stream);
 }
@@ -841,8 +844,8 @@ size_t moe_workspace(MoeParams& p, void* base) {
     if (tile) {
         p.tiles = static_cast<int4*>(take(16 * tile_count(p)));
         p.tile_count = static_cast<int32_t*>(take(4));
-        p.x_sums = static_cast<float*>(take(4 * p.T * (p.H / 128)));
-        p.h_sums = static_cast<float*>(take(4 * slots * (p.I / 128)));
+        p.x_sums = static_cast<float*>(take(4 * p.T * (p.H / p.G)));
+        p.h_sums = static_cast<float*>(take(4 * slots * (p.I / p.G)));
     } else {
         p.runs = static_cast<int4*>(take(16 * p.E));
     }
@@ -851,10 +854,6 @@ size_t moe_workspace(MoeParams& p, void* base) {
 
 hipError_t launch_moe(const MoeParams& p, hipStream_t stream) {
     if (dot_form(p)) return launch_dot(p, stream);
-    if (tile_form(p)) {
-        const hipError_t e = launch_tiles(p, stream);
-        return e != hipSuccess ? e : launch_join(p, stream);
-    }
     switch (p.G) {
         case 32: return launch_moe_g<32>(p, stream);
         case 64: return launch_moe_g<64>(p, stream);

@@ -56,8 +56,8 @@ struct MoeParams {
     // tiled products
     int4* tiles;             // expert, first place in `order`, rows
     int32_t* tile_count;
-    float* x_sums;           // [T, H / 128] row sums of X
-    float* h_sums;           // [T k, I / 128] of h, in the order of `order`
+    float* x_sums;           // [T, H / G] row sums of X
+    float* h_sums;           // [T k, I / G] of h, in the order of `order`
 };
 // bytes of the workspace, and the pointers into it
 size_t moe_workspace(MoeParams& p, void* base);
@@ -66,7 +66,7 @@ hipError_t launch_moe(const MoeParams& p, hipStream_t stream);
 // the tiled products (moe_tile.hip): rows of a tile, the most row sums of one
 // (they lie in LDS), and the launch for at most `tiles` tiles
 constexpr int kMoeTileRows = 64;
-constexpr int kMoeTileSums = 8192;
+constexpr int kMoeTileSums = 16384;
 hipError_t launch_moe_tile(const MoeParams& p, bool up, int64_t tiles, hipStream_t stream);
 
 }  // namespace w4

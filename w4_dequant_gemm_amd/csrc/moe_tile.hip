@@ -1,8 +1,8 @@
 // The products of a mixture of experts with many tokens, on gfx950's matrix
-// cores (groups of 128): tiles of 64 of one expert's rows.
+// cores: tiles of 64 of one expert's rows.
 //
 //   up:    h = bf16(w act(Wg x) * (Wu x)) of every slot, in the order of the
-//          experts' rows, and h's sums over each group of 128
+//          experts' rows, and h's sums over each group
 //   down:  part[slot] = Wd h, fp32
 //
 // A workgroup of four waves computes 64 rows by 128 columns of h (or 256
@@ -51,8 +51,12 @@ __device__ __forceinline__ float quick_activation(int act, float x) {
     return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-y));
 }
 
-template <bool UP>
-__global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
+// Two workgroups a compute unit; one with groups of 64, where 256 registers a
+// lane leave 45 of them in memory (1391 rows on 5 experts of 2048 x 1024: 92 us
+// with two, 74 with one; groups of 32: 87 with two, 102 with one).
+template <int G, bool UP>
+__global__ void __launch_bounds__(kThreads, G == 64 ? 1 : 2) moe_tile_kernel(MoeParams p) {
+    constexpr int GS = kStepK / G, PER = 8 / GS;     // groups in a step, slots (MFMAs of a tile) in a group
     __shared__ __attribute__((aligned(16))) uint8_t lds_a0[kStage];
     __shared__ __attribute__((aligned(16))) uint8_t lds_a1[kStage];
     __shared__ __attribute__((aligned(16))) uint8_t lds_a2[kStage];
@@ -71,7 +75,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     int job = static_cast<int>(xcd_tile(blockIdx.x, total));
     const int z = job % zs;
     job /= zs;
-    const int kb = z * (K / kStepK) / zs, KT = (z + 1) * (K / kStepK) / zs - kb;
+    // (K may end inside the last step of groups below 128: its activations are
+    // zeros there)
+    const int steps = (K + kStepK - 1) / kStepK, kb = z * steps / zs, KT = (z + 1) * steps / zs - kb;
     const int4 t4 = p.tiles[job / nt];
     const int expert = __builtin_amdgcn_readfirstlane(t4.x);
     const int first = __builtin_amdgcn_readfirstlane(t4.y);
@@ -79,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     const int n0 = (job % nt) * COLS;
     // weights: block j's 32 columns are two 16-row blocks of the layout (N is a
     // multiple of 32); lane (c, h) reads tile 4 kt + 2 m + h of its column
-    const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * (K / kStepK);
+    const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * (K / G);
     const uint32_t* wb[2];
     const uint32_t* sb[2];
 #pragma unroll
@@ -89,22 +95,32 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
         r0 = r0 < N ? r0 : N - 32;                   // (columns past N are not stored)
         r0 += c & 16;
         wb[j] = w.wq + expert * words + static_cast<int64_t>(r0) * (K / 8) + 4 * (c & 15) + 64 * h;
-        sb[j] = w.sz + expert * groups + static_cast<int64_t>(r0) * (K / kStepK) + (c & 15);
+        sb[j] = w.sz + expert * groups + static_cast<int64_t>(r0) * (K / G) + (c & 15);
     }
     struct Regs {
         u32x4_t q[2][2];     // [block][64-k half]
-        uint32_t s[2];
+        uint32_t s[2][GS];
     };
     auto load_w = [&](int kt, Regs& r) {
         kt = kb + (kt < KT ? kt : KT - 1);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int m = 0; m < 2; ++m) r.q[j][m] = *reinterpret_cast<const u32x4_t*>(wb[j] + 64 * (4 * kt + 2 * m));
-            r.s[j] = sb[j][16 * kt];
+            for (int m = 0; m < 2; ++m) {
+                int t = 4 * kt + 2 * m;
+                // (the last tile, where K ends before; its activations are zeros)
+                if constexpr (GS > 1) t = t + h < K / 32 ? t : K / 32 - 1 - h;
+                r.q[j][m] = *reinterpret_cast<const u32x4_t*>(wb[j] + 64 * t);
+            }
+#pragma unroll
+            for (int g = 0; g < GS; ++g) {
+                int gg = GS * kt + g;
+                if constexpr (GS > 1) gg = gg < K / G ? gg : K / G - 1;
+                r.s[j][g] = sb[j][16 * gg];
+            }
         }
     };
-    constexpr int kWLoads = 6;
+    constexpr int kWLoads = 2 * (2 + GS);
     // the first weights need no list of rows
     Regs rr[2];
     load_w(0, rr[0]);
@@ -139,8 +155,14 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
                                 static_cast<uint32_t>((kDma * wave + it) * 1024);
             // (a load to LDS may follow a write of M0 after one wait state; it
             // has no register result, and the wait at a step's start covers it)
+            uint32_t voff = a_voff[it];
+            // (chunks past K: past the buffer's end, zeros)
+            if constexpr (GS > 1) {
+                const int r = 4 * (kDma * wave + it) + (lane >> 4);
+                if ((kb + kt) * kStepK + 8 * ((lane & 15) ^ (r & 15)) >= K) voff = 0x80000000u;
+            }
             asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
-                         ::"v"(a_voff[it]), "s"(a_rsrc), "s"(m0), "s"(soff) : "memory", "m0");
+                         ::"v"(voff), "s"(a_rsrc), "s"(m0), "s"(soff) : "memory", "m0");
         }
     };
 
@@ -148,8 +170,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     dma(1, lds_a1);
     {
         const int r = tid % kRows;
-        const float* const from = (UP ? p.x_sums : p.h_sums) + static_cast<int64_t>(lds_row[r]) * (K / kStepK) + kb;
-        for (int g = tid / kRows; g < KT; g += kThreads / kRows) lds_x1[g * kRows + r] = from[g];
+        const float* const from = (UP ? p.x_sums : p.h_sums) + static_cast<int64_t>(lds_row[r]) * (K / G) + kb * GS;
+        for (int g = tid / kRows; g < KT * GS; g += kThreads / kRows)
+            lds_x1[g * kRows + r] = GS == 1 || kb * GS + g < K / G ? from[g] : 0.0f;
     }
 
     float16_t acc[2][2];
@@ -165,11 +188,24 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     __builtin_amdgcn_s_waitcnt(0);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    // code word f of a step's two columns as MFMA operands
-    auto convert = [&](const Regs& r, int f, bf16x8_t (&o)[2]) __attribute__((always_inline)) {
+    // code word f of a step's two columns as MFMA operands.  Groups of 32: an MFMA
+    // stays inside a tile, half h of the lanes taking its words 2 i + h; a swap of
+    // the halves turns the words 2 i and 2 i + 1 of both halves' tiles into those
+    // of the one and of the other.
+    auto convert = [&](Regs& r, int f, bf16x8_t (&o)[2]) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const uint32_t w = r.q[j][f >> 2][f & 3];
+            u32x4_t& q = r.q[j][f >> 2];
+            if constexpr (G == 32) {
+                if ((f & 3) < 2) {
+                    const int i = f & 1;
+                    const auto both = __builtin_amdgcn_permlane32_swap(q[2 * i], q[2 * i + 1], false, false);
+                    q[2 * i] = both[0];
+                    q[2 * i + 1] = both[1];
+                }
+            }
+            // (the first tile's words are now 0 and 2, the second's 1 and 3)
+            const uint32_t w = q[G == 32 ? 2 * (f & 1) + ((f >> 1) & 1) : f & 3];
             o[j] = __builtin_bit_cast(bf16x8_t, u32x4_t{nibble_pair_bf16(w, 0, bias), nibble_pair_bf16(w, 1, bias),
                                                         nibble_pair_bf16(w, 2, bias), nibble_pair_bf16(w, 3, bias)});
         }
@@ -178,18 +214,44 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     // the one before
     bf16x8_t b[2][2];
     convert(rr[0], 0, b[0]);
-    auto step = [&](int kt, const uint8_t* A, uint8_t* Ad, const Regs& cur, Regs& next) __attribute__((always_inline)) {
+    auto step = [&](int kt, const uint8_t* A, uint8_t* Ad, Regs& cur, Regs& next) __attribute__((always_inline)) {
         load_w(kt + 1, next);
         asm volatile("" ::: "memory");
         float16_t T[2][2];
         auto frag = [&](int i, int f) {
-            return *reinterpret_cast<const bf16x8_t*>(A + (32 * i + c) * 256 + 16 * ((8 * (f >> 2) + 4 * h + (f & 3)) ^ (c & 15)));
+            const int ch = G == 32 ? 2 * f + h : 8 * (f >> 2) + 4 * h + (f & 3);
+            return *reinterpret_cast<const bf16x8_t*>(A + (32 * i + c) * 256 + 16 * (ch ^ (c & 15)));
+        };
+        // group g's products into the sums.  Register e of lane (c, h): row 8 (e / 4)
+        // + 4 h + e % 4 of its block, column c
+        auto scale = [&](int g) __attribute__((always_inline)) {
+            float sc[2], zc[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                sc[j] = half_bits_to_float(cur.s[j][g]);
+                zc[j] = 128.0f + half_bits_to_float(cur.s[j][g] >> 16);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float4_t x1 = *reinterpret_cast<const float4_t*>(lds_x1 + (kt * GS + g) * kRows + 32 * i + 8 * r + 4 * h);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 4 * r; e < 4 * r + 4; ++e)
+                            acc[i][j][e] = fmaf(sc[j], fmaf(-zc[j], x1[e % 4], T[i][j][e]), acc[i][j][e]);
+                }
         };
         bf16x8_t a[2][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) a[0][i] = frag(i, 0);
 #pragma unroll
         for (int f = 0; f < 8; ++f) {
+            if (f > 0 && f % PER == 0) {
+                __builtin_amdgcn_sched_barrier(0);
+                scale(f / PER - 1);
+            }
             // A slot: the fragments of the next one are fetched and its code words
             // converted between this one's MFMAs.
             __builtin_amdgcn_sched_barrier(0);
@@ -205,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float16_t zero = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-                    T[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[f & 1][i], b[f & 1][j], f == 0 ? zero : T[i][j], 0, 0, 0);
+                    T[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[f & 1][i], b[f & 1][j], f % PER == 0 ? zero : T[i][j], 0, 0, 0);
                 }
             if (f < 7) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // LDS reads
 #pragma unroll
@@ -218,25 +280,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
         // (behind the use of the next step's first code words: the compiler's wait
         // for those, which does not know these loads, would wait for them as well)
         dma(kt + 2, Ad);
-        // register e of lane (c, h): row 8 (e / 4) + 4 h + e % 4 of its block, column c
-        float sc[2], zc[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            sc[j] = half_bits_to_float(cur.s[j]);
-            zc[j] = 128.0f + half_bits_to_float(cur.s[j] >> 16);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float4_t x1 = *reinterpret_cast<const float4_t*>(lds_x1 + kt * kRows + 32 * i + 8 * g + 4 * h);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 4 * g; e < 4 * g + 4; ++e)
-                        acc[i][j][e] = fmaf(sc[j], fmaf(-zc[j], x1[e % 4], T[i][j][e]), acc[i][j][e]);
-            }
-        }
+        scale(GS - 1);
         // the next step's activations are in LDS: all loads done but the last
         // step's and this one's weights and activations
         asm volatile("" ::: "memory");
@@ -284,11 +328,13 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
             const u32x4_t v = *reinterpret_cast<const u32x4_t*>(hl + r * 128 + 8 * ((4 * part + b) ^ (r & 15)));
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum += bf16_lo(v[e]) + bf16_hi(v[e]);
-            if (r < rows) *reinterpret_cast<u32x4_t*>(p.hi + static_cast<int64_t>(first + r) * N + n0 + 32 * part + 8 * b) = v;
+            if (r < rows && n0 + 32 * part < N) *reinterpret_cast<u32x4_t*>(p.hi + static_cast<int64_t>(first + r) * N + n0 + 32 * part + 8 * b) = v;
         }
-        sum += __shfl_xor(sum, 1, kWave);
-        sum += __shfl_xor(sum, 2, kWave);
-        if (r < rows && part == 0) p.h_sums[static_cast<int64_t>(first + r) * (N / 128) + n0 / 128] = sum;
+        // sums over the groups: one, two or four quarters
+        if constexpr (G >= 64) sum += __shfl_xor(sum, 1, kWave);
+        if constexpr (G >= 128) sum += __shfl_xor(sum, 2, kWave);
+        const int n = n0 + 32 * part;
+        if (r < rows && n < N && n % G == 0) p.h_sums[static_cast<int64_t>(first + r) * (N / G) + n / G] = sum;
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -308,16 +354,26 @@ __global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
 
 }  // namespace
 
-hipError_t launch_moe_tile(const MoeParams& p, bool up, int64_t tiles, hipStream_t stream) {
-    const int K = up ? p.H : p.I, N = up ? p.I : p.H, cols = up ? 128 : 256;
-    const int zs = up ? 1 : p.splits;
-    const int64_t grid = tiles * ((N + cols - 1) / cols) * zs;
-    const size_t lds = static_cast<size_t>((K / kStepK + zs - 1) / zs) * kRows * sizeof(float);
-    if (p.G != kStepK || K % kStepK != 0 || N % 128 != 0 || lds > 4 * kMoeTileSums || grid <= 0 || grid > 0x7FFFFFFF)
-        return hipErrorInvalidValue;
-    if (up) hipLaunchKernelGGL((moe_tile_kernel<true>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, stream, p);
-    else hipLaunchKernelGGL((moe_tile_kernel<false>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, stream, p);
+namespace {
+template <int G>
+hipError_t launch_tile_g(const MoeParams& p, bool up, unsigned grid, size_t lds, hipStream_t stream) {
+    if (up) hipLaunchKernelGGL((moe_tile_kernel<G, true>), dim3(grid), dim3(kThreads), lds, stream, p);
+    else hipLaunchKernelGGL((moe_tile_kernel<G, false>), dim3(grid), dim3(kThreads), lds, stream, p);
     return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_moe_tile(const MoeParams& p, bool up, int64_t tiles, hipStream_t stream) {
+    const int K = up ? p.H : p.I, N = up ? p.I : p.H, cols = up ? 128 : 256, zs = up ? 1 : p.splits;
+    const int64_t grid = tiles * ((N + cols - 1) / cols) * zs;
+    const int steps = (K + kStepK - 1) / kStepK;
+    const size_t lds = static_cast<size_t>((steps + zs - 1) / zs) * (kStepK / p.G) * kRows * sizeof(float);
+    if (N % 32 != 0 || lds > sizeof(float) * kMoeTileSums || grid <= 0 || grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    switch (p.G) {
+        case 32: return launch_tile_g<32>(p, up, static_cast<unsigned>(grid), lds, stream);
+        case 64: return launch_tile_g<64>(p, up, static_cast<unsigned>(grid), lds, stream);
+        default: return launch_tile_g<128>(p, up, static_cast<unsigned>(grid), lds, stream);
+    }
 }
 
 }  // namespace w4
