@@ -154,6 +154,28 @@ def lib():
     return L
 
 
+_call_path = os.path.join(HERE, "_w4call.so")
+_call = None
+
+
+def _short():
+    """The compiled way of the usual small calls (``csrc/pycall.cpp``), bound to the loaded library."""
+    global _call
+    if _call is None:
+        import importlib.util
+        if not os.path.exists(_call_path):
+            raise RuntimeError(f"W4 binding not built: {_call_path} is missing "
+                               "(run __graft_entry__.build() or python w4_dequant_gemm_amd/build.py)")
+        spec = importlib.util.spec_from_file_location("_w4call", _call_path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        names = ("w4a16_linear", "w4a8_linear", "w4_gemm_workspace_bytes", "w4a8_gemm_workspace_bytes", "w4_route",
+                 "w4_route_workspace_bytes", "w4a16_moe", "w4a16_moe_workspace_bytes", "w4_adjust_logits")
+        module.bind(*(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names))
+        _call = module
+    return _call
+
+
 def w4_status_string(status: int) -> str:
     return lib().w4_status_string(status).decode()
 
@@ -222,12 +244,12 @@ def _gpu(fn: str, t: torch.Tensor, name: str) -> int:
 
 # the current stream's handle as an integer, without building a Stream object
 # (about 2 us of host time per call otherwise, as much as a launch)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _stream(device, stream=None):
     if stream is None:
-        if _raw_stream is not None and device.index is not None:
+        if device.index is not None:
             return _raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream
@@ -555,6 +577,12 @@ def w4a16_linear(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *,
     """``w4a16_gemm`` with its epilogue: ``Y[M, N] = bf16(act(X . W'^T + bias) + residual)``.  ``bias`` is fp32 [N],
     ``act`` None, ``"silu"``, ``"gelu_tanh"``, ``"gelu"`` (erf) or ``"relu"``, ``residual`` bf16 [M, N] (may be ``Y``)."""
     fn = "w4a16_linear"
+    if Y is None and workspace is None and stream is None and act in _LINEAR_ACTS:
+        gpu = X.get_device()
+        if gpu >= 0 and gpu == _current_device():
+            r = (_call or _short()).linear(gpu, _raw_stream(gpu), X, wq, sz, G, bias, _LINEAR_ACTS[act], residual, 0)
+            if r is not None:
+                return r
     M, K, N = _linear_shapes(fn, X, wq, sz, G, Y)
     dev = X.device
     b, a, r = _epilogue_args(fn, M, N, bias, act, residual, X.get_device())
@@ -573,6 +601,12 @@ def w4a8_linear(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *, 
                 Y=None, xq=None, xscale=None, workspace=None, stream=None):
     """``w4a8_gemm`` with the epilogue of ``w4a16_linear``; returns (Y, xq, xscale)."""
     fn = "w4a8_linear"
+    if Y is None and xq is None and xscale is None and workspace is None and stream is None and act in _LINEAR_ACTS:
+        gpu = X.get_device()
+        if gpu >= 0 and gpu == _current_device():
+            r = (_call or _short()).linear(gpu, _raw_stream(gpu), X, wq, sz, G, bias, _LINEAR_ACTS[act], residual, 1)
+            if r is not None:
+                return r
     M, K, N = _linear_shapes(fn, X, wq, sz, G, Y, xq, xscale)
     dev = X.device
     b, a, r = _epilogue_args(fn, M, N, bias, act, residual, X.get_device())
@@ -709,6 +743,12 @@ def w4_route(X: torch.Tensor, router: torch.Tensor, top_k: int, *, score="softma
     weights fp32 [T, top_k]).  ``score`` is ``"softmax"`` or ``"sigmoid"``; ``bias`` (fp32 [E]) is added to the
     scores to choose but not to weigh."""
     fn = "w4_route"
+    if ids is None and weights is None and workspace is None and stream is None and score in _SCORES:
+        gpu = X.get_device()
+        if gpu >= 0 and gpu == _current_device():
+            r = (_call or _short()).route(gpu, _raw_stream(gpu), X, router, top_k, _SCORES[score], bias, renormalize, scale)
+            if r is not None:
+                return r
     xs, rs = X.shape, router.shape
     if len(xs) != 2 or len(rs) != 2 or xs[1] != rs[1]:
         raise ValueError(f"{fn}: X must be [T, H] and router [E, H], got {tuple(xs)} and {tuple(rs)}")
@@ -753,6 +793,13 @@ def w4a16_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: d
     experts: none) with ``weights`` (fp32).  ``gate``, ``up`` and ``down`` are GPU layouts of ``w4_prepack`` stacked
     over the experts (``wq`` [E, N, K/8], ``sz`` [E, N, K/G]).  Returns bf16 [T, H], ``residual`` (bf16 [T, H]) added."""
     fn = "w4a16_moe"
+    if Y is None and workspace is None and stream is None and act in _ACTS:
+        gpu = X.get_device()
+        if gpu >= 0 and gpu == _current_device():
+            r = (_call or _short()).moe(gpu, _raw_stream(gpu), X, ids, weights, gate["wq"], gate["sz"], up["wq"], up["sz"],
+                                        down["wq"], down["sz"], G, _ACTS[act], residual)
+            if r is not None:
+                return r
     xs, js, gs = X.shape, ids.shape, gate["wq"].shape
     if len(xs) != 2 or len(js) != 2 or js[0] != xs[0] or weights.shape != js:
         raise ValueError(f"{fn}: X must be [T, H], ids and weights [T, top_k], got {tuple(xs)}, {tuple(js)} and "
@@ -1011,6 +1058,13 @@ def w4_adjust_logits(logits: torch.Tensor, *, history=None, history_start=None, 
     ``mask``: int32 [B, ceil(V / 32)] or [1, ...] for all rows, a bit a token, 0 forbids it.  Returns ``out`` (new
     by default; ``out=logits`` works in place)."""
     fn = "w4_adjust_logits"
+    if out is None and stream is None:
+        gpu = logits.get_device()
+        if gpu >= 0 and gpu == _current_device():
+            r = (_call or _short()).adjust(gpu, _raw_stream(gpu), logits, history, history_start, prompt_len, repetition,
+                                           presence, frequency, bias_start, bias_ids, bias_values, mask)
+            if r is not None:
+                return r
     xp, f32, xs = _logits_arg(fn, logits, "logits")
     (B, V), dev, gpu = logits.shape, logits.device, _gpu(fn, logits, "logits")
     if out is None:

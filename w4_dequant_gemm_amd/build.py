@@ -19,6 +19,9 @@ OUT = os.path.join(HERE, "libw4.so")
 # measurement-only streaming-read kernel (bench.py), a library of its own
 PROBE_SRC = "probe_read.hip"
 PROBE_OUT = os.path.join(HERE, "libw4probe.so")
+# the Python binding's short way for small calls (CPython and torch headers)
+CALL_SRC = "pycall.cpp"
+CALL_OUT = os.path.join(HERE, "_w4call.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -49,6 +52,19 @@ def _run(cmd, verbose):
         print("\n".join(lines), flush=True)
 
 
+def _call_command(out: str) -> list:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    root = os.path.dirname(torch.__file__)
+    include = [x for d in (sysconfig.get_paths()["include"], *cpp_extension.include_paths()) for x in ("-isystem", d)]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *include, "-isystem", "/opt/rocm/include",
+            os.path.join(CSRC, CALL_SRC), f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-o", out]
+
+
 def build(verbose: bool = False, jobs: int = 8) -> str:
     os.makedirs(BUILD, exist_ok=True)
     jobs_list = []
@@ -65,10 +81,12 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
         jobs_list.append([HIPCC, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__",
                           "-I", os.path.join(ROOT, "include"), "-I", "/opt/rocm/include", "-c",
                           os.path.join(CSRC, host_src), "-o", obj])
+    jobs_list.append(_call_command(CALL_OUT + ".tmp"))
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
         for f in [ex.submit(_run, cmd, verbose) for cmd in jobs_list]:
             f.result()
-    objs = [cmd[-1] for cmd in jobs_list]
+    os.replace(CALL_OUT + ".tmp", CALL_OUT)
+    objs = [cmd[-1] for cmd in jobs_list[:-1]]
     tmp = OUT + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
     os.replace(tmp, OUT)
