@@ -51,11 +51,11 @@ __device__ __forceinline__ float quick_activation(int act, float x) {
     return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-y));
 }
 
-// Two workgroups a compute unit; one with groups of 64, where 256 registers a
-// lane leave 45 of them in memory (1391 rows on 5 experts of 2048 x 1024: 92 us
-// with two, 74 with one; groups of 32: 87 with two, 102 with one).
+// Two workgroups a compute unit: 256 registers a lane.  (One, with 512: 1999
+// tokens on 64 experts of 2048 x 1024, groups of 64, 370 us in place of 287;
+// 1391 rows on 5 experts, groups of 32, 102 in place of 87.)
 template <int G, bool UP>
-__global__ void __launch_bounds__(kThreads, G == 64 ? 1 : 2) moe_tile_kernel(MoeParams p) {
+__global__ void __launch_bounds__(kThreads, 2) moe_tile_kernel(MoeParams p) {
     constexpr int GS = kStepK / G, PER = 8 / GS;     // groups in a step, slots (MFMAs of a tile) in a group
     __shared__ __attribute__((aligned(16))) uint8_t lds_a0[kStage];
     __shared__ __attribute__((aligned(16))) uint8_t lds_a1[kStage];
@@ -241,6 +241,10 @@ __global__ void __launch_bounds__(kThreads, G == 64 ? 1 : 2) moe_tile_kernel(Moe
 #pragma unroll
                         for (int e = 4 * r; e < 4 * r + 4; ++e)
                             acc[i][j][e] = fmaf(sc[j], fmaf(-zc[j], x1[e % 4], T[i][j][e]), acc[i][j][e]);
+                    // (with groups of 64 the scheduler would fetch all the sums at
+                    // once, and 45 registers would have to go to memory)
+                    if constexpr (G == 64)
+                        if (r % 2 == 1) __builtin_amdgcn_sched_barrier(0);
                 }
         };
         bf16x8_t a[2][2];
