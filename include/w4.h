@@ -408,8 +408,8 @@ size_t w4_route_workspace_bytes(int64_t T, int64_t H, int64_t E);
  *   h_j  = w_j act(Wg'[e_j] . X[t]) * (Wu'[e_j] . X[t])
  *   Y[t] = bf16(residual[t] + sum_j Wd'[e_j] . h_j)
  * with W' = (q - z) s exact, fp32 accumulation, and h kept between the products as
- * the sum of two bf16 numbers (16 bits of mantissa), or, where 24 rows an expert
- * or more (T top_k >= 24 E, above 64) take the tiled kernels, rounded to bf16.  An id outside 0..E-1 is no
+ * the sum of two bf16 numbers (16 bits of mantissa), or, where 16 rows an expert
+ * or more (T top_k >= 16 E, above 64) take the tiled kernels, rounded to bf16.  An id outside 0..E-1 is no
  * expert (padding, or one that another process holds): its choice adds nothing,
  * and a token without any gets its residual (or zeros).  A token may choose an
  * expert twice.  Results do not depend on timing.

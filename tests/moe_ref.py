@@ -59,8 +59,8 @@ def moe(x, ids, weights, gate, up, down, act, residual=None):
         # |act'| < 1.13; the activation itself: eight roundings of at most |g|
         h = a * u
         dh = 1.13 * u.abs() * dg + a.abs() * du + 1.13 * dg * du + 8 * U * g.abs() * u.abs() + 3 * U * h.abs()
-        # h is kept as hi + lo, the rest of a rounding to bf16 rounded to bf16, or, from 24 rows an expert on, as bf16
-        dh = dh + (BF16 if ids.numel() > 64 and ids.numel() >= 24 * E else 2.0 ** -16) * (h.abs() + dh)
+        # h is kept as hi + lo, the rest of a rounding to bf16 rounded to bf16, or, from 16 rows an expert on, as bf16
+        dh = dh + (BF16 if ids.numel() > 64 and ids.numel() >= 16 * E else 2.0 ** -16) * (h.abs() + dh)
         for j in range(ids.shape[1]):
             w = share[:, j:j + 1]
             o, do = product(w * h, w.abs() * dh, down, e)

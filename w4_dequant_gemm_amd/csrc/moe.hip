@@ -5,13 +5,21 @@
 //
 // With few tokens an expert the layer is bound by streaming the chosen
 // experts' packed weights, as the W4A16 products of few rows are.  A slot is
-// a (token, choice) pair; the slots are first put in order of their expert, so
-// that an expert's weights are read once for all of its rows.
+// a (token, choice) pair; the slots are put in order of their expert, so that an
+// expert's weights are read once for all of its rows.  Three forms:
 //
-// A workgroup owns 16 columns of one expert's gate and up weights (or 16 FJ
-// columns of its down weight) and up to 16 MB of the expert's rows at a time;
-// its wk waves take every wk-th 128-k step.  Lane (c, q) loads the 16 bytes of
-// the 32-k tile 4 s + q of column c (1 KB contiguous in the blocked layout).
+// - one or two tokens: each slot by itself on dot products (moe_*_dot_kernel; one
+//   token, 8 of 64 experts of 2048 x 1024: 8.0 and 8.6 us, of which the
+//   weights' bytes are 5.5 together: launches and the chains of first reads);
+// - rows streamed past (moe_stream_kernel): a wave owns 16 columns of one
+//   expert's gate and up weight, or 32 of its down weight, and reads them once;
+//   the workgroup's waves multiply them by the same 16 MB rows, which lie in
+//   LDS.  Lane (c, q) loads the 16 bytes of the 32-k tile 4 s + q of column c
+//   (1 KB contiguous in the blocked layout).  24 tokens, 2 of 8 experts of
+//   4096 x 14336: 87 to 95 us for the 499 MB of gate and up (5.2 to 5.7 TB/s)
+//   and 51 to 59 for the 250 MB of down;
+// - from 16 rows an expert, tiles on the matrix cores (moe_tile.hip).
+//
 // The codes become the exact bf16 values 128 + u; with P the product with them
 // and x1 the sum of the activations over a group (an MFMA against ones),
 //   acc += s (P - (128 + z) x1)
@@ -21,10 +29,11 @@
 // transposed (two swaps of 32 lanes and two of 16), after which MFMA t takes
 // exactly tile t, quarter q the 8 k at 32 t + 8 q.
 //
-// h carries the token's weight w_j already.  It is kept as two bf16 numbers,
-// h = hi + lo (16 bits of mantissa), and the down product multiplies both: with
-// h rounded to bf16 once the result was 1.4 times as far from the exact one
-// as its own rounding to bf16 leaves it.
+// h carries the token's weight w_j already.  Where the weights' bytes bound the
+// down product it is kept as two bf16 numbers, h = hi + lo (16 bits of
+// mantissa), and the product multiplies both: with h rounded to bf16 once the
+// result is 1.4 times as far from the exact one as its own rounding to bf16
+// leaves it.  (The tiles, which the matrix cores bound, round it once.)
 #include "device.hpp"
 #include "moe_kernels.hpp"
 
@@ -452,7 +461,9 @@ __global__ void __launch_bounds__(512, 2) moe_stream_kernel(MoeParams p) {
     }
 }
 
-// One or two tokens: every slot by itself.  The matrix cores would multiply 16
+// One or two tokens: every slot by itself (against streaming, one token: 8 of 64
+// experts of 2048 x 1024 15.7 and 25.6 us, 2 of 8 of 576 x 1536 9.7 and 15.6;
+// two tokens: 30.7 and 31.0, 12.1 and 16.0).  The matrix cores would multiply 16
 // rows where there is one, and each wave would load every row 16 times over;
 // here the rows lie in LDS, each lane multiplies the 32 codes it loads by the 32
 // activations of its tile (v_dot2_f32_bf16 on the exact 128 + u), and the
@@ -763,8 +774,11 @@ hipError_t launch_dot(const MoeParams& p, hipStream_t stream) {
 }
 
 // The rows of an expert in tiles on the matrix cores (moe_tile.hip), where an
-// expert has enough of them.
-constexpr int64_t kTileFrom = 24;
+// expert has enough of them.  Tiles against streaming, 64 experts of 2048 x
+// 1024: 8 rows an expert 82 and 60 us, 16 rows 75 and 86, 32 rows 76 and 137;
+// groups of 64, 16 rows 91 and 97; 8 experts of 4096 x 14336: 15 rows 227 and
+// 227, 25 rows 215 and 270.
+constexpr int64_t kTileFrom = 16;
 int64_t tile_count(const MoeParams& p) {
     const int64_t slots = p.T * p.k;
     return slots / kMoeTileRows + (slots < p.E ? slots : p.E);
@@ -815,7 +829,9 @@ hipError_t launch_moe_g(const MoeParams& p, hipStream_t stream) {
         if (e != hipSuccess) return e;
     }
     // an expert's rows, were the choices even: 16 at a time, or 32 (each read of
-    // the weights then serves twice as many)
+    // the weights then serves twice as many; 8 experts of 4096 x 14336: 10 rows an
+    // expert 164 us with 16 at a time, 191 with 32, 15 rows 221 and 220, 20 rows
+    // 297 and 233; 64 experts of 2048 x 1024: 12 rows 79 and 81, 16 rows 90 and 83)
     const bool few = slots <= 12 * static_cast<int64_t>(p.E);
     e = few ? launch_stream<1, G, true>(p, stream) : launch_stream<2, G, true>(p, stream);
     if (e != hipSuccess) return e;
