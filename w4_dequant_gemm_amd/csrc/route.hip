@@ -118,46 +118,38 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, float (&
     }
 }
 
-// acc[j] += 16 tokens from t0 on times experts 16 j .. of `NB` blocks, the
-// wave's steps; register i of lane (c, h): token 4 h + i, expert c of its block
-template <int NB>
-__device__ __forceinline__ void logits16(const RouteParams& p, int64_t t0, int e0, int first, int steps, int wave, int wk, int lane,
-                                         float4_t (&acc)[NB]) {
+// 16 tokens from t0 on times 16 experts from e0 on, the wave's steps; register i
+// of lane (c, h): token 4 h + i, expert c
+__device__ __forceinline__ float4_t logits16(const RouteParams& p, int64_t t0, int e0, int first, int steps, int wave, int wk, int lane) {
     const int c = lane & 15, h = lane >> 4;
     const int64_t t = t0 + c < p.T ? t0 + c : p.T - 1;
+    const int e = e0 + c < p.E ? e0 + c : p.E - 1;
     const uint16_t* const x = p.X + t * p.H;
-    const uint16_t* r[NB];
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-        const int e = e0 + 16 * j + c < p.E ? e0 + 16 * j + c : p.E - 1;
-        r[j] = p.router + static_cast<int64_t>(e) * p.H;
-        acc[j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+    const uint16_t* const r = p.router + static_cast<int64_t>(e) * p.H;
+    float4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
     const u32x4_t zero = {0u, 0u, 0u, 0u};
     constexpr int AHEAD = 4;                        // steps in flight
     const int end = first + steps;
     for (int s0 = first + wave; s0 < end; s0 += AHEAD * wk) {
-        u32x4_t a[AHEAD], b[AHEAD][NB];
+        u32x4_t a[AHEAD], b[AHEAD];
 #pragma unroll
         for (int d = 0; d < AHEAD; ++d) {
             const int k = kStep * (s0 + d * wk) + 8 * h;
             const bool in = s0 + d * wk < end && k < p.H;   // (H is a multiple of 8)
             a[d] = *reinterpret_cast<const u32x4_t*>(x + (in ? k : 0));
-#pragma unroll
-            for (int j = 0; j < NB; ++j) b[d][j] = *reinterpret_cast<const u32x4_t*>(r[j] + (in ? k : 0));
+            b[d] = *reinterpret_cast<const u32x4_t*>(r + (in ? k : 0));
         }
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int d = 0; d < AHEAD; ++d) {
+            // (both zero past H: an infinity there would be NaN)
             const bool in = s0 + d * wk < end && kStep * (s0 + d * wk) + 8 * h < p.H;
-            const bf16x8_t av = __builtin_bit_cast(bf16x8_t, in ? a[d] : zero);
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-                // (both zero past H: an infinity there would be NaN)
-                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8_t, in ? b[d][j] : zero), acc[j], 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, in ? a[d] : zero),
+                                                          __builtin_bit_cast(bf16x8_t, in ? b[d] : zero), acc, 0, 0, 0);
         }
     }
+    return acc;
 }
 
 // at most 16 experts of 16 tokens, and the choice
@@ -166,10 +158,9 @@ __global__ void __launch_bounds__(1024) route_kernel(RouteParams p, int wk) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t0 = 16 * static_cast<int64_t>(blockIdx.x);
-    float4_t acc[1];
-    logits16<1>(p, t0, 0, 0, (p.H + kStep - 1) / kStep, wave, wk, lane, acc);
+    const float4_t acc = logits16(p, t0, 0, 0, (p.H + kStep - 1) / kStep, wave, wk, lane);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave][16 * (4 * (lane >> 4) + i) + (lane & 15)] = acc[0][i];
+    for (int i = 0; i < 4; ++i) red[wave][16 * (4 * (lane >> 4) + i) + (lane & 15)] = acc[i];
     __syncthreads();
     for (int t = wave; t < 16 && t0 + t < p.T; t += wk) {
         float l[1] = {0.0f};
@@ -187,10 +178,9 @@ __global__ void __launch_bounds__(1024) route_logits_kernel(RouteParams p, int w
     const int64_t t0 = 16 * static_cast<int64_t>(blockIdx.y);
     const int steps = (p.H + kStep - 1) / kStep, z = blockIdx.z;
     const int first = z * steps / p.splits;
-    float4_t acc[1];
-    logits16<1>(p, t0, e0, first, (z + 1) * steps / p.splits - first, wave, wk, lane, acc);
+    const float4_t acc = logits16(p, t0, e0, first, (z + 1) * steps / p.splits - first, wave, wk, lane);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave][16 * (4 * (lane >> 4) + i) + (lane & 15)] = acc[0][i];
+    for (int i = 0; i < 4; ++i) red[wave][16 * (4 * (lane >> 4) + i) + (lane & 15)] = acc[i];
     __syncthreads();
     for (int o = threadIdx.x; o < 256; o += blockDim.x) {
         float y = 0.0f;
