@@ -201,6 +201,9 @@ hipError_t launch_adjust_t(const AdjustParams& p, int slice, hipStream_t stream)
 // there can be to read it (3 rows of 131072 tokens with histories of 100000:
 // 12.0 us, 14.8 with 512 threads, 20 with slices of 1024).  With more, slices of
 // 4096 by 512 threads (200 rows: 37 us, 38 with 256 threads, 40 with 1024).
+// (Runs of slices in one workgroup, the first tokens of the history in registers
+// and the next slice's logits on their way: 39 us with two rounds of workgroups,
+// 47 to 51 with one.  The many short workgroups cover each other's waits better.)
 hipError_t launch_adjust(const AdjustParams& p, hipStream_t stream) {
     for (int slice = 512; slice <= 4096; slice *= 2)
         if (static_cast<int64_t>(p.B) * ((p.V + slice - 1) / slice) <= 256) return launch_adjust_t<1024>(p, slice, stream);
