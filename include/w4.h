@@ -359,7 +359,8 @@ int w4a8_gemm_e4m3(const uint8_t* xq, const float* xscale, int64_t M, int64_t K,
  * paths).
  *   bias       [N] fp32 or NULL.
  *   act        W4_ACT_NONE, _SILU, _GELU_TANH, _RELU or _GELU (the erf form).
- *   residual   [M, N] bf16, 16-byte aligned, or NULL; may be Y itself.
+ *   residual   [M, N] bf16, 16-byte aligned, or NULL; may be Y or X.
+ *   Y          [M, N] bf16 out, not X.
  *   Without any of the three the results are those of the plain products.
  *   Workspaces (w4_gemm_workspace_bytes, w4a8_gemm_workspace_bytes) and the other
  *   arguments as for those.

@@ -179,3 +179,19 @@ def test_adjust_then_sample():
     y = w4.w4_adjust_logits(x, mask=mask)
     tokens, probs = w4.w4_sample(y, torch.rand(3, device=dev()), temperature=torch.tensor([1.0, 1.0, 0.0], device=dev()))
     assert tokens.tolist() == [3207, -1, int(x[2].argmax())] and probs[0] == 1.0
+
+
+def test_adjust_between_the_rows_of_its_logits():
+    """Results in the same array, beside the logits of each row or behind all of them."""
+    require_gpu()
+    import torch
+    B, V = 4, 1001
+    d = _case(12, B, V, 100, 8)
+    wide = torch.randn((B, 2 * V), device=dev())
+    want = torch.from_numpy(_want(d, wide[:, :V].cpu().numpy()))
+    assert torch.equal(_run(d, wide[:, :V], out=wide[:, V:]).cpu(), want)
+    flat = torch.randn((2 * B, V), device=dev())
+    for first in (0, B):
+        x, out = flat[first:first + B], flat[B - first:2 * B - first]
+        want = torch.from_numpy(_want(d, x.cpu().numpy()))
+        assert torch.equal(_run(d, x, out=out).cpu(), want)

@@ -236,6 +236,37 @@ def test_workspace_as_long_as_asked(shape):
                 w4.w4a16_moe(x, ids, weights, *w, G, workspace=ws[:need - 1])
 
 
+def test_calls_of_two_threads():
+    """Each of two host threads on a stream of its own, at the same time: every result as by itself."""
+    require_gpu()
+    import threading
+
+    import torch
+    import w4_dequant_gemm_amd as w4
+    calls = [(what, call) for what, _, call in _all_calls(w4)]
+    want = [[t.clone() for t in call()] for _, call in calls]
+    torch.cuda.synchronize()
+    start, wrong = threading.Barrier(2), []
+
+    def run(backwards):
+        stream = torch.cuda.Stream()
+        start.wait()
+        with torch.cuda.stream(stream):
+            for _ in range(3):
+                got = {i: calls[i][1]() for i in (reversed(range(len(calls))) if backwards else range(len(calls)))}
+                stream.synchronize()
+                for i, r in got.items():
+                    wrong.extend(calls[i][0] for a, b in zip(r, want[i])
+                                 if not torch.equal(a.view(torch.uint8), b.view(torch.uint8)))
+
+    threads = [threading.Thread(target=run, args=(b,)) for b in (False, True)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_experts_behind_32_bits():
     """1024 experts of 4 MB of codes a matrix: the last ones lie past 2^32 bytes, and give what they give by
     themselves.  (All forms: their rules come out alike for 1024 and for 64 experts at these numbers of tokens.)"""

@@ -166,3 +166,25 @@ def test_binding_refusals():
             w4.w4a16_moe(**{**good, **bad})
     with pytest.raises(ValueError, match="logits"):
         w4.w4_adjust_logits(torch.zeros(2, 8))
+
+
+def test_results_on_their_inputs_are_refused(lib):
+    """A product's result in place of its activations, and logits that partly lie on their own results: refused.  (In
+    place of the logits, between their rows, and on the residual is allowed: tested where it runs.)"""
+    import w4_dequant_gemm_amd as w4
+    place = ctypes.c_void_p(0x2000)
+    for call in (lambda: lib.w4a16_linear(place, 2, 96, FAKE, FAKE, 96, 32, None, 0, place, place, None, 0, None),
+                 lambda: lib.w4a8_linear(place, 2, 96, FAKE, FAKE, 96, 32, None, 0, None, place, FAKE, FAKE, None, 0, None),
+                 lambda: lib.w4a8_linear_e4m3(place, FAKE, 2, 96, FAKE, FAKE, 96, 32, None, 0, None, place, None, 0, None)):
+        assert call() == 1 and "Y must not be X" in w4.w4_last_error()
+
+    def adjust(B, V, xs, os, shift, dtype=0):
+        size = 4 if dtype else 2
+        return lib.w4_adjust_logits(ctypes.c_void_p(0x100000), dtype, B, V, xs, None, 0, None, None, None, None, None, None, None,
+                                    None, 0, None, 0, ctypes.c_void_p(0x100000 + size * shift), os, None)
+
+    for dtype in (0, 1):
+        for a in ((1, 100, 100, 100, 1), (1, 100, 500, 100, 99), (1, 100, 100, 100, -99), (4, 100, 250, 250, 99),
+                  (4, 100, 250, 250, 151), (4, 100, 250, 250, 250), (4, 100, 250, 250, -250), (4, 100, 250, 250, 750),
+                  (4, 100, 250, 250, 849), (4, 100, 250, 250, -849), (3, 100, 100, 100, 200), (3, 100, 100, 100, -101)):
+            assert adjust(*a, dtype=dtype) == 1 and "overlaps" in w4.w4_last_error(), a

@@ -333,6 +333,11 @@ int check_epilogue(const char* fn, const Epilogue* epi) {
     if (epi->residual && !aligned16(epi->residual)) return fail(W4_EINVAL, "%s: residual is not 16-byte aligned", fn);
     return W4_OK;
 }
+// A residual may be Y, so X in Y's place is close at hand: workgroups would still
+// read what others have written.
+int check_place(const char* fn, const Epilogue* epi, const void* X, const void* Y) {
+    return epi && Y == X ? fail(W4_EINVAL, "%s: Y must not be X", fn) : W4_OK;
+}
 void set_epilogue(w4::MulParams& p, const Epilogue* epi) {
     // with nothing to do the plain kernels run
     if (!epi || (!epi->bias && epi->act == W4_ACT_NONE && !epi->residual)) return;
@@ -348,6 +353,7 @@ int w4a16_run(const char* fn, const uint16_t* X, int64_t M, int64_t K, const uin
     W4_TRY(check_epilogue(fn, epi));
     W4_TRY(mul_common(fn, X, M, K, wq, sz, N, G, Y, workspace, workspace_bytes, false));
     if (M == 0 || N == 0) return W4_OK;
+    W4_TRY(check_place(fn, epi, X, Y));
     w4::MulParams p{X, nullptr, M, K, N, G, wq, sz, Y, false};
     set_epilogue(p, epi);
     if (!w4a16_tiled(M, K, N, workspace, workspace_bytes))
@@ -361,6 +367,7 @@ int w4a8_run(const char* fn, const uint16_t* X, int64_t M, int64_t K, const uint
     W4_TRY(check_epilogue(fn, epi));
     W4_TRY(mul_common(fn, X, M, K, wq, sz, N, G, Y, workspace, workspace_bytes, true));
     if (M == 0 || N == 0) return W4_OK;
+    W4_TRY(check_place(fn, epi, X, Y));
     W4_REQUIRE_PTR(fn, xq);
     if (!xscale) return fail(W4_EINVAL, "%s: xscale is NULL", fn);
     if (w4::skinny_quantizes_rows(M, K)) {
@@ -393,6 +400,7 @@ int w4a8_e4m3_run(const char* fn, const uint8_t* xq, const float* xscale, int64_
     W4_TRY(mul_common(fn, reinterpret_cast<const uint16_t*>(xq), M, K, wq, sz, N, G, Y, workspace, workspace_bytes,
                       true));
     if (M == 0 || N == 0) return W4_OK;
+    W4_TRY(check_place(fn, epi, xq, Y));
     if (K % 16 != 0) return fail(W4_EINVAL, "%s: K = %lld must be a multiple of 16", fn, static_cast<long long>(K));
     if (!xscale) return fail(W4_EINVAL, "%s: xscale is NULL", fn);
     w4::MulParams p{xq, xscale, M, K, N, G, wq, sz, Y, true};

@@ -231,6 +231,16 @@ int w4_adjust_logits(const void* logits, int dtype, int64_t B, int64_t V, int64_
     const uintptr_t size = dtype == W4_LOGITS_F32 ? 4 : 2;
     if (reinterpret_cast<uintptr_t>(logits) % size != 0 || reinterpret_cast<uintptr_t>(out) % size != 0)
         return fail(W4_EINVAL, "%s: logits or out is not aligned to its elements", fn);
+    // (rows equally far apart: whether some row of out meets another place of the logits)
+    if (logits != out && (row_stride == out_stride || B == 1)) {
+        const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(logits)) /
+                          static_cast<int64_t>(size);
+        for (int64_t m = d / out_stride - 1; m <= d / out_stride + 1; ++m) {
+            const int64_t apart = d - m * out_stride;
+            if (m > -B && m < B && apart < V && apart > -V)
+                return fail(W4_EINVAL, "%s: out overlaps the logits without being them", fn);
+        }
+    }
     if (logits == out && row_stride != out_stride && B > 1)
         return fail(W4_EINVAL, "%s: in place, the rows of logits and out must be equally far apart", fn);
     if (history && !history_start) return fail(W4_EINVAL, "%s: history without history_start", fn);
