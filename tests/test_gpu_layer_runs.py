@@ -31,7 +31,7 @@ class _Absent:
 # tokens, choices, experts, hidden, inner, group: dot products; rows of one pass with the lists in it; with lists of
 # their own; two passes' rows; tiles with each group size, and with the down product's k split
 MOE = [(1, 2, 8, 256, 384, 32), (2, 8, 16, 512, 256, 128), (12, 4, 4, 256, 1024, 64), (30, 8, 64, 256, 256, 128),
-       (40, 4, 12, 256, 2048, 128), (200, 4, 6, 256, 256, 32), (200, 4, 6, 256, 512, 64), (90, 3, 3, 256, 4096, 128)]
+       (52, 2, 8, 128, 4352, 128), (200, 4, 6, 256, 256, 32), (200, 4, 6, 256, 512, 64), (90, 3, 3, 256, 4096, 128)]
 
 
 def _moe_calls(w4, seed, T, k, E, H, I, G):

@@ -36,8 +36,9 @@ def _check(got, want, bound, what):
     (500, 6, 16, 384, 256, 128), (2, 32, 32, 128, 128, 128), (1, 1, 1, 32, 32, 32), (64, 1, 64, 256, 128, 64),
     (16, 8, 40, 256, 256, 128), (9, 8, 16, 160, 224, 32), (2, 8, 64, 512, 320, 64), (1, 2, 4, 256, 14336, 128), (2, 4, 9, 8192, 96, 32),
     (32, 2, 70, 256, 128, 128),
-    # 32 rows at a time
-    (14, 4, 4, 96, 160, 32), (60, 2, 9, 256, 384, 128), (45, 3, 10, 288, 320, 32), (42, 2, 6, 320, 192, 64),
+    # 32 rows at a time (many columns), and 16 in turn or beside each other
+    (52, 2, 8, 64, 4352, 32), (52, 2, 8, 64, 4352, 64), (52, 2, 8, 128, 4352, 128), (14, 4, 4, 64, 8320, 32),
+    (40, 2, 8, 128, 4352, 128), (14, 4, 4, 96, 160, 32), (60, 2, 9, 256, 384, 128), (45, 3, 10, 288, 320, 32), (42, 2, 6, 320, 192, 64),
     # rows in tiles: ragged, one tile and several an expert, columns past the last tile's, long inner sums
     (100, 2, 4, 128, 128, 128), (200, 6, 16, 384, 640, 128), (700, 4, 32, 640, 256, 128), (90, 3, 3, 256, 4096, 128),
     (65, 1, 1, 4096, 256, 128), (1000, 8, 64, 256, 384, 128),

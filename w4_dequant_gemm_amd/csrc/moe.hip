@@ -275,9 +275,10 @@ __device__ __forceinline__ void store_h(const MoeParams& p, int64_t at, float h)
 // global memory into LDS a piece of CS steps ahead (waves that split the k
 // instead read the rows from L2 for every 32 columns anew, four times the bytes
 // of the weights: 8 experts of 14336 x 4096, 24 tokens, down product 78 us).
-// With blockIdx.z the down product's k are split over workgroups.
+// With blockIdx.z an expert's blocks of 16 MB rows are dealt out to `rs`
+// workgroups, and the down product's k are split over others.
 template <int MB, int G, bool UP, bool SCAN>
-__global__ void __launch_bounds__(512, 2) moe_stream_kernel(MoeParams p) {
+__global__ void __launch_bounds__(512, 2) moe_stream_kernel(MoeParams p, int rs) {
     static_assert(UP || !SCAN, "the lists are made by then");
     constexpr int FJ = 2, NG = kStepK / G;
     constexpr int AP = UP ? 1 : 2;                 // parts of an activation
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(512, 2) moe_stream_kernel(MoeParams p) {
     if constexpr (SCAN) {
         const int slots = static_cast<int>(p.T * p.k);
         if (blockIdx.y == gridDim.y - 1) {
-            if (blockIdx.x > 0) return;
+            if (blockIdx.x > 0 || blockIdx.z > 0) return;
             __shared__ RunMem mem;
             build_runs<false>(p, mem, tid, blockDim.x);
             return;
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(512, 2) moe_stream_kernel(MoeParams p) {
     }
     const int K = UP ? p.H : p.I, N = UP ? p.I : p.H;
     const int KS = (K + kStepK - 1) / kStepK;
-    const int z = blockIdx.z, zs = gridDim.z;
+    const int z = blockIdx.z / rs, zs = gridDim.z / rs;
     const int first = z * KS / zs, n = (z + 1) * KS / zs - first;    // the workgroup's steps
     const int n0 = COLS * (blockIdx.x * waves + wave);
     const int64_t words = static_cast<int64_t>(N) * (K / 8), groups = static_cast<int64_t>(N) * (K / G);
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(512, 2) moe_stream_kernel(MoeParams p) {
     StepB<FJ, G> b[DEPTH];
     auto load = [&](int i, int d) { load_b<FJ, G>(b[d], wb, sb, first + i, K, c, q); };
 
-    for (int m0 = 0; m0 < rows; m0 += RM) {
+    for (int m0 = RM * (blockIdx.z % rs); m0 < rows; m0 += RM * rs) {
         const int some = rows - m0 < RM ? rows - m0 : RM;
         // the first steps' weights need no list; the rows of m0 in LDS
 #pragma unroll
@@ -736,20 +737,21 @@ int stream_waves(int64_t columns, int per_wave, int64_t experts) {
     return w;
 }
 template <int MB, int G, bool UP>
-hipError_t launch_stream(const MoeParams& p, hipStream_t stream) {
+hipError_t launch_stream(const MoeParams& p, int rs, hipStream_t stream) {
     const int N = UP ? p.I : p.H, per = UP ? 16 : 32;
     const int64_t slots = p.T * p.k, experts = slots < p.E ? slots : p.E;
-    const int w = stream_waves(N, per, experts * (UP ? 1 : p.splits));
-    dim3 grid(static_cast<unsigned>((N + w * per - 1) / (w * per)), static_cast<unsigned>(experts), UP ? 1u : static_cast<unsigned>(p.splits));
+    const int w = stream_waves(N, per, experts * rs * (UP ? 1 : p.splits));
+    dim3 grid(static_cast<unsigned>((N + w * per - 1) / (w * per)), static_cast<unsigned>(experts),
+              static_cast<unsigned>(rs * (UP ? 1 : p.splits)));
     const dim3 block(static_cast<unsigned>(64 * w));
     if constexpr (UP) {
         if (slots <= kWave) {
             grid.y += 1;
-            hipLaunchKernelGGL((moe_stream_kernel<MB, G, true, true>), grid, block, 0, stream, p);
+            hipLaunchKernelGGL((moe_stream_kernel<MB, G, true, true>), grid, block, 0, stream, p, rs);
             return hipGetLastError();
         }
     }
-    hipLaunchKernelGGL((moe_stream_kernel<MB, G, UP, false>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((moe_stream_kernel<MB, G, UP, false>), grid, block, 0, stream, p, rs);
     return hipGetLastError();
 }
 
@@ -832,10 +834,20 @@ hipError_t launch_moe_g(const MoeParams& p, hipStream_t stream) {
     // the weights then serves twice as many; 8 experts of 4096 x 14336: 10 rows an
     // expert 164 us with 16 at a time, 191 with 32, 15 rows 221 and 220, 20 rows
     // 297 and 233; 64 experts of 2048 x 1024: 12 rows 79 and 81, 16 rows 90 and 83)
-    const bool few = slots <= 12 * static_cast<int64_t>(p.E);
-    e = few ? launch_stream<1, G, true>(p, stream) : launch_stream<2, G, true>(p, stream);
+    // Where gate and up have fewer waves than two a SIMD, 16 rows at a time, the
+    // next ones in workgroups beside them: the time is then that of one wave's
+    // steps, not of the weights' bytes (51 tokens, 3 of 12 experts of 2048 x 768,
+    // groups of 32: 43 us in place of 76; 150 tokens, 2 of 24, groups of 128: 36
+    // in place of 46).  One workgroup for each 8 rows of the mean, since the
+    // choices are not even.
+    const int64_t experts = slots < p.E ? slots : p.E;
+    const bool narrow = experts * (p.I / 16) <= 2048;
+    const bool few = narrow || slots <= 12 * static_cast<int64_t>(p.E);
+    const int64_t rows = (slots + 8 * p.E - 1) / (8 * p.E);
+    const int rs = !narrow ? 1 : (rows > 4 ? 4 : static_cast<int>(rows));
+    e = few ? launch_stream<1, G, true>(p, rs, stream) : launch_stream<2, G, true>(p, rs, stream);
     if (e != hipSuccess) return e;
-    e = few ? launch_stream<1, G, false>(p, stream) : launch_stream<2, G, false>(p, stream);
+    e = few ? launch_stream<1, G, false>(p, rs, stream) : launch_stream<2, G, false>(p, rs, stream);
     if (e != hipSuccess) return e;
     return launch_join(p, stream);
 }
