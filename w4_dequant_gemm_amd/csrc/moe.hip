@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(512, 2) moe_stream_kernel(MoeParams p, int rs)
     // waits (four of each: 138 registers and 64 KB of LDS, one workgroup, down
     // products 5 to 10 us slower)
     constexpr int DEPTH = 2;
-    constexpr int CS = MB * AP <= 4 ? 2 : 1;
+    constexpr int CS = 2;
     constexpr int ROW = CS * kStepK * 2;           // its bytes in a row
     constexpr int RPD = 1024 / ROW;                // rows of a load to LDS
     constexpr int LOADS = FJ * (1 + NG);           // loads of one
