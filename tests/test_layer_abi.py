@@ -188,3 +188,43 @@ def test_results_on_their_inputs_are_refused(lib):
                   (4, 100, 250, 250, 151), (4, 100, 250, 250, 250), (4, 100, 250, 250, -250), (4, 100, 250, 250, 750),
                   (4, 100, 250, 250, 849), (4, 100, 250, 250, -849), (3, 100, 100, 100, 200), (3, 100, 100, 100, -101)):
             assert adjust(*a, dtype=dtype) == 1 and "overlaps" in w4.w4_last_error(), a
+
+
+def test_logits_of_one_row_or_other_strides_on_their_results_are_refused(lib):
+    """One row of logits for all, or rows of logits and results not equally far apart: refused where any row of the
+    results shares an element with one of the logits, against a list of the elements."""
+    import random
+
+    import w4_dequant_gemm_amd as w4
+    base = 0x100000
+
+    def refused(B, V, xs, os, shift, dtype):
+        # (a length of no array is refused behind the overlap, so nothing runs on these addresses)
+        size = 4 if dtype else 2
+        assert lib.w4_adjust_logits(ctypes.c_void_p(base), dtype, B, V, xs, None, 0, None, None, None, None, None, None, None,
+                                    None, 1, None, 0, ctypes.c_void_p(base + size * shift), os, None) == 1
+        assert "overlaps" in w4.w4_last_error() or "bias_len" in w4.w4_last_error()
+        return "overlaps" in w4.w4_last_error()
+
+    def meets(B, V, xs, os, shift):
+        given = {i * xs + v for i in range(B) for v in range(V)}
+        return any(shift + j * os + v in given for j in range(B) for v in range(V))
+
+    # the second of the results' rows is the logits' one row; rows 100 apart against rows 130 apart
+    for a in ((3, 100, 0, 100, -100), (3, 100, 0, 100, 99), (3, 100, 0, 250, -599), (3, 100, 130, 100, -150), (3, 100, 130, 100, 100),
+              (2, 100, 100, 400, -301), (2, 100, 400, 100, 301)):
+        assert meets(*a), a
+        for dtype in (0, 1):
+            assert refused(*a, dtype), a
+    rng = random.Random(3)
+    both = [0, 0]
+    for _ in range(400):
+        B, V = rng.randint(1, 6), rng.randint(1, 9)
+        xs, os = rng.choice([0, V + rng.randint(0, 30)]), V + rng.randint(0, 30)
+        shift = rng.randint(-200, 200)
+        if shift == 0:
+            continue
+        met = meets(B, V, xs, os, shift)
+        both[met] += 1
+        assert refused(B, V, xs, os, shift, 1) == met, (B, V, xs, os, shift)
+    assert min(both) > 40

@@ -69,6 +69,25 @@ bool attention_sizes_ok(int64_t T, int64_t B, int hq, int hk, int64_t max_q, int
 }
 }  // namespace
 
+namespace {
+// Whether one of B rows of V elements, `os` apart and from `d` on, shares an
+// element with one of B rows from 0 on, `xs` apart (0: one row).
+bool rows_meet(int64_t d, int64_t B, int64_t V, int64_t xs, int64_t os) {
+    // equally far apart, a row meets those that lie as many rows on as the first one does
+    const bool alike = xs == os;
+    const int64_t rows = alike || xs == 0 ? 1 : B;
+    for (int64_t i = 0; i < rows; ++i) {
+        // rows j with |d + j os - i xs| < V: at most two, beside the quotient
+        const int64_t from = i * xs - d, q = from / os;
+        for (int64_t j = q - 1; j <= q + 1; ++j) {
+            const int64_t apart = j * os - from;
+            if (j > (alike ? -B : -1) && j < B && apart < V && apart > -V) return true;
+        }
+    }
+    return false;
+}
+}  // namespace
+
 extern "C" {
 
 int w4_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
@@ -231,16 +250,10 @@ int w4_adjust_logits(const void* logits, int dtype, int64_t B, int64_t V, int64_
     const uintptr_t size = dtype == W4_LOGITS_F32 ? 4 : 2;
     if (reinterpret_cast<uintptr_t>(logits) % size != 0 || reinterpret_cast<uintptr_t>(out) % size != 0)
         return fail(W4_EINVAL, "%s: logits or out is not aligned to its elements", fn);
-    // (rows equally far apart: whether some row of out meets another place of the logits)
-    if (logits != out && (row_stride == out_stride || B == 1)) {
-        const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(logits)) /
-                          static_cast<int64_t>(size);
-        for (int64_t m = d / out_stride - 1; m <= d / out_stride + 1; ++m) {
-            const int64_t apart = d - m * out_stride;
-            if (m > -B && m < B && apart < V && apart > -V)
-                return fail(W4_EINVAL, "%s: out overlaps the logits without being them", fn);
-        }
-    }
+    if (logits != out &&
+        rows_meet(static_cast<int64_t>(reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(logits)) / static_cast<int64_t>(size), B, V,
+                  row_stride, out_stride))
+        return fail(W4_EINVAL, "%s: out overlaps the logits without being them", fn);
     if (logits == out && row_stride != out_stride && B > 1)
         return fail(W4_EINVAL, "%s: in place, the rows of logits and out must be equally far apart", fn);
     if (history && !history_start) return fail(W4_EINVAL, "%s: history without history_start", fn);
