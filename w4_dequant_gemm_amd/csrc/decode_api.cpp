@@ -73,6 +73,8 @@ namespace {
 // Whether one of B rows of V elements, `os` apart and from `d` on, shares an
 // element with one of B rows from 0 on, `xs` apart (0: one row).
 bool rows_meet(int64_t d, int64_t B, int64_t V, int64_t xs, int64_t os) {
+    // (mostly the rows of one all lie behind those of the other)
+    if (d >= (B - 1) * xs + V || -d >= (B - 1) * os + V) return false;
     // equally far apart, a row meets those that lie as many rows on as the first one does
     const bool alike = xs == os;
     const int64_t rows = alike || xs == 0 ? 1 : B;
