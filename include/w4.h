@@ -360,7 +360,9 @@ int w4a8_gemm_e4m3(const uint8_t* xq, const float* xscale, int64_t M, int64_t K,
  *   bias       [N] fp32 or NULL.
  *   act        W4_ACT_NONE, _SILU, _GELU_TANH, _RELU or _GELU (the erf form).
  *   residual   [M, N] bf16, 16-byte aligned, or NULL; may be Y or X.
- *   Y          [M, N] bf16 out, not X.
+ *   Y          [M, N] bf16 out; shares no byte with X or the bias, and none with
+ *              the residual unless it is the residual.  The codes and scales of
+ *              w4a8_linear share none with any of these or each other.
  *   Without any of the three the results are those of the plain products.
  *   Workspaces (w4_gemm_workspace_bytes, w4a8_gemm_workspace_bytes) and the other
  *   arguments as for those.

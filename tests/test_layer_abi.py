@@ -228,3 +228,43 @@ def test_logits_of_one_row_or_other_strides_on_their_results_are_refused(lib):
         both[met] += 1
         assert refused(B, V, xs, os, shift, 1) == met, (B, V, xs, os, shift)
     assert min(both) > 40
+
+
+def test_products_whose_results_overlap_their_inputs_are_refused(lib):
+    """Y on a part of X or of the residual, and codes or scales on a part of X, Y, the residual or each other."""
+    import w4_dequant_gemm_amd as w4
+    M, K, N, G = 4, 96, 64, 32
+    at = lambda a: ctypes.c_void_p(a)                                       # noqa: E731
+    # places far apart: X 4 x 96 x 2 bytes = 768, Y and the residual 512, codes 384, scales 16
+    far = dict(X=0x10000, res=0x20000, Y=0x30000, xq=0x40000, xs=0x50000)
+
+    def a16(X, res, Y, xq, xs):
+        return lib.w4a16_linear(at(X), M, K, FAKE, FAKE, N, G, None, 1, at(res), at(Y), None, 0, None)
+
+    def a8(X, res, Y, xq, xs):
+        return lib.w4a8_linear(at(X), M, K, FAKE, FAKE, N, G, None, 1, at(res), at(Y), at(xq), at(xs), None, 0, None)
+
+    def e4m3(X, res, Y, xq, xs):
+        return lib.w4a8_linear_e4m3(at(X), at(xs), M, K, FAKE, FAKE, N, G, None, 1, at(res), at(Y), None, 0, None)
+
+    def refused(call, text, **places):
+        assert call(**{**far, **places}) == 1 and text in w4.w4_last_error(), (places, w4.w4_last_error())
+
+    for call, x_bytes in ((a16, 768), (a8, 768), (e4m3, 384)):
+        for shift in (16, x_bytes - 16, -16, 16 - 512):
+            refused(call, "Y overlaps X", Y=far["X"] + shift)
+        for shift in (16, 512 - 16, -16, 16 - 512):
+            refused(call, "Y overlaps the residual", Y=far["res"] + shift)
+        refused(call, "Y must not be X", Y=far["X"], res=far["X"])
+    for name, text, n in (("X", "X", 768), ("Y", "Y", 512), ("res", "the residual", 512)):
+        for shift in (16, n - 16, 16 - 384):
+            refused(a8, f"xq overlaps {text}", xq=far[name] + shift)
+        refused(a8, f"xq must not be {text}", xq=far[name])
+        for shift in (4, n - 4, -12):
+            refused(a8, f"xscale overlaps {text}", xs=far[name] + shift)
+    refused(a8, "xscale overlaps xq", xs=far["xq"] + 380)
+    refused(a8, "xscale overlaps xq", xs=far["xq"] - 12)
+    # the bias, which all rows read, and the scales of ready codes
+    for shift in (0, 16, -16):
+        assert lib.w4a16_linear(at(far["X"]), M, K, FAKE, FAKE, N, G, at(far["Y"] - shift), 1, None, at(far["Y"]), None, 0, None) == 1
+        refused(e4m3, "xscale", xs=far["Y"] + max(shift, 0))

@@ -334,9 +334,27 @@ int check_epilogue(const char* fn, const Epilogue* epi) {
     return W4_OK;
 }
 // A residual may be Y, so X in Y's place is close at hand: workgroups would still
-// read what others have written.
-int check_place(const char* fn, const Epilogue* epi, const void* X, const void* Y) {
-    return epi && Y == X ? fail(W4_EINVAL, "%s: Y must not be X", fn) : W4_OK;
+// read what others have written.  The same holds where Y lies on a part of X, on
+// a part of the residual, or on the bias; `size` is that of X's elements.
+int check_place(const char* fn, const Epilogue* epi, const void* X, int64_t M, int64_t K, int64_t size, const void* Y, int64_t N) {
+    if (!epi) return W4_OK;
+    const w4::Span y = w4::span(Y, M, N, 2, "Y");
+    W4_TRY(w4::check_apart(fn, y, w4::span(X, M, K, size, "X")));
+    W4_TRY(w4::check_apart(fn, y, w4::span(epi->bias, N, 1, 4, "the bias")));
+    return epi->residual == Y ? W4_OK : w4::check_apart(fn, y, w4::span(epi->residual, M, N, 2, "the residual"));
+}
+// The row quantizer writes codes and scales while others of its workgroups read X,
+// and the product reads them while it writes Y.
+int check_codes_place(const char* fn, const Epilogue* epi, const void* X, int64_t M, int64_t K, const void* xq, const void* xscale,
+                      const void* Y, int64_t N) {
+    if (!epi) return W4_OK;
+    const w4::Span q = w4::span(xq, M, K, 1, "xq"), s = w4::span(xscale, M, 1, 4, "xscale");
+    W4_TRY(w4::check_apart(fn, s, q));
+    for (const w4::Span& in : {w4::span(X, M, K, 2, "X"), w4::span(Y, M, N, 2, "Y"), w4::span(epi->residual, M, N, 2, "the residual")}) {
+        W4_TRY(w4::check_apart(fn, q, in));
+        W4_TRY(w4::check_apart(fn, s, in));
+    }
+    return W4_OK;
 }
 void set_epilogue(w4::MulParams& p, const Epilogue* epi) {
     // with nothing to do the plain kernels run
@@ -353,7 +371,7 @@ int w4a16_run(const char* fn, const uint16_t* X, int64_t M, int64_t K, const uin
     W4_TRY(check_epilogue(fn, epi));
     W4_TRY(mul_common(fn, X, M, K, wq, sz, N, G, Y, workspace, workspace_bytes, false));
     if (M == 0 || N == 0) return W4_OK;
-    W4_TRY(check_place(fn, epi, X, Y));
+    W4_TRY(check_place(fn, epi, X, M, K, 2, Y, N));
     w4::MulParams p{X, nullptr, M, K, N, G, wq, sz, Y, false};
     set_epilogue(p, epi);
     if (!w4a16_tiled(M, K, N, workspace, workspace_bytes))
@@ -367,9 +385,10 @@ int w4a8_run(const char* fn, const uint16_t* X, int64_t M, int64_t K, const uint
     W4_TRY(check_epilogue(fn, epi));
     W4_TRY(mul_common(fn, X, M, K, wq, sz, N, G, Y, workspace, workspace_bytes, true));
     if (M == 0 || N == 0) return W4_OK;
-    W4_TRY(check_place(fn, epi, X, Y));
+    W4_TRY(check_place(fn, epi, X, M, K, 2, Y, N));
     W4_REQUIRE_PTR(fn, xq);
     if (!xscale) return fail(W4_EINVAL, "%s: xscale is NULL", fn);
+    W4_TRY(check_codes_place(fn, epi, X, M, K, xq, xscale, Y, N));
     if (w4::skinny_quantizes_rows(M, K)) {
         // one kernel: row quantization (same arithmetic) and product
         w4::MulParams p{X, nullptr, M, K, N, G, wq, sz, Y, true, xq, xscale};
@@ -400,9 +419,10 @@ int w4a8_e4m3_run(const char* fn, const uint8_t* xq, const float* xscale, int64_
     W4_TRY(mul_common(fn, reinterpret_cast<const uint16_t*>(xq), M, K, wq, sz, N, G, Y, workspace, workspace_bytes,
                       true));
     if (M == 0 || N == 0) return W4_OK;
-    W4_TRY(check_place(fn, epi, xq, Y));
+    W4_TRY(check_place(fn, epi, xq, M, K, 1, Y, N));
     if (K % 16 != 0) return fail(W4_EINVAL, "%s: K = %lld must be a multiple of 16", fn, static_cast<long long>(K));
     if (!xscale) return fail(W4_EINVAL, "%s: xscale is NULL", fn);
+    if (epi) W4_TRY(w4::check_apart(fn, w4::span(Y, M, N, 2, "Y"), w4::span(xscale, M, 1, 4, "xscale")));
     w4::MulParams p{xq, xscale, M, K, N, G, wq, sz, Y, true};
     set_epilogue(p, epi);
     if (M <= w4::kSkinnyMaxM && !f8_product(M, K, N, G))
