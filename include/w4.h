@@ -422,9 +422,11 @@ size_t w4_route_workspace_bytes(int64_t T, int64_t H, int64_t E);
  *              weights.  H and I are multiples of G = 32, 64 or 128.
  *   act        W4_ACT_SILU or W4_ACT_GELU_TANH.
  *   residual   [T, H] bf16 or NULL; may be X or Y.
- *   Y          [T, H] bf16 out, not X.
+ *   Y          [T, H] bf16 out; shares no byte with X, ids or weights, and none with
+ *              the residual unless it is the residual.
  *   workspace  w4a16_moe_workspace_bytes bytes, 16-byte aligned, its contents
- *              irrelevant; calls in flight together need separate ones.
+ *              irrelevant, apart from all of these; calls in flight together need
+ *              separate ones.
  */
 int w4a16_moe(const uint16_t* X, int64_t T, int64_t H, const int32_t* ids, const float* weights, int top_k,
               const uint32_t* wq_gate, const uint32_t* sz_gate, const uint32_t* wq_up, const uint32_t* sz_up,

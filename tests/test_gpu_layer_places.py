@@ -48,3 +48,26 @@ def test_linear_beside_its_inputs(M):
     # in place of the residual, which is the activations' neighbour
     a, b = _beside(x, res)
     assert torch.equal(w4.w4a16_linear(a, wq, sz, G, bias=bias, act="silu", residual=b, Y=b), want)
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 200])
+def test_experts_beside_their_inputs(T):
+    require_gpu()
+    import torch
+    import w4_dequant_gemm_amd as w4
+    g = torch.Generator(device=dev()).manual_seed(T)
+    k, E, H, I, G = 4, 6, 256, 128, 64
+    w = [ref.experts(g, E, n, kk, G, dev()) for n, kk in ((I, H), (I, H), (H, I))]
+    x, res = (torch.randn((T, H), generator=g, device=dev()).to(torch.bfloat16) for _ in range(2))
+    ids = torch.randint(0, E, (T, k), generator=g, device=dev(), dtype=torch.int32)
+    weights = torch.rand((T, k), generator=g, device=dev())
+    want = w4.w4a16_moe(x, ids, weights, *w, G, residual=res)
+    need = (w4.w4a16_moe_workspace_bytes(T, k, E, H, I, G) + 15) // 16 * 16
+    for order in ("xyriws", "swiryx", "iysxwr"):
+        made = {"x": x, "y": torch.zeros_like(x), "r": res, "i": ids, "w": weights,
+                "s": torch.zeros(need, dtype=torch.uint8, device=dev())}
+        v = dict(zip(order, _beside(*(made[c] for c in order))))
+        got = w4.w4a16_moe(v["x"], v["i"], v["w"], *w, G, residual=v["r"], Y=v["y"], workspace=v["s"])
+        assert torch.equal(got, want) and torch.equal(v["x"], x) and torch.equal(v["i"], ids) and torch.equal(v["r"], res)
+    a, b = _beside(x, res)
+    assert torch.equal(w4.w4a16_moe(a, ids, weights, *w, G, residual=b, Y=b), want)

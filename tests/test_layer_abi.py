@@ -268,3 +268,29 @@ def test_products_whose_results_overlap_their_inputs_are_refused(lib):
     for shift in (0, 16, -16):
         assert lib.w4a16_linear(at(far["X"]), M, K, FAKE, FAKE, N, G, at(far["Y"] - shift), 1, None, at(far["Y"]), None, 0, None) == 1
         refused(e4m3, "xscale", xs=far["Y"] + max(shift, 0))
+
+
+def test_experts_whose_results_overlap_their_inputs_are_refused(lib):
+    """Y or the workspace on a part of what the call reads."""
+    import w4_dequant_gemm_amd as w4
+    T, k, E, H, I, G = 3, 2, 8, 128, 64, 64
+    need = lib.w4a16_moe_workspace_bytes(T, k, E, H, I, G)
+    at = lambda a: ctypes.c_void_p(a)                                       # noqa: E731
+    far = dict(X=0x10000, ids=0x20000, w=0x30000, res=0x40000, Y=0x50000, ws=0x100000)
+
+    def refused(text, **places):
+        a = {**far, **places}
+        status = lib.w4a16_moe(at(a["X"]), T, H, at(a["ids"]), at(a["w"]), k, *[FAKE] * 6, E, I, G, 1, at(a["res"]), at(a["Y"]),
+                               at(a["ws"]), need, None)
+        assert status == 1 and text in w4.w4_last_error(), (places, w4.w4_last_error())
+
+    rows = T * H * 2
+    for name, text, n in (("X", "X", rows), ("res", "the residual", rows), ("ids", "ids", 24), ("w", "weights", 24)):
+        for shift in (16, 16 - rows):
+            refused(f"Y overlaps {text}", Y=far[name] + shift)
+            refused(f"the workspace overlaps {text}", ws=far[name] + 16 - need // 16 * 16)
+        if name != "res":
+            refused(f"Y must not be {text}", Y=far[name], res=far[name] if name == "X" else far["res"])
+        refused(f"the workspace must not be {text}", ws=far[name])
+    refused("the workspace must not be Y", ws=far["Y"])
+    refused("the workspace overlaps Y", ws=far["Y"] + rows - 16)

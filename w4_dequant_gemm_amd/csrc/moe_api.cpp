@@ -103,7 +103,11 @@ int w4a16_moe(const uint16_t* X, int64_t T, int64_t H, const int32_t* ids, const
     W4_REQUIRE_PTR(fn, sz_down);
     W4_REQUIRE_PTR(fn, Y);
     if (residual && !aligned16(residual)) return fail(W4_EINVAL, "%s: residual is not 16-byte aligned", fn);
-    if (Y == X) return fail(W4_EINVAL, "%s: Y must not be X", fn);
+    // (the join reads the ids again while it writes Y)
+    const w4::Span y = w4::span(Y, T, H, 2, "Y"), x = w4::span(X, T, H, 2, "X"), i = w4::span(ids, T, top_k, 4, "ids"),
+                   w = w4::span(weights, T, top_k, 4, "weights"), r = w4::span(residual, T, H, 2, "the residual");
+    for (const w4::Span& in : {x, i, w}) W4_TRY(w4::check_apart(fn, y, in));
+    if (residual != Y) W4_TRY(w4::check_apart(fn, y, r));
     W4_REQUIRE_PTR(fn, workspace);
     w4::MoeParams p{};
     p.X = X;
@@ -124,6 +128,8 @@ int w4a16_moe(const uint16_t* X, int64_t T, int64_t H, const int32_t* ids, const
     const size_t need = w4::moe_workspace(p, workspace);
     if (workspace_bytes < need)
         return fail(W4_EINVAL, "%s: workspace of %zu bytes, these sizes need %zu (w4a16_moe_workspace_bytes)", fn, workspace_bytes, need);
+    const w4::Span ws{workspace, need, "the workspace"};
+    for (const w4::Span& in : {x, i, w, r, y}) W4_TRY(w4::check_apart(fn, ws, in));
     return hip_status(w4::launch_moe(p, stream), fn);
 }
 
