@@ -395,7 +395,8 @@ int w4a8_linear_e4m3(const uint8_t* xq, const float* xscale, int64_t M, int64_t 
  * over the choices if renormalize, then times scale.
  *   X [T, H], router [E, H]  bf16;  H a multiple of 8;  E <= 1024, top_k <= 32.
  *   bias       [E] fp32 or NULL.
- *   ids        [T, top_k] int32 out;  weights [T, top_k] fp32 out.
+ *   ids        [T, top_k] int32 out;  weights [T, top_k] fp32 out; they share no byte
+ *              with the inputs, the workspace or each other.
  *   workspace  w4_route_workspace_bytes(T, H, E) bytes (0: none), 16-byte aligned,
  *              its contents irrelevant.
  */

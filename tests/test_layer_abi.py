@@ -294,3 +294,29 @@ def test_experts_whose_results_overlap_their_inputs_are_refused(lib):
         refused(f"the workspace must not be {text}", ws=far[name])
     refused("the workspace must not be Y", ws=far["Y"])
     refused("the workspace overlaps Y", ws=far["Y"] + rows - 16)
+
+
+def test_routing_whose_results_overlap_its_inputs_is_refused(lib):
+    import w4_dequant_gemm_amd as w4
+    T, H, E, k = 3, 64, 20, 2
+    need = lib.w4_route_workspace_bytes(T, H, E)
+    assert need == 240
+    at = lambda a: ctypes.c_void_p(a)                                       # noqa: E731
+    far = dict(X=0x10000, R=0x20000, bias=0x30000, ids=0x40000, w=0x50000, ws=0x60000)
+
+    def refused(text, **places):
+        a = {**far, **places}
+        status = lib.w4_route(at(a["X"]), T, H, at(a["R"]), E, k, 0, at(a["bias"]), 1, 1.0, at(a["ids"]), at(a["w"]), at(a["ws"]),
+                              need, None)
+        assert status == 1 and text in w4.w4_last_error(), (places, w4.w4_last_error())
+
+    for name, text, n in (("X", "X", T * H * 2), ("R", "router", E * H * 2), ("bias", "bias", 80)):
+        for shift in (4, n - 4, -20):
+            refused(f"ids overlaps {text}", ids=far[name] + shift)
+            refused(f"weights overlaps {text}", w=far[name] + shift)
+        for shift in (16, n - 16, 16 - need):
+            refused(f"the workspace overlaps {text}", ws=far[name] + shift)
+    refused("ids must not be weights", w=far["ids"])
+    refused("ids overlaps weights", w=far["ids"] + 20)
+    refused("the workspace overlaps ids", ws=far["ids"] + 16)
+    refused("the workspace overlaps weights", ws=far["w"] - 224)

@@ -61,6 +61,19 @@ int w4_route(const uint16_t* X, int64_t T, int64_t H, const uint16_t* router, in
     if (need > 0) W4_REQUIRE_PTR(fn, workspace);
     if (workspace_bytes < need)
         return fail(W4_EINVAL, "%s: workspace of %zu bytes, these sizes need %zu (w4_route_workspace_bytes)", fn, workspace_bytes, need);
+    // workgroups read all of these while others write: choices and weights are no
+    // part of what is read, nor of each other, nor of the partial logits
+    const w4::Span x = w4::span(X, T, H, 2, "X"), r = w4::span(router, E, H, 2, "router"), b = w4::span(bias, E, 1, 4, "bias"),
+                   i = w4::span(ids, T, top_k, 4, "ids"), w = w4::span(weights, T, top_k, 4, "weights"),
+                   ws{workspace, need, "the workspace"};
+    for (const w4::Span& in : {x, r, b}) {
+        W4_TRY(w4::check_apart(fn, i, in));
+        W4_TRY(w4::check_apart(fn, w, in));
+        W4_TRY(w4::check_apart(fn, ws, in));
+    }
+    W4_TRY(w4::check_apart(fn, i, w));
+    W4_TRY(w4::check_apart(fn, ws, i));
+    W4_TRY(w4::check_apart(fn, ws, w));
     const w4::RouteParams p{X, T, static_cast<int>(H), router, static_cast<int>(E), top_k, score == W4_SCORE_SIGMOID, bias,
                             renormalize != 0, scale, ids, weights, static_cast<float*>(workspace),
                             w4::route_splits(T, static_cast<int>(E), static_cast<int>(H))};
