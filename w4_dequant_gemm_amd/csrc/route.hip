@@ -6,6 +6,11 @@
 // The k experts with the largest l (with a selection bias: the largest s +
 // bias), ties to the lower index; their weights are s, divided by their sum if
 // renormalized, times a factor.  NaN logits count as -inf.
+// Where the scores chosen leave the range of fp32 (sigmoids of logits below
+// -88, or experts that a bias chose far below the largest logit), their ratios
+// do not: a sigmoid of l << 0 is exp(l) to exp(l) of itself, a softmax score
+// exp(l) over a sum that all share, so the shares are then
+//   exp(l_j - max l) / sum of the same over the choices.
 //
 // The logits are v_mfma_f32_16x16x32_bf16 products of 16 tokens by 16 experts,
 // a wave taking every wk-th step of 32 k; the waves' sums are added through LDS
@@ -48,12 +53,12 @@ __device__ __forceinline__ float wave_max_dpp(float v) {
 template <int NV>
 __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, float (&l)[NV], int lane) {
     const float ninf = -__builtin_inff();
-    float rank[NV];
+    float rank[NV], raw[NV];
     float top = ninf;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         l[i] = 64 * i + lane < p.E && l[i] == l[i] ? l[i] : ninf;
-        rank[i] = l[i];
+        raw[i] = rank[i] = l[i];
         top = fmaxf(top, l[i]);
     }
     if (p.sigmoid) {
@@ -84,6 +89,7 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, float (&
 #pragma unroll
     for (int i = 0; i < NV; ++i) open |= 64 * i + lane < p.E ? 1u << i : 0u;
     float mine = 0.0f, all = 0.0f;   // lane j: the weight of choice j
+    float my_raw = ninf, most = ninf;   // its logit, and the largest of the choices'
     int my_id = 0;
     for (int j = 0; j < p.k; ++j) {
         float best = ninf;
@@ -92,7 +98,7 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, float (&
         best = wave_max_dpp(best);
         // the lowest expert that has it: the first value i with one, its lowest lane
         int id = 0;
-        float score = 0.0f;
+        float score = 0.0f, logit = ninf;
         bool found = false;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -102,14 +108,23 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, float (&
                 found = true;
                 id = 64 * i + at;
                 score = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(l[i]), at));
+                logit = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(raw[i]), at));
                 if (lane == at) open &= ~(1u << i);
             }
         }
         if (lane == j) {
             mine = score;
+            my_raw = logit;
             my_id = id;
         }
         all += score;
+        most = fmaxf(most, logit);
+    }
+    // (2^-60: what fp32 holds of a score above 2^-126 is whole, and smaller ones
+    // are less than a rounding of such a sum; the largest logit has 1 whatever it is)
+    if (p.renormalize && all < 0x1p-60f && most > ninf) {
+        mine = lane >= p.k ? 0.0f : (my_raw == most ? 1.0f : expf(my_raw - most));
+        all = wave_sum(mine);
     }
     if (lane < p.k) {
         if (p.renormalize) mine = all > 0.0f ? mine / all : 0.0f;
