@@ -686,10 +686,13 @@ __global__ void __launch_bounds__(1024) moe_down_dot_kernel(MoeParams p, int wk)
 }
 
 // Y = bf16(residual + the slots' shares in the order of the choices), four
-// columns a thread
-__global__ void __launch_bounds__(256) moe_join_kernel(MoeParams p) {
+// columns a thread.  A launch has fewer than 2^32 threads (the runtime starts
+// only what is left of a larger number, without an error), and a million tokens
+// may have more columns than that: `turn` is which 2^30 threads these are.
+constexpr int64_t kJoinThreads = int64_t{1} << 30;
+__global__ void __launch_bounds__(256) moe_join_kernel(MoeParams p, int turn) {
     const int per = p.H / 4;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t i = kJoinThreads * turn + static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= p.T * per) return;
     const int64_t t = i / per;
     const int n = static_cast<int>(i % per) * 4;
@@ -804,8 +807,14 @@ hipError_t launch_tiles(const MoeParams& p, hipStream_t stream) {
 }
 
 hipError_t launch_join(const MoeParams& p, hipStream_t stream) {
-    hipLaunchKernelGGL(moe_join_kernel, dim3(static_cast<unsigned>((p.T * (p.H / 4) + 255) / 256)), dim3(256), 0, stream, p);
-    return hipGetLastError();
+    int turn = 0;
+    for (int64_t left = p.T * (p.H / 4); left > 0; left -= kJoinThreads) {
+        const int64_t threads = left < kJoinThreads ? left : kJoinThreads;
+        hipLaunchKernelGGL(moe_join_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, stream, p, turn++);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // K ranges of the down product, towards two workgroups of 256 columns a compute
