@@ -122,15 +122,29 @@ hipError_t launch_rowquant(const RowQuantParams& p, hipStream_t stream) {
 #ifndef W4_RQ_WIDE_K
 #define W4_RQ_WIDE_K 12288
 #endif
-    // long rows: four times the threads, so that the quantizing pass of one
-    // row (all on one compute unit) takes a quarter of the time (M = 2048:
-    // K = 28672 38.2 -> 32.9 us; at K = 8192 the 256-thread blocks are 4%
-    // faster)
-    if (p.K >= W4_RQ_WIDE_K)
-        hipLaunchKernelGGL((rowquant_kernel<1024, 4>), dim3(static_cast<unsigned>(p.M)), dim3(1024), 0, stream, p);
-    else
-        hipLaunchKernelGGL((rowquant_kernel<256, 16>), dim3(static_cast<unsigned>(p.M)), dim3(256), 0, stream, p);
-    return hipGetLastError();
+    // A launch has fewer than 2^32 threads (the runtime starts only what is left
+    // of a larger number, without an error): more rows go piece by piece.
+    constexpr int64_t kPiece = int64_t{1} << 21;
+    for (int64_t m = 0; m < p.M; m += kPiece) {
+        RowQuantParams q = p;
+        q.M = p.M - m < kPiece ? p.M - m : kPiece;
+        q.X = p.X + m * p.K;
+        q.xq = p.xq + m * p.K;
+        q.xscale = p.xscale + m;
+        if (p.xw) q.xw = p.xw + m * p.K;
+        if (p.amax_part) q.amax_part = p.amax_part + m * p.amax_tiles;
+        // long rows: four times the threads, so that the quantizing pass of one
+        // row (all on one compute unit) takes a quarter of the time (M = 2048:
+        // K = 28672 38.2 -> 32.9 us; at K = 8192 the 256-thread blocks are 4%
+        // faster)
+        if (p.K >= W4_RQ_WIDE_K)
+            hipLaunchKernelGGL((rowquant_kernel<1024, 4>), dim3(static_cast<unsigned>(q.M)), dim3(1024), 0, stream, q);
+        else
+            hipLaunchKernelGGL((rowquant_kernel<256, 16>), dim3(static_cast<unsigned>(q.M)), dim3(256), 0, stream, q);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace w4
