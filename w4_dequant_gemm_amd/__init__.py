@@ -221,6 +221,11 @@ def _ptr(fn: str, t: torch.Tensor, name: str, dtype, device: int):
     raise ValueError(f"{fn}: {name} must be contiguous")
 
 
+def _any_ptr(fn: str, t: Optional[torch.Tensor], name: str, device: int):
+    """As ``_ptr`` for a workspace or codes of any one-byte type; None stays None."""
+    return None if t is None else _ptr(fn, t, name, t.dtype, device)
+
+
 def _vec_ptr(fn: str, t, name: str, n: int, dtype, device: int):
     if t is None:
         return None
@@ -587,6 +592,7 @@ def w4a16_linear(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *,
     dev = X.device
     b, a, r = _epilogue_args(fn, M, N, bias, act, residual, X.get_device())
     gpu = _gpu(fn, X, "X")
+    _any_ptr(fn, workspace, "workspace", gpu)
     Y = _empty((M, N), torch.bfloat16, dev, stream) if Y is None else Y
     ws, ws_bytes = _workspace(M, K, N, dev, workspace, stream)
     rc = lib().w4a16_linear(_ptr(fn, X, "X", torch.bfloat16, gpu), M, K, _ptr(fn, wq, "wq", torch.int32, gpu),
@@ -611,13 +617,14 @@ def w4a8_linear(X: torch.Tensor, wq: torch.Tensor, sz: torch.Tensor, G: int, *, 
     dev = X.device
     b, a, r = _epilogue_args(fn, M, N, bias, act, residual, X.get_device())
     gpu = _gpu(fn, X, "X")
+    _any_ptr(fn, workspace, "workspace", gpu)
     Y = _empty((M, N), torch.bfloat16, dev, stream) if Y is None else Y
     xq = _empty((M, K), torch.uint8, dev, stream) if xq is None else xq
     xscale = _empty((M,), torch.float32, dev, stream) if xscale is None else xscale
     ws, ws_bytes = _workspace(M, K, N, dev, workspace, stream, w4a8=True)
     rc = lib().w4a8_linear(_ptr(fn, X, "X", torch.bfloat16, gpu), M, K, _ptr(fn, wq, "wq", torch.int32, gpu),
                            _ptr(fn, sz, "sz", torch.int32, gpu), N, G, b, a, r, _ptr(fn, Y, "Y", torch.bfloat16, gpu),
-                           _dev(xq, "xq"), _ptr(fn, xscale, "xscale", torch.float32, gpu), ws, ws_bytes,
+                           _any_ptr(fn, xq, "xq", gpu), _ptr(fn, xscale, "xscale", torch.float32, gpu), ws, ws_bytes,
                            _stream(dev, stream))
     if rc:
         _check(fn, rc)
@@ -635,6 +642,7 @@ def w4a8_linear_e4m3(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, s
     dev = xq.device
     b, a, r = _epilogue_args(fn, M, N, bias, act, residual, xq.get_device())
     gpu = _gpu(fn, xq, "xq")
+    _any_ptr(fn, workspace, "workspace", gpu)
     Y = _empty((M, N), torch.bfloat16, dev, stream) if Y is None else Y
     ws, ws_bytes = _workspace(M, K, N, dev, workspace, stream, w4a8=True)
     rc = lib().w4a8_linear_e4m3(_ptr(fn, xq, "xq", xq.dtype, gpu), _ptr(fn, xscale, "xscale", torch.float32, gpu), M, K,
@@ -763,7 +771,7 @@ def w4_route(X: torch.Tensor, router: torch.Tensor, top_k: int, *, score="softma
     need = w4_route_workspace_bytes(T, H, E)
     if need:
         workspace = _scratch(need, dev, stream) if workspace is None else workspace
-        ws, ws_bytes = _dev(workspace, "workspace"), workspace.nbytes
+        ws, ws_bytes = _any_ptr(fn, workspace, "workspace", gpu), workspace.nbytes
     rc = lib().w4_route(_ptr(fn, X, "X", torch.bfloat16, gpu), T, H, _ptr(fn, router, "router", torch.bfloat16, gpu), E, top_k,
                         _SCORES[score], b, renormalize, scale, _vec_ptr(fn, ids, "ids", T * top_k, torch.int32, gpu),
                         _vec_ptr(fn, weights, "weights", T * top_k, torch.float32, gpu), ws, ws_bytes, _stream(dev, stream))
@@ -822,7 +830,7 @@ def w4a16_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: d
     rc = lib().w4a16_moe(_ptr(fn, X, "X", torch.bfloat16, gpu), T, H, _ptr(fn, ids, "ids", torch.int32, gpu),
                          _ptr(fn, weights, "weights", torch.float32, gpu), top_k, g[0], g[1], u[0], u[1], d[0], d[1], E, I, G,
                          _ACTS[act], None if residual is None else _ptr(fn, residual, "residual", torch.bfloat16, gpu),
-                         _ptr(fn, Y, "Y", torch.bfloat16, gpu), _dev(workspace, "workspace"), workspace.nbytes,
+                         _ptr(fn, Y, "Y", torch.bfloat16, gpu), _any_ptr(fn, workspace, "workspace", gpu), workspace.nbytes,
                          _stream(dev, stream))
     if rc:
         _check(fn, rc)
