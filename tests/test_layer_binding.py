@@ -112,3 +112,15 @@ def test_tensors_on_another_gpu_are_refused(w4, which):
     for name, t in kw.items():
         with pytest.raises(ValueError, match="cuda:"):
             f(*args, **{**kw, name: t.at(1)})
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_streams_of_another_gpu_are_refused(w4, which):
+    from types import SimpleNamespace
+    f, args, kw = (_linear(w4) + _experts(w4) + _logits(w4))[which]
+    if which == 1:
+        kw.update(xq=On((200, 4096), U8), xscale=On((200,), F32))
+    with pytest.raises(AssertionError, match="was called"):
+        f(*args, **kw, stream=SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 0)))
+    with pytest.raises(ValueError, match="the stream is one of cuda:1"):
+        f(*args, **kw, stream=SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 1)))

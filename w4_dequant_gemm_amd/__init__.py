@@ -257,6 +257,10 @@ def _stream(device, stream=None):
         if device.index is not None:
             return _raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
+    else:
+        its = getattr(stream, "device", device).index      # (anything with a handle may be a stream)
+        if device.index is not None and its is not None and its != device.index:
+            raise ValueError(f"the stream is one of cuda:{its}, and the tensors are on {device}")
     return stream.cuda_stream
 
 
