@@ -124,3 +124,10 @@ def test_streams_of_another_gpu_are_refused(w4, which):
         f(*args, **kw, stream=SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 0)))
     with pytest.raises(ValueError, match="the stream is one of cuda:1"):
         f(*args, **kw, stream=SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 1)))
+
+
+@pytest.mark.parametrize("act", ["relu", None, "tanh", 7])
+def test_experts_have_two_activations(w4, act):
+    f, args, kw = _experts(w4)[1]
+    with pytest.raises(ValueError, match="act must be 'silu' or 'gelu_tanh'"):
+        f(*args, act, **kw)

@@ -812,6 +812,8 @@ def w4a16_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: d
                                         down["wq"], down["sz"], G, _ACTS[act], residual)
             if r is not None:
                 return r
+    if act not in _ACTS:
+        raise ValueError(f"{fn}: act must be 'silu' or 'gelu_tanh', got {act!r}")
     xs, js, gs = X.shape, ids.shape, gate["wq"].shape
     if len(xs) != 2 or len(js) != 2 or js[0] != xs[0] or weights.shape != js:
         raise ValueError(f"{fn}: X must be [T, H], ids and weights [T, top_k], got {tuple(xs)}, {tuple(js)} and "
