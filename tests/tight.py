@@ -37,11 +37,12 @@ def tiled(T, k, E, H, I, G):
     return T * k > 64 and T * k >= 16 * E and -(-wide // 128) * (128 // G) * 64 <= 16384 and 2 * T * k * wide < 2 ** 31
 
 
-def moe_limit(shape):
+def moe_limit(shape, once=None):
     """Root mean square of the error over that of the result, the result's own rounding taken off.  h is off by STEP or
     TWICE of itself, term by term; the first product's sums and the second's by U times what passes through (40 times the
-    sum, which is that of u - z), and the roundings of chains of at most some 400: 40 * 20 U; what is left is rounded."""
-    h = STEP if tiled(*shape) else TWICE
+    sum, which is that of u - z), and the roundings of chains of at most some 400: 40 * 20 U; what is left is rounded.
+    `once`: whether h may be rounded once (by default what the shape's form does)."""
+    h = STEP if (tiled(*shape) if once is None else once) else TWICE
     return h + 3 * 40 * 20 * U + STEP * STEP
 
 
