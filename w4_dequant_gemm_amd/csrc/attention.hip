@@ -22,6 +22,7 @@
 // comes from one more product with ones, so a weight that dominates is not
 // biased by its rounding.
 #include "attention.hpp"
+#include "launch.hpp"
 
 namespace w4 {
 namespace {
@@ -634,7 +635,7 @@ hipError_t launch_kind(const AttentionParams& p, const AttentionPlan& pl, hipStr
     const int64_t groups = static_cast<int64_t>(pl.splits) * p.cache.heads * p.B;
     const bool tiled = pl.tile_rows > 32;
     const int64_t wgs = tiled ? (groups + 7) / 8 * 8 * pl.tiles : groups;
-    if (wgs > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    if (!launch_fits(wgs, 256)) return hipErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(wgs);
     if constexpr (D == 256) {
         // 64 KB of shared memory: two workgroups a compute unit

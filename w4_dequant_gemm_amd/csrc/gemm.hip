@@ -28,6 +28,7 @@
 #include "device.hpp"
 #include "epilogue.hpp"
 #include "kernels.hpp"
+#include "launch.hpp"
 
 namespace w4 {
 namespace {
@@ -1425,6 +1426,7 @@ hipError_t launch_mid(const MulParams& p, hipStream_t stream) {
     if (q.splits > q.K / big::BK || q.split_t0 < 0 || q.split_t0 > tiles || (q.splits > 1 && !q.ws))
         return hipErrorInvalidValue;
     const int64_t wgs = q.split_t0 + (tiles - q.split_t0) * q.splits;
+    if (!launch_fits(wgs, 256)) return hipErrorInvalidConfiguration;
     if (q.epi)
         hipLaunchKernelGGL((gemm_mid_kernel<TBM, TBN, 2, 2, XF8, false, true>), dim3(static_cast<unsigned>(wgs)), dim3(256), 0, stream, q);
     else
@@ -1445,6 +1447,7 @@ hipError_t launch_pair_t(const MulParams& p, hipStream_t stream) {
     q.splits = 1;
     q.split_t0 = tiles;
     q.ws = nullptr;
+    if (!launch_fits(tiles, 256)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((gemm_mid_kernel<TBM, 2 * OUTN, 2, 2, XF8, true>), dim3(static_cast<unsigned>(tiles)), dim3(256), 0,
                        stream, q);
     return hipGetLastError();
@@ -1484,6 +1487,7 @@ hipError_t launch_gemm_pair(const MulParams& p, hipStream_t stream) {
             return hipErrorInvalidValue;
         }
         const int64_t wgs = q.split_t0 + (g.tiles - q.split_t0) * q.splits;
+        if (!launch_fits(wgs, 64 * W4_BREG_PAIR_NW)) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((gemm256_breg_kernel<true, W4_BREG_PAIR_NW>), dim3(static_cast<unsigned>(wgs)),
                            dim3(breg::Geom<W4_BREG_PAIR_NW>::NT), 0, stream, q);
         if (q.splits > 1) {
@@ -1578,6 +1582,7 @@ hipError_t launch_gemm(const MulParams& p, hipStream_t stream) {
         if (q.splits > q.K / big::BK || q.split_t0 < 0 || q.split_t0 > tiles || (q.splits > 1 && !q.ws))
             return hipErrorInvalidValue;
         const int64_t wgs = q.split_t0 + (tiles - q.split_t0) * q.splits;
+        if (!launch_fits(wgs, 512)) return hipErrorInvalidConfiguration;
         const dim3 grid(static_cast<unsigned>(wgs));
         // W4A8 on the widened activations runs the bf16 kernel, row scales in
         // its epilogue (or in the split sum)
@@ -1599,8 +1604,9 @@ hipError_t launch_gemm(const MulParams& p, hipStream_t stream) {
         }
         return hipGetLastError();
     }
-    const dim3 grid(static_cast<unsigned>((p.N + small::BN - 1) / small::BN),
-                    static_cast<unsigned>((p.M + small::BM - 1) / small::BM));
+    const int64_t cols = (p.N + small::BN - 1) / small::BN, rows = (p.M + small::BM - 1) / small::BM;
+    if (!launch_fits(cols, 256) || !launch_fits(rows, 1)) return hipErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(cols), static_cast<unsigned>(rows));
     auto launch = [&](auto xf8, auto epi) {
         hipLaunchKernelGGL((gemm_kernel<decltype(xf8)::value, decltype(epi)::value>), grid, dim3(256), 0, stream, p);
     };

@@ -32,6 +32,7 @@
 // loop has no barrier.
 #include "device.hpp"
 #include "kernels.hpp"
+#include "launch.hpp"
 
 #pragma clang fp contract(off)
 
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(kGemvThreads) nf4_gemv_kernel(Nf4GemvParams p,
 hipError_t launch_nf4_quantize(const Nf4QuantParams& p, hipStream_t stream) {
     if (p.n_blocks == 0) return hipSuccess;
     const int64_t groups = (p.n_blocks + kNf4Group - 1) / kNf4Group;
+    if (!launch_fits(groups, kNf4Group)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(nf4_quantize_kernel, dim3(static_cast<unsigned>(groups)), dim3(kNf4Group), 0, stream, p);
     return hipGetLastError();
 }
@@ -247,6 +249,7 @@ hipError_t launch_nf4_gemv_rp(const Nf4GemvParams& p, int64_t rows_per_wave, hip
     const int items_per_group = static_cast<int>((nch + 64 * PU - 1) / (64 * PU));
     const int64_t waves = (p.N + rows_per_wave - 1) / rows_per_wave;
     const int64_t wgs = (waves + kGemvWaves - 1) / kGemvWaves;
+    if (!launch_fits(wgs, kGemvThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((nf4_gemv_kernel<R, PU, D>), dim3(static_cast<unsigned>(wgs)), dim3(kGemvThreads), 0, stream,
                        p, rows_per_wave, items_per_group);
     return hipGetLastError();

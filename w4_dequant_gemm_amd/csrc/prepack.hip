@@ -22,6 +22,7 @@
 // group g of row r0 + c at r0 (K/G) + g nr + c.
 #include "device.hpp"
 #include "kernels.hpp"
+#include "launch.hpp"
 
 namespace w4 {
 namespace {
@@ -68,6 +69,7 @@ hipError_t launch_prepack(const PrepackParams& p, hipStream_t stream) {
     if (n_words == 0) return hipSuccess;
     const int threads = 256;
     const int64_t blocks = (n_words + threads - 1) / threads;
+    if (!launch_fits(blocks, threads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(prepack_kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, stream, p);
     return hipGetLastError();
 }

@@ -26,6 +26,7 @@
 // covers 64 consecutive groups, i.e. a contiguous 64*G*4-byte span of W.
 #include "device.hpp"
 #include "kernels.hpp"
+#include "launch.hpp"
 
 #pragma clang fp contract(off)
 
@@ -333,6 +334,7 @@ __global__ void __launch_bounds__(kRowThreads) quantize_row_kernel(QuantizeParam
 
 template <int RPT, bool ASYM>
 hipError_t launch_row(const QuantizeParams& p, int64_t K, hipStream_t stream) {
+    if (!launch_fits(p.n_groups, kRowThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((quantize_row_kernel<RPT, ASYM>), dim3(static_cast<unsigned>(p.n_groups)), dim3(kRowThreads), 0,
                        stream, p, K);
     return hipGetLastError();
@@ -358,6 +360,7 @@ template <int G, bool ASYM>
 hipError_t launch(const QuantizeParams& p, hipStream_t stream) {
     const int threads = 256;
     const int64_t blocks = (p.n_groups + threads - 1) / threads;
+    if (!launch_fits(blocks, threads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((quantize_kernel<G, ASYM>), dim3(static_cast<unsigned>(blocks)), dim3(threads), 0,
                        stream, p);
     return hipGetLastError();

@@ -16,6 +16,7 @@
 // once (kept in registers between the two passes) up to 32768 per row.
 #include "device.hpp"
 #include "kernels.hpp"
+#include "launch.hpp"
 
 #pragma clang fp contract(off)
 
@@ -122,8 +123,7 @@ hipError_t launch_rowquant(const RowQuantParams& p, hipStream_t stream) {
 #ifndef W4_RQ_WIDE_K
 #define W4_RQ_WIDE_K 12288
 #endif
-    // A launch has fewer than 2^32 threads (the runtime starts only what is left
-    // of a larger number, without an error): more rows go piece by piece.
+    // (launch_fits: more rows go piece by piece)
     constexpr int64_t kPiece = int64_t{1} << 21;
     for (int64_t m = 0; m < p.M; m += kPiece) {
         RowQuantParams q = p;

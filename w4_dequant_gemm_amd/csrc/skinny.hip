@@ -41,6 +41,7 @@
 #include "device.hpp"
 #include "epilogue.hpp"
 #include "kernels.hpp"
+#include "launch.hpp"
 
 namespace w4 {
 namespace {
@@ -751,6 +752,7 @@ hipError_t launch_skinny_e(const MulParams& p, int wk, hipStream_t stream) {
     const int64_t blocks = (p.N + cols - 1) / cols * (split ? p.splits : 1);
     size_t lds = static_cast<size_t>(wk) * (MODE >= kDot ? 16 : 256) * MB * FJ * sizeof(float);
     if (MODE == kDotLds || MODE == kDotLdsQ) lds += static_cast<size_t>(MB) * staged_words_row(p.K) * sizeof(uint32_t);
+    if (!launch_fits(blocks, 64 * wk) || (split && !launch_fits((p.M * p.N + 255) / 256, 256))) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((gemm_skinny_kernel<MB, FJ, XF8, MODE, EPI>), dim3(static_cast<unsigned>(blocks)), dim3(64 * wk), lds,
                        stream, p, wk);
     if (split) {
