@@ -24,7 +24,7 @@ __device__ __forceinline__ float linear_activation(int act, float x) {
 
 // one output
 template <bool EPI>
-__device__ __forceinline__ uint16_t finish(const MulParams& p, int64_t row, int64_t col, float y) {
+__device__ __forceinline__ uint16_t finish(const KernelParams<EPI>& p, int64_t row, int64_t col, float y) {
     if constexpr (EPI) {
         if (p.bias) y += p.bias[col];
         y = linear_activation(p.out_act, y);
@@ -36,7 +36,7 @@ __device__ __forceinline__ uint16_t finish(const MulParams& p, int64_t row, int6
 // four outputs of a row from column `col` on (a multiple of 4; those past N
 // are left out), their sums in y
 template <bool EPI>
-__device__ __forceinline__ void finish4(const MulParams& p, int64_t row, int64_t col, float4 y) {
+__device__ __forceinline__ void finish4(const KernelParams<EPI>& p, int64_t row, int64_t col, float4 y) {
     float v[4] = {y.x, y.y, y.z, y.w};
     const int64_t at = row * p.N + col;
     const bool whole = col + 3 < p.N && p.N % 4 == 0;

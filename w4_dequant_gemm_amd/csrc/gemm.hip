@@ -70,7 +70,7 @@ constexpr int LDS_STRIDE = BK + 8;   // bf16 elements per LDS row (16 bytes of p
 }  // namespace small
 
 template <bool XF8, bool EPI>
-__global__ void __launch_bounds__(256) gemm_kernel(MulParams p) {
+__global__ void __launch_bounds__(256) gemm_kernel(KernelParams<EPI> p) {
     using namespace small;
     __shared__ __attribute__((aligned(16))) uint16_t As[BM * LDS_STRIDE];
     __shared__ __attribute__((aligned(16))) uint16_t Bs[BN * LDS_STRIDE];
@@ -267,7 +267,7 @@ struct TileJob {
     int kb, KT;        // first K step and number of K steps
     int64_t part;      // partial-tile index in ws, or -1: write Y
 };
-__device__ __forceinline__ TileJob tile_job(const MulParams& p) {
+__device__ __forceinline__ TileJob tile_job(const ProductParams& p) {
     const int64_t b = blockIdx.x;
     const int64_t nt = (p.N + BN - 1) / BN;
     const int KT_all = static_cast<int>(p.K / BK);
@@ -295,7 +295,7 @@ __device__ __forceinline__ TileJob tile_job(const MulParams& p) {
 }  // namespace big
 
 template <int WM, int WN, bool XF8, bool EPI>
-__global__ void __launch_bounds__(64 * WM * WN) gemm256_kernel(MulParams p) {
+__global__ void __launch_bounds__(64 * WM * WN) gemm256_kernel(KernelParams<EPI> p) {
     using namespace big;
     constexpr int NT = 64 * WM * WN;         // threads
     constexpr int TM = BM / WM, TN = BN / WN; // wave tile
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm256_kernel(MulParams p) {
     if (kt < KT) step(kt, r0, r1);
 
     // epilogue: register r of lane l holds row (r%4) + 4(l/32) + 8(r/4), column l%32
-    if (EPI && job.part < 0) {
+    if constexpr (EPI) if (job.part < 0) {
         // a 32-row block of one wave row a round
         float* const sums = reinterpret_cast<float*>(lds);
         static_assert(!EPI || 32 * BN * 4 <= sizeof(lds), "a round fits the operand stages");
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm256_kernel(MulParams p) {
 // The work of one workgroup of the TBM x TBN kernels (same scheme as
 // big::tile_job).
 template <int TBM, int TBN>
-__device__ __forceinline__ big::TileJob tile_job_t(const MulParams& p) {
+__device__ __forceinline__ big::TileJob tile_job_t(const ProductParams& p) {
     const int64_t b = blockIdx.x;
     const int64_t nt = (p.N + TBN - 1) / TBN;
     const int KT_all = static_cast<int>(p.K / big::BK);
@@ -582,7 +582,7 @@ __device__ __forceinline__ big::TileJob tile_job_t(const MulParams& p) {
 // gate products and those of column 1 up products for the same outputs; at
 // the end the up sums go through LDS and H = bf16(act(gate) * up).
 template <int TBM, int TBN, int WM, int WN, bool XF8, bool PAIR = false, bool EPI = false>
-__global__ void __launch_bounds__(64 * WM * WN) gemm_mid_kernel(MulParams p) {
+__global__ void __launch_bounds__(64 * WM * WN) gemm_mid_kernel(KernelParams<EPI> p) {
     using big::BK;
     using big::lds_off;
     constexpr int NT = 64 * WM * WN;
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_mid_kernel(MulParams p) {
         return;
     }
 
-    if (EPI && job.part < 0) {
+    if constexpr (EPI) if (job.part < 0) {
         // a 32-row block of every wave row a round
         float* const sums = reinterpret_cast<float*>(lds);
         static_assert(!EPI || 32 * WM * TBN * 4 <= sizeof(lds), "a round fits the operand stages");
@@ -893,7 +893,7 @@ __device__ __forceinline__ int swz(int row) { return big::swizzle_fn(W4_DSWZ, ro
 }  // namespace breg
 
 template <bool PAIR, int NW = 4, bool EPI = false>
-__global__ void __launch_bounds__(64 * NW) gemm256_breg_kernel(MulParams p) {
+__global__ void __launch_bounds__(64 * NW) gemm256_breg_kernel(KernelParams<EPI> p) {
     using namespace breg;
     static_assert(!PAIR || NW % 2 == 0, "the pair form pairs waves w and w + NW / 2");
     constexpr int NT = Geom<NW>::NT, ADMA = Geom<NW>::ADMA, FJ = Geom<NW>::FJ, BLOAD = Geom<NW>::BLOAD;
@@ -1175,7 +1175,7 @@ __global__ void __launch_bounds__(64 * NW) gemm256_breg_kernel(MulParams p) {
             }
         return;
     }
-    if (EPI && job.part < 0) {
+    if constexpr (EPI) if (job.part < 0) {
         // a 32-row block of all waves a round, in the free activation stage
         float* const sums = reinterpret_cast<float*>(lds_a0);
         static_assert(32 * BN * 4 <= sizeof(lds_a0), "a round fits a stage");
@@ -1225,7 +1225,7 @@ __global__ void __launch_bounds__(64 * NW) gemm256_breg_kernel(MulParams p) {
 // (W4A8), rounded to bf16.  A thread takes four consecutive columns of one
 // tile row (16-byte loads; consecutive lanes read consecutive addresses).
 template <int BM, int BN, bool EPI>
-__global__ void __launch_bounds__(256) splitk_reduce_kernel(MulParams p) {
+__global__ void __launch_bounds__(256) splitk_reduce_kernel(KernelParams<EPI> p) {
     const int64_t e4 = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;   // element of the split tiles
     const int64_t j = e4 / (BM * BN);
     const int lr = static_cast<int>((e4 % (BM * BN)) / BN), lc = static_cast<int>(e4 % BN);
@@ -1252,7 +1252,7 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(MulParams p) {
 // output tiles: partial tile [256][256] holds the gate sums in columns
 // 0..127 and the up sums in 128..255; H = bf16(act(g) u) with g and u added
 // in split order.  A thread takes four consecutive output columns of a row.
-__global__ void __launch_bounds__(256) splitk_reduce_pair_kernel(MulParams p) {
+__global__ void __launch_bounds__(256) splitk_reduce_pair_kernel(ProductParams p) {
     constexpr int BM = big::BM, BN = big::BN, BNO = BN / 2;
     const int64_t e4 = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;   // output of the split tiles
     const int64_t j = e4 / (BM * BNO);

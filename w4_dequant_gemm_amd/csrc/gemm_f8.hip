@@ -94,7 +94,7 @@ struct F8Job {
     int64_t part;      // partial-tile index in ws, or -1: write Y
 };
 template <int BM, int BN>
-__device__ __forceinline__ F8Job f8_job(const MulParams& p) {
+__device__ __forceinline__ F8Job f8_job(const ProductParams& p) {
     using namespace f8;
     const int64_t b = blockIdx.x;
     const int64_t nt = (p.N + BN - 1) / BN;     // BN: output columns of a tile
@@ -187,7 +187,7 @@ __device__ __forceinline__ float4_t mfma_f8_16x16x128(const int8x_t& a, const in
 // against ones, and per group and output acc += s (T - (128 + z) X1): exact
 // weights, any zero point.
 template <int BM_, int BN_, int WR_, int WC_, bool PAIR = false, int SA_ = 3, int DW_ = 2, bool A16 = false, bool EPI = false>
-__global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(MulParams p) {
+__global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(KernelParams<EPI> p) {
     using namespace f8;
     using Gm = Geom<BM_, BN_, WR_, WC_>;
     constexpr int AB = A16 ? 2 : 1;               // bytes per activation
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(64 * WR_ * WC_) gemm_f8_kernel(MulParams p) {
         return;
     }
     const bool whole = job.part < 0;
-    if (EPI && whole) {
+    if constexpr (EPI) if (whole) {
         // as many row blocks of every wave as fit an activation stage a round
         constexpr int FIT = STAGE / (16 * WR_ * BN * 4), RPR = FIT < RB ? FIT : RB;
         static_assert(!EPI || (RPR >= 1 && RB % RPR == 0), "whole rounds");

@@ -94,7 +94,7 @@ template <int MB, int MODE>
 constexpr int skinny_max_threads() { return MODE == kDotLds || MODE == kDotLdsQ ? 1024 : 512; }
 
 template <int MB, int FJ, bool XF8, int MODE, bool EPI>
-__global__ void __launch_bounds__((skinny_max_threads<MB, MODE>())) gemm_skinny_kernel(MulParams p, int wk) {
+__global__ void __launch_bounds__((skinny_max_threads<MB, MODE>())) gemm_skinny_kernel(KernelParams<EPI> p, int wk) {
     constexpr bool CORR = MODE == kCorr, QX = MODE == kDotLdsQ, DOTL = MODE == kDotLds || QX,
                    DOT = MODE == kDot || DOTL;
     static_assert(!QX || XF8, "in-kernel row quantization is the W4A8 product");
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__((skinny_max_threads<MB, MODE>())) gemm_skinny_
 // Sum of the K-split partials of the streaming kernel: Y = bf16(sum over the
 // ranges in order, times the row scale for W4A8).
 template <bool EPI>
-__global__ void __launch_bounds__(256) skinny_reduce_kernel(MulParams p) {
+__global__ void __launch_bounds__(256) skinny_reduce_kernel(KernelParams<EPI> p) {
     const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int64_t mn = p.M * p.N;
     if (e >= mn) return;
