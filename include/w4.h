@@ -393,7 +393,7 @@ int w4a8_linear_e4m3(const uint8_t* xq, const float* xscale, int64_t M, int64_t 
  * largest s + bias[e] where a selection bias is given, in that order, ties to
  * the lower index (NaN counts as -inf); their weights are s, divided by the sum
  * over the choices if renormalize, then times scale.
- *   X [T, H], router [E, H]  bf16;  H a multiple of 8;  E <= 1024, top_k <= 32.
+ *   X [T, H], router [E, H]  bf16;  T <= 10^6;  H a multiple of 8, <= 65536;  E <= 1024, top_k <= 32.
  *   bias       [E] fp32 or NULL.
  *   ids        [T, top_k] int32 out;  weights [T, top_k] fp32 out; they share no byte
  *              with the inputs, the workspace or each other.
@@ -412,15 +412,21 @@ size_t w4_route_workspace_bytes(int64_t T, int64_t H, int64_t E);
  *   h_j  = w_j act(Wg'[e_j] . X[t]) * (Wu'[e_j] . X[t])
  *   Y[t] = bf16(residual[t] + sum_j Wd'[e_j] . h_j)
  * with W' = (q - z) s exact, fp32 accumulation, and h kept between the products as
- * the sum of two bf16 numbers (16 bits of mantissa), or, where 16 rows an expert
- * or more (T top_k >= 16 E, above 64) take the tiled kernels, rounded to bf16.  An id outside 0..E-1 is no
+ * the sum of two bf16 numbers (16 bits of mantissa), or, in the tiled kernels,
+ * rounded to bf16.  Those take calls with 16 rows an expert or more (T top_k >=
+ * 16 E, and > 64) whose larger width, H or I, is at most 8192 in groups of 32,
+ * 16384 in groups of 64 and 32768 in groups of 128, and at most 2^30 / (T top_k);
+ * other calls of that many rows go through the weights 16 or 32 rows at a time,
+ * in six times the time (512 rows an expert, groups of 32).
+ * An id outside 0..E-1 is no
  * expert (padding, or one that another process holds): its choice adds nothing,
  * and a token without any gets its residual (or zeros).  A token may choose an
  * expert twice.  Results do not depend on timing.
- *   X          [T, H] bf16;  ids [T, top_k] int32;  weights [T, top_k] fp32.
+ *   X          [T, H] bf16;  ids [T, top_k] int32;  weights [T, top_k] fp32;
+ *              T <= 10^6, E <= 1024, top_k <= 32.
  *   wq_gate, sz_gate, wq_up, sz_up   the GPU layouts (w4_prepack) of the E experts'
  *              [I, H] weights, one after the other; wq_down, sz_down of their [H, I]
- *              weights.  H and I are multiples of G = 32, 64 or 128.
+ *              weights.  H and I are multiples of G = 32, 64 or 128, up to 65536.
  *   act        W4_ACT_SILU or W4_ACT_GELU_TANH.
  *   residual   [T, H] bf16 or NULL; may be X or Y.
  *   Y          [T, H] bf16 out; shares no byte with X, ids or weights, and none with
@@ -626,8 +632,8 @@ int w4_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_s
  *   mask bit 0:  x = -inf
  * NaN stays NaN unless masked.  A mask may leave a row nothing: all -inf.
  *   logits       bf16 or fp32 (W4_LOGITS_*), [B, V], rows row_stride elements
- *                apart (0: the same row for all); V <= 2^20.  No alignment
- *                beyond the elements'.
+ *                apart (0: the same row for all); B <= 65535, V <= 2^20,
+ *                distances of rows up to 2^40.  No alignment beyond the elements'.
  *   history      [history_len] int32, row b's tokens are history_start[b] ..
  *                history_start[b + 1] - 1 (history_start [B + 1] int32; cut to
  *                the array); tokens outside 0..V-1 are not counted.  NULL: none.
@@ -642,7 +648,8 @@ int w4_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_s
  *                mask_stride words apart (0: one mask for all rows).  NULL: all
  *                allowed.
  *   out          as logits, rows out_stride >= V elements apart; may be logits
- *                itself, with the same stride, but must not overlap it otherwise.
+ *                itself, with the same stride, but must not overlap it otherwise
+ *                (refused; rows between those of the logits are allowed).
  */
 int w4_adjust_logits(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride, const int32_t* history,
                      int64_t history_len, const int32_t* history_start, const int32_t* prompt_len, const float* repetition,

@@ -8,7 +8,8 @@
 // a (token, choice) pair; the slots are put in order of their expert, so that an
 // expert's weights are read once for all of its rows.  Three forms:
 //
-// - one or two tokens: each slot by itself on dot products (moe_*_dot_kernel; one
+// - one or two tokens whose rows fit 48 KB of LDS (two slots of inner sizes up to
+//   5952, eight up to 1472): each slot by itself on dot products (moe_*_dot_kernel; one
 //   token, 8 of 64 experts of 2048 x 1024: 8.0 and 8.6 us, of which the
 //   weights' bytes are 5.5 together: launches and the chains of first reads);
 // - rows streamed past (moe_stream_kernel): a wave owns 16 columns of one
@@ -18,7 +19,8 @@
 //   (1 KB contiguous in the blocked layout).  24 tokens, 2 of 8 experts of
 //   4096 x 14336: 87 to 95 us for the 499 MB of gate and up (5.2 to 5.7 TB/s)
 //   and 51 to 59 for the 250 MB of down;
-// - from 16 rows an expert, tiles on the matrix cores (moe_tile.hip).
+// - from 16 rows an expert, within the widths and sizes of tile_form(), tiles on
+//   the matrix cores (moe_tile.hip).
 //
 // The codes become the exact bf16 values 128 + u; with P the product with them
 // and x1 the sum of the activations over a group (an MFMA against ones),
@@ -284,9 +286,15 @@ __global__ void __launch_bounds__(512, 2) moe_stream_kernel(MoeParams p, int rs)
     constexpr int AP = UP ? 1 : 2;                 // parts of an activation
     constexpr int RM = 16 * MB;                    // rows at a time
     // steps of weights in flight, and steps of a piece of the rows: with two of
-    // each, two workgroups of 8 waves share a compute unit and cover each other's
-    // waits (four of each: 138 registers and 64 KB of LDS, one workgroup, down
-    // products 5 to 10 us slower)
+    // each, 16 rows at a time in groups of 128 and 64 take 92 to 114 registers, so
+    // that two workgroups of 8 waves share a compute unit and cover each other's
+    // waits (four of each, groups of 128: 138 registers and 64 KB of LDS, one
+    // workgroup, down products 5 to 10 us slower).  Groups of 32 take 140 and 148,
+    // one workgroup: four words of scales a column and step, and the transposed
+    // codes.  32 rows at a time have one workgroup in any case (148 to 202
+    // registers), in groups of 32 with 38 to 43 of 256 in memory.  33 tokens, 8 of
+    // 128 experts of 2048 x 768, up and down product: groups of 128 39 and 25 us,
+    // of 64 46 and 31, of 32 64 and 43.
     constexpr int DEPTH = 2;
     constexpr int CS = 2;
     constexpr int ROW = CS * kStepK * 2;           // its bytes in a row
@@ -396,8 +404,15 @@ __global__ void __launch_bounds__(512, 2) moe_stream_kernel(MoeParams p, int rs)
         for (int i = 0; i < MB; ++i)
 #pragma unroll
             for (int j = 0; j < FJ; ++j) acc[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        // the piece that step i begins is in LDS for all waves (`behind`: loads
-        // issued after it that may be under way), and the next one on its way
+        // The piece that step i begins is in LDS for all waves, and the next one on
+        // its way.  `all`: the CS steps before it were whole, each with its load of
+        // weights, so exactly kBehind = CS LOADS loads of this wave came behind the
+        // piece's own, and as they end in order, waiting until no more than those are
+        // under way is enough.  That rests on load_b's FJ (1 + NG) loads a step: with
+        // fewer the wait would be over before the piece is there (more, and what the
+        // compiler adds, only make it longer).  Before the first step no load came
+        // behind the piece, and in the last steps fewer than kBehind do: then all are
+        // waited for.
         auto piece = [&](int i, bool all) {
             asm volatile("" ::: "memory");
             constexpr int kBehind = CS * LOADS;
@@ -779,7 +794,12 @@ hipError_t launch_dot(const MoeParams& p, hipStream_t stream) {
 }
 
 // The rows of an expert in tiles on the matrix cores (moe_tile.hip), where an
-// expert has enough of them.  Tiles against streaming, 64 experts of 2048 x
+// expert has enough of them, all row sums of a tile fit its LDS (widths up to 8192
+// in groups of 32, 16384 of 64, 32768 of 128), and the offsets of all rows fit 31
+// bits.  Beyond these limits the streamed form takes any number of rows: 2048
+// tokens, 2 of 8 experts of 4096 x 14336, groups of 32, 6.1 + 4.2 ms, 38 to 43
+// registers of a lane in memory, where the tiles of groups of 128 take 1.08 + 0.60
+// (the whole call 10.3 and 1.64, in groups of 64 2.34); 65536 tokens, 8 of 128 of 2048 x 768, 17.5 ms.  Tiles against streaming, 64 experts of 2048 x
 // 1024: 8 rows an expert 82 and 60 us, 16 rows 75 and 86, 32 rows 76 and 137;
 // groups of 64, 16 rows 91 and 97; 8 experts of 4096 x 14336: 15 rows 227 and
 // 227, 25 rows 215 and 270.
