@@ -1,6 +1,7 @@
 """What the binding of a layer's calls refuses before it calls the library, without a GPU: tensors on another GPU than
 the call's, in the form of objects that say they are there."""
 import math
+import os
 
 import pytest
 import torch
@@ -51,6 +52,9 @@ BF, I32, F32, U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 def w4(monkeypatch):
     """The binding with GPU 0 current and a library that may be asked for sizes only."""
     import w4_dequant_gemm_amd as w4
+    if not os.path.exists(w4.library_path):
+        from w4_dequant_gemm_amd import build
+        build.build()
     real = w4.lib()
 
     class Sizes:
